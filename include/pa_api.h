@@ -84,6 +84,7 @@ typedef enum pa_status {
 #define PA_DEVERR_WAIT_TIMEOUT 5 /* a kernel's bounded wait on a copy gave up */
 #define PA_DEVERR_PREFIX 6       /* pa_attention_cascade: a request's table does not start
                                     with request 0's common-prefix blocks */
+#define PA_DEVERR_POSITION 7     /* pa_norm_rope_write_kv: a position outside the table */
 
 /*
  * One-time per-device set-up for the current device (see the conventions).
@@ -200,6 +201,53 @@ pa_status pa_attention_fp8(const void* q, const void* k_cache, const void* v_cac
                            void* stream);
 
 /*
+ * Per-head norm, position rotation and KV-cache write in one pass: what a
+ * decoder layer does with its projections before attention. The scatter is
+ * pa_write_kv's ("vLLM v1 Deep Dive: How LLM(...) and the Server Boot and
+ * Generate", Part 3, "Aside - KV cache and prefix caching"); the norm and the
+ * rotation in front of it are the pages' "model" side and have no counterpart
+ * there.
+ *   q  [num_tokens][num_q_heads][head_dim], k, v [num_tokens][num_kv_heads]
+ *      [head_dim], bf16. A token's heads are contiguous; tokens are q_stride /
+ *      k_stride / v_stride elements apart (at least one token's heads, a
+ *      multiple of 8), so the three may be parts of one projection's output.
+ *   q_weight, k_weight  [head_dim] bf16, or NULL: that kind of head is not
+ *      normalised. y = x * w / sqrt(mean(x^2) + eps); eps finite and >= 0.
+ *   positions, cos_sin  positions[t] (int32) picks row cos_sin[positions[t]]
+ *      of the table [max_position][rotary_dim] fp32: the rotary_dim / 2
+ *      cosines, then the sines. rotary_dim is a multiple of 16 up to head_dim;
+ *      0 turns the rotation off (positions and cos_sin may then be NULL).
+ *   interleaved  0: elements i and i + rotary_dim / 2 are a pair; else 2i and
+ *      2i + 1. Elements past rotary_dim keep their value.
+ *   q_out  [num_tokens][num_q_heads][head_dim] bf16, contiguous; it may be q
+ *      itself where q is contiguous, and overlaps no other argument.
+ *   k_cache, v_cache, slot_mapping  as for pa_write_kv. A negative slot marks
+ *      a padding token, of which nothing is written, q_out included.
+ * Arithmetic is binary32, each result rounded once. head_dim 64 or 128, any
+ * number of heads. A slot outside the pool sets PA_DEVERR_SLOT and a position
+ * outside the table PA_DEVERR_POSITION; such a token is skipped whole.
+ */
+pa_status pa_norm_rope_write_kv(const void* q, const void* k, const void* v, long long q_stride,
+                                long long k_stride, long long v_stride, const int32_t* positions,
+                                const float* cos_sin, const void* q_weight, const void* k_weight,
+                                float eps, int rotary_dim, int interleaved, int max_position,
+                                const int64_t* slot_mapping, void* q_out, void* k_cache,
+                                void* v_cache, int num_tokens, int num_q_heads, int num_kv_heads,
+                                int head_dim, int block_size, int num_blocks, void* stream);
+
+/* The same into E4M3 caches: each element of K and V is stored as
+ * E4M3(y / scale), as pa_write_kv_fp8 does, from the binary32 y. */
+pa_status pa_norm_rope_write_kv_fp8(const void* q, const void* k, const void* v,
+                                    long long q_stride, long long k_stride, long long v_stride,
+                                    const int32_t* positions, const float* cos_sin,
+                                    const void* q_weight, const void* k_weight, float eps,
+                                    int rotary_dim, int interleaved, int max_position,
+                                    const int64_t* slot_mapping, void* q_out, void* k_cache,
+                                    void* v_cache, float k_scale, float v_scale, int num_tokens,
+                                    int num_q_heads, int num_kv_heads, int head_dim,
+                                    int block_size, int num_blocks, void* stream);
+
+/*
  * Cascade attention for a batch whose requests all share one common prefix
  * ("vLLM: An Exhaustive Technical Study for Kernel Engineers", 2.3 Automatic
  * prefix caching & KV reuse, cascade attention: when every request of a batch
@@ -241,6 +289,97 @@ pa_status pa_attention_cascade(const void* q, const void* k_cache, const void* v
                                int max_blocks_per_req, int max_query_len, int max_seq_len,
                                int common_prefix_len, void* workspace, size_t workspace_bytes,
                                void* stream);
+
+/*
+ * Accumulated attention weight of every cached key: what pa_evict_kv goes by.
+ * The pages have no counterpart.
+ *   out[r][h][i] = (i < ctx ? weights[r][h][i] : 0) + sum over the request's
+ *                  new tokens and the G query heads of KV head h of the softmax
+ *                  weight pa_attention gives key i
+ * with ctx = seq_lens[r] minus the new tokens, for 0 <= i < seq_lens[r]; a key
+ * that is new in this step starts at zero, so a fresh request's row needs no
+ * clearing. Entries past seq_lens[r], and the rows of requests without new
+ * tokens, are left untouched. Call it on the arguments of pa_attention, before
+ * or after it.
+ *   weights, out  [num_reqs][num_kv_heads][weights_stride] fp32; out may be
+ *                 weights itself (accumulation in place), else they must not
+ *                 overlap
+ *   workspace     at least pa_attention_weights_workspace_size(...) bytes,
+ *                 256-byte aligned, no initial contents required, used by one
+ *                 call at a time. The size grows with num_reqs x max_seq_len:
+ *                 4 bytes per (request, query head, key) for a decode batch.
+ * The other arguments are pa_attention's, and so are the limits (head_dim 64 or
+ * 128, groups of 1, 2, 4 or 8) and the errors. A request longer than
+ * weights_stride sets PA_DEVERR_LENGTHS and is skipped. Scores and sums are
+ * binary32; results do not depend on the order in which CTAs run.
+ */
+size_t pa_attention_weights_workspace_size(int num_reqs, int num_tokens, int num_q_heads,
+                                           int num_kv_heads, int head_dim, int max_query_len,
+                                           int max_seq_len);
+
+pa_status pa_attention_weights(const void* q, const void* k_cache, const int32_t* block_tables,
+                               const int32_t* seq_lens, const int32_t* query_start_loc,
+                               float scale, const float* weights, float* out,
+                               long long weights_stride, int num_reqs, int num_tokens,
+                               int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                               int num_blocks, int max_blocks_per_req, int max_query_len,
+                               int max_seq_len, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* The same over an E4M3 key cache (keys are value(code) * k_scale). */
+pa_status pa_attention_weights_fp8(const void* q, const void* k_cache,
+                                   const int32_t* block_tables, const int32_t* seq_lens,
+                                   const int32_t* query_start_loc, float scale, float k_scale,
+                                   const float* weights, float* out, long long weights_stride,
+                                   int num_reqs, int num_tokens, int num_q_heads,
+                                   int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                   int max_blocks_per_req, int max_query_len, int max_seq_len,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Cut a cache to `keep` tokens per KV head by accumulated attention weight.
+ * The pages leave eviction at the block level ("Inside the vLLM Engine", "The
+ * pool, the queue, and the hash"); this one drops tokens of a live request.
+ *
+ * Every request r with seq_lens[r] > keep is cut: each of its KV heads keeps
+ * the first `sinks` tokens, the last `recent` ones, and of the tokens between
+ * them the keep - sinks - recent with the largest weights (equal weights: the
+ * lowest position; a NaN counts less than any number). Their K and V rows are
+ * copied, in order of position, to the blocks new_block_tables[r]: the n-th
+ * kept token of a head to row n % 16 of block new_block_tables[r][n / 16].
+ * Rows past `keep` of the last new block are left untouched, and so are the
+ * old blocks. The heads of a request choose separately, so a slot no longer
+ * holds one token in all heads; attention does not need it to. Keys are moved
+ * as they are: a rotation by position stays the one they were written with.
+ * Requests with seq_lens[r] <= keep are left as they are: only new_seq_lens[r]
+ * is written for them.
+ *   k_cache, v_cache  the pool, elem_bytes (2: bf16, 1: E4M3 codes) per element
+ *   weights           [num_reqs][num_kv_heads][weights_stride] fp32, entries
+ *                     past a request's length not read (pa_attention_weights
+ *                     makes them)
+ *   new_block_tables  [num_reqs][max_new_blocks], max_new_blocks >=
+ *                     ceil(keep / 16). The blocks named for the requests that
+ *                     are cut must be distinct, and none of them may be a block
+ *                     that a request still holds: the copy is out of place.
+ *   new_seq_lens      [num_reqs] int32: min(seq_lens[r], keep); not seq_lens itself
+ *   kept              [num_reqs][num_kv_heads][keep] int32: the positions kept,
+ *                     rising (written for the requests that are cut)
+ *   new_weights       [num_reqs][num_kv_heads][new_weights_stride] fp32 or
+ *                     NULL: the kept tokens' weights; it must not overlap weights
+ *   max_seq_len       upper bound of seq_lens; a longer request, or one that
+ *                     its table or weights do not hold, sets PA_DEVERR_LENGTHS
+ *                     and is skipped
+ * sinks, recent >= 0, keep >= 1, sinks + recent <= keep (PA_ERR_INVALID_ARG).
+ * head_dim 64 or 128, block_size 16. A block id outside the pool sets
+ * PA_DEVERR_BLOCK_ID and its rows are not copied.
+ */
+pa_status pa_evict_kv(void* k_cache, void* v_cache, const int32_t* block_tables,
+                      const int32_t* seq_lens, const float* weights,
+                      const int32_t* new_block_tables, int32_t* new_seq_lens, int32_t* kept,
+                      float* new_weights, int num_reqs, int num_kv_heads, int head_dim,
+                      int elem_bytes, int block_size, int num_blocks, int max_blocks_per_req,
+                      int max_new_blocks, long long weights_stride, long long new_weights_stride,
+                      int max_seq_len, int keep, int recent, int sinks, void* stream);
 
 /*
  * pa_attention without a caller-provided workspace, for callers that cannot
@@ -315,7 +454,8 @@ pa_status pa_mapped_pointer(const void* host_ptr, void** device_ptr);
  * created by the caller) around every later launch of the given kernel on its
  * stream; pass NULL events to stop. Kernel ids: 0 write_kv, 1 planner,
  * 2 decode (split-KV), 3 prefill chunk, 4 cascade prefix pass, 5 split-KV
- * merge pass. Process-wide setting, not thread-safe.
+ * merge pass, 6 accumulated weights, 7 eviction (the last two: all launches of
+ * the call). Process-wide setting, not thread-safe.
  */
 pa_status pa_set_kernel_timer(int kernel_id, void* start_event, void* stop_event);
 

@@ -37,8 +37,10 @@ STATUS = {0: "PA_OK", -1: "PA_ERR_INVALID_ARG", -2: "PA_ERR_UNSUPPORTED",
           -3: "PA_ERR_WORKSPACE", -4: "PA_ERR_CUDA", -5: "PA_ERR_BOUNDS", -6: "PA_ERR_TIMEOUT"}
 DEVICE_ERRORS = {0: "none", 1: "slot outside the pool", 2: "block id outside the pool",
                  3: "inconsistent lengths", 4: "query_start_loc out of range",
-                 5: "bounded wait timed out", 6: "table does not start with the common prefix"}
-KERNEL_IDS = {"write_kv": 0, "plan": 1, "decode": 2, "prefill": 3, "prefix": 4, "merge": 5}
+                 5: "bounded wait timed out", 6: "table does not start with the common prefix",
+                 7: "position outside the rotation table"}
+KERNEL_IDS = {"write_kv": 0, "plan": 1, "decode": 2, "prefill": 3, "prefix": 4, "merge": 5,
+              "weights": 6, "evict": 7}
 
 
 class PagedAttentionError(RuntimeError):
@@ -85,6 +87,23 @@ def lib() -> ctypes.CDLL:
                                        _c_i, _c_i, _c_i, _c_i, _c_i, _c_i, _c_i, _c_p,
                                        ctypes.c_size_t, _c_p]
         L.pa_attention_fp8.restype = _c_i
+        _ll, _f = ctypes.c_longlong, ctypes.c_float
+        nr = [_c_p, _c_p, _c_p, _ll, _ll, _ll, _c_p, _c_p, _c_p, _c_p, _f, _c_i, _c_i, _c_i, _c_p,
+              _c_p, _c_p, _c_p]
+        L.pa_norm_rope_write_kv.argtypes = nr + [_c_i] * 6 + [_c_p]
+        L.pa_norm_rope_write_kv.restype = _c_i
+        L.pa_norm_rope_write_kv_fp8.argtypes = nr + [_f, _f] + [_c_i] * 6 + [_c_p]
+        L.pa_norm_rope_write_kv_fp8.restype = _c_i
+        L.pa_attention_weights_workspace_size.argtypes = [_c_i] * 7
+        L.pa_attention_weights_workspace_size.restype = ctypes.c_size_t
+        L.pa_attention_weights.argtypes = ([_c_p] * 5 + [_f, _c_p, _c_p, _ll] + [_c_i] * 10 +
+                                           [_c_p, ctypes.c_size_t, _c_p])
+        L.pa_attention_weights.restype = _c_i
+        L.pa_attention_weights_fp8.argtypes = ([_c_p] * 5 + [_f, _f, _c_p, _c_p, _ll] +
+                                               [_c_i] * 10 + [_c_p, ctypes.c_size_t, _c_p])
+        L.pa_attention_weights_fp8.restype = _c_i
+        L.pa_evict_kv.argtypes = [_c_p] * 9 + [_c_i] * 8 + [_ll, _ll] + [_c_i] * 4 + [_c_p]
+        L.pa_evict_kv.restype = _c_i
         L.pa_status_string.argtypes = [_c_i]
         L.pa_status_string.restype = ctypes.c_char_p
         L.pa_get_device_error.argtypes = [ctypes.POINTER(_c_i), ctypes.POINTER(ctypes.c_longlong),
@@ -167,6 +186,107 @@ def write_kv(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
                            _dev(v_cache, torch.bfloat16, "v_cache"), T, hkv, d, bs, nb,
                            _stream_ptr(stream))
     _check(st, "pa_write_kv")
+
+
+def _here(*tensors) -> None:
+    """The new operators take tensors of the current device only: the launch
+    goes there, whatever device a tensor lives on."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor on {t.device}; the current device is cuda:{dev}")
+
+
+def _heads(t: torch.Tensor, name: str) -> tuple[int, int]:
+    """(address, token stride in elements) of [tokens, heads, head_dim] whose
+    tokens may lie apart (a part of a wider projection)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    st = t.stride()
+    T, h, d = t.shape
+    if (d > 1 and st[2] != 1) or (h > 1 and st[1] != d):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return t.data_ptr(), (st[0] if T > 1 else h * d)
+
+
+def _norm_rope(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight,
+               eps, interleaved, out, cache_dtype, stream):
+    if q.dim() != 3 or k.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q, k and v are [tokens, heads, head_dim], a cache [blocks, Hkv, 16, D]")
+    T, hq, d = q.shape
+    nb, hkv, bs, d2 = k_cache.shape
+    if k.shape != (T, hkv, d) or v.shape != k.shape or v_cache.shape != k_cache.shape or d2 != d:
+        raise ValueError("shape mismatch between q, k, v and the caches")
+    if slot_mapping.shape != (T,):
+        raise ValueError("slot_mapping must be [num_tokens]")
+    if (positions is None) != (cos_sin is None):
+        raise ValueError("positions and cos_sin come together")
+    rot = max_pos = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2 or positions.shape != (T,):
+            raise ValueError("cos_sin must be [max_position, rotary_dim], positions [num_tokens]")
+        max_pos, rot = cos_sin.shape
+    for w in (q_weight, k_weight):
+        if w is not None and w.shape != (d,):
+            raise ValueError("a norm weight must be [head_dim]")
+    if out is None:
+        out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    _here(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight, out)
+    qp, qs = _heads(q, "q")
+    kp, ks = _heads(k, "k")
+    vp, vs = _heads(v, "v")
+    return out, (qp, kp, vp, qs, ks, vs,
+                 None if positions is None else _dev(positions, torch.int32, "positions"),
+                 None if cos_sin is None else _dev(cos_sin, torch.float32, "cos_sin"),
+                 None if q_weight is None else _dev(q_weight, torch.bfloat16, "q_weight"),
+                 None if k_weight is None else _dev(k_weight, torch.bfloat16, "k_weight"),
+                 float(eps), rot, int(bool(interleaved)), max_pos,
+                 _dev(slot_mapping, torch.int64, "slot_mapping"),
+                 _dev(out, torch.bfloat16, "out"), _dev(k_cache, cache_dtype, "k_cache"),
+                 _dev(v_cache, cache_dtype, "v_cache")), (T, hq, hkv, d, bs, nb,
+                                                          _stream_ptr(stream))
+
+
+def norm_rope_write_kv(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                       positions: torch.Tensor | None, cos_sin: torch.Tensor | None,
+                       slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                       *, q_weight: torch.Tensor | None = None,
+                       k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                       interleaved: bool = False, out: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+    """pa_norm_rope_write_kv: norm and rotate the heads of q [T, Hq, D] and k
+    [T, Hkv, D], scatter k and v into the caches, return the queries [T, Hq, D].
+
+    q, k and v may be views into one projection's output (tokens apart, a
+    token's heads contiguous). ``cos_sin`` is fp32 [max_position, rotary_dim],
+    cosines then sines; ``positions`` is int32 [T]; both None: no rotation.
+    """
+    out, a, b = _norm_rope(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight,
+                           k_weight, eps, interleaved, out, torch.bfloat16, stream)
+    _check(lib().pa_norm_rope_write_kv(*a, *b), "pa_norm_rope_write_kv")
+    return out
+
+
+def norm_rope_write_kv_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                           positions: torch.Tensor | None, cos_sin: torch.Tensor | None,
+                           slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                           v_cache: torch.Tensor, k_scale: float, v_scale: float, *,
+                           q_weight: torch.Tensor | None = None,
+                           k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                           interleaved: bool = False, out: torch.Tensor | None = None,
+                           stream=None) -> torch.Tensor:
+    """pa_norm_rope_write_kv_fp8: the same into E4M3 caches (uint8)."""
+    out, a, b = _norm_rope(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight,
+                           k_weight, eps, interleaved, out, torch.uint8, stream)
+    _check(lib().pa_norm_rope_write_kv_fp8(*a, float(k_scale), float(v_scale), *b),
+           "pa_norm_rope_write_kv_fp8")
+    return out
 
 
 def workspace_size(num_reqs: int, num_tokens: int, num_q_heads: int, num_kv_heads: int,
@@ -293,6 +413,120 @@ def attention_cascade(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
         _dev(workspace, torch.uint8, "workspace"), int(workspace.numel()), _stream_ptr(stream))
     _check(st, "pa_attention_cascade")
     return out
+
+
+def weights_workspace_size(num_reqs: int, num_tokens: int, num_q_heads: int, num_kv_heads: int,
+                           head_dim: int, max_query_len: int, max_seq_len: int) -> int:
+    return int(lib().pa_attention_weights_workspace_size(num_reqs, num_tokens, num_q_heads,
+                                                         num_kv_heads, head_dim, max_query_len,
+                                                         max_seq_len))
+
+
+def _weights(q, k_cache, block_tables, seq_lens, query_start_loc, scales, weights, max_query_len,
+             max_seq_len, out, workspace, cache_dtype, stream, name):
+    T, hq, d = q.shape
+    nb, hkv, bs, d2 = k_cache.shape
+    R = int(seq_lens.shape[0])
+    if d2 != d:
+        raise ValueError("shape mismatch between q and the cache")
+    if query_start_loc.shape != (R + 1,) or block_tables.dim() != 2 or block_tables.shape[0] != R:
+        raise ValueError("metadata shapes must be qsl [R+1], block_tables [R, max_blocks]")
+    if weights.dim() != 3 or weights.shape[:2] != (R, hkv):
+        raise ValueError("weights must be [num_reqs, num_kv_heads, width]")
+    if out is None:
+        out = weights
+    elif out.shape != weights.shape:
+        raise ValueError("out must have weights' shape")
+    if workspace is None:
+        need = weights_workspace_size(R, T, hq, hkv, d, int(max_query_len), int(max_seq_len))
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    _here(q, k_cache, block_tables, seq_lens, query_start_loc, weights, out, workspace)
+    st = getattr(lib(), name)(
+        _dev(q, torch.bfloat16, "q"), _dev(k_cache, cache_dtype, "k_cache"),
+        _dev(block_tables, torch.int32, "block_tables"), _dev(seq_lens, torch.int32, "seq_lens"),
+        _dev(query_start_loc, torch.int32, "query_start_loc"), *scales,
+        _dev(weights, torch.float32, "weights"), _dev(out, torch.float32, "out"),
+        int(weights.shape[2]), R, T, hq, hkv, d, bs, nb, int(block_tables.shape[1]),
+        int(max_query_len), int(max_seq_len), _dev(workspace, torch.uint8, "workspace"),
+        int(workspace.numel()), _stream_ptr(stream))
+    _check(st, name)
+    return out
+
+
+def attention_weights(q: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.Tensor,
+                      seq_lens: torch.Tensor, query_start_loc: torch.Tensor, scale: float,
+                      weights: torch.Tensor, *, max_query_len: int, max_seq_len: int,
+                      out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """pa_attention_weights: add this step's attention weight of every key,
+    summed over the new tokens and the query heads of its KV head, to
+    ``weights`` fp32 [R, Hkv, width >= seq_len]; in place unless ``out`` is given."""
+    return _weights(q, k_cache, block_tables, seq_lens, query_start_loc, (float(scale),), weights,
+                    max_query_len, max_seq_len, out, workspace, torch.bfloat16, stream,
+                    "pa_attention_weights")
+
+
+def attention_weights_fp8(q: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.Tensor,
+                          seq_lens: torch.Tensor, query_start_loc: torch.Tensor, scale: float,
+                          k_scale: float, weights: torch.Tensor, *, max_query_len: int,
+                          max_seq_len: int, out: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """pa_attention_weights_fp8: the same over an E4M3 key cache (uint8)."""
+    return _weights(q, k_cache, block_tables, seq_lens, query_start_loc,
+                    (float(scale), float(k_scale)), weights, max_query_len, max_seq_len, out,
+                    workspace, torch.uint8, stream, "pa_attention_weights_fp8")
+
+
+def evict_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+             seq_lens: torch.Tensor, weights: torch.Tensor, new_block_tables: torch.Tensor, *,
+             keep: int, recent: int, sinks: int = 0, max_seq_len: int,
+             new_seq_lens: torch.Tensor | None = None, kept: torch.Tensor | None = None,
+             new_weights: torch.Tensor | None = None, stream=None):
+    """pa_evict_kv: cut every request longer than ``keep`` to ``keep`` tokens per
+    KV head (its first ``sinks``, last ``recent`` and heaviest others), copying
+    the rows kept into the blocks of ``new_block_tables`` [R, >= ceil(keep / 16)].
+
+    ``weights`` is fp32 [R, Hkv, width] (:func:`attention_weights`). Returns
+    ``(new_seq_lens [R] int32, kept [R, Hkv, keep] int32, new_weights
+    [R, Hkv, >= keep] fp32)``; given buffers are filled, missing ones allocated.
+    Requests of at most ``keep`` tokens stay in their old blocks: their rows of
+    ``kept`` and ``new_weights`` are not written.
+    """
+    nb, hkv, bs, d = k_cache.shape
+    R = int(seq_lens.shape[0])
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("the caches must be alike")
+    if k_cache.dtype not in (torch.bfloat16, torch.uint8):
+        raise TypeError("a cache must be torch.bfloat16 or torch.uint8 (E4M3 codes)")
+    if weights.dim() != 3 or weights.shape[:2] != (R, hkv):
+        raise ValueError("weights must be [num_reqs, num_kv_heads, width]")
+    for t in (block_tables, new_block_tables):
+        if t.dim() != 2 or t.shape[0] != R:
+            raise ValueError("block tables must be [num_reqs, blocks]")
+    dev = k_cache.device
+    if new_seq_lens is None:
+        new_seq_lens = torch.empty(R, dtype=torch.int32, device=dev)
+    if kept is None:
+        kept = torch.empty((R, hkv, max(int(keep), 0)), dtype=torch.int32, device=dev)
+    if new_weights is None:
+        new_weights = torch.empty((R, hkv, max(int(keep), 0)), dtype=torch.float32, device=dev)
+    if new_seq_lens.shape != (R,) or kept.shape != (R, hkv, keep) or \
+            new_weights.dim() != 3 or new_weights.shape[:2] != (R, hkv):
+        raise ValueError("new_seq_lens must be [R], kept [R, Hkv, keep], new_weights [R, Hkv, width]")
+    _here(k_cache, v_cache, block_tables, seq_lens, weights, new_block_tables, new_seq_lens, kept,
+          new_weights)
+    st = lib().pa_evict_kv(
+        _dev(k_cache, k_cache.dtype, "k_cache"), _dev(v_cache, v_cache.dtype, "v_cache"),
+        _dev(block_tables, torch.int32, "block_tables"), _dev(seq_lens, torch.int32, "seq_lens"),
+        _dev(weights, torch.float32, "weights"),
+        _dev(new_block_tables, torch.int32, "new_block_tables"),
+        _dev(new_seq_lens, torch.int32, "new_seq_lens"), _dev(kept, torch.int32, "kept"),
+        _dev(new_weights, torch.float32, "new_weights"), R, hkv, d, k_cache.element_size(), bs,
+        nb, int(block_tables.shape[1]), int(new_block_tables.shape[1]), int(weights.shape[2]),
+        int(new_weights.shape[2]), int(max_seq_len), int(keep), int(recent), int(sinks),
+        _stream_ptr(stream))
+    _check(st, "pa_evict_kv")
+    return new_seq_lens, kept, new_weights
 
 
 def get_device_error(clear: bool = True) -> tuple[int, int]:

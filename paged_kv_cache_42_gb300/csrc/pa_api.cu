@@ -45,7 +45,7 @@ std::atomic<int> g_token_major{1};  // pa_set_option(PA_OPT_DECODE_TOKEN_MAJOR, 
 std::atomic<int> g_cascade_overlap{1};  // pa_set_option(PA_OPT_CASCADE_OVERLAP, ...)
 std::atomic<int> g_tm_ctas{2};  // pa_set_option(PA_OPT_DECODE_TM_CTAS_PER_SM, ...)
 std::atomic<int> g_mixed_ctas{0};  // pa_set_option(PA_OPT_MIXED_PREFILL_CTAS, ...): 0 = planned
-constexpr int kNumTimers = 6;  // write, plan, decode, prefill, cascade prefix, merge
+constexpr int kNumTimers = 8;  // write, plan, decode, prefill, cascade prefix, merge, weights, evict
 cudaEvent_t g_timer_start[kNumTimers] = {};
 cudaEvent_t g_timer_stop[kNumTimers] = {};
 
@@ -207,9 +207,105 @@ pa_status write_kv_impl(const void* k, const void* v, const int64_t* slot_mappin
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+pa_status norm_rope_write_impl(const void* q, const void* k, const void* v, long long q_stride,
+                               long long k_stride, long long v_stride, const int32_t* positions,
+                               const float* cos_sin, const void* q_weight, const void* k_weight,
+                               float eps, int rotary_dim, int interleaved, int max_position,
+                               const int64_t* slot_mapping, void* q_out, void* k_cache,
+                               void* v_cache, int kv_fp8, float k_scale, float v_scale,
+                               int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                               int block_size, int num_blocks, void* stream) {
+  if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || num_blocks < 0 ||
+      rotary_dim < 0 || rotary_dim > head_dim || max_position < 0 || !(eps >= 0.f && eps < INFINITY))
+    return PA_ERR_INVALID_ARG;
+  if (kv_fp8 && !(k_scale > 0.f && k_scale < INFINITY && v_scale > 0.f && v_scale < INFINITY))
+    return PA_ERR_INVALID_ARG;
+  if (block_size != kBlockSize || (head_dim != 64 && head_dim != 128) || rotary_dim % 16 != 0)
+    return PA_ERR_UNSUPPORTED;
+  const NvtxRange range(kv_fp8 ? "pa_norm_rope_write_kv_fp8" : "pa_norm_rope_write_kv");
+  if (num_tokens == 0) return PA_OK;
+  if (!q || !k || !v || !slot_mapping || !q_out || !k_cache || !v_cache ||
+      (rotary_dim > 0 && (!positions || !cos_sin)))
+    return PA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) ||
+      !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(q_weight) ||
+      !aligned16(k_weight) || !aligned16(cos_sin) ||
+      (reinterpret_cast<uintptr_t>(positions) & 3u) ||
+      (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+    return PA_ERR_INVALID_ARG;
+  const long long q_row = (long long)num_q_heads * head_dim;
+  const long long kv_row = (long long)num_kv_heads * head_dim;
+  if (q_stride < q_row || k_stride < kv_row || v_stride < kv_row || q_stride % 8 != 0 ||
+      k_stride % 8 != 0 || v_stride % 8 != 0)
+    return PA_ERR_INVALID_ARG;
+  if (q_out == q && q_stride != q_row) return PA_ERR_INVALID_ARG;  // rows would overtake each other
+  DeviceState* d = nullptr;
+  if (pa_status st = device_state(&d)) return st;
+  NormRopeParams p;
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.positions = positions;
+  p.cos_sin = cos_sin;
+  p.q_weight = static_cast<const uint16_t*>(q_weight);
+  p.k_weight = static_cast<const uint16_t*>(k_weight);
+  p.eps = eps;
+  p.rotary_dim = rotary_dim;
+  p.interleaved = interleaved ? 1 : 0;
+  p.max_position = rotary_dim > 0 ? max_position : 1;  // no table: position 0 stands for all
+  p.slot_mapping = slot_mapping;
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.kv_fp8 = kv_fp8;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.num_tokens = num_tokens;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.num_slots = (long long)num_blocks * kBlockSize;
+  p.err = d->err;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  TimerScope timer(0, s);
+  const cudaError_t e = launch_norm_rope_write(p, head_dim, s);
+  g_launches.fetch_add(1);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
+
+pa_status pa_norm_rope_write_kv(const void* q, const void* k, const void* v, long long q_stride,
+                                long long k_stride, long long v_stride, const int32_t* positions,
+                                const float* cos_sin, const void* q_weight, const void* k_weight,
+                                float eps, int rotary_dim, int interleaved, int max_position,
+                                const int64_t* slot_mapping, void* q_out, void* k_cache,
+                                void* v_cache, int num_tokens, int num_q_heads, int num_kv_heads,
+                                int head_dim, int block_size, int num_blocks, void* stream) {
+  return norm_rope_write_impl(q, k, v, q_stride, k_stride, v_stride, positions, cos_sin, q_weight,
+                              k_weight, eps, rotary_dim, interleaved, max_position, slot_mapping,
+                              q_out, k_cache, v_cache, 0, 1.f, 1.f, num_tokens, num_q_heads,
+                              num_kv_heads, head_dim, block_size, num_blocks, stream);
+}
+
+pa_status pa_norm_rope_write_kv_fp8(const void* q, const void* k, const void* v,
+                                    long long q_stride, long long k_stride, long long v_stride,
+                                    const int32_t* positions, const float* cos_sin,
+                                    const void* q_weight, const void* k_weight, float eps,
+                                    int rotary_dim, int interleaved, int max_position,
+                                    const int64_t* slot_mapping, void* q_out, void* k_cache,
+                                    void* v_cache, float k_scale, float v_scale, int num_tokens,
+                                    int num_q_heads, int num_kv_heads, int head_dim,
+                                    int block_size, int num_blocks, void* stream) {
+  return norm_rope_write_impl(q, k, v, q_stride, k_stride, v_stride, positions, cos_sin, q_weight,
+                              k_weight, eps, rotary_dim, interleaved, max_position, slot_mapping,
+                              q_out, k_cache, v_cache, 1, k_scale, v_scale, num_tokens,
+                              num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, stream);
+}
 
 pa_status pa_write_kv(const void* k, const void* v, const int64_t* slot_mapping, void* k_cache,
                       void* v_cache, int num_tokens, int num_kv_heads, int head_dim,
@@ -527,6 +623,191 @@ pa_status pa_attention_cascade(const void* q, const void* k_cache, const void* v
                         num_reqs, num_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
                         num_blocks, max_blocks_per_req, max_query_len, max_seq_len,
                         common_prefix_len, 0, 1.f, 1.f, workspace, workspace_bytes, stream);
+}
+
+size_t pa_attention_weights_workspace_size(int num_reqs, int num_tokens, int num_q_heads,
+                                           int num_kv_heads, int head_dim, int max_query_len,
+                                           int max_seq_len) {
+  if (num_reqs < 0 || num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
+      head_dim <= 0 || num_q_heads % num_kv_heads != 0 || max_query_len < 0 || max_seq_len < 0 ||
+      !supported_group(num_q_heads / num_kv_heads))
+    return 0;
+  const size_t n = weights_layout(num_reqs, num_tokens, num_q_heads, num_kv_heads, max_query_len,
+                                  max_seq_len).total;
+  return n ? n : 256;
+}
+
+}  // extern "C"
+
+namespace {
+
+pa_status weights_impl(const void* q, const void* k_cache, const int32_t* block_tables,
+                       const int32_t* seq_lens, const int32_t* query_start_loc, float scale,
+                       int kv_fp8, float k_scale, const float* weights, float* out,
+                       long long weights_stride, int num_reqs, int num_tokens, int num_q_heads,
+                       int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                       int max_blocks_per_req, int max_query_len, int max_seq_len,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  bool nothing = false;
+  // pa_attention's checks; there is no V here and out is checked below
+  if (pa_status st = check_attention_args(
+          q, k_cache, k_cache, block_tables, seq_lens, query_start_loc, scale, q, num_reqs,
+          num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+          max_blocks_per_req, max_query_len, max_seq_len, 0, kv_fp8, k_scale, 1.f, &nothing))
+    return st;
+  if (weights_stride < 0) return PA_ERR_INVALID_ARG;
+  if (nothing) return PA_OK;
+  if (!weights || !out || (reinterpret_cast<uintptr_t>(weights) & 3u) ||
+      (reinterpret_cast<uintptr_t>(out) & 3u))
+    return PA_ERR_INVALID_ARG;
+  if (max_query_len == 0 || max_seq_len == 0) return PA_OK;  // no request can have a new token
+  if (max_seq_len > (1 << 30)) return PA_ERR_UNSUPPORTED;  // key positions are 32-bit
+  const WeightsLayout lay = weights_layout(num_reqs, num_tokens, num_q_heads, num_kv_heads,
+                                           max_query_len, max_seq_len);
+  // grids and work lists are indexed with 32 bits
+  const long long rh = (long long)num_reqs * num_kv_heads;
+  if (rh * (lay.padded_len / 128 + 1) >= (1LL << 31) ||
+      (long long)lay.num_slots * num_kv_heads * (lay.padded_len / 2048 + 1) >= (1LL << 31))
+    return PA_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < lay.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return PA_ERR_WORKSPACE;
+  DeviceState* d = nullptr;
+  if (pa_status st = device_state(&d)) return st;
+  const NvtxRange range(kv_fp8 ? "pa_attention_weights_fp8" : "pa_attention_weights");
+  unsigned char* const ws = static_cast<unsigned char*>(workspace);
+  WeightsParams p;
+  p.q = static_cast<const uint16_t*>(q);
+  p.k_cache = k_cache;
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.qsl = query_start_loc;
+  p.weights = weights;
+  p.out = out;
+  p.weights_stride = weights_stride;
+  p.scale_log2 = scale * 1.4426950408889634f * (kv_fp8 ? k_scale : 1.f);
+  p.num_reqs = num_reqs;
+  p.num_tokens = num_tokens;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.group = num_q_heads / num_kv_heads;
+  p.num_blocks = num_blocks;
+  p.bt_stride = max_blocks_per_req;
+  p.max_query_len = max_query_len;
+  p.max_seq_len = max_seq_len;
+  p.num_chunks = lay.num_chunks;
+  p.padded_len = lay.padded_len;
+  p.stored_rows = lay.stored_rows;
+  p.num_slots = lay.num_slots;
+  p.max_items[0] = lay.max_items[0];
+  p.max_items[1] = lay.max_items[1];
+  p.stats = reinterpret_cast<float*>(ws + lay.stats_off);
+  p.scores = reinterpret_cast<float*>(ws + lay.scores_off);
+  p.counts = reinterpret_cast<int*>(ws + lay.counts_off);
+  p.parts = reinterpret_cast<int*>(ws + lay.parts_off);
+  p.items[0] = reinterpret_cast<int4*>(ws + lay.items1_off);
+  p.items[1] = reinterpret_cast<int4*>(ws + lay.items2_off);
+  p.lse = reinterpret_cast<float*>(ws + lay.lse_off);
+  p.partial = reinterpret_cast<float2*>(ws + lay.partial_off);
+  p.err = d->err;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  TimerScope timer(6, s);
+  int launches = 0;
+  const cudaError_t e = launch_weights(p, head_dim, kv_fp8 != 0, d->num_sms, s, &launches);
+  g_launches.fetch_add(launches);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status pa_attention_weights(const void* q, const void* k_cache, const int32_t* block_tables,
+                               const int32_t* seq_lens, const int32_t* query_start_loc,
+                               float scale, const float* weights, float* out,
+                               long long weights_stride, int num_reqs, int num_tokens,
+                               int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                               int num_blocks, int max_blocks_per_req, int max_query_len,
+                               int max_seq_len, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  return weights_impl(q, k_cache, block_tables, seq_lens, query_start_loc, scale, 0, 1.f, weights,
+                      out, weights_stride, num_reqs, num_tokens, num_q_heads, num_kv_heads,
+                      head_dim, block_size, num_blocks, max_blocks_per_req, max_query_len,
+                      max_seq_len, workspace, workspace_bytes, stream);
+}
+
+pa_status pa_attention_weights_fp8(const void* q, const void* k_cache,
+                                   const int32_t* block_tables, const int32_t* seq_lens,
+                                   const int32_t* query_start_loc, float scale, float k_scale,
+                                   const float* weights, float* out, long long weights_stride,
+                                   int num_reqs, int num_tokens, int num_q_heads,
+                                   int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                   int max_blocks_per_req, int max_query_len, int max_seq_len,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  return weights_impl(q, k_cache, block_tables, seq_lens, query_start_loc, scale, 1, k_scale,
+                      weights, out, weights_stride, num_reqs, num_tokens, num_q_heads,
+                      num_kv_heads, head_dim, block_size, num_blocks, max_blocks_per_req,
+                      max_query_len, max_seq_len, workspace, workspace_bytes, stream);
+}
+
+pa_status pa_evict_kv(void* k_cache, void* v_cache, const int32_t* block_tables,
+                      const int32_t* seq_lens, const float* weights,
+                      const int32_t* new_block_tables, int32_t* new_seq_lens, int32_t* kept,
+                      float* new_weights, int num_reqs, int num_kv_heads, int head_dim,
+                      int elem_bytes, int block_size, int num_blocks, int max_blocks_per_req,
+                      int max_new_blocks, long long weights_stride, long long new_weights_stride,
+                      int max_seq_len, int keep, int recent, int sinks, void* stream) {
+  if (num_reqs < 0 || num_kv_heads <= 0 || head_dim <= 0 || num_blocks < 0 ||
+      max_blocks_per_req < 0 || max_new_blocks < 0 || weights_stride < 0 || max_seq_len < 0 ||
+      keep < 1 || recent < 0 || sinks < 0 || (long long)sinks + recent > keep)
+    return PA_ERR_INVALID_ARG;
+  if (block_size != kBlockSize || (head_dim != 64 && head_dim != 128) ||
+      (elem_bytes != 1 && elem_bytes != 2))
+    return PA_ERR_UNSUPPORTED;
+  if (max_new_blocks < (keep - 1) / kBlockSize + 1 || (new_weights && new_weights_stride < keep))
+    return PA_ERR_INVALID_ARG;
+  const NvtxRange range("pa_evict_kv");
+  if (num_reqs == 0) return PA_OK;
+  if (!k_cache || !v_cache || !block_tables || !seq_lens || !weights || !new_block_tables ||
+      !new_seq_lens || !kept || new_weights == weights || new_seq_lens == seq_lens)
+    return PA_ERR_INVALID_ARG;
+  const void* words[] = {block_tables, seq_lens,     weights, new_block_tables,
+                         new_seq_lens, kept, new_weights};
+  for (const void* w : words)
+    if (reinterpret_cast<uintptr_t>(w) & 3u) return PA_ERR_INVALID_ARG;
+  if (!aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_INVALID_ARG;
+  // the row lists are one CTA per (request, KV head) and 64 kept tokens
+  if ((long long)num_reqs * num_kv_heads * ((keep - 1) / 64 + 1) >= (1LL << 31))
+    return PA_ERR_UNSUPPORTED;
+  DeviceState* d = nullptr;
+  if (pa_status st = device_state(&d)) return st;
+  EvictParams p;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.weights = weights;
+  p.new_block_tables = new_block_tables;
+  p.new_seq_lens = new_seq_lens;
+  p.kept = kept;
+  p.new_weights = new_weights;
+  p.num_reqs = num_reqs;
+  p.num_kv_heads = num_kv_heads;
+  p.num_blocks = num_blocks;
+  p.max_blocks_per_req = max_blocks_per_req;
+  p.max_new_blocks = max_new_blocks;
+  p.weights_stride = weights_stride;
+  p.new_weights_stride = new_weights_stride;
+  p.max_seq_len = max_seq_len;
+  p.keep = keep;
+  p.recent = recent;
+  p.sinks = sinks;
+  p.smem_keys = 0;
+  p.err = d->err;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  TimerScope timer(7, s);
+  const cudaError_t e = launch_evict(p, head_dim * elem_bytes, s);
+  g_launches.fetch_add(2);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 pa_status pa_mapped_pointer(const void* host_ptr, void** device_ptr) {

@@ -302,6 +302,83 @@ struct WriteParams {
   unsigned long long* err;
 };
 
+struct NormRopeParams {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  long long q_stride, k_stride, v_stride;  // elements from one token to the next
+  const int32_t* positions;
+  const float* cos_sin;                    // [max_position][rotary_dim]: cosines, then sines
+  const uint16_t* q_weight;                // null: that head kind is not normalised
+  const uint16_t* k_weight;
+  float eps;
+  int rotary_dim, interleaved, max_position;
+  const int64_t* slot_mapping;
+  uint16_t* q_out;
+  void* k_cache;  // bf16, or E4M3 codes when kv_fp8
+  void* v_cache;
+  int kv_fp8;
+  float k_scale, v_scale;
+  int num_tokens, num_q_heads, num_kv_heads;
+  long long num_slots;
+  unsigned long long* err;
+};
+
+// Workspace of pa_attention_weights (host only; 256-byte aligned regions).
+struct WeightsLayout {
+  // few rows: per (request, kv head, 256-key chunk) 8 x {max, sum}; scaled
+  // scores [request][kv head][padded_len][stored_rows]
+  size_t stats_off, scores_off;
+  // many rows: item counts, key parts per row tile, the two work lists, row
+  // statistics [kv head][slot][128] and their parts [part][kv head][slot][128]
+  size_t counts_off, parts_off, items1_off, items2_off, lse_off, partial_off;
+  size_t total;
+  int num_chunks, padded_len, stored_rows, num_slots;
+  int max_items[2];  // entries of the work lists
+};
+WeightsLayout weights_layout(int num_reqs, int num_tokens, int num_q_heads, int num_kv_heads,
+                             int max_query_len, int max_seq_len);
+
+struct WeightsParams {
+  const uint16_t* q;
+  const void* k_cache;  // bf16, or E4M3 codes
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* qsl;
+  const float* weights;  // [num_reqs][num_kv_heads][weights_stride]
+  float* out;            // the same shape; may be weights itself
+  long long weights_stride;
+  float scale_log2;  // scale x log2(e) (x k_scale): scores in base-2 exponent units
+  int num_reqs, num_tokens, num_q_heads, num_kv_heads, group, num_blocks, bt_stride;
+  int max_query_len, max_seq_len;
+  int num_chunks, padded_len, stored_rows, num_slots, max_items[2];  // see WeightsLayout
+  float* stats;
+  float* scores;
+  int* counts;
+  int* parts;
+  int4* items[2];
+  float* lse;
+  float2* partial;
+  unsigned long long* err;
+};
+
+struct EvictParams {
+  void* k_cache;
+  void* v_cache;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const float* weights;  // [num_reqs][num_kv_heads][weights_stride]
+  const int32_t* new_block_tables;
+  int32_t* new_seq_lens;
+  int32_t* kept;       // [num_reqs][num_kv_heads][keep]
+  float* new_weights;  // [num_reqs][num_kv_heads][new_weights_stride]; null: not wanted
+  int num_reqs, num_kv_heads, num_blocks, max_blocks_per_req, max_new_blocks;
+  long long weights_stride, new_weights_stride;
+  int max_seq_len, keep, recent, sinks;
+  int smem_keys;  // weights the select kernel keeps in shared memory (set at launch)
+  unsigned long long* err;
+};
+
 // Device error word: [0] = code, [1] = detail. First error wins.
 __device__ inline void report_error(unsigned long long* err, int code, long long detail) {
   if (atomicCAS(err, 0ull, (unsigned long long)code) == 0ull)
@@ -323,6 +400,12 @@ pa_status check_attention_args(const void* q, const void* k_cache, const void* v
 
 // Launchers (return the launch's cudaError_t).
 cudaError_t launch_write_kv(const WriteParams& p, cudaStream_t s);
+cudaError_t launch_norm_rope_write(const NormRopeParams& p, int head_dim, cudaStream_t s);
+// The accumulated-weight kernels, in order; *launches: how many.
+cudaError_t launch_weights(const WeightsParams& p, int head_dim, bool f8, int num_sms,
+                           cudaStream_t s, int* launches);
+// The two eviction kernels, in order; row_bytes = head_dim x element bytes.
+cudaError_t launch_evict(EvictParams p, int row_bytes, cudaStream_t s);
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t s);
 // head_dim / G select the instantiation; unsupported combinations return
 // cudaErrorInvalidValue. occ_cap bounds the resident CTAs per SM (the grid is

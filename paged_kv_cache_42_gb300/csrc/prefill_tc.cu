@@ -194,38 +194,6 @@ __device__ __forceinline__ Item get_item(const PrefillParams& p, int t) {
   return it;
 }
 
-// One key row of an E4M3 tile widened to bf16 into a 128B-swizzled operand
-// tile (row r: 16-byte unit u of 64-element chunk c lives at
-// c * CHUNK + r * 128 + (u ^ (r & 7)) * 16). A row that is not a key of the
-// sequence is written as zeros.
-template <int D>
-__device__ __forceinline__ void widen_e4m3_row(const unsigned char* src, bool valid,
-                                               unsigned char* tile, int r) {
-  constexpr int CHUNK = 128 * 128;
-  uint4 raw[D / 16];
-#pragma unroll
-  for (int j = 0; j < D / 16; ++j)
-    raw[j] = valid ? __ldg(reinterpret_cast<const uint4*>(src) + j) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-  for (int j = 0; j < D / 16; ++j) {
-    const uint32_t w4[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-    uint32_t o[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 a = e4m3x2_to_float2((uint16_t)(w4[i] & 0xffffu));
-      const float2 b = e4m3x2_to_float2((uint16_t)(w4[i] >> 16));
-      o[2 * i] = float2_to_bf16x2(a.x, a.y);
-      o[2 * i + 1] = float2_to_bf16x2(b.x, b.y);
-    }
-    // elements 16j .. 16j+15: chunk 16j / 64, units (16j % 64) / 8 and the next
-    const int c = (16 * j) / 64, u = ((16 * j) % 64) / 8;
-    unsigned char* const rowp = tile + c * CHUNK + r * 128;
-    *reinterpret_cast<uint4*>(rowp + ((u ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-    *reinterpret_cast<uint4*>(rowp + (((u + 1) ^ (r & 7)) << 4)) =
-        make_uint4(o[4], o[5], o[6], o[7]);
-  }
-}
-
 // The r-th work item of CTA blockIdx.x among the g CTAs that take items.
 // Items come sorted longest first; rounds of g items alternate direction (CTA b takes b, then 2g-1-b, then
 // 2g+b, ...), so a CTA that drew a long item in one round draws a short one
