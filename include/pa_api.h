@@ -291,6 +291,42 @@ pa_status pa_attention_cascade(const void* q, const void* k_cache, const void* v
                                void* stream);
 
 /*
+ * Attention with a sliding window and visible first tokens: pa_attention where
+ * a new token at position p (its request's context plus its place in the span)
+ * attends to keys i <= p with i > p - window or i < sinks, i.e. to the last
+ * `window` keys, its own included, and the first `sinks`. The pages name
+ * sliding-window layers ("vLLM: An Exhaustive Technical Study for Kernel
+ * Engineers", 2.1, hybrid KV cache groups) and sinks (2.4, the TRT-LLM
+ * backend) without describing either.
+ *   window >= 1, sinks >= 0 (PA_ERR_INVALID_ARG). A window of max_seq_len keys
+ *   or more is pa_attention, bit for bit.
+ * The other arguments, the workspace and the errors are pa_attention's (_fp8:
+ * pa_attention_fp8's). The tables keep their logical layout, so a request's
+ * blocks that none of its new tokens attends to may have been released: their
+ * table entries are not read, whatever they hold. Of the keys in a block that
+ * is read, those that no new token of the request attends to may hold
+ * anything; K and V of the others must be finite, as for pa_attention. Time
+ * and bytes follow the keys attended to, not the sequence length.
+ */
+pa_status pa_attention_window(const void* q, const void* k_cache, const void* v_cache,
+                              const int32_t* block_tables, const int32_t* seq_lens,
+                              const int32_t* query_start_loc, float scale, void* out,
+                              int num_reqs, int num_tokens, int num_q_heads, int num_kv_heads,
+                              int head_dim, int block_size, int num_blocks,
+                              int max_blocks_per_req, int max_query_len, int max_seq_len,
+                              int window, int sinks, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+pa_status pa_attention_window_fp8(const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* block_tables, const int32_t* seq_lens,
+                                  const int32_t* query_start_loc, float scale, float k_scale,
+                                  float v_scale, void* out, int num_reqs, int num_tokens,
+                                  int num_q_heads, int num_kv_heads, int head_dim,
+                                  int block_size, int num_blocks, int max_blocks_per_req,
+                                  int max_query_len, int max_seq_len, int window, int sinks,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Accumulated attention weight of every cached key: what pa_evict_kv goes by.
  * The pages have no counterpart.
  *   out[r][h][i] = (i < ctx ? weights[r][h][i] : 0) + sum over the request's

@@ -94,6 +94,12 @@ def lib() -> ctypes.CDLL:
         L.pa_norm_rope_write_kv.restype = _c_i
         L.pa_norm_rope_write_kv_fp8.argtypes = nr + [_f, _f] + [_c_i] * 6 + [_c_p]
         L.pa_norm_rope_write_kv_fp8.restype = _c_i
+        L.pa_attention_window.argtypes = ([_c_p] * 6 + [_f, _c_p] + [_c_i] * 12 +
+                                          [_c_p, ctypes.c_size_t, _c_p])
+        L.pa_attention_window.restype = _c_i
+        L.pa_attention_window_fp8.argtypes = ([_c_p] * 6 + [_f, _f, _f, _c_p] + [_c_i] * 12 +
+                                              [_c_p, ctypes.c_size_t, _c_p])
+        L.pa_attention_window_fp8.restype = _c_i
         L.pa_attention_weights_workspace_size.argtypes = [_c_i] * 7
         L.pa_attention_weights_workspace_size.restype = ctypes.c_size_t
         L.pa_attention_weights.argtypes = ([_c_p] * 5 + [_f, _c_p, _c_p, _ll] + [_c_i] * 10 +
@@ -413,6 +419,61 @@ def attention_cascade(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
         _dev(workspace, torch.uint8, "workspace"), int(workspace.numel()), _stream_ptr(stream))
     _check(st, "pa_attention_cascade")
     return out
+
+
+def _window(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scales, window, sinks,
+            max_query_len, max_seq_len, out, workspace, cache_dtype, stream, name):
+    T, hq, d = q.shape
+    nb, hkv, bs, d2 = k_cache.shape
+    R = int(seq_lens.shape[0])
+    if d2 != d or v_cache.shape != k_cache.shape:
+        raise ValueError("shape mismatch between q and the caches")
+    if query_start_loc.shape != (R + 1,) or block_tables.dim() != 2 or block_tables.shape[0] != R:
+        raise ValueError("metadata shapes must be qsl [R+1], block_tables [R, max_blocks]")
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if workspace is None:
+        need = workspace_size(R, T, hq, hkv, d)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    _here(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, workspace,
+          out if out.is_cuda else None)
+    st = getattr(lib(), name)(
+        _dev(q, torch.bfloat16, "q"), _dev(k_cache, cache_dtype, "k_cache"),
+        _dev(v_cache, cache_dtype, "v_cache"), _dev(block_tables, torch.int32, "block_tables"),
+        _dev(seq_lens, torch.int32, "seq_lens"),
+        _dev(query_start_loc, torch.int32, "query_start_loc"), *scales, _out(out), R, T, hq, hkv,
+        d, bs, nb, int(block_tables.shape[1]), int(max_query_len), int(max_seq_len), int(window),
+        int(sinks), _dev(workspace, torch.uint8, "workspace"), int(workspace.numel()),
+        _stream_ptr(stream))
+    _check(st, name)
+    return out
+
+
+def attention_window(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                     block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                     query_start_loc: torch.Tensor, scale: float, *, window: int, sinks: int = 0,
+                     max_query_len: int, max_seq_len: int, out: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """pa_attention_window: :func:`attention` where a token attends to the last
+    ``window`` keys (its own included) and the first ``sinks``. The workspace is
+    ``workspace_size(...)`` bytes, as for :func:`attention`."""
+    return _window(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, (float(scale),),
+                   window, sinks, max_query_len, max_seq_len, out, workspace, torch.bfloat16,
+                   stream, "pa_attention_window")
+
+
+def attention_window_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                         block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                         query_start_loc: torch.Tensor, scale: float, k_scale: float,
+                         v_scale: float, *, window: int, sinks: int = 0, max_query_len: int,
+                         max_seq_len: int, out: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """pa_attention_window_fp8: the same over E4M3 caches (uint8)."""
+    return _window(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc,
+                   (float(scale), float(k_scale), float(v_scale)), window, sinks, max_query_len,
+                   max_seq_len, out, workspace, torch.uint8, stream, "pa_attention_window_fp8")
 
 
 def weights_workspace_size(num_reqs: int, num_tokens: int, num_q_heads: int, num_kv_heads: int,

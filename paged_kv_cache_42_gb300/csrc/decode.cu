@@ -140,7 +140,10 @@ struct Loc {
   int k, tok, req, len, base;
 };
 
-template <int D, int G, int WARPS, int NSTAGE, bool F8>
+// WIN: windowed attention (win_span): a unit's positions are the blocks its
+// token attends to, and a key of such a block outside the window is treated
+// as one past the sequence end.
+template <int D, int G, int WARPS, int NSTAGE, bool F8, bool WIN>
 __device__ __forceinline__ void decode_body(const DecodeParams& p) {
   using C = Cfg<D, G, F8>;
   using WS = WarpSmem<D, G, NSTAGE, F8>;
@@ -187,7 +190,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
                    qlen > p.max_query_len || L > p.max_seq_len) {
           report_error(p.err, PA_DEVERR_LENGTHS, r);
         } else if (qlen == 1) {
-          n = Hkv_ * ((L + kBlockSize - 1) / kBlockSize);
+          n = Hkv_ * (WIN ? win_span(L, p.window, p.sinks).nb : (L + kBlockSize - 1) / kBlockSize);
         }
       }
       int incl = n;  // warp inclusive scan of positions
@@ -266,6 +269,11 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
     b.len = kl.len;
     const int base = kl.base;
     int nb = (b.len + kBlockSize - 1) / kBlockSize - kstart;  // blocks after a cascade prefix
+    WinSpan ws{0, 0, 0, 0};
+    if constexpr (WIN) {
+      ws = win_span(b.len, p.window, p.sinks);
+      nb = ws.nb;
+    }
     nb = nb < 1 ? 1 : nb;
     b.nb = nb;
     b.end = base + nb * Hkv;
@@ -274,7 +282,8 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
     b.blk = off - b.kv * nb;
     int pid = 0;
     if (y < E) {
-      pid = __ldg(p.block_tables + (size_t)kl.req * p.bt_stride + kstart + b.blk);
+      pid = __ldg(p.block_tables + (size_t)kl.req * p.bt_stride +
+                  (WIN ? win_block(ws, b.blk) : kstart + b.blk));
       if (pid < 0 || pid >= p.num_blocks) {
         report_error(p.err, PA_DEVERR_BLOCK_ID, y);
         pid = 0;
@@ -449,7 +458,17 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
       l_run = 0.f;
     }
 
-    const int nvalid = min(kBlockSize, len - (kstart + blk) * kBlockSize);
+    int nvalid = min(kBlockSize, len - (kstart + blk) * kBlockSize);
+    // WIN: bit t set: the token attends to the block's key t; stand: a set bit
+    uint32_t seen = 0;
+    int stand = 0;
+    if constexpr (WIN) {
+      const WinSpan ws = win_span(len, p.window, p.sinks);
+      const int key0 = win_block(ws, blk) * kBlockSize;
+      nvalid = min(kBlockSize, len - key0);
+      seen = __ballot_sync(kFull, lane < kBlockSize && win_sees(ws, key0 + lane, len, p.sinks));
+      stand = __ffs((int)seen) - 1;
+    }
 
     // ---- scores: s = (q * scale * log2 e) . k for the lane's (head, token) ---------
     float sc[C::NPASS];
@@ -498,7 +517,11 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
       }
       sc[ps] = reduce_heads<G, C::TPT>(part, lane);
     }
-    if (nvalid < kBlockSize) {  // keys past the sequence end (their slots may hold anything)
+    if constexpr (WIN) {
+#pragma unroll
+      for (int ps = 0; ps < C::NPASS; ++ps)
+        if (!(seen >> (ps * C::TPP + tg) & 1u)) sc[ps] = -INFINITY;
+    } else if (nvalid < kBlockSize) {  // keys past the sequence end (their slots may hold anything)
 #pragma unroll
       for (int ps = 0; ps < C::NPASS; ++ps)
         if (ps * C::TPP + tg >= nvalid) sc[ps] = -INFINITY;
@@ -547,7 +570,8 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
         const int t = stp * C::RPS + rrow;
         {
           float2 vf[C::VD / 2];
-          const unsigned char* const vrow = vbase + min(t, tmax) * D * C::EB;
+          const unsigned char* const vrow =
+              vbase + (WIN ? ((seen >> t & 1u) ? t : stand) : min(t, tmax)) * D * C::EB;
           if constexpr (F8) {  // v_scale is applied to the output
             if constexpr (C::VD == 8) {
               const uint2 vv = *reinterpret_cast<const uint2*>(vrow);
@@ -752,9 +776,9 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
   }
 }
 
-template <int D, int G, int WARPS, int NSTAGE, bool F8>
+template <int D, int G, int WARPS, int NSTAGE, bool F8, bool WIN>
 __global__ void __launch_bounds__(WARPS * 32) pa_decode_kernel(const DecodeParams p) {
-  decode_body<D, G, WARPS, NSTAGE, F8>(p);
+  decode_body<D, G, WARPS, NSTAGE, F8, WIN>(p);
   // overlapped cascade: complete only after the prefix pass's grid, so that
   // the merge pass after this grid sees the prefix partials too
   if (p.overlap && threadIdx.x == 0) griddep_wait();
@@ -772,9 +796,9 @@ constexpr int decode_smem(bool self_plan) {
          (self_plan ? (int)sizeof(UnitInfo) * (kSelfPlanMaxReqs + 1) : 0);
 }
 
-template <int D, int G, int WARPS, int NSTAGE, bool F8>
+template <int D, int G, int WARPS, int NSTAGE, bool F8, bool WIN>
 cudaError_t decode_grid(int num_sms, int occ_cap, bool self_plan, int* grid_out) {
-  auto kern = pa_decode_kernel<D, G, WARPS, NSTAGE, F8>;
+  auto kern = pa_decode_kernel<D, G, WARPS, NSTAGE, F8, WIN>;
   const int smem = decode_smem<D, G, WARPS, NSTAGE, F8>(self_plan);
   static int occ_cache[64][2] = {};
   int dev = 0;
@@ -797,13 +821,13 @@ cudaError_t decode_grid(int num_sms, int occ_cap, bool self_plan, int* grid_out)
   return cudaSuccess;
 }
 
-template <int D, int G, int WARPS, int NSTAGE, bool F8>
+template <int D, int G, int WARPS, int NSTAGE, bool F8, bool WIN>
 cudaError_t launch_decode_t(const DecodeParams& p, int num_sms, int occ_cap, cudaStream_t s,
                             int* workers_out) {
-  auto kern = pa_decode_kernel<D, G, WARPS, NSTAGE, F8>;
+  auto kern = pa_decode_kernel<D, G, WARPS, NSTAGE, F8, WIN>;
   const int smem = decode_smem<D, G, WARPS, NSTAGE, F8>(p.self_plan != 0);
   int grid = 0;
-  cudaError_t e = decode_grid<D, G, WARPS, NSTAGE, F8>(num_sms, occ_cap, p.self_plan != 0, &grid);
+  cudaError_t e = decode_grid<D, G, WARPS, NSTAGE, F8, WIN>(num_sms, occ_cap, p.self_plan != 0, &grid);
   if (e != cudaSuccess) return e;
   *workers_out = grid * WARPS;
   cudaLaunchConfig_t cfg = {};
@@ -867,15 +891,20 @@ template <int D, int G, bool F8>
 cudaError_t launch_one(const DecodeParams& p, int num_sms, int occ_cap, cudaStream_t s,
                        int* workers_out) {
   using T = Tuning<D, G, F8>;
-  return launch_decode_t<D, G, T::WARPS, T::STAGES, F8>(p, num_sms, occ_cap, s, workers_out);
+  return p.window > 0
+             ? launch_decode_t<D, G, T::WARPS, T::STAGES, F8, true>(p, num_sms, occ_cap, s, workers_out)
+             : launch_decode_t<D, G, T::WARPS, T::STAGES, F8, false>(p, num_sms, occ_cap, s,
+                                                                     workers_out);
 }
 
 template <int D, int G, bool F8>
-int workers_one(int num_sms, int occ_cap) {
+int workers_one(bool windowed, int num_sms, int occ_cap) {
   using T = Tuning<D, G, F8>;
   int grid = 0;
-  if (decode_grid<D, G, T::WARPS, T::STAGES, F8>(num_sms, occ_cap, false, &grid) != cudaSuccess)
-    return 0;
+  const cudaError_t e =
+      windowed ? decode_grid<D, G, T::WARPS, T::STAGES, F8, true>(num_sms, occ_cap, false, &grid)
+               : decode_grid<D, G, T::WARPS, T::STAGES, F8, false>(num_sms, occ_cap, false, &grid);
+  if (e != cudaSuccess) return 0;
   return grid * T::WARPS;
 }
 
@@ -905,8 +934,8 @@ cudaError_t launch_decode(const DecodeParams& p, int head_dim, int group, bool f
   PA_DECODE_DISPATCH(launch_one, cudaErrorInvalidValue, p, num_sms, occ_cap, s, workers_out);
 }
 
-int decode_workers(int head_dim, int group, bool f8, int num_sms, int occ_cap) {
-  PA_DECODE_DISPATCH(workers_one, 0, num_sms, occ_cap);
+int decode_workers(int head_dim, int group, bool f8, bool windowed, int num_sms, int occ_cap) {
+  PA_DECODE_DISPATCH(workers_one, 0, windowed, num_sms, occ_cap);
 }
 
 }  // namespace pa

@@ -249,7 +249,11 @@ struct TcDecodeParams {
   DecodeParams d;
 };
 
-template <int G, bool F8>
+// WIN: windowed attention. A unit's positions are then the blocks its token
+// attends to (win_span), which may skip from the sinks to the window inside a
+// tile; a key of such a block that the token does not attend to is treated as
+// one past the sequence end (P = 0, its V row cleared).
+template <int G, bool F8, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     pa_decode_tc_kernel(const __grid_constant__ TcDecodeParams tp) {
   using L = TcL<F8>;
@@ -323,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                    qlen > p.max_query_len || Lr > p.max_seq_len) {
           report_error(p.err, PA_DEVERR_LENGTHS, r);
         } else if (qlen == 1) {
-          n = Hkv_ * ((Lr + kBlockSize - 1) / kBlockSize);
+          n = Hkv_ * (WIN ? win_span(Lr, p.window, p.sinks).nb : (Lr + kBlockSize - 1) / kBlockSize);
         }
       }
       int incl = n;  // warp inclusive scan of positions
@@ -392,6 +396,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     int k = 0;
     UnitInfo U{0, 0, 0, 0}, Un{0, 0, 0, 0};
     int nb = 1, kv = 0, blk = 0, y = S, pstart = 0, np = 0;
+    WinSpan ws{0, 0, 0, 0};  // WIN: the current unit's blocks
+    // the unit's blocks on this path
+    auto unit_blocks = [&]() -> int {
+      if constexpr (WIN) {
+        ws = win_span(U.len, p.window, p.sinks);
+        return max(1, ws.nb);
+      }
+      return max(1, (U.len + kBlockSize - 1) / kBlockSize - kstart);
+    };
     bool pfirst = true;  // the current portion has not been in a tile yet
     if (S < E) {
       int lo = 0, hi = K;  // base[lo] <= S < base[hi]
@@ -411,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       k = lo;
       U = load_unit(k);
       Un = load_unit(k + 1);
-      nb = max(1, (U.len + kBlockSize - 1) / kBlockSize - kstart);
+      nb = unit_blocks();
       const int off = S - U.base;
       kv = off / nb;
       blk = off - kv * nb;
@@ -468,7 +481,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (F8 && (lane >> 3) == j)
           t.invl = __ldg(p.qinv + ((size_t)U.tok * Hkv + kv) * 8 + (lane & 7));
         if (lane >= t.nblk && lane < t.nblk + n) {
-          t.pid = __ldg(p.block_tables + (size_t)U.req * p.bt_stride + kstart + blk + (lane - t.nblk));
+          int b = kstart + blk + (lane - t.nblk);
+          if constexpr (WIN) b = win_block(ws, b);
+          t.pid = __ldg(p.block_tables + (size_t)U.req * p.bt_stride + b);
           t.kvl = kv;
         }
         pfirst = false;
@@ -489,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               U = Un;
               Un = load_unit(k + 1);
             } while (U.len <= 0);
-            nb = max(1, (U.len + kBlockSize - 1) / kBlockSize - kstart);
+            nb = unit_blocks();
           }
         }
       }
@@ -877,8 +892,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool in0 = (r0.flags & F_ACTIVE) && m >= r0.row0 && m < r0.row0 + r0.nrows;
       const bool in1 = (r1.flags & F_ACTIVE) && m >= r1.row0 && m < r1.row0 + r1.nrows;
       const int my = in0 ? 0 : (in1 ? 1 : -1);
-      const bool valid = in0 ? (r0.key0 + (m - r0.row0) < r0.len)
-                             : (in1 ? (r1.key0 + (m - r1.row0) < r1.len) : false);
+      bool valid = in0 ? (r0.key0 + (m - r0.row0) < r0.len)
+                       : (in1 ? (r1.key0 + (m - r1.row0) < r1.len) : false);
+      if constexpr (WIN) {
+        const int len = in0 ? r0.len : r1.len;
+        const int vk = in0 ? r0.key0 + (m - r0.row0) : r1.key0 + (m - r1.row0);  // list position x 16
+        const WinSpan sp = win_span(len, p.window, p.sinks);
+        const int key = win_block(sp, vk / kBlockSize) * kBlockSize + vk % kBlockSize;
+        valid = (in0 || in1) && win_sees(sp, key, len, p.sinks);
+      }
       // P^T buffer b is free once the P.V of tile i - kSP has completed
       if (i >= kSP && !wait(M::B_PFREE + b, i / kSP - 1)) { ok = false; break; }
       // One pass per active slot (two only where the tile crosses from one
@@ -1108,7 +1130,7 @@ __global__ void __launch_bounds__(256) pa_qsplit_kernel(const DecodeParams p) {
 // ---------------------------------------------------------------------------------------
 namespace {
 
-template <int G, bool F8>
+template <int G, bool F8, bool WIN>
 cudaError_t launch_tc_t(const DecodeParams& d, int grid, cudaStream_t s) {
   TcDecodeParams tp;
   tp.d = d;
@@ -1139,7 +1161,7 @@ cudaError_t launch_tc_t(const DecodeParams& d, int grid, cudaStream_t s) {
         !encode_tmap_bf16(&tp.tm_v, 4, d.v_cache, cd, cs, cb))
       return cudaErrorInvalidValue;
   }
-  auto kern = pa_decode_tc_kernel<G, F8>;
+  auto kern = pa_decode_tc_kernel<G, F8, WIN>;
   static bool attr_set[64] = {false};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1163,6 +1185,13 @@ cudaError_t launch_tc_t(const DecodeParams& d, int grid, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, tp);
+}
+
+template <int G>
+cudaError_t launch_tc_g(const DecodeParams& p, bool f8, int grid, cudaStream_t s) {
+  if (p.window > 0)
+    return f8 ? launch_tc_t<G, true, true>(p, grid, s) : launch_tc_t<G, false, true>(p, grid, s);
+  return f8 ? launch_tc_t<G, true, false>(p, grid, s) : launch_tc_t<G, false, false>(p, grid, s);
 }
 
 template <int G>
@@ -1198,10 +1227,10 @@ cudaError_t launch_decode_tc(const DecodeParams& p, int group, bool f8, int num_
   const int grid = decode_tc_workers(num_sms);
   *workers_out = grid;
   switch (group) {
-    case 1: return f8 ? launch_tc_t<1, true>(p, grid, s) : launch_tc_t<1, false>(p, grid, s);
-    case 2: return f8 ? launch_tc_t<2, true>(p, grid, s) : launch_tc_t<2, false>(p, grid, s);
-    case 4: return f8 ? launch_tc_t<4, true>(p, grid, s) : launch_tc_t<4, false>(p, grid, s);
-    case 8: return f8 ? launch_tc_t<8, true>(p, grid, s) : launch_tc_t<8, false>(p, grid, s);
+    case 1: return launch_tc_g<1>(p, f8, grid, s);
+    case 2: return launch_tc_g<2>(p, f8, grid, s);
+    case 4: return launch_tc_g<4>(p, f8, grid, s);
+    case 8: return launch_tc_g<8>(p, f8, grid, s);
   }
   return cudaErrorInvalidValue;
 }

@@ -155,7 +155,7 @@ struct TmDecodeParams {
   DecodeParams d;
 };
 
-template <int G, int CPS>
+template <int G, int CPS, bool WIN>
 __global__ void __launch_bounds__(kTmThreads, CPS)
     pa_decode_tm_kernel(const __grid_constant__ TmDecodeParams tp) {
   using L = TmL<G, CPS>;
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kTmThreads, CPS)
                    qlen > p.max_query_len || Lr > p.max_seq_len) {
           report_error(p.err, PA_DEVERR_LENGTHS, r);
         } else if (qlen == 1) {
-          n = (Lr + kBlockSize - 1) / kBlockSize;
+          n = WIN ? win_span(Lr, p.window, p.sinks).nb : (Lr + kBlockSize - 1) / kBlockSize;
         }
       }
       int incl = n;
@@ -275,6 +275,14 @@ __global__ void __launch_bounds__(kTmThreads, CPS)
     int k = 0;
     UnitInfo U{0, 0, 0, 0}, Un{0, 0, 0, 0};
     int nb = 1, blk = 0, y = S, pstart = 0, np = 0;
+    WinSpan ws{0, 0, 0, 0};  // WIN: the current token's blocks
+    auto token_blocks = [&]() -> int {
+      if constexpr (WIN) {
+        ws = win_span(U.len, p.window, p.sinks);
+        return max(1, ws.nb);
+      }
+      return max(1, (U.len + kBlockSize - 1) / kBlockSize);
+    };
     bool pfirst = true;
     if (S < E) {
       int lo = 0, hi = K;  // base[lo] <= S < base[hi]
@@ -294,7 +302,7 @@ __global__ void __launch_bounds__(kTmThreads, CPS)
       k = lo;
       U = load_unit(k);
       Un = load_unit(k + 1);
-      nb = max(1, (U.len + kBlockSize - 1) / kBlockSize);
+      nb = token_blocks();
       blk = S - U.base;
       pstart = blk;
       if (w > 0 && lane == 0) {  // the merge task of the slice boundary before this worker
@@ -334,14 +342,15 @@ __global__ void __launch_bounds__(kTmThreads, CPS)
       t.inv0 = t.inv1 = 0.f;
       if (y >= E) return t;
       const bool last = blk + 1 == nb || y + 1 == E;
-      t.r = TmRec{U.tok, U.len, blk * kBlockSize,
+      const int b = WIN ? win_block(ws, blk) : blk;  // the logical block
+      t.r = TmRec{U.tok, U.len, b * kBlockSize,
                   (pfirst ? T_FIRST : 0) | (last ? T_LAST : 0) |
                       ((last && blk + 1 == nb && pstart == 0) ? T_WHOLE : 0) |
                       ((np & 1) ? T_PAR : 0),
                   {0, 0, 0, 0}};
       t.live = 1;
       t.lastblk = blk + 1 == nb;
-      if (lane == 0) t.pid = __ldg(p.block_tables + (size_t)U.req * p.bt_stride + blk);
+      if (lane == 0) t.pid = __ldg(p.block_tables + (size_t)U.req * p.bt_stride + b);
       if (waited) load_inv(t);
       pfirst = false;
       ++y;
@@ -352,7 +361,7 @@ __global__ void __launch_bounds__(kTmThreads, CPS)
           U = Un;
           Un = load_unit(k + 1);
         } while (U.len <= 0);
-        nb = max(1, (U.len + kBlockSize - 1) / kBlockSize);
+        nb = token_blocks();
         blk = 0;
         pstart = 0;
         pfirst = true;
@@ -609,7 +618,10 @@ __global__ void __launch_bounds__(kTmThreads, CPS)
       const int b = i & 1;  // S^T and P'^T buffer of this tile
       if (!wait(L::B_S + b, i >> 1)) { ok = false; break; }
       tc_fence_after();
-      const bool valid = rec.key0 + kk < rec.len;
+      // WIN: a key outside the token's window is treated as one past the end
+      const bool valid = WIN ? win_sees(win_span(rec.len, p.window, p.sinks), rec.key0 + kk,
+                                        rec.len, p.sinks)
+                             : rec.key0 + kk < rec.len;
       // P'^T buffer b is free once the P.V of tile i - 2 has completed
       if (i >= 2 && !wait(L::B_PFREE + b, (i >> 1) - 1)) { ok = false; break; }
       // scores of this thread's key for its KV head's G query rows (hi + lo,
@@ -757,8 +769,8 @@ __global__ void __launch_bounds__(kTmThreads, CPS)
 // ---------------------------------------------------------------------------------------
 namespace {
 
-template <int G, int CPS>
-cudaError_t launch_tm_t(const DecodeParams& d, int grid, cudaStream_t s) {
+template <int G, int CPS, bool WIN>
+cudaError_t launch_tm_w(const DecodeParams& d, int grid, cudaStream_t s) {
   using L = TmL<G, CPS>;
   TmDecodeParams tp;
   tp.d = d;
@@ -776,7 +788,7 @@ cudaError_t launch_tm_t(const DecodeParams& d, int grid, cudaStream_t s) {
       !encode_tmap_u8(&tp.tm_k, 2, d.k_cache, cd, cs, cb) ||
       !encode_tmap_u8(&tp.tm_v, 2, d.v_cache, cd, cs, cb))
     return cudaErrorInvalidValue;
-  auto kern = pa_decode_tm_kernel<G, CPS>;
+  auto kern = pa_decode_tm_kernel<G, CPS, WIN>;
   static bool attr_set[64] = {false};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -803,6 +815,12 @@ cudaError_t launch_tm_t(const DecodeParams& d, int grid, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, tp);
+}
+
+template <int G, int CPS>
+cudaError_t launch_tm_t(const DecodeParams& d, int grid, cudaStream_t s) {
+  return d.window > 0 ? launch_tm_w<G, CPS, true>(d, grid, s)
+                      : launch_tm_w<G, CPS, false>(d, grid, s);
 }
 
 }  // namespace

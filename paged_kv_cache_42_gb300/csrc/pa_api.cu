@@ -348,10 +348,12 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
                          const int32_t* query_start_loc, float scale, void* out, int num_reqs,
                          int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
                          int block_size, int num_blocks, int max_blocks_per_req,
-                         int max_query_len, int max_seq_len, int prefix_len, int kv_fp8,
-                         float k_scale, float v_scale, void* workspace,
+                         int max_query_len, int max_seq_len, int prefix_len, int window,
+                         int sinks, int kv_fp8, float k_scale, float v_scale, void* workspace,
                          size_t workspace_bytes, void* stream) {
   bool nothing = false;
+  // a window that holds every key of the batch hides none
+  if (window >= max_seq_len) window = sinks = 0;
   if (pa_status st = check_attention_args(
           q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale, out, num_reqs,
           num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
@@ -370,6 +372,7 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
   DeviceState* d = nullptr;
   if (pa_status st = device_state(&d)) return st;
   const NvtxRange range(prefix_len > 0 ? "pa_attention_cascade"
+                        : window > 0   ? (kv_fp8 ? "pa_attention_window_fp8" : "pa_attention_window")
                                        : (kv_fp8 ? "pa_attention_fp8" : "pa_attention"));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
@@ -437,11 +440,14 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
       decode_tm_supported(head_dim, group, num_kv_heads, decode_tm_workers(group, d->num_sms, tm_cps));
   const int launched = use_tm   ? decode_tm_workers(group, d->num_sms, tm_cps)
                        : use_tc ? decode_tc_workers(d->num_sms)
-                                : decode_workers(head_dim, pp.group, kv_fp8 != 0, dec_sms, occ_cap);
+                                : decode_workers(head_dim, pp.group, kv_fp8 != 0, window > 0, dec_sms,
+                                                occ_cap);
   if (launched <= 0) return PA_ERR_CUDA;
   const int cap = g_max_workers.load();
   pp.num_workers = (cap > 0 && cap < launched) ? cap : launched;
   pp.token_major = use_tm ? 1 : 0;
+  pp.window = window;
+  pp.sinks = sinks;
   // A mixed batch on the tensor-core split-KV kernel (bf16) may run its
   // prefill chunks on a few SMs beside the split-KV work (the planner decides
   // how many, or none); the E4M3 path keeps its query-split pass between them.
@@ -489,6 +495,8 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
     pl.scale_log2 = scale * 1.4426950408889634f * (kv_fp8 ? k_scale : 1.f);
     pl.overlap = prefix_len > 0 ? c_overlap : overlap;
     pl.prefix_ctas = prefix_ctas;
+    pl.window = window;
+    pl.sinks = sinks;
     pl.err = d->err;
     TimerScope timer(prefix_len > 0 ? 4 : 3, s);
     const cudaError_t e = launch_prefill(pl, d->num_sms, s);
@@ -532,6 +540,8 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
   dp.qinv = reinterpret_cast<const float*>(ws + lay.qinv_off);
   dp.overlap = (overlap || c_overlap) ? 1 : 0;
   dp.fold_later = c_overlap;
+  dp.window = window;
+  dp.sinks = sinks;
   dp.err = d->err;
   if (use_tc && kv_fp8) {  // the E4M3 tensor-core kernel takes the queries split
     const cudaError_t e = launch_qsplit(dp, group, s);
@@ -592,8 +602,8 @@ pa_status pa_attention(const void* q, const void* k_cache, const void* v_cache,
                        size_t workspace_bytes, void* stream) {
   return attention_impl(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale, out,
                         num_reqs, num_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
-                        num_blocks, max_blocks_per_req, max_query_len, max_seq_len, 0, 0, 1.f,
-                        1.f, workspace, workspace_bytes, stream);
+                        num_blocks, max_blocks_per_req, max_query_len, max_seq_len, 0, 0, 0, 0,
+                        1.f, 1.f, workspace, workspace_bytes, stream);
 }
 
 pa_status pa_attention_fp8(const void* q, const void* k_cache, const void* v_cache,
@@ -606,7 +616,7 @@ pa_status pa_attention_fp8(const void* q, const void* k_cache, const void* v_cac
                            void* stream) {
   return attention_impl(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale, out,
                         num_reqs, num_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
-                        num_blocks, max_blocks_per_req, max_query_len, max_seq_len, 0, 1,
+                        num_blocks, max_blocks_per_req, max_query_len, max_seq_len, 0, 0, 0, 1,
                         k_scale, v_scale, workspace, workspace_bytes, stream);
 }
 
@@ -622,7 +632,37 @@ pa_status pa_attention_cascade(const void* q, const void* k_cache, const void* v
   return attention_impl(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale, out,
                         num_reqs, num_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
                         num_blocks, max_blocks_per_req, max_query_len, max_seq_len,
-                        common_prefix_len, 0, 1.f, 1.f, workspace, workspace_bytes, stream);
+                        common_prefix_len, 0, 0, 0, 1.f, 1.f, workspace, workspace_bytes, stream);
+}
+
+pa_status pa_attention_window(const void* q, const void* k_cache, const void* v_cache,
+                              const int32_t* block_tables, const int32_t* seq_lens,
+                              const int32_t* query_start_loc, float scale, void* out,
+                              int num_reqs, int num_tokens, int num_q_heads, int num_kv_heads,
+                              int head_dim, int block_size, int num_blocks,
+                              int max_blocks_per_req, int max_query_len, int max_seq_len,
+                              int window, int sinks, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  if (window < 1 || sinks < 0) return PA_ERR_INVALID_ARG;
+  return attention_impl(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale, out,
+                        num_reqs, num_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
+                        num_blocks, max_blocks_per_req, max_query_len, max_seq_len, 0, window,
+                        sinks, 0, 1.f, 1.f, workspace, workspace_bytes, stream);
+}
+
+pa_status pa_attention_window_fp8(const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* block_tables, const int32_t* seq_lens,
+                                  const int32_t* query_start_loc, float scale, float k_scale,
+                                  float v_scale, void* out, int num_reqs, int num_tokens,
+                                  int num_q_heads, int num_kv_heads, int head_dim,
+                                  int block_size, int num_blocks, int max_blocks_per_req,
+                                  int max_query_len, int max_seq_len, int window, int sinks,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  if (window < 1 || sinks < 0) return PA_ERR_INVALID_ARG;
+  return attention_impl(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale, out,
+                        num_reqs, num_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
+                        num_blocks, max_blocks_per_req, max_query_len, max_seq_len, 0, window,
+                        sinks, 1, k_scale, v_scale, workspace, workspace_bytes, stream);
 }
 
 size_t pa_attention_weights_workspace_size(int num_reqs, int num_tokens, int num_q_heads,

@@ -52,6 +52,36 @@ struct UnitInfo {
 };
 static_assert(sizeof(UnitInfo) == 16, "UnitInfo is loaded as one 16-byte vector");
 
+// Windowed attention: a token that sees `len` keys at most attends to the first
+// `sinks` and the last `window` of them. WinSpan lists the 16-key blocks that
+// hold a key it attends to: logical blocks 0 .. sb - 1, then from block
+// sb + gap on, nb in all (position b of that list is block b, or b + gap from
+// position sb on). Every listed block holds at least one such key, so a
+// running maximum taken from any of them is finite. window 0: no window, all
+// blocks listed.
+struct WinSpan {
+  int nb, sb, gap;
+  int lo;  // keys sinks .. lo - 1 are not attended to (lo <= sinks: all are)
+};
+__host__ __device__ inline WinSpan win_span(int len, int window, int sinks) {
+  WinSpan s;
+  s.nb = s.sb = (len + kBlockSize - 1) / kBlockSize;
+  s.gap = 0;
+  s.lo = window > 0 && len > window ? len - window : 0;
+  if (s.lo <= sinks) return s;
+  s.sb = (sinks + kBlockSize - 1) / kBlockSize;  // sinks < lo here: no overflow
+  s.gap = s.lo / kBlockSize - s.sb;  // -1: the window starts in the last sink block
+  if (s.gap < 0) s.gap = 0;
+  s.nb -= s.gap;
+  return s;
+}
+__host__ __device__ inline int win_block(const WinSpan& s, int b) {
+  return b < s.sb ? b : b + s.gap;
+}
+__host__ __device__ inline bool win_sees(const WinSpan& s, int key, int len, int sinks) {
+  return key < len && (key >= s.lo || key < sinks);
+}
+
 struct WsHeader {
   int num_units;      // K: tokens with work on the split-KV path
   int num_positions;  // W: sum over units of Hkv * ceil(len / 16)
@@ -83,6 +113,22 @@ constexpr float kOverlapMargin = 0.85f;  // prefill share planned to end this ea
 #define PA_PREFILL_MIN_QLEN 16
 #endif
 constexpr int kPrefillMinQlen = PA_PREFILL_MIN_QLEN;
+
+// Windowed prefill item: its first row is at position `first`, its last key
+// `last`; the 128-key tiles it reads are the first `st` (sinks), then those
+// from tile wt on, n in all. lo: the first key of any row's window.
+struct WinTiles {
+  int n, st, wt, lo;
+};
+__host__ __device__ inline WinTiles win_tiles(int first, int last, int window, int sinks) {
+  WinTiles t;
+  t.lo = first + 1 > window ? first + 1 - window : 0;
+  t.wt = t.lo / 128;
+  t.st = (int)(((long long)sinks + 127) / 128);
+  if (t.st > t.wt) t.st = t.wt;
+  t.n = t.st + last / 128 + 1 - t.wt;
+  return t;
+}
 
 // One prefill work item: two 128-row tiles of request `req`, kv head `kv`,
 // chunk tokens j0 .. j0 + 2*128/G - 1, attending to nkv 128-key tiles.
@@ -178,6 +224,7 @@ struct PlanParams {
   int overlap, num_sms, position_bytes;
   int prefill_ctas_override;  // > 0: the prefill-chunk grid's share, instead of the cost model
   int token_major;  // positions per token are its blocks (all kv heads at once)
+  int window, sinks;  // windowed attention (window 0: none)
   WsHeader* header;
   UnitInfo* units;
   PrefillTile* tiles;
@@ -212,6 +259,7 @@ struct PrefillLaunch {
   // Overlapped cascade (prefix pass): prefix_ctas CTAs take the items, and the
   // grid releases the suffix split-KV grid once the planner has completed.
   int overlap, prefix_ctas;
+  int window, sinks;  // windowed attention (window 0: none)
   unsigned long long* err;
 };
 
@@ -256,6 +304,7 @@ struct DecodeParams {
   // overlapped cascade: every (token, kv head) leaves partials, whole ones
   // too; the merge pass folds them with the prefix partials (MergeParams::all_units)
   int fold_later;
+  int window, sinks;  // windowed attention (window 0: none, the plain instantiations)
   unsigned long long* err;
 };
 
@@ -416,7 +465,7 @@ cudaError_t launch_decode(const DecodeParams& p, int head_dim, int group, bool f
 // The merge pass after a split-KV launch of num_workers workers (p.num_workers).
 cudaError_t launch_merge(const MergeParams& p, int head_dim, int group, cudaStream_t s);
 // Split-KV workers launch_decode will use on this device (0 on error).
-int decode_workers(int head_dim, int group, bool f8, int num_sms, int occ_cap);
+int decode_workers(int head_dim, int group, bool f8, bool windowed, int num_sms, int occ_cap);
 
 // Tensor-core split-KV decode (decode_tc.cu): one CTA per SM is one worker.
 // Supported for head_dim 128, over a bf16 cache (a cascade's suffix pass

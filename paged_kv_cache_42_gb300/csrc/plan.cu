@@ -13,6 +13,8 @@
 //    requests must see the whole prefix and start with request 0's prefix
 //    blocks, which is checked here.
 // Invalid spans or lengths are skipped and reported on the device error word.
+//  - Windowed calls count only the blocks (tiles) that hold a key the token
+//    (an item's rows) attends to.
 // A decode-only batch needs no planner: the split-KV kernel builds its own
 // unit list.
 #include "pa_internal.h"
@@ -101,6 +103,7 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
   };
   auto tile_nkv = [&](int L, int ctx, int j0) -> int {  // 128-key tiles the item needs
     const int last = min(L - 1, ctx + j0 + tok_per_item - 1);  // last key of the item's rows
+    if (p.window > 0) return win_tiles(ctx + j0, last, p.window, p.sinks).n;
     return last / 128 + 1;
   };
 
@@ -175,7 +178,8 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
     const int t = c0 + threadIdx.x;
     const int2 u = t < T ? raw[t] : make_int2(-1, 0);
     // blocks on the split-KV path: all the token sees, less a cascade prefix
-    const int nb = max(0, (u.y + kBlockSize - 1) / kBlockSize - p.prefix_blocks);
+    // (windowed: those that hold a key it attends to)
+    const int nb = max(0, win_span(u.y, p.window, p.sinks).nb - p.prefix_blocks);
     // (token-major split-KV: one position per block, every kv head at once)
     const long long packed =
         ((long long)(nb > 0) << 40) | ((long long)nb * (p.token_major ? 1 : p.num_kv_heads));

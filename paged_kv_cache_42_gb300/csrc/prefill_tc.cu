@@ -150,6 +150,7 @@ struct PrefillParams {
   const unsigned char* v_cache8;
   float v_scale;
   int overlap;  // PrefillLaunch::overlap
+  int window, sinks;  // WIN
   unsigned long long* err;
 };
 
@@ -162,9 +163,21 @@ struct Item {
   int L;      // keys that exist (sequence length; prefix length)
   int tok0;   // batch token of the pair's first row
   int chunk;  // key chunk (prefix pass)
+  WinTiles wt;  // WIN: the key tiles of the item's rows
 };
 
-template <int D, int G, bool PREFIX>
+// Key tile i of an item as a tile of the sequence.
+template <bool WIN>
+__device__ __forceinline__ int key_tile(const Item& it, int i) {
+  if constexpr (WIN) return i < it.wt.st ? i : i - it.wt.st + it.wt.wt;
+  return it.i0 + i;
+}
+// WIN: whether any row of the item may see a key of [key, key + n).
+__device__ __forceinline__ bool item_sees(const Item& it, int key, int n, int sinks) {
+  return key < it.L && (key + n > it.wt.lo || key < sinks);
+}
+
+template <int D, int G, bool PREFIX, bool WIN = false>
 __device__ __forceinline__ Item get_item(const PrefillParams& p, int t) {
   using C = PCfg<D, G>;
   Item it;
@@ -190,6 +203,10 @@ __device__ __forceinline__ Item get_item(const PrefillParams& p, int t) {
     it.L = __ldg(p.seq_lens + tl.req);
     it.tok0 = __ldg(p.qsl + tl.req) + tl.j0;
     it.chunk = 0;
+    if constexpr (WIN) {
+      const int first = it.L - (__ldg(p.qsl + tl.req + 1) - (it.tok0 - tl.j0)) + tl.j0;
+      it.wt = win_tiles(first, min(it.L - 1, first + 2 * C::TOK - 1), p.window, p.sinks);
+    }
   }
   return it;
 }
@@ -203,7 +220,13 @@ __device__ __forceinline__ int snake_item(int r, int g) {
   return r * g + ((r & 1) ? g - 1 - b : b);
 }
 
-template <int D, int G, bool PREFIX, bool F8>
+// WIN: windowed attention. An item reads the key tiles that some row of it
+// sees (win_tiles: the sinks', then the windows'), every row masks its own
+// keys, and a block that no row sees is not read at all - its table entry may
+// be stale - and counts as zeros in V. A row may see no key of its item's
+// first tiles; its running maximum then starts at a finite floor, so that the
+// first tile it does see rescales a zero O by zero.
+template <int D, int G, bool PREFIX, bool F8, bool WIN>
 __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
     pa_prefill_kernel(const __grid_constant__ PrefillParams p) {
   using C = PCfg<D, G>;
@@ -276,11 +299,17 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
     int g = 0, it = 0;
     bool ok = true;
     for (int t = snake_item(it, ctas); ok && t < ntiles; t = snake_item(++it, ctas)) {
-      const Item tl = get_item<D, G, PREFIX>(p, t);
+      const Item tl = get_item<D, G, PREFIX, WIN>(p, t);
       const int nb = (tl.L + kBlockSize - 1) / kBlockSize;
       const int32_t* const bt_row = p.block_tables + (size_t)tl.req * p.bt_stride;
       auto load_group = [&](int grp) -> int {  // blocks of key tiles i0 + 4 grp .. + 3
-        const int b = tl.i0 * 8 + grp * 32 + lane;
+        int b = tl.i0 * 8 + grp * 32 + lane;
+        if constexpr (WIN) {
+          const int i = grp * 4 + (lane >> 3);
+          if (i >= tl.n) return -1;
+          b = key_tile<WIN>(tl, i) * 8 + (lane & 7);
+          if (!item_sees(tl, b * kBlockSize, kBlockSize, p.sinks)) return -1;
+        }
         if (b >= nb) return -1;
         const int pid = __ldg(bt_row + b);
         if (pid < 0 || pid >= p.num_blocks) {
@@ -345,7 +374,7 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
     int it = 0;
     bool ok = true;
     for (int t = snake_item(it, ctas); ok && t < ntiles; t = snake_item(++it, ctas)) {
-      const Item tl = get_item<D, G, PREFIX>(p, t);
+      const Item tl = get_item<D, G, PREFIX, WIN>(p, t);
       const int L = tl.L;
       if (!wait(B_Q_FULL, it & 1)) { ok = false; break; }
 
@@ -380,8 +409,18 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
         ++np[rt];
         if (rt == 0) {
           if (!wait(B_V_FULL + vst, (gv / C::VSTAGES) & 1)) return false;
-          const int kv0 = (tl.i0 + i) * 128;
-          if (!F8 && kv0 + 128 > L) {  // (the converters write such rows as zeros)
+          const int kv0 = key_tile<WIN>(tl, i) * 128;
+          if (WIN && !F8 && (kv0 + 128 > L || (kv0 < tl.wt.lo && kv0 + 128 > p.sinks))) {
+            // rows of keys no row of the item sees, whose blocks were not read
+            for (int idx = lane; idx < 128 * 8 * C::NCH; idx += 32) {
+              const int c = idx >> 10, row = (idx >> 3) & 127, u = idx & 7;
+              if (!item_sees(tl, kv0 + row, 1, p.sinks))
+                *reinterpret_cast<uint4*>(gbase + C::OFF_V + vst * C::KV_BYTES + c * C::CHUNK +
+                                          row * 128 + u * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          } else if (!WIN && !F8 && kv0 + 128 > L) {  // (the converters write such rows as zeros)
             // Rows of keys past the sequence end may hold anything (NaN too);
             // their P is 0, but 0 * NaN would poison O, so clear them.
             const int r0 = L - kv0;
@@ -466,7 +505,7 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
     int ns = 0, it = 0;  // S_rt events consumed; work items done
     bool ok = true;
     for (int t = snake_item(it, ctas); ok && t < ntiles; t = snake_item(++it, ctas)) {
-      const Item tl = get_item<D, G, PREFIX>(p, t);
+      const Item tl = get_item<D, G, PREFIX, WIN>(p, t);
       const int L = tl.L;
       int qlen = 0, j = 0, lim;
       if constexpr (PREFIX) {
@@ -484,8 +523,11 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
         if (!wait(B_S_FULL + rt, ns & 1)) { ok = false; break; }
         ++ns;
         tc_fence_after();
-        const int kv0 = (tl.i0 + i) * 128;
-        const bool unmasked = __all_sync(kAll, kv0 + 127 <= lim);
+        const int kv0 = key_tile<WIN>(tl, i) * 128;
+        bool unmasked = __all_sync(kAll, kv0 + 127 <= lim);
+        const int lo = WIN ? lim - p.window + 1 : 0;  // the row sees lo .. lim and the sinks
+        if constexpr (WIN)
+          unmasked = unmasked && __all_sync(kAll, kv0 >= lo || kv0 + 127 < p.sinks);
         // pass 1: row max of the raw scores over visible keys
         float mx = -INFINITY;
 #pragma unroll 1
@@ -499,8 +541,11 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
             for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(r[e]));
           } else {
             const int lim_c = lim - kv0 - c * 32;  // columns e <= lim_c are visible
+            const int lo_c = lo - kv0 - c * 32, s_c = WIN ? p.sinks - kv0 - c * 32 : 0;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, e <= lim_c ? __uint_as_float(r[e]) : -INFINITY);
+            for (int e = 0; e < 32; ++e)
+              mx = fmaxf(mx, e <= lim_c && (!WIN || e >= lo_c || e < s_c) ? __uint_as_float(r[e])
+                                                                          : -INFINITY);
           }
         }
         mx = exchange(mx, true, ok);         // the whole row's max
@@ -510,6 +555,7 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
         bool resc = false;
         if (i == 0) {
           m_used = mt;  // the item's first key is always visible: finite
+          if constexpr (WIN) m_used = fmaxf(mt, -1e30f);
         } else if (mt > m_used + 8.f) {
           alpha = exp2f(m_used - mt);
           m_used = mt;
@@ -552,11 +598,13 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
             }
           } else {
             const int lim_c = lim - kv0 - c * 32;
+            const int lo_c = lo - kv0 - c * 32, s_c = WIN ? p.sinks - kv0 - c * 32 : 0;
+            auto sees = [&](int e) { return e <= lim_c && (!WIN || e >= lo_c || e < s_c); };
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float p0 = 2 * e <= lim_c ? ex2_approx(fmaf(__uint_as_float(r[2 * e]), sc, nm)) : 0.f;
+              const float p0 = sees(2 * e) ? ex2_approx(fmaf(__uint_as_float(r[2 * e]), sc, nm)) : 0.f;
               const float p1 =
-                  2 * e + 1 <= lim_c ? ex2_approx(fmaf(__uint_as_float(r[2 * e + 1]), sc, nm)) : 0.f;
+                  sees(2 * e + 1) ? ex2_approx(fmaf(__uint_as_float(r[2 * e + 1]), sc, nm)) : 0.f;
               l2[e & 1] += p0 + p1;
               w[e] = float2_to_bf16x2(p0, p1);
             }
@@ -636,11 +684,11 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
     int g = 0, it = 0;
     bool ok = true;
     for (int t = snake_item(it, ctas); ok && t < ntiles; t = snake_item(++it, ctas)) {
-      const Item tl = get_item<D, G, PREFIX>(p, t);
+      const Item tl = get_item<D, G, PREFIX, WIN>(p, t);
       const int32_t* const bt_row = p.block_tables + (size_t)tl.req * p.bt_stride;
       for (int i = 0; i < tl.n; ++i, ++g) {
-        const int key = (tl.i0 + i) * 128 + r;
-        bool valid = key < tl.L;
+        const int key = key_tile<WIN>(tl, i) * 128 + r;
+        bool valid = WIN ? item_sees(tl, key, 1, p.sinks) : key < tl.L;
         size_t src = 0;
         if (valid) {
           const int pid = __ldg(bt_row + key / kBlockSize);
@@ -756,7 +804,7 @@ bool encode_tmap_u8(void* tmap, int rank, const void* ptr, const uint64_t* dims,
 
 namespace {
 
-template <int D, int G, bool PREFIX, bool F8>
+template <int D, int G, bool PREFIX, bool F8, bool WIN>
 cudaError_t launch_prefill_t(const PrefillLaunch& a, int num_sms, cudaStream_t s) {
   using C = PCfg<D, G>;
   PrefillParams p;
@@ -796,6 +844,8 @@ cudaError_t launch_prefill_t(const PrefillLaunch& a, int num_sms, cudaStream_t s
   p.v_cache8 = F8 ? static_cast<const unsigned char*>(a.v_cache) : nullptr;
   p.v_scale = F8 ? a.v_scale : 1.f;
   p.overlap = a.overlap;
+  p.window = a.window;
+  p.sinks = a.sinks;
   int grid = num_sms;
   if (PREFIX) {
     const int items = p.prefix_pairs * a.num_kv_heads * a.prefix_chunks;
@@ -804,7 +854,7 @@ cudaError_t launch_prefill_t(const PrefillLaunch& a, int num_sms, cudaStream_t s
     if (a.overlap && a.prefix_ctas > 0 && a.prefix_ctas < grid) grid = a.prefix_ctas;
   }
 
-  auto kern = pa_prefill_kernel<D, G, PREFIX, F8>;
+  auto kern = pa_prefill_kernel<D, G, PREFIX, F8, WIN>;
   static bool attr_set[64] = {false};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -829,22 +879,22 @@ cudaError_t launch_prefill_t(const PrefillLaunch& a, int num_sms, cudaStream_t s
 
 }  // namespace
 
-template <bool PREFIX, bool F8>
+template <bool PREFIX, bool F8, bool WIN>
 cudaError_t launch_prefill_mode(const PrefillLaunch& a, int num_sms, cudaStream_t s) {
   const int G = a.num_q_heads / a.num_kv_heads;
   if (a.head_dim == 128) {
     switch (G) {
-      case 1: return launch_prefill_t<128, 1, PREFIX, F8>(a, num_sms, s);
-      case 2: return launch_prefill_t<128, 2, PREFIX, F8>(a, num_sms, s);
-      case 4: return launch_prefill_t<128, 4, PREFIX, F8>(a, num_sms, s);
-      case 8: return launch_prefill_t<128, 8, PREFIX, F8>(a, num_sms, s);
+      case 1: return launch_prefill_t<128, 1, PREFIX, F8, WIN>(a, num_sms, s);
+      case 2: return launch_prefill_t<128, 2, PREFIX, F8, WIN>(a, num_sms, s);
+      case 4: return launch_prefill_t<128, 4, PREFIX, F8, WIN>(a, num_sms, s);
+      case 8: return launch_prefill_t<128, 8, PREFIX, F8, WIN>(a, num_sms, s);
     }
   } else if (a.head_dim == 64) {
     switch (G) {
-      case 1: return launch_prefill_t<64, 1, PREFIX, F8>(a, num_sms, s);
-      case 2: return launch_prefill_t<64, 2, PREFIX, F8>(a, num_sms, s);
-      case 4: return launch_prefill_t<64, 4, PREFIX, F8>(a, num_sms, s);
-      case 8: return launch_prefill_t<64, 8, PREFIX, F8>(a, num_sms, s);
+      case 1: return launch_prefill_t<64, 1, PREFIX, F8, WIN>(a, num_sms, s);
+      case 2: return launch_prefill_t<64, 2, PREFIX, F8, WIN>(a, num_sms, s);
+      case 4: return launch_prefill_t<64, 4, PREFIX, F8, WIN>(a, num_sms, s);
+      case 8: return launch_prefill_t<64, 8, PREFIX, F8, WIN>(a, num_sms, s);
     }
   }
   return cudaErrorInvalidValue;
@@ -854,10 +904,13 @@ cudaError_t launch_prefill(const PrefillLaunch& a, int num_sms, cudaStream_t s) 
   if (!get_encoder()) return cudaErrorNotSupported;
   if (a.kv_fp8) {
     if (a.prefix_len > 0) return cudaErrorNotSupported;  // no FP8 cascade
-    return launch_prefill_mode<false, true>(a, num_sms, s);
+    return a.window > 0 ? launch_prefill_mode<false, true, true>(a, num_sms, s)
+                        : launch_prefill_mode<false, true, false>(a, num_sms, s);
   }
-  return a.prefix_len > 0 ? launch_prefill_mode<true, false>(a, num_sms, s)
-                          : launch_prefill_mode<false, false>(a, num_sms, s);
+  if (a.window > 0)  // never with a prefix
+    return launch_prefill_mode<false, false, true>(a, num_sms, s);
+  return a.prefix_len > 0 ? launch_prefill_mode<true, false, false>(a, num_sms, s)
+                          : launch_prefill_mode<false, false, false>(a, num_sms, s);
 }
 
 }  // namespace pa
