@@ -456,6 +456,72 @@ pa_status pa_attention_noalloc(const void* q, const void* k_cache, const void* v
                                int max_blocks_per_req, int max_query_len, int max_seq_len,
                                void* stream);
 
+/*
+ * The calls above with many arguments, taking them in a struct: for bindings
+ * that pay per argument (a foreign-function layer spends longer converting
+ * twenty-five arguments than a small kernel runs). kv_fp8 selects the _fp8
+ * form and its scales, which are ignored otherwise; pa_evict_kv has none. The
+ * results and errors are those of the calls they stand for; args == NULL is
+ * PA_ERR_INVALID_ARG. The structs hold pointers first, then 64-bit, then
+ * 32-bit members, without padding but for the end; pa_args_size(i) is the
+ * size of the i-th struct below, for a binding to check its layout against
+ * (0 for another i).
+ */
+typedef struct pa_norm_rope_write_args { /* 0 */
+  const void *q, *k, *v;
+  const int32_t* positions;
+  const float* cos_sin;
+  const void *q_weight, *k_weight;
+  const int64_t* slot_mapping;
+  void *q_out, *k_cache, *v_cache, *stream;
+  long long q_stride, k_stride, v_stride;
+  float eps, k_scale, v_scale;
+  int rotary_dim, interleaved, max_position, kv_fp8;
+  int num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks;
+} pa_norm_rope_write_args;
+pa_status pa_norm_rope_write_kv_args(const pa_norm_rope_write_args* args);
+
+typedef struct pa_window_args { /* 1 */
+  const void *q, *k_cache, *v_cache;
+  const int32_t *block_tables, *seq_lens, *query_start_loc;
+  void *out, *workspace, *stream;
+  size_t workspace_bytes;
+  float scale, k_scale, v_scale;
+  int kv_fp8, num_reqs, num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks;
+  int max_blocks_per_req, max_query_len, max_seq_len, window, sinks;
+} pa_window_args;
+pa_status pa_attention_window_args(const pa_window_args* args);
+
+typedef struct pa_weights_args { /* 2 */
+  const void *q, *k_cache;
+  const int32_t *block_tables, *seq_lens, *query_start_loc;
+  const float* weights;
+  float* out;
+  void *workspace, *stream;
+  size_t workspace_bytes;
+  long long weights_stride;
+  float scale, k_scale;
+  int kv_fp8, num_reqs, num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks;
+  int max_blocks_per_req, max_query_len, max_seq_len;
+} pa_weights_args;
+pa_status pa_attention_weights_args(const pa_weights_args* args);
+
+typedef struct pa_evict_args { /* 3 */
+  void *k_cache, *v_cache;
+  const int32_t *block_tables, *seq_lens;
+  const float* weights;
+  const int32_t* new_block_tables;
+  int32_t *new_seq_lens, *kept;
+  float* new_weights;
+  void* stream;
+  long long weights_stride, new_weights_stride;
+  int num_reqs, num_kv_heads, head_dim, elem_bytes, block_size, num_blocks;
+  int max_blocks_per_req, max_new_blocks, max_seq_len, keep, recent, sinks;
+} pa_evict_args;
+pa_status pa_evict_kv_args(const pa_evict_args* args);
+
+size_t pa_args_size(int which);
+
 /* Size of the fixed scratch array used by pa_attention_noalloc. */
 size_t pa_noalloc_scratch_bytes(void);
 

@@ -23,6 +23,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -32,6 +33,7 @@ _LIB = None
 
 _c_p = ctypes.c_void_p
 _c_i = ctypes.c_int
+_INT_MAX = 2 ** 31 - 1  # counts beyond it mean the same as it
 
 STATUS = {0: "PA_OK", -1: "PA_ERR_INVALID_ARG", -2: "PA_ERR_UNSUPPORTED",
           -3: "PA_ERR_WORKSPACE", -4: "PA_ERR_CUDA", -5: "PA_ERR_BOUNDS", -6: "PA_ERR_TIMEOUT"}
@@ -91,15 +93,18 @@ def lib() -> ctypes.CDLL:
         nr = [_c_p, _c_p, _c_p, _ll, _ll, _ll, _c_p, _c_p, _c_p, _c_p, _f, _c_i, _c_i, _c_i, _c_p,
               _c_p, _c_p, _c_p]
         L.pa_norm_rope_write_kv.argtypes = nr + [_c_i] * 6 + [_c_p]
-        L.pa_norm_rope_write_kv.restype = _c_i
         L.pa_norm_rope_write_kv_fp8.argtypes = nr + [_f, _f] + [_c_i] * 6 + [_c_p]
-        L.pa_norm_rope_write_kv_fp8.restype = _c_i
         L.pa_attention_window.argtypes = ([_c_p] * 6 + [_f, _c_p] + [_c_i] * 12 +
                                           [_c_p, ctypes.c_size_t, _c_p])
-        L.pa_attention_window.restype = _c_i
         L.pa_attention_window_fp8.argtypes = ([_c_p] * 6 + [_f, _f, _f, _c_p] + [_c_i] * 12 +
                                               [_c_p, ctypes.c_size_t, _c_p])
-        L.pa_attention_window_fp8.restype = _c_i
+        # the struct forms: one packed argument (see _ARGS)
+        for i, (name, layout) in enumerate(_ARGS.items()):
+            fn = getattr(L, name)
+            fn.argtypes = [ctypes.c_char_p]
+            fn.restype = _c_i
+            if L.pa_args_size(i) != -(-layout.size // 8) * 8:
+                raise RuntimeError(f"{name}: the library's argument struct has another layout")
         L.pa_attention_weights_workspace_size.argtypes = [_c_i] * 7
         L.pa_attention_weights_workspace_size.restype = ctypes.c_size_t
         L.pa_attention_weights.argtypes = ([_c_p] * 5 + [_f, _c_p, _c_p, _ll] + [_c_i] * 10 +
@@ -125,6 +130,15 @@ def lib() -> ctypes.CDLL:
         L.pa_version.restype = _c_i
         _LIB = L
     return _LIB
+
+
+# The argument structs of include/pa_api.h, packed with one call instead of a
+# ctypes conversion per argument (25 of them take longer than a small kernel).
+_ARGS = {"pa_norm_rope_write_kv_args": struct.Struct("@12P3q3f10i"),
+         "pa_attention_window_args": struct.Struct("@9PN3f13i"),
+         "pa_attention_weights_args": struct.Struct("@9PNq2f11i"),
+         "pa_evict_kv_args": struct.Struct("@10P2q12i")}
+_pack_nr, _pack_win, _pack_wts, _pack_evict = (s.pack for s in _ARGS.values())
 
 
 def _check(status: int, what: str) -> None:
@@ -194,69 +208,99 @@ def write_kv(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
     _check(st, "pa_write_kv")
 
 
-def _here(*tensors) -> None:
-    """The new operators take tensors of the current device only: the launch
-    goes there, whatever device a tensor lives on."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"a tensor on {t.device}; the current device is cuda:{dev}")
+def _refuse(t, dtype, dev: int, name: str):
+    """Say what is wrong with a tensor that _ptr did not take."""
+    _dev(t, dtype, name)
+    raise ValueError(f"{name} is on {t.device}; the current device is cuda:{dev}, where the "
+                     "kernels run")
 
 
-def _heads(t: torch.Tensor, name: str) -> tuple[int, int]:
+def _ptr(t: torch.Tensor, dtype, dev: int, name: str) -> int:
+    """Address of a contiguous tensor of the current device (a launch goes
+    there, whatever device a tensor lives on). The checks of a call cost more
+    host time than a small kernel takes, so this is the short way of _dev."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _refuse(t, dtype, dev, name)
+
+
+def _where(stream) -> tuple[int, int]:
+    """(current device, raw stream)."""
+    if not torch.cuda.is_initialized():
+        torch.cuda.init()
+    dev = torch._C._cuda_getDevice()
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    return dev, int(stream.cuda_stream)
+
+
+def _heads(t: torch.Tensor, shape: tuple, dev: int, name: str) -> tuple[int, int]:
     """(address, token stride in elements) of [tokens, heads, head_dim] whose
     tokens may lie apart (a part of a wider projection)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    st = t.stride()
-    T, h, d = t.shape
-    if (d > 1 and st[2] != 1) or (h > 1 and st[1] != d):
+    if t.shape != shape:
+        raise ValueError(f"shape mismatch: {name} is {tuple(t.shape)}, not {shape}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device cuda:{dev}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != shape[2] and shape[1] > 1):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return t.data_ptr(), (st[0] if T > 1 else h * d)
+    return t.data_ptr(), (s0 if shape[0] > 1 else shape[1] * shape[2])
 
 
 def _norm_rope(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight,
-               eps, interleaved, out, cache_dtype, stream):
-    if q.dim() != 3 or k.dim() != 3 or k_cache.dim() != 4:
-        raise ValueError("q, k and v are [tokens, heads, head_dim], a cache [blocks, Hkv, 16, D]")
-    T, hq, d = q.shape
-    nb, hkv, bs, d2 = k_cache.shape
-    if k.shape != (T, hkv, d) or v.shape != k.shape or v_cache.shape != k_cache.shape or d2 != d:
-        raise ValueError("shape mismatch between q, k, v and the caches")
-    if slot_mapping.shape != (T,):
-        raise ValueError("slot_mapping must be [num_tokens]")
-    if (positions is None) != (cos_sin is None):
-        raise ValueError("positions and cos_sin come together")
-    rot = max_pos = 0
+               eps, interleaved, out, fp8, k_scale, v_scale, stream):
+    T, hq, d = qshape = q.shape
+    cshape = k_cache.shape
+    nb, hkv, bs, d2 = cshape
+    if v_cache.shape != cshape or d2 != d:
+        raise ValueError("shape mismatch between q and the caches")
+    dev, raw_stream = _where(stream)
+    rot = max_pos = pos_p = cs_p = qw_p = kw_p = 0
     if cos_sin is not None:
-        if cos_sin.dim() != 2 or positions.shape != (T,):
-            raise ValueError("cos_sin must be [max_position, rotary_dim], positions [num_tokens]")
+        if positions is None:
+            raise ValueError("positions and cos_sin come together")
         max_pos, rot = cos_sin.shape
-    for w in (q_weight, k_weight):
-        if w is not None and w.shape != (d,):
+        pos_p = _ptr(positions, torch.int32, dev, "positions")
+        cs_p = _ptr(cos_sin, torch.float32, dev, "cos_sin")
+        if positions.numel() != T:
+            raise ValueError("positions must be [num_tokens]")
+    elif positions is not None:
+        raise ValueError("positions and cos_sin come together")
+    if q_weight is not None:
+        qw_p = _ptr(q_weight, torch.bfloat16, dev, "q_weight")
+        if q_weight.numel() != d:
+            raise ValueError("a norm weight must be [head_dim]")
+    if k_weight is not None:
+        kw_p = _ptr(k_weight, torch.bfloat16, dev, "k_weight")
+        if k_weight.numel() != d:
             raise ValueError("a norm weight must be [head_dim]")
     if out is None:
-        out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=q.device)
-    elif out.shape != q.shape:
+        out = torch.empty(qshape, dtype=torch.bfloat16, device=q.device)
+    elif out.shape != qshape:
         raise ValueError("out must have q's shape")
-    _here(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight, out)
-    qp, qs = _heads(q, "q")
-    kp, ks = _heads(k, "k")
-    vp, vs = _heads(v, "v")
-    return out, (qp, kp, vp, qs, ks, vs,
-                 None if positions is None else _dev(positions, torch.int32, "positions"),
-                 None if cos_sin is None else _dev(cos_sin, torch.float32, "cos_sin"),
-                 None if q_weight is None else _dev(q_weight, torch.bfloat16, "q_weight"),
-                 None if k_weight is None else _dev(k_weight, torch.bfloat16, "k_weight"),
-                 float(eps), rot, int(bool(interleaved)), max_pos,
-                 _dev(slot_mapping, torch.int64, "slot_mapping"),
-                 _dev(out, torch.bfloat16, "out"), _dev(k_cache, cache_dtype, "k_cache"),
-                 _dev(v_cache, cache_dtype, "v_cache")), (T, hq, hkv, d, bs, nb,
-                                                          _stream_ptr(stream))
+    qp, qs = _heads(q, qshape, dev, "q")
+    kshape = (T, hkv, d)
+    kp, ks = _heads(k, kshape, dev, "k")
+    vp, vs = _heads(v, kshape, dev, "v")
+    sp = _ptr(slot_mapping, torch.int64, dev, "slot_mapping")
+    if slot_mapping.numel() != T:
+        raise ValueError("slot_mapping must be [num_tokens]")
+    cache_dtype = torch.uint8 if fp8 else torch.bfloat16
+    st = lib().pa_norm_rope_write_kv_args(_pack_nr(
+        qp, kp, vp, pos_p, cs_p, qw_p, kw_p, sp, _ptr(out, torch.bfloat16, dev, "out"),
+        _ptr(k_cache, cache_dtype, dev, "k_cache"), _ptr(v_cache, cache_dtype, dev, "v_cache"),
+        raw_stream, qs, ks, vs, eps, k_scale, v_scale, rot, 1 if interleaved else 0, max_pos, fp8,
+        T, hq, hkv, d, bs, nb))
+    if st:
+        _check(st, "pa_norm_rope_write_kv_fp8" if fp8 else "pa_norm_rope_write_kv")
+    return out
 
 
 def norm_rope_write_kv(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -273,10 +317,8 @@ def norm_rope_write_kv(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     token's heads contiguous). ``cos_sin`` is fp32 [max_position, rotary_dim],
     cosines then sines; ``positions`` is int32 [T]; both None: no rotation.
     """
-    out, a, b = _norm_rope(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight,
-                           k_weight, eps, interleaved, out, torch.bfloat16, stream)
-    _check(lib().pa_norm_rope_write_kv(*a, *b), "pa_norm_rope_write_kv")
-    return out
+    return _norm_rope(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight,
+                      k_weight, eps, interleaved, out, 0, 1.0, 1.0, stream)
 
 
 def norm_rope_write_kv_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -288,11 +330,8 @@ def norm_rope_write_kv_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                            interleaved: bool = False, out: torch.Tensor | None = None,
                            stream=None) -> torch.Tensor:
     """pa_norm_rope_write_kv_fp8: the same into E4M3 caches (uint8)."""
-    out, a, b = _norm_rope(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight,
-                           k_weight, eps, interleaved, out, torch.uint8, stream)
-    _check(lib().pa_norm_rope_write_kv_fp8(*a, float(k_scale), float(v_scale), *b),
-           "pa_norm_rope_write_kv_fp8")
-    return out
+    return _norm_rope(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight,
+                      k_weight, eps, interleaved, out, 1, k_scale, v_scale, stream)
 
 
 def workspace_size(num_reqs: int, num_tokens: int, num_q_heads: int, num_kv_heads: int,
@@ -421,33 +460,38 @@ def attention_cascade(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     return out
 
 
-def _window(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scales, window, sinks,
-            max_query_len, max_seq_len, out, workspace, cache_dtype, stream, name):
-    T, hq, d = q.shape
-    nb, hkv, bs, d2 = k_cache.shape
-    R = int(seq_lens.shape[0])
-    if d2 != d or v_cache.shape != k_cache.shape:
+def _window(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale, window, sinks,
+            max_query_len, max_seq_len, out, workspace, fp8, k_scale, v_scale, stream):
+    T, hq, d = qshape = q.shape
+    cshape = k_cache.shape
+    nb, hkv, bs, d2 = cshape
+    R = seq_lens.shape[0]
+    if d2 != d or v_cache.shape != cshape:
         raise ValueError("shape mismatch between q and the caches")
-    if query_start_loc.shape != (R + 1,) or block_tables.dim() != 2 or block_tables.shape[0] != R:
+    mr, mb = block_tables.shape
+    if query_start_loc.numel() != R + 1 or mr != R:
         raise ValueError("metadata shapes must be qsl [R+1], block_tables [R, max_blocks]")
     if out is None:
         out = torch.empty_like(q)
-    elif out.shape != q.shape:
+    elif out.shape != qshape:
         raise ValueError("out must have q's shape")
     if workspace is None:
         need = workspace_size(R, T, hq, hkv, d)
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-    _here(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, workspace,
-          out if out.is_cuda else None)
-    st = getattr(lib(), name)(
-        _dev(q, torch.bfloat16, "q"), _dev(k_cache, cache_dtype, "k_cache"),
-        _dev(v_cache, cache_dtype, "v_cache"), _dev(block_tables, torch.int32, "block_tables"),
-        _dev(seq_lens, torch.int32, "seq_lens"),
-        _dev(query_start_loc, torch.int32, "query_start_loc"), *scales, _out(out), R, T, hq, hkv,
-        d, bs, nb, int(block_tables.shape[1]), int(max_query_len), int(max_seq_len), int(window),
-        int(sinks), _dev(workspace, torch.uint8, "workspace"), int(workspace.numel()),
-        _stream_ptr(stream))
-    _check(st, name)
+    dev, raw_stream = _where(stream)
+    out_p = _ptr(out, torch.bfloat16, dev, "out") if out.is_cuda else _out(out)
+    cache_dtype = torch.uint8 if fp8 else torch.bfloat16
+    st = lib().pa_attention_window_args(_pack_win(
+        _ptr(q, torch.bfloat16, dev, "q"), _ptr(k_cache, cache_dtype, dev, "k_cache"),
+        _ptr(v_cache, cache_dtype, dev, "v_cache"),
+        _ptr(block_tables, torch.int32, dev, "block_tables"),
+        _ptr(seq_lens, torch.int32, dev, "seq_lens"),
+        _ptr(query_start_loc, torch.int32, dev, "query_start_loc"), out_p,
+        _ptr(workspace, torch.uint8, dev, "workspace"), raw_stream, workspace.numel(), scale,
+        k_scale, v_scale, fp8, R, T, hq, hkv, d, bs, nb, mb, max_query_len, max_seq_len,
+        min(window, _INT_MAX), min(sinks, _INT_MAX)))
+    if st:
+        _check(st, "pa_attention_window_fp8" if fp8 else "pa_attention_window")
     return out
 
 
@@ -459,9 +503,8 @@ def attention_window(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     """pa_attention_window: :func:`attention` where a token attends to the last
     ``window`` keys (its own included) and the first ``sinks``. The workspace is
     ``workspace_size(...)`` bytes, as for :func:`attention`."""
-    return _window(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, (float(scale),),
-                   window, sinks, max_query_len, max_seq_len, out, workspace, torch.bfloat16,
-                   stream, "pa_attention_window")
+    return _window(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale, window,
+                   sinks, max_query_len, max_seq_len, out, workspace, 0, 1.0, 1.0, stream)
 
 
 def attention_window_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -471,9 +514,8 @@ def attention_window_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
                          max_seq_len: int, out: torch.Tensor | None = None,
                          workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """pa_attention_window_fp8: the same over E4M3 caches (uint8)."""
-    return _window(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc,
-                   (float(scale), float(k_scale), float(v_scale)), window, sinks, max_query_len,
-                   max_seq_len, out, workspace, torch.uint8, stream, "pa_attention_window_fp8")
+    return _window(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale, window,
+                   sinks, max_query_len, max_seq_len, out, workspace, 1, k_scale, v_scale, stream)
 
 
 def weights_workspace_size(num_reqs: int, num_tokens: int, num_q_heads: int, num_kv_heads: int,
@@ -483,34 +525,38 @@ def weights_workspace_size(num_reqs: int, num_tokens: int, num_q_heads: int, num
                                                          max_seq_len))
 
 
-def _weights(q, k_cache, block_tables, seq_lens, query_start_loc, scales, weights, max_query_len,
-             max_seq_len, out, workspace, cache_dtype, stream, name):
+def _weights(q, k_cache, block_tables, seq_lens, query_start_loc, scale, weights, max_query_len,
+             max_seq_len, out, workspace, fp8, k_scale, stream):
     T, hq, d = q.shape
     nb, hkv, bs, d2 = k_cache.shape
-    R = int(seq_lens.shape[0])
+    R = seq_lens.shape[0]
     if d2 != d:
         raise ValueError("shape mismatch between q and the cache")
-    if query_start_loc.shape != (R + 1,) or block_tables.dim() != 2 or block_tables.shape[0] != R:
+    mr, mb = block_tables.shape
+    if query_start_loc.numel() != R + 1 or mr != R:
         raise ValueError("metadata shapes must be qsl [R+1], block_tables [R, max_blocks]")
-    if weights.dim() != 3 or weights.shape[:2] != (R, hkv):
+    wshape = weights.shape
+    if len(wshape) != 3 or wshape[0] != R or wshape[1] != hkv:
         raise ValueError("weights must be [num_reqs, num_kv_heads, width]")
     if out is None:
         out = weights
-    elif out.shape != weights.shape:
+    elif out.shape != wshape:
         raise ValueError("out must have weights' shape")
     if workspace is None:
-        need = weights_workspace_size(R, T, hq, hkv, d, int(max_query_len), int(max_seq_len))
+        need = weights_workspace_size(R, T, hq, hkv, d, max_query_len, max_seq_len)
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-    _here(q, k_cache, block_tables, seq_lens, query_start_loc, weights, out, workspace)
-    st = getattr(lib(), name)(
-        _dev(q, torch.bfloat16, "q"), _dev(k_cache, cache_dtype, "k_cache"),
-        _dev(block_tables, torch.int32, "block_tables"), _dev(seq_lens, torch.int32, "seq_lens"),
-        _dev(query_start_loc, torch.int32, "query_start_loc"), *scales,
-        _dev(weights, torch.float32, "weights"), _dev(out, torch.float32, "out"),
-        int(weights.shape[2]), R, T, hq, hkv, d, bs, nb, int(block_tables.shape[1]),
-        int(max_query_len), int(max_seq_len), _dev(workspace, torch.uint8, "workspace"),
-        int(workspace.numel()), _stream_ptr(stream))
-    _check(st, name)
+    dev, raw_stream = _where(stream)
+    st = lib().pa_attention_weights_args(_pack_wts(
+        _ptr(q, torch.bfloat16, dev, "q"),
+        _ptr(k_cache, torch.uint8 if fp8 else torch.bfloat16, dev, "k_cache"),
+        _ptr(block_tables, torch.int32, dev, "block_tables"),
+        _ptr(seq_lens, torch.int32, dev, "seq_lens"),
+        _ptr(query_start_loc, torch.int32, dev, "query_start_loc"),
+        _ptr(weights, torch.float32, dev, "weights"), _ptr(out, torch.float32, dev, "out"),
+        _ptr(workspace, torch.uint8, dev, "workspace"), raw_stream, workspace.numel(), wshape[2],
+        scale, k_scale, fp8, R, T, hq, hkv, d, bs, nb, mb, max_query_len, max_seq_len))
+    if st:
+        _check(st, "pa_attention_weights_fp8" if fp8 else "pa_attention_weights")
     return out
 
 
@@ -522,9 +568,8 @@ def attention_weights(q: torch.Tensor, k_cache: torch.Tensor, block_tables: torc
     """pa_attention_weights: add this step's attention weight of every key,
     summed over the new tokens and the query heads of its KV head, to
     ``weights`` fp32 [R, Hkv, width >= seq_len]; in place unless ``out`` is given."""
-    return _weights(q, k_cache, block_tables, seq_lens, query_start_loc, (float(scale),), weights,
-                    max_query_len, max_seq_len, out, workspace, torch.bfloat16, stream,
-                    "pa_attention_weights")
+    return _weights(q, k_cache, block_tables, seq_lens, query_start_loc, scale, weights,
+                    max_query_len, max_seq_len, out, workspace, 0, 1.0, stream)
 
 
 def attention_weights_fp8(q: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.Tensor,
@@ -533,9 +578,8 @@ def attention_weights_fp8(q: torch.Tensor, k_cache: torch.Tensor, block_tables: 
                           max_seq_len: int, out: torch.Tensor | None = None,
                           workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """pa_attention_weights_fp8: the same over an E4M3 key cache (uint8)."""
-    return _weights(q, k_cache, block_tables, seq_lens, query_start_loc,
-                    (float(scale), float(k_scale)), weights, max_query_len, max_seq_len, out,
-                    workspace, torch.uint8, stream, "pa_attention_weights_fp8")
+    return _weights(q, k_cache, block_tables, seq_lens, query_start_loc, scale, weights,
+                    max_query_len, max_seq_len, out, workspace, 1, k_scale, stream)
 
 
 def evict_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
@@ -564,29 +608,28 @@ def evict_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.T
     for t in (block_tables, new_block_tables):
         if t.dim() != 2 or t.shape[0] != R:
             raise ValueError("block tables must be [num_reqs, blocks]")
-    dev = k_cache.device
     if new_seq_lens is None:
-        new_seq_lens = torch.empty(R, dtype=torch.int32, device=dev)
+        new_seq_lens = torch.empty(R, dtype=torch.int32, device=k_cache.device)
     if kept is None:
-        kept = torch.empty((R, hkv, max(int(keep), 0)), dtype=torch.int32, device=dev)
+        kept = torch.empty((R, hkv, max(keep, 0)), dtype=torch.int32, device=k_cache.device)
     if new_weights is None:
-        new_weights = torch.empty((R, hkv, max(int(keep), 0)), dtype=torch.float32, device=dev)
+        new_weights = torch.empty((R, hkv, max(keep, 0)), dtype=torch.float32,
+                                  device=k_cache.device)
     if new_seq_lens.shape != (R,) or kept.shape != (R, hkv, keep) or \
             new_weights.dim() != 3 or new_weights.shape[:2] != (R, hkv):
         raise ValueError("new_seq_lens must be [R], kept [R, Hkv, keep], new_weights [R, Hkv, width]")
-    _here(k_cache, v_cache, block_tables, seq_lens, weights, new_block_tables, new_seq_lens, kept,
-          new_weights)
-    st = lib().pa_evict_kv(
-        _dev(k_cache, k_cache.dtype, "k_cache"), _dev(v_cache, v_cache.dtype, "v_cache"),
-        _dev(block_tables, torch.int32, "block_tables"), _dev(seq_lens, torch.int32, "seq_lens"),
-        _dev(weights, torch.float32, "weights"),
-        _dev(new_block_tables, torch.int32, "new_block_tables"),
-        _dev(new_seq_lens, torch.int32, "new_seq_lens"), _dev(kept, torch.int32, "kept"),
-        _dev(new_weights, torch.float32, "new_weights"), R, hkv, d, k_cache.element_size(), bs,
-        nb, int(block_tables.shape[1]), int(new_block_tables.shape[1]), int(weights.shape[2]),
-        int(new_weights.shape[2]), int(max_seq_len), int(keep), int(recent), int(sinks),
-        _stream_ptr(stream))
-    _check(st, "pa_evict_kv")
+    dev, raw_stream = _where(stream)
+    st = lib().pa_evict_kv_args(_pack_evict(
+        _ptr(k_cache, k_cache.dtype, dev, "k_cache"), _ptr(v_cache, k_cache.dtype, dev, "v_cache"),
+        _ptr(block_tables, torch.int32, dev, "block_tables"),
+        _ptr(seq_lens, torch.int32, dev, "seq_lens"), _ptr(weights, torch.float32, dev, "weights"),
+        _ptr(new_block_tables, torch.int32, dev, "new_block_tables"),
+        _ptr(new_seq_lens, torch.int32, dev, "new_seq_lens"), _ptr(kept, torch.int32, dev, "kept"),
+        _ptr(new_weights, torch.float32, dev, "new_weights"), raw_stream, weights.shape[2],
+        new_weights.shape[2], R, hkv, d, k_cache.element_size(), bs, nb, block_tables.shape[1],
+        new_block_tables.shape[1], max_seq_len, keep, min(recent, _INT_MAX), min(sinks, _INT_MAX)))
+    if st:
+        _check(st, "pa_evict_kv")
     return new_seq_lens, kept, new_weights
 
 

@@ -231,7 +231,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
   }
   if (W <= 0) return;
   const int launched = (int)gridDim.x * WARPS;
-  const int NW = plan_workers(W, launched < p.max_workers ? launched : p.max_workers);
+  const int NW = plan_workers(W, launched < p.max_workers ? launched : p.max_workers, p.min_pos);
   const int w = blockIdx.x * WARPS + warp;
   if (w >= NW) return;
   const int S = worker_begin(w, W, NW);

@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int w = (int)blockIdx.x;
   int all = (int)gridDim.x < p.max_workers ? (int)gridDim.x : p.max_workers;
   if (p.overlap) all = min(all, __ldcg(&p.header->decode_workers));
-  const int NW = W > 0 ? plan_workers(W, all) : 0;
+  const int NW = W > 0 ? plan_workers(W, all, p.min_pos) : 0;
   int S = 0, E = 0;
   if (w < NW) {
     S = worker_begin(w, W, NW);

@@ -46,28 +46,29 @@ __global__ void __launch_bounds__(kMergeWarps * 32) pa_merge_kernel(const MergeP
     if (k >= __ldcg(&p.header->num_units)) return;
     const int4 u = __ldcg(reinterpret_cast<const int4*>(p.units + k));
     const int nb = max(1, (u.z + kBlockSize - 1) / kBlockSize - p.key_start_blocks);
-    const int first = u.w + kv * nb, NW = plan_workers(W, nw);
+    const int first = u.w + kv * nb, NW = plan_workers(W, nw, p.min_pos);
     tok = u.x;
     wf = worker_of(first, W, NW);
     wl = worker_of(first + nb - 1, W, NW);
   } else {
-    const int w = (int)blockIdx.x + 1;
+    const int w = (int)blockIdx.x / (p.tm_wide ? p.num_kv_heads : 1) + 1;
     const int4 task = __ldcg(p.tasks + w);
     // tasks past this call's worker count are stale
-    if (w >= plan_workers(W, nw) || task.x < 0) return;
+    if (w >= plan_workers(W, nw, p.min_pos) || task.x < 0) return;
     tok = task.x;
     wf = task.z;
     wl = task.w;
-    kv = task.y;
+    kv = p.tm_wide ? (int)blockIdx.x % p.num_kv_heads : task.y;
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
   // The partials: the suffix slots wf .. wl, then (cascade) the prefix chunks.
-  // Worker wf + i's slot: u + wf + i (u = token * Hkv + kv head).
+  // Worker wf + i's slot: u + wf + i (u = token * Hkv + kv head), or, of
+  // token-major partials, (token + wf + i) * Hkv + kv head.
   const int u = tok * p.num_kv_heads + kv;
   const int ns = wl - wf + 1, n = ns + p.prefix_chunks;
   auto slot = [&](int i) -> const float* {
-    const size_t s0 = (size_t)(u + wf + i);
+    const size_t s0 = p.tm_wide ? (size_t)(tok + wf + i) * p.num_kv_heads + kv : (size_t)(u + wf + i);
     return i < ns ? p.partials + s0 * p.slot_floats
                   : p.prefix_partials +
                         (((size_t)(i - ns) * p.num_tokens + tok) * p.num_kv_heads + kv) *
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) pa_merge_tm_kernel(const Mer
   if (W <= 0) return;
   const int w = (int)blockIdx.x + 1;
   const int4 task = __ldcg(p.tasks + w);
-  if (w >= plan_workers(W, nw) || task.x < 0) return;  // stale task past this call's workers
+  if (w >= plan_workers(W, nw, p.min_pos) || task.x < 0) return;  // stale task past this call's workers
   const int kv = (int)(threadIdx.x >> 5), lane = (int)(threadIdx.x & 31);
   if (kv >= p.num_kv_heads) return;
   const int tok = task.x, wf = task.z, n = task.w - task.z + 1;
@@ -234,7 +235,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) pa_merge_tm_kernel(const Mer
 template <int D, int G>
 cudaError_t launch_merge_t(const MergeParams& p, cudaStream_t s) {
   // one CTA per slice boundary, or per (token, kv head)
-  const int boundaries = p.all_units ? p.num_tokens * p.num_kv_heads : p.num_workers - 1;
+  const int boundaries = p.all_units ? p.num_tokens * p.num_kv_heads
+                                     : (p.num_workers - 1) * (p.tm_wide ? p.num_kv_heads : 1);
   if (boundaries <= 0) return cudaSuccess;  // one worker: nothing is ever split
   // token-major partials: eight KV heads, no cascade (the split-KV kernel's own limits)
   if (p.token_major && (p.all_units || p.prefix_chunks != 0 || p.num_kv_heads > kMergeWarps))
@@ -251,7 +253,7 @@ cudaError_t launch_merge_t(const MergeParams& p, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (p.token_major) {  // a CTA per boundary, a warp per KV head
+  if (p.token_major && !p.tm_wide) {  // a CTA per boundary, a warp per KV head
     cfg.blockDim = dim3(32 * p.num_kv_heads);
     return cudaLaunchKernelEx(&cfg, pa_merge_tm_kernel<D, G>, p);
   }

@@ -13,16 +13,19 @@
 // between the load and the store is binary32 and each result is rounded once
 // (for an E4M3 cache straight from binary32: E4M3(y / scale)).
 //
-// What bounds it: bytes, each element once in and once out; for a few tokens
-// the launch and two dependent loads (position, then table row).
+// What bounds it: bytes, each element once in and once out, with arithmetic
+// close behind; for a few tokens the launch and two dependent loads (position,
+// then table row).
 //
-// Layout of the work. A lane holds 8 consecutive elements (one 16-byte load),
-// a head is D / 8 lanes, so a warp holds 2 (D = 128) or 4 (D = 64) heads and a
-// norm's sum is 3 or 4 shuffles. The partner of a rotation pair is in the same
-// lane (interleaved) or R / 16 lanes away (one shuffle per element). A warp
-// takes kIter such groups of heads of ONE token: their loads are all in flight
-// together, before anything depends on the position, and the token's cosines
-// and sines are loaded once into registers for all of them.
+// Layout of the work. A lane holds 4 pairs of one head: elements 4i .. 4i + 3
+// and their partners R / 2 further on (two 8-byte loads), or 8 consecutive
+// elements when interleaved (one 16-byte load). A rotation is then arithmetic
+// within the lane, on 4 cosines and 4 sines; elements past R pair up the same
+// way under the angle zero. A head is D / 8 lanes, a warp 2 (D = 128) or 4
+// (D = 64) heads, a norm's sum 4 or 3 shuffles. A warp takes ITER such groups
+// of heads of ONE token: their loads are all in flight together, before
+// anything depends on the position, and the token's cosines and sines are
+// loaded once for all of them.
 #include "pa_internal.h"
 #include "ptx.cuh"
 
@@ -31,68 +34,106 @@ namespace pa {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kIter = 2;     // head groups per warp
 constexpr int kThreads = 128;
+constexpr int kManyIter = 6;  // head groups per warp when there are many tokens
 
-__device__ __forceinline__ void unpack8(uint4 r, float (&x)[8]) {
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = bf16x2_to_float2(w[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
+// A lane's 8 values as 4 pairs {a, b}: x[0], x[1] the a's of pairs 0 1 and
+// 2 3, x[2], x[3] the b's.
+struct Pairs {
+  float2 x[4];
+};
+
+// a's and b's in separate words (half split) or side by side (interleaved)
+template <bool INTER>
+__device__ __forceinline__ Pairs unpack(uint4 r) {
+  Pairs v;
+  if constexpr (INTER) {
+    const float2 p0 = bf16x2_to_float2(r.x), p1 = bf16x2_to_float2(r.y);
+    const float2 p2 = bf16x2_to_float2(r.z), p3 = bf16x2_to_float2(r.w);
+    v.x[0] = make_float2(p0.x, p1.x);
+    v.x[1] = make_float2(p2.x, p3.x);
+    v.x[2] = make_float2(p0.y, p1.y);
+    v.x[3] = make_float2(p2.y, p3.y);
+  } else {
+    v.x[0] = bf16x2_to_float2(r.x);
+    v.x[1] = bf16x2_to_float2(r.y);
+    v.x[2] = bf16x2_to_float2(r.z);
+    v.x[3] = bf16x2_to_float2(r.w);
   }
+  return v;
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(float2_to_bf16x2(x[0], x[1]), float2_to_bf16x2(x[2], x[3]),
-                    float2_to_bf16x2(x[4], x[5]), float2_to_bf16x2(x[6], x[7]));
+template <bool INTER>
+__device__ __forceinline__ uint4 pack(const Pairs& v) {
+  if constexpr (INTER)
+    return make_uint4(
+        float2_to_bf16x2(v.x[0].x, v.x[2].x), float2_to_bf16x2(v.x[0].y, v.x[2].y),
+        float2_to_bf16x2(v.x[1].x, v.x[3].x), float2_to_bf16x2(v.x[1].y, v.x[3].y));
+  return make_uint4(float2_to_bf16x2(v.x[0].x, v.x[0].y), float2_to_bf16x2(v.x[1].x, v.x[1].y),
+                    float2_to_bf16x2(v.x[2].x, v.x[2].y), float2_to_bf16x2(v.x[3].x, v.x[3].y));
 }
 
-// 8 values over `scale` as E4M3 codes (correctly rounded quotient, then
-// round-to-nearest-even with saturation, as pa_write_kv_fp8).
-__device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8], float scale) {
-  uint32_t o[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint16_t a = float2_to_e4m3x2(__fdiv_rn(x[4 * i], scale), __fdiv_rn(x[4 * i + 1], scale));
-    const uint16_t b =
-        float2_to_e4m3x2(__fdiv_rn(x[4 * i + 2], scale), __fdiv_rn(x[4 * i + 3], scale));
-    o[i] = (uint32_t)a | ((uint32_t)b << 16);
-  }
-  return make_uint2(o[0], o[1]);
+// The values over `scale` as E4M3 codes (correctly rounded quotient, then
+// round-to-nearest-even with saturation, as pa_write_kv_fp8), in memory order.
+template <bool INTER>
+__device__ __forceinline__ uint2 pack_e4m3(const Pairs& v, float scale) {
+  auto two = [&](float a, float b) -> uint32_t {
+    return float2_to_e4m3x2(__fdiv_rn(a, scale), __fdiv_rn(b, scale));
+  };
+  if constexpr (INTER)
+    return make_uint2(two(v.x[0].x, v.x[2].x) | two(v.x[0].y, v.x[2].y) << 16,
+                      two(v.x[1].x, v.x[3].x) | two(v.x[1].y, v.x[3].y) << 16);
+  return make_uint2(two(v.x[0].x, v.x[0].y) | two(v.x[1].x, v.x[1].y) << 16,
+                    two(v.x[2].x, v.x[2].y) | two(v.x[3].x, v.x[3].y) << 16);
 }
 
-template <int D, bool F8>
+template <int D, bool F8, bool INTER, int ITER>
 __global__ void __launch_bounds__(kThreads) pa_norm_rope_write_kernel(const NormRopeParams p) {
-  constexpr int LPH = D / 8;    // lanes per head
+  constexpr int LPH = D / 8;     // lanes per head
   constexpr int HPG = 32 / LPH;  // heads per group
   const int lane = threadIdx.x & 31;
   const int sub = lane % LPH, hsub = lane / LPH;
-  const int rows = p.num_q_heads + 2 * p.num_kv_heads;
-  const int chunks = (rows + HPG * kIter - 1) / (HPG * kIter);
-  const long long wid = blockIdx.x * (long long)(kThreads / 32) + (threadIdx.x >> 5);
-  const long long t = wid / chunks;
+  const int nq = p.num_q_heads, nk = p.num_kv_heads, rows = nq + 2 * nk;
+  const unsigned chunks = (unsigned)(rows + HPG * ITER - 1) / (HPG * ITER);
+  const unsigned wid = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int t = (int)(wid / chunks);
   if (t >= p.num_tokens) return;
-  const int row0 = (int)(wid - t * chunks) * (HPG * kIter) + hsub;
+  const int row0 = (int)(wid - (unsigned)t * chunks) * (HPG * ITER) + hsub;
 
+  // first elements of this lane's two halves within a head
+  const int half = p.rotary_dim >> 1;
+  const bool turned = sub * 4 < half;  // interleaved: elements 8 sub .. 8 sub + 7 < 2 half alike
+  int ea, eb;
+  if constexpr (INTER) {
+    ea = sub * 8;
+    eb = ea + 4;
+  } else {
+    ea = turned ? sub * 4 : half + sub * 4;
+    eb = turned ? ea + half : ea + (D - p.rotary_dim) / 2;
+  }
   // every load that needs no position first
   const long long slot = __ldg(p.slot_mapping + t);
   const int pos = p.rotary_dim > 0 ? __ldg(p.positions + t) : 0;
-  uint4 raw[kIter];
+  auto load8 = [&](const uint16_t* src) -> uint4 {
+    if constexpr (INTER) return *reinterpret_cast<const uint4*>(src + ea);
+    const uint2 a = *reinterpret_cast<const uint2*>(src + ea);
+    const uint2 b = *reinterpret_cast<const uint2*>(src + eb);
+    return make_uint4(a.x, a.y, b.x, b.y);
+  };
+  uint4 raw[ITER];
 #pragma unroll
-  for (int i = 0; i < kIter; ++i) {
+  for (int i = 0; i < ITER; ++i) {
     const int row = row0 + i * HPG;
     raw[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (row < rows) {
+    if (row < rows) {  // q_out may be q: no read-only path
       const uint16_t* src;
-      if (row < p.num_q_heads)
-        src = p.q + t * p.q_stride + (long long)row * D;
-      else if (row < p.num_q_heads + p.num_kv_heads)
-        src = p.k + t * p.k_stride + (long long)(row - p.num_q_heads) * D;
+      if (row < nq)
+        src = p.q + t * p.q_stride + row * D;
+      else if (row < nq + nk)
+        src = p.k + t * p.k_stride + (row - nq) * D;
       else
-        src = p.v + t * p.v_stride + (long long)(row - p.num_q_heads - p.num_kv_heads) * D;
-      raw[i] = *(reinterpret_cast<const uint4*>(src) + sub);  // q_out may be q: no read-only path
+        src = p.v + t * p.v_stride + (row - nq - nk) * D;
+      raw[i] = load8(src);
     }
   }
   if (slot < 0) return;  // a padding token: nothing of it is written
@@ -104,88 +145,79 @@ __global__ void __launch_bounds__(kThreads) pa_norm_rope_write_kernel(const Norm
     if (lane == 0) report_error(p.err, PA_DEVERR_POSITION, t);
     return;
   }
-
-  // cosines and sines of this lane's elements: c[e], s[e] with the sign of
-  // the partner's term in s (element a: -sin, element b: +sin)
-  const int half = p.rotary_dim >> 1;
-  const int e0 = sub * 8;
-  const bool turned = e0 < p.rotary_dim;
-  float c[8], s[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    c[e] = 1.f;
-    s[e] = 0.f;
-  }
+  float2 c[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)};  // of this lane's pairs
+  float2 s[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   if (turned) {
-    const float* const cs = p.cos_sin + (long long)pos * p.rotary_dim;
-    if (p.interleaved) {
-      const float4 cv = __ldg(reinterpret_cast<const float4*>(cs + e0 / 2));
-      const float4 sv = __ldg(reinterpret_cast<const float4*>(cs + half + e0 / 2));
-      c[0] = c[1] = cv.x;
-      c[2] = c[3] = cv.y;
-      c[4] = c[5] = cv.z;
-      c[6] = c[7] = cv.w;
-      s[0] = -sv.x, s[1] = sv.x;
-      s[2] = -sv.y, s[3] = sv.y;
-      s[4] = -sv.z, s[5] = sv.z;
-      s[6] = -sv.w, s[7] = sv.w;
-    } else {
-      const bool first = e0 < half;
-      const int m = first ? e0 : e0 - half;
-      const float sg = first ? -1.f : 1.f;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 cv = __ldg(reinterpret_cast<const float4*>(cs + m) + i);
-        const float4 sv = __ldg(reinterpret_cast<const float4*>(cs + half + m) + i);
-        c[4 * i] = cv.x, c[4 * i + 1] = cv.y, c[4 * i + 2] = cv.z, c[4 * i + 3] = cv.w;
-        s[4 * i] = sg * sv.x, s[4 * i + 1] = sg * sv.y;
-        s[4 * i + 2] = sg * sv.z, s[4 * i + 3] = sg * sv.w;
-      }
-    }
+    const float* const cs = p.cos_sin + (long long)pos * p.rotary_dim + sub * 4;
+    const float4 cv = __ldg(reinterpret_cast<const float4*>(cs));
+    const float4 sv = __ldg(reinterpret_cast<const float4*>(cs + half));
+    c[0] = make_float2(cv.x, cv.y);
+    c[1] = make_float2(cv.z, cv.w);
+    s[0] = make_float2(sv.x, sv.y);
+    s[1] = make_float2(sv.z, sv.w);
   }
-  // the lane holding the other half of this lane's pairs (itself when untouched)
-  const int hl = half / 8;
-  const int partner = !turned || p.interleaved ? lane : (e0 < half ? lane + hl : lane - hl);
 
 #pragma unroll
-  for (int i = 0; i < kIter; ++i) {
+  for (int i = 0; i < ITER; ++i) {
     const int row = row0 + i * HPG;
-    const bool is_q = row < p.num_q_heads;
-    const bool is_v = row >= p.num_q_heads + p.num_kv_heads;
-    float x[8];
-    unpack8(raw[i], x);
+    const bool is_q = row < nq, is_v = row >= nq + nk;
+    Pairs v = unpack<INTER>(raw[i]);
     const uint16_t* const w = is_q ? p.q_weight : p.k_weight;
-    float ss = 0.f;
+    // the head's sum of squares (every lane of the warp takes the shuffles)
+    float2 sq = fmul2(v.x[0], v.x[0]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+    for (int e = 1; e < 4; ++e) sq = ffma2(v.x[e], v.x[e], sq);
+    float ss = sq.x + sq.y;
 #pragma unroll
     for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(kAll, ss, o);
-    if (w != nullptr && !is_v) {
-      const float r = rsqrtf(ss * (1.f / D) + p.eps);
-      float wf[8];
-      unpack8(__ldg(reinterpret_cast<const uint4*>(w) + sub), wf);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = x[e] * r * wf[e];
-    }
-    float y[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float far = __shfl_sync(kAll, x[e], partner);
-      const float other = p.interleaved ? x[e ^ 1] : far;
-      y[e] = is_v || !turned ? x[e] : fmaf(other, s[e], x[e] * c[e]);
-    }
     if (row >= rows) continue;
+    if (!is_v) {
+      if (w != nullptr) {
+        const float r = rsqrtf(ss * (1.f / D) + p.eps);
+        const Pairs wv = unpack<INTER>(load8(w));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v.x[e] = fmul2(fmul2(v.x[e], make_float2(r, r)), wv.x[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float2 a = v.x[e], b = v.x[2 + e];
+        const float2 ns = make_float2(-s[e].x, -s[e].y);
+        v.x[e] = ffma2(b, ns, fmul2(a, c[e]));
+        v.x[2 + e] = ffma2(a, s[e], fmul2(b, c[e]));
+      }
+    }
     if (is_q) {
-      *(reinterpret_cast<uint4*>(p.q_out + (t * p.num_q_heads + row) * D) + sub) = pack8(y);
+      uint16_t* const dst = p.q_out + ((long long)t * nq + row) * D;
+      const uint4 o = pack<INTER>(v);
+      if constexpr (INTER) {
+        *reinterpret_cast<uint4*>(dst + ea) = o;
+      } else {
+        *reinterpret_cast<uint2*>(dst + ea) = make_uint2(o.x, o.y);
+        *reinterpret_cast<uint2*>(dst + eb) = make_uint2(o.z, o.w);
+      }
+      continue;
+    }
+    const int h = row - nq - (is_v ? nk : 0);
+    const long long dst = (((slot >> 4) * nk + h) * kBlockSize + (slot & 15)) * D;
+    void* const cache = is_v ? p.v_cache : p.k_cache;
+    if constexpr (F8) {
+      unsigned char* const at = static_cast<unsigned char*>(cache) + dst;
+      const uint2 o = pack_e4m3<INTER>(v, is_v ? p.v_scale : p.k_scale);
+      if constexpr (INTER) {
+        *reinterpret_cast<uint2*>(at + ea) = o;
+      } else {
+        *reinterpret_cast<uint32_t*>(at + ea) = o.x;
+        *reinterpret_cast<uint32_t*>(at + eb) = o.y;
+      }
     } else {
-      const int h = row - p.num_q_heads - (is_v ? p.num_kv_heads : 0);
-      const long long dst =
-          (((slot >> 4) * p.num_kv_heads + h) * kBlockSize + (slot & 15)) * LPH + sub;
-      void* const cache = is_v ? p.v_cache : p.k_cache;
-      if constexpr (F8)
-        static_cast<uint2*>(cache)[dst] = pack8_e4m3(y, is_v ? p.v_scale : p.k_scale);
-      else
-        static_cast<uint4*>(cache)[dst] = pack8(y);
+      uint16_t* const at = static_cast<uint16_t*>(cache) + dst;
+      const uint4 o = is_v ? raw[i] : pack<INTER>(v);
+      if constexpr (INTER) {
+        *reinterpret_cast<uint4*>(at + ea) = o;
+      } else {
+        *reinterpret_cast<uint2*>(at + ea) = make_uint2(o.x, o.y);
+        *reinterpret_cast<uint2*>(at + eb) = make_uint2(o.z, o.w);
+      }
     }
   }
   // The split-KV kernel that follows may be a programmatic dependent that
@@ -195,27 +227,43 @@ __global__ void __launch_bounds__(kThreads) pa_norm_rope_write_kernel(const Norm
   __threadfence();
 }
 
+template <int D, bool F8, bool INTER>
+cudaError_t launch_nr(const NormRopeParams& p, int num_sms, cudaStream_t s) {
+  constexpr int HPG = 32 / (D / 8);
+  const long long rows = p.num_q_heads + 2 * p.num_kv_heads;
+  auto blocks = [&](int iter) {
+    const long long chunks = (rows + HPG * iter - 1) / (HPG * iter);
+    return (p.num_tokens * chunks + kThreads / 32 - 1) / (kThreads / 32);
+  };
+#ifndef kManyIter
+#define kManyIter 6
+#endif
+  // Few tokens: one group of heads per warp, the shortest chain. Once that
+  // would be more than the warps an SM holds, kManyIter groups per warp.
+  const bool small = blocks(1) <= 8LL * num_sms;
+  const long long grid = small ? blocks(1) : blocks(kManyIter);
+  if (grid > 0x3fffffffLL) return cudaErrorInvalidValue;  // warps are counted in 32 bits
+  if (small)
+    pa_norm_rope_write_kernel<D, F8, INTER, 1><<<(unsigned)grid, kThreads, 0, s>>>(p);
+  else
+    pa_norm_rope_write_kernel<D, F8, INTER, kManyIter><<<(unsigned)grid, kThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_nr_d(const NormRopeParams& p, int num_sms, cudaStream_t s) {
+  if (p.kv_fp8)
+    return p.interleaved ? launch_nr<D, true, true>(p, num_sms, s)
+                         : launch_nr<D, true, false>(p, num_sms, s);
+  return p.interleaved ? launch_nr<D, false, true>(p, num_sms, s)
+                       : launch_nr<D, false, false>(p, num_sms, s);
+}
+
 }  // namespace
 
-cudaError_t launch_norm_rope_write(const NormRopeParams& p, int head_dim, cudaStream_t s) {
-  const int hpg = 32 / (head_dim / 8);
-  const int rows = p.num_q_heads + 2 * p.num_kv_heads;
-  const long long chunks = (rows + hpg * kIter - 1) / (hpg * kIter);
-  const long long blocks = (p.num_tokens * chunks + kThreads / 32 - 1) / (kThreads / 32);
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const unsigned grid = (unsigned)blocks;
-  if (head_dim == 128) {
-    if (p.kv_fp8)
-      pa_norm_rope_write_kernel<128, true><<<grid, kThreads, 0, s>>>(p);
-    else
-      pa_norm_rope_write_kernel<128, false><<<grid, kThreads, 0, s>>>(p);
-  } else {
-    if (p.kv_fp8)
-      pa_norm_rope_write_kernel<64, true><<<grid, kThreads, 0, s>>>(p);
-    else
-      pa_norm_rope_write_kernel<64, false><<<grid, kThreads, 0, s>>>(p);
-  }
-  return cudaGetLastError();
+cudaError_t launch_norm_rope_write(const NormRopeParams& p, int head_dim, int num_sms,
+                                   cudaStream_t s) {
+  return head_dim == 128 ? launch_nr_d<128>(p, num_sms, s) : launch_nr_d<64>(p, num_sms, s);
 }
 
 }  // namespace pa

@@ -270,7 +270,7 @@ pa_status norm_rope_write_impl(const void* q, const void* k, const void* v, long
   p.err = d->err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   TimerScope timer(0, s);
-  const cudaError_t e = launch_norm_rope_write(p, head_dim, s);
+  const cudaError_t e = launch_norm_rope_write(p, head_dim, d->num_sms, s);
   g_launches.fetch_add(1);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
@@ -448,6 +448,12 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
   pp.token_major = use_tm ? 1 : 0;
   pp.window = window;
   pp.sinks = sinks;
+  // A window leaves short units, and a batch of a few of them is a chain of
+  // blocks in a handful of warps: there the CUDA-core kernel's workers take
+  // single blocks (four tokens of a 16-key window at head_dim 64: MINPOS us
+  // against 15 us with eight blocks each). The tensor-core kernels' workers
+  // keep a whole tile.
+  pp.min_pos = window > 0 && !use_tc ? 1 : PA_DEC_MIN_POS;
   // A mixed batch on the tensor-core split-KV kernel (bf16) may run its
   // prefill chunks on a few SMs beside the split-KV work (the planner decides
   // how many, or none); the E4M3 path keeps its query-split pass between them.
@@ -542,6 +548,7 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
   dp.fold_later = c_overlap;
   dp.window = window;
   dp.sinks = sinks;
+  dp.min_pos = pp.min_pos;
   dp.err = d->err;
   if (use_tc && kv_fp8) {  // the E4M3 tensor-core kernel takes the queries split
     const cudaError_t e = launch_qsplit(dp, group, s);
@@ -570,6 +577,11 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
   mp.num_workers = workers;
   mp.workers_from_header = overlap;
   mp.token_major = pp.token_major;
+  // Few tokens over many workers (a window over long sequences): a token's
+  // partials are shared by the warps of a CTA per KV head (eight tokens over
+  // 152 workers: MERGE us against 16 us for a warp per KV head).
+  mp.tm_wide = window > 0 && use_tm && workers > 4 * num_tokens ? 1 : 0;
+  mp.min_pos = pp.min_pos;
   mp.num_q_heads = num_q_heads;
   mp.num_kv_heads = num_kv_heads;
   mp.num_tokens = num_tokens;
@@ -740,13 +752,14 @@ pa_status weights_impl(const void* q, const void* k_cache, const int32_t* block_
   p.num_slots = lay.num_slots;
   p.max_items[0] = lay.max_items[0];
   p.max_items[1] = lay.max_items[1];
+  p.cluster = 0;
   p.stats = reinterpret_cast<float*>(ws + lay.stats_off);
   p.scores = reinterpret_cast<float*>(ws + lay.scores_off);
   p.counts = reinterpret_cast<int*>(ws + lay.counts_off);
   p.parts = reinterpret_cast<int*>(ws + lay.parts_off);
   p.items[0] = reinterpret_cast<int4*>(ws + lay.items1_off);
   p.items[1] = reinterpret_cast<int4*>(ws + lay.items2_off);
-  p.lse = reinterpret_cast<float*>(ws + lay.lse_off);
+  p.neg_lse = reinterpret_cast<float*>(ws + lay.lse_off);
   p.partial = reinterpret_cast<float2*>(ws + lay.partial_off);
   p.err = d->err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -841,13 +854,69 @@ pa_status pa_evict_kv(void* k_cache, void* v_cache, const int32_t* block_tables,
   p.keep = keep;
   p.recent = recent;
   p.sinks = sinks;
+  p.cluster = 1;
   p.smem_keys = 0;
   p.err = d->err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   TimerScope timer(7, s);
-  const cudaError_t e = launch_evict(p, head_dim * elem_bytes, s);
+  const cudaError_t e = launch_evict(p, head_dim * elem_bytes, d->num_sms, s);
   g_launches.fetch_add(2);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// The struct forms.
+size_t pa_args_size(int which) {
+  switch (which) {
+    case 0: return sizeof(pa_norm_rope_write_args);
+    case 1: return sizeof(pa_window_args);
+    case 2: return sizeof(pa_weights_args);
+    case 3: return sizeof(pa_evict_args);
+  }
+  return 0;
+}
+
+pa_status pa_norm_rope_write_kv_args(const pa_norm_rope_write_args* a) {
+  if (!a) return PA_ERR_INVALID_ARG;
+  return norm_rope_write_impl(a->q, a->k, a->v, a->q_stride, a->k_stride, a->v_stride, a->positions,
+                              a->cos_sin, a->q_weight, a->k_weight, a->eps, a->rotary_dim,
+                              a->interleaved, a->max_position, a->slot_mapping, a->q_out,
+                              a->k_cache, a->v_cache, a->kv_fp8 ? 1 : 0, a->kv_fp8 ? a->k_scale : 1.f,
+                              a->kv_fp8 ? a->v_scale : 1.f, a->num_tokens, a->num_q_heads,
+                              a->num_kv_heads, a->head_dim, a->block_size, a->num_blocks, a->stream);
+}
+
+pa_status pa_attention_window_args(const pa_window_args* a) {
+  if (!a) return PA_ERR_INVALID_ARG;
+  if (a->kv_fp8)
+    return pa_attention_window_fp8(
+        a->q, a->k_cache, a->v_cache, a->block_tables, a->seq_lens, a->query_start_loc, a->scale,
+        a->k_scale, a->v_scale, a->out, a->num_reqs, a->num_tokens, a->num_q_heads, a->num_kv_heads,
+        a->head_dim, a->block_size, a->num_blocks, a->max_blocks_per_req, a->max_query_len,
+        a->max_seq_len, a->window, a->sinks, a->workspace, a->workspace_bytes, a->stream);
+  return pa_attention_window(a->q, a->k_cache, a->v_cache, a->block_tables, a->seq_lens,
+                             a->query_start_loc, a->scale, a->out, a->num_reqs, a->num_tokens,
+                             a->num_q_heads, a->num_kv_heads, a->head_dim, a->block_size,
+                             a->num_blocks, a->max_blocks_per_req, a->max_query_len, a->max_seq_len,
+                             a->window, a->sinks, a->workspace, a->workspace_bytes, a->stream);
+}
+
+pa_status pa_attention_weights_args(const pa_weights_args* a) {
+  if (!a) return PA_ERR_INVALID_ARG;
+  return weights_impl(a->q, a->k_cache, a->block_tables, a->seq_lens, a->query_start_loc, a->scale,
+                      a->kv_fp8 ? 1 : 0, a->kv_fp8 ? a->k_scale : 1.f, a->weights, a->out,
+                      a->weights_stride, a->num_reqs, a->num_tokens, a->num_q_heads,
+                      a->num_kv_heads, a->head_dim, a->block_size, a->num_blocks,
+                      a->max_blocks_per_req, a->max_query_len, a->max_seq_len, a->workspace,
+                      a->workspace_bytes, a->stream);
+}
+
+pa_status pa_evict_kv_args(const pa_evict_args* a) {
+  if (!a) return PA_ERR_INVALID_ARG;
+  return pa_evict_kv(a->k_cache, a->v_cache, a->block_tables, a->seq_lens, a->weights,
+                     a->new_block_tables, a->new_seq_lens, a->kept, a->new_weights, a->num_reqs,
+                     a->num_kv_heads, a->head_dim, a->elem_bytes, a->block_size, a->num_blocks,
+                     a->max_blocks_per_req, a->max_new_blocks, a->weights_stride,
+                     a->new_weights_stride, a->max_seq_len, a->keep, a->recent, a->sinks, a->stream);
 }
 
 pa_status pa_mapped_pointer(const void* host_ptr, void** device_ptr) {

@@ -27,8 +27,8 @@ constexpr int kSelfPlanMaxReqs = 512;
 #ifndef PA_DEC_MIN_POS
 #define PA_DEC_MIN_POS 8
 #endif
-__host__ __device__ inline int plan_workers(int W, int all) {
-  int n = W / PA_DEC_MIN_POS;
+__host__ __device__ inline int plan_workers(int W, int all, int min_pos = PA_DEC_MIN_POS) {
+  int n = W / min_pos;
   return n < 1 ? 1 : (n > all ? all : n);
 }
 // Worker w of NW takes positions [worker_begin(w), worker_begin(w + 1)) of
@@ -225,6 +225,7 @@ struct PlanParams {
   int prefill_ctas_override;  // > 0: the prefill-chunk grid's share, instead of the cost model
   int token_major;  // positions per token are its blocks (all kv heads at once)
   int window, sinks;  // windowed attention (window 0: none)
+  int min_pos;        // positions a worker gets at least (plan_workers)
   WsHeader* header;
   UnitInfo* units;
   PrefillTile* tiles;
@@ -305,6 +306,7 @@ struct DecodeParams {
   // too; the merge pass folds them with the prefix partials (MergeParams::all_units)
   int fold_later;
   int window, sinks;  // windowed attention (window 0: none, the plain instantiations)
+  int min_pos;        // positions a worker gets at least (plan_workers)
   unsigned long long* err;
 };
 
@@ -330,6 +332,10 @@ struct MergeParams {
   int token_major;          // token-major split-KV: a task {token, -, wf, wl} covers every
                             // kv head (a CTA per boundary, a warp per kv head), slot
                             // (token + w) * Hkv + kv head
+  // token-major partials, but a CTA per (boundary, kv head) whose warps share
+  // the head's partials: for few tokens over many workers
+  int tm_wide;
+  int min_pos;  // as the split-KV kernel's
   int num_q_heads, num_kv_heads, num_tokens;
   int key_start_blocks;
   const float* prefix_partials;
@@ -401,12 +407,13 @@ struct WeightsParams {
   int num_reqs, num_tokens, num_q_heads, num_kv_heads, group, num_blocks, bt_stride;
   int max_query_len, max_seq_len;
   int num_chunks, padded_len, stored_rows, num_slots, max_items[2];  // see WeightsLayout
+  int cluster;  // CTAs per (request, kv head), set at launch; 0: the two-kernel form
   float* stats;
   float* scores;
   int* counts;
   int* parts;
   int4* items[2];
-  float* lse;
+  float* neg_lse;  // minus the log2-sum-exp of every row, -inf for rows past a span
   float2* partial;
   unsigned long long* err;
 };
@@ -424,7 +431,9 @@ struct EvictParams {
   int num_reqs, num_kv_heads, num_blocks, max_blocks_per_req, max_new_blocks;
   long long weights_stride, new_weights_stride;
   int max_seq_len, keep, recent, sinks;
-  int smem_keys;  // weights the select kernel keeps in shared memory (set at launch)
+  // set at launch: CTAs per (request, KV head) of the select kernel, and the
+  // keys each keeps in shared memory
+  int cluster, smem_keys;
   unsigned long long* err;
 };
 
@@ -449,12 +458,13 @@ pa_status check_attention_args(const void* q, const void* k_cache, const void* v
 
 // Launchers (return the launch's cudaError_t).
 cudaError_t launch_write_kv(const WriteParams& p, cudaStream_t s);
-cudaError_t launch_norm_rope_write(const NormRopeParams& p, int head_dim, cudaStream_t s);
+cudaError_t launch_norm_rope_write(const NormRopeParams& p, int head_dim, int num_sms,
+                                   cudaStream_t s);
 // The accumulated-weight kernels, in order; *launches: how many.
-cudaError_t launch_weights(const WeightsParams& p, int head_dim, bool f8, int num_sms,
-                           cudaStream_t s, int* launches);
+cudaError_t launch_weights(WeightsParams p, int head_dim, bool f8, int num_sms, cudaStream_t s,
+                           int* launches);
 // The two eviction kernels, in order; row_bytes = head_dim x element bytes.
-cudaError_t launch_evict(EvictParams p, int row_bytes, cudaStream_t s);
+cudaError_t launch_evict(EvictParams p, int row_bytes, int num_sms, cudaStream_t s);
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t s);
 // head_dim / G select the instantiation; unsupported combinations return
 // cudaErrorInvalidValue. occ_cap bounds the resident CTAs per SM (the grid is

@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
   // split-KV kernel), found by binary search over the units' first positions
   __syncthreads();
   if (ubase) {
-    const int NW = plan_workers(W, s_workers);
+    const int NW = plan_workers(W, s_workers, p.min_pos);
     for (int w = threadIdx.x; w < NW; w += blockDim.x) {
       const int S = (int)((long long)w * W / NW);
       int lo = 0, hi = K;  // ubase[lo] <= S < ubase[hi]

@@ -524,19 +524,30 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
         ++ns;
         tc_fence_after();
         const int kv0 = key_tile<WIN>(tl, i) * 128;
-        bool unmasked = __all_sync(kAll, kv0 + 127 <= lim);
-        const int lo = WIN ? lim - p.window + 1 : 0;  // the row sees lo .. lim and the sinks
-        if constexpr (WIN)
-          unmasked = unmasked && __all_sync(kAll, kv0 >= lo || kv0 + 127 < p.sinks);
+        const bool unmasked = __all_sync(kAll, kv0 + 127 <= lim);
+        // WIN: the row sees lo .. lim and the sinks; whole and empty runs of 32
+        // columns are told apart, since a window has two edges to every item
+        const int lo = WIN ? lim - p.window + 1 : 0;
+        uint32_t whole = unmasked ? 15u : 0u, empty = 0u;  // bit c: columns 32 c .. 32 c + 31
+        if constexpr (WIN) {
+          whole = 0u;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int k0 = kv0 + c * 32;
+            if (__all_sync(kAll, k0 + 31 <= lim && (k0 >= lo || k0 + 31 < p.sinks))) whole |= 1u << c;
+            if (__all_sync(kAll, k0 > lim || (k0 + 31 < lo && k0 >= p.sinks))) empty |= 1u << c;
+          }
+        }
         // pass 1: row max of the raw scores over visible keys
         float mx = -INFINITY;
 #pragma unroll 1
         for (int cc = 0; cc < C::CPH; ++cc) {
           const int c = hf * C::CPH + cc;
+          if (WIN && (empty >> c & 1u)) continue;
           uint32_t r[32];
           tmem_ld32(s_addr + c * 32, r);
           tmem_wait_ld();
-          if (unmasked) {
+          if (whole >> c & 1u) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(r[e]));
           } else {
@@ -584,11 +595,17 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
 #pragma unroll 1
         for (int cc = 0; cc < C::CPH; ++cc) {
           const int c = hf * C::CPH + cc;
+          uint32_t w[16];
+          if (WIN && (empty >> c & 1u)) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = 0u;
+            tmem_st16(s_addr + C::pcol(c), w);
+            continue;
+          }
           uint32_t r[32];
           tmem_ld32(s_addr + c * 32, r);
           tmem_wait_ld();
-          uint32_t w[16];
-          if (unmasked) {
+          if (whole >> c & 1u) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const float p0 = ex2_approx(fmaf(__uint_as_float(r[2 * e]), sc, nm));

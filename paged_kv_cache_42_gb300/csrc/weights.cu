@@ -33,7 +33,7 @@
 //   pass 2  X = 128 keys, Y = the query row tiles that see them: the thread
 //           sums exp2(s - lse) over its key's columns, in a fixed order, and
 //           writes the key's weight. No atomics and no partial sums.
-// Two softmax warpgroups take the Y tiles in turn; four S buffers in TMEM let
+// The softmax warpgroups take the Y tiles in turn; four S buffers in TMEM let
 // the MMAs run ahead of them. A pass's pace is the exponentials: 128 x 128 of
 // them are 1024 cycles of an SM's special-function unit, the MMA about half.
 #include <cuda.h>
@@ -49,9 +49,14 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kFewRows = 8;          // rows the bandwidth-bound form takes (the MMA's N)
 constexpr int kChunkBlocks = 16;     // 16-key blocks per warp
 constexpr int kScoreWarps = 4;
+constexpr int kClusterWarps = 8;
+constexpr int kClusterSmem = 64 * 1024;  // scores of one CTA of a cluster, at most: three CTAs on an SM
 constexpr int kFinishThreads = 256;
-constexpr int kFinishKeys = 1024;    // keys of one finish CTA
-constexpr int kSplitTiles = 16;      // key tiles of one part in pass 1
+
+constexpr int kFinishRound = 1024;   // keys of one round of a finish CTA
+constexpr int kFinishKeys = 4 * kFinishRound;  // keys of one finish CTA (joining the chunks costs
+                                                 // each CTA the same, whatever its keys)
+constexpr int kSplitTiles = 32;      // key tiles of one part in pass 1
 constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = 1024;
 constexpr float kNone = -1e30f;      // a running maximum before the first key
@@ -83,11 +88,24 @@ __device__ __forceinline__ Span get_span(const WeightsParams& p, int r, bool rep
 // ---------------------------------------------------------------------------------------
 // few rows
 // ---------------------------------------------------------------------------------------
+// K passes through once.
 __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
   uint4 v;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
+  return v;
+}
+
+// Cluster-wide barrier, and a read of another CTA's shared memory.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ float2 ld_cluster_f2(const void* mine, int rank) {
+  uint32_t at;
+  float2 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(mine)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
   return v;
 }
 
@@ -119,25 +137,310 @@ __device__ __forceinline__ uint32_t float2_to_f16x2(float lo, float hi) {
   return r;
 }
 
-// NR: rows stored per key (the batch's largest count: G for decodes, else 8).
+// The query operand of up to 8 rows (row g: token g / G, head g % G of KV head
+// h) as B fragments, this lane's elements; unscale: of row g (E4M3 form).
+template <int D, bool F8>
+struct QFrag {
+  uint32_t b[D / 16][2];
+  float unscale;
+};
+template <int D, bool F8>
+__device__ __forceinline__ void load_query(const WeightsParams& p, const Span& sp, int h, int rows,
+                                           int lane, QFrag<D, F8>& q) {
+  constexpr int NK = D / 16, NJ = D * (F8 ? 1 : 2) / 64;
+  const int g = lane >> 2, t = lane & 3, G = p.group;
+  q.unscale = 1.f;
+#pragma unroll
+  for (int i = 0; i < NK; ++i) q.b[i][0] = q.b[i][1] = 0u;
+  const uint4* const qrow = reinterpret_cast<const uint4*>(
+      p.q + ((size_t)(sp.q0 + g / G) * p.num_q_heads + (size_t)h * G + g % G) * D);
+  if constexpr (F8) {
+    uint4 raw[NJ][2];
+    float mx = 0.f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        raw[j][e] = g < rows ? __ldg(qrow + (j * 4 + t) * 2 + e) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t w[4] = {raw[j][e].x, raw[j][e].y, raw[j][e].z, raw[j][e].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = bf16x2_to_float2(w[i]);
+          mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+    mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 2));
+    int ex = 0;  // 13 - floor(log2 mx), from the exponent field
+    if (mx > 0.f) {
+      ex = 13 - (((int)(__float_as_uint(mx) >> 23) & 0xff) - 127);
+      ex = ex < -120 ? -120 : (ex > 120 ? 120 : ex);
+    }
+    const float sc = __uint_as_float((uint32_t)(127 + ex) << 23);
+    q.unscale = __uint_as_float((uint32_t)(127 - ex) << 23);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const uint32_t w[8] = {raw[j][0].x, raw[j][0].y, raw[j][0].z, raw[j][0].w,
+                             raw[j][1].x, raw[j][1].y, raw[j][1].z, raw[j][1].w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 f = bf16x2_to_float2(w[i]);
+        q.b[4 * j + i / 2][i & 1] = float2_to_f16x2(f.x * sc, f.y * sc);
+      }
+    }
+  } else if (g < rows) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const uint4 v = __ldg(qrow + j * 4 + t);
+      q.b[2 * j][0] = v.x;
+      q.b[2 * j][1] = v.y;
+      q.b[2 * j + 1][0] = v.z;
+      q.b[2 * j + 1][1] = v.w;
+    }
+  }
+}
+
+// A 16-key block of K as A fragments: keys g and g + 8, this lane's elements.
+template <int D, bool F8>
+struct KFrag {
+  uint4 a[D * (F8 ? 1 : 2) / 64][2];
+};
+template <int D, bool F8>
+__device__ __forceinline__ void load_block(const WeightsParams& p, int h, int id, int lane,
+                                           KFrag<D, F8>& f) {
+  constexpr int VPR = D * (F8 ? 1 : 2) / 16, NJ = VPR / 4;  // vectors of a row, of a lane
+  const uint4* const src = static_cast<const uint4*>(p.k_cache) +
+                           (((size_t)(id < 0 ? 0 : id) * p.num_kv_heads + h) * kBlockSize +
+                            (lane >> 2)) * VPR + (lane & 3);
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    f.a[j][0] = f.a[j][1] = make_uint4(0u, 0u, 0u, 0u);
+    if (id >= 0) {
+      f.a[j][0] = ld_stream(src + 4 * j);
+      f.a[j][1] = ld_stream(src + 8 * VPR + 4 * j);
+    }
+  }
+}
+
+// Scores n >= 1 blocks: id(j) and take(j, fragment) for block j, the next
+// block's loads issued before a block is scored (deeper rings of three and four
+// blocks measured slower: their registers cost more warps than they add loads).
+template <int D, bool F8, typename ID, typename TAKE>
+__device__ __forceinline__ void stream_blocks(const WeightsParams& p, int h, int lane, int n, ID id,
+                                              TAKE take) {
+  KFrag<D, F8> fa, fb;
+  load_block<D, F8>(p, h, id(0), lane, fa);
+#pragma unroll 1
+  for (int j = 0; j < n; j += 2) {
+    if (j + 1 < n) load_block<D, F8>(p, h, id(j + 1), lane, fb);
+    take(j, fa);
+    if (j + 1 >= n) break;
+    if (j + 2 < n) load_block<D, F8>(p, h, id(j + 2), lane, fa);
+    take(j + 1, fb);
+  }
+}
+
+// The running softmax maximum and sum of the two rows a lane holds.
+struct Run2 {
+  float m0, m1, l0, l1;
+  __device__ __forceinline__ void clear() {
+    m0 = m1 = kNone;
+    l0 = l1 = 0.f;
+  }
+  __device__ __forceinline__ void add(float x0, float y0, float x1, float y1) {
+    const float k0 = fmaxf(m0, fmaxf(x0, y0)), k1 = fmaxf(m1, fmaxf(x1, y1));
+    l0 = l0 * ex2_approx(m0 - k0) + (ex2_approx(x0 - k0) + ex2_approx(y0 - k0));
+    l1 = l1 * ex2_approx(m1 - k1) + (ex2_approx(x1 - k1) + ex2_approx(y1 - k1));
+    m0 = k0;
+    m1 = k1;
+  }
+  __device__ __forceinline__ void over_lanes() {  // the lanes of a row are those of equal lane % 4
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      const float a = __shfl_xor_sync(kAll, m0, o), b = __shfl_xor_sync(kAll, m1, o);
+      const float la = __shfl_xor_sync(kAll, l0, o), lb = __shfl_xor_sync(kAll, l1, o);
+      const float k0 = fmaxf(m0, a), k1 = fmaxf(m1, b);
+      l0 = l0 * ex2_approx(m0 - k0) + la * ex2_approx(a - k0);
+      l1 = l1 * ex2_approx(m1 - k1) + lb * ex2_approx(b - k1);
+      m0 = k0;
+      m1 = k1;
+    }
+  }
+};
+
+// Scores of a block: x0, x1 of key `key` (the lane's first) for rows n0, n1, y0,
+// y1 of key + 8, scaled; -inf where the row does not see the key or the block
+// is missing. They go to `at` (+ 8 NR: of key + 8), NR values per key, and into
+// the running maxima and sums.
+template <int D, bool F8, int NR>
+__device__ __forceinline__ void score_block(const KFrag<D, F8>& f, const QFrag<D, F8>& q, int t,
+                                            bool have, int key, int lim0, int lim1, float sc0,
+                                            float sc1, float* at, Run2& run) {
+  constexpr int NJ = D * (F8 ? 1 : 2) / 64;
+  float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // two chains of MMAs
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const uint4 u = f.a[j][0], v = f.a[j][1];
+    if constexpr (F8) {
+      const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        mma_16x8x16<true>(c[e & 1], e4m3x2_to_f16x2((uint16_t)(uw[e] & 0xffffu)),
+                          e4m3x2_to_f16x2((uint16_t)(vw[e] & 0xffffu)),
+                          e4m3x2_to_f16x2((uint16_t)(uw[e] >> 16)),
+                          e4m3x2_to_f16x2((uint16_t)(vw[e] >> 16)), q.b[4 * j + e][0],
+                          q.b[4 * j + e][1]);
+    } else {
+      mma_16x8x16<false>(c[0], u.x, v.x, u.y, v.y, q.b[2 * j][0], q.b[2 * j][1]);
+      mma_16x8x16<false>(c[1], u.z, v.z, u.w, v.w, q.b[2 * j + 1][0], q.b[2 * j + 1][1]);
+    }
+  }
+  const float x0 = have && key <= lim0 ? (c[0][0] + c[1][0]) * sc0 : -INFINITY;
+  const float x1 = have && key <= lim1 ? (c[0][1] + c[1][1]) * sc1 : -INFINITY;
+  const float y0 = have && key + 8 <= lim0 ? (c[0][2] + c[1][2]) * sc0 : -INFINITY;
+  const float y1 = have && key + 8 <= lim1 ? (c[0][3] + c[1][3]) * sc1 : -INFINITY;
+  if constexpr (NR == 1) {
+    if (t == 0) {
+      at[0] = x0;
+      at[8] = y0;
+    }
+  } else if (2 * t < NR) {
+    *reinterpret_cast<float2*>(at) = make_float2(x0, x1);
+    *reinterpret_cast<float2*>(at + 8 * NR) = make_float2(y0, y1);
+  }
+  run.add(x0, y0, x1, y1);
+}
+
+// Few rows, all of a (request, KV head)'s scores in shared memory: a cluster of
+// 1 to 8 CTAs shares its blocks, a warp takes every kClusterWarps-th block of
+// its CTA's part, the maxima and sums are exchanged over distributed shared
+// memory, and each CTA turns its own scores into weights. NR: rows stored per
+// key (the batch's largest count: G for decodes, else 8).
+template <int D, bool F8, int NR>
+__global__ void __launch_bounds__(32 * kClusterWarps, 2) pa_weights_cluster_kernel(const WeightsParams p) {
+  extern __shared__ __align__(16) float score_sm[];  // [keys of the part][NR]
+  __shared__ float2 s_run[kClusterWarps][kFewRows];
+  __shared__ float2 s_cta[kFewRows];                 // this CTA's {max, sum} of each row
+  __shared__ float2 s_row[kFewRows];                 // the request's {max, 1 / sum}
+  if (p.num_slots > 0) griddep_launch_dependents();  // prompt chunks' passes need nothing of this
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int C = p.cluster, rank = (int)(blockIdx.x % (unsigned)C);
+  const int rh = (int)(blockIdx.x / (unsigned)C);
+  const int r = rh / p.num_kv_heads, h = rh - r * p.num_kv_heads;
+  const Span sp = get_span(p, r, rank == 0 && h == 0 && threadIdx.x == 0);
+  const int G = p.group, rows = sp.qlen * G;
+  if (!sp.ok || rows == 0 || rows > kFewRows) {  // the whole cluster alike
+    if (p.num_slots > 0) griddep_wait();  // completes after the plan before it
+    return;
+  }
+  const int nb = (sp.L + kBlockSize - 1) / kBlockSize;
+  const int part = (nb + C - 1) / C;
+  const int b0 = min(nb, rank * part), n = min(nb, b0 + part) - b0;  // this CTA's blocks
+  const int g = lane >> 2, t = lane & 3;
+  QFrag<D, F8> q;
+  load_query<D, F8>(p, sp, h, rows, lane, q);
+  // the two rows whose scores this lane holds, their scales and last keys
+  const int n0 = 2 * t, n1 = 2 * t + 1;
+  float sc0 = p.scale_log2, sc1 = p.scale_log2;
+  if constexpr (F8) {
+    sc0 *= __shfl_sync(kAll, q.unscale, n0 * 4);
+    sc1 *= __shfl_sync(kAll, q.unscale, n1 * 4);
+  }
+  const int ctx = sp.L - sp.qlen;
+  const int lim0 = n0 < rows ? ctx + n0 / G : -1, lim1 = n1 < rows ? ctx + n1 / G : -1;
+  Run2 run;
+  run.clear();
+  // this warp's blocks: warp, warp + kClusterWarps, ... of the part; 32 ids at
+  // a time, the next block on its way while one is scored
+  const int mine = n > warp ? (n - warp + kClusterWarps - 1) / kClusterWarps : 0;
+  const int32_t* const table = p.block_tables + (size_t)r * p.bt_stride + b0 + warp;
+  for (int j0 = 0; j0 < mine; j0 += 32) {
+    int pid = -1;
+    if (j0 + lane < mine) {
+      pid = __ldg(table + (j0 + lane) * kClusterWarps);
+      if (pid < 0 || pid >= p.num_blocks) {
+        report_error(p.err, PA_DEVERR_BLOCK_ID, b0 + warp + (j0 + lane) * kClusterWarps);
+        pid = -1;
+      }
+    }
+    const int nj = min(32, mine - j0);
+    auto take = [&](int j, const KFrag<D, F8>& f) {
+      const int b = warp + (j0 + j) * kClusterWarps;  // block of the part
+      score_block<D, F8, NR>(f, q, t, __shfl_sync(kAll, pid, j) >= 0, (b0 + b) * kBlockSize + g, lim0,
+                             lim1, sc0, sc1, score_sm + (size_t)(b * kBlockSize + g) * NR + n0, run);
+    };
+    stream_blocks<D, F8>(p, h, lane, nj, [&](int j) { return __shfl_sync(kAll, pid, j); }, take);
+  }
+  run.over_lanes();
+  if (g == 0) {
+    s_run[warp][n0] = make_float2(run.m0, run.l0);
+    s_run[warp][n1] = make_float2(run.m1, run.l1);
+  }
+  __syncthreads();
+  if (threadIdx.x < kFewRows) {
+    float m = kNone, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kClusterWarps; ++w) m = fmaxf(m, s_run[w][threadIdx.x].x);
+#pragma unroll
+    for (int w = 0; w < kClusterWarps; ++w)
+      l += s_run[w][threadIdx.x].y * ex2_approx(s_run[w][threadIdx.x].x - m);
+    s_cta[threadIdx.x] = make_float2(m, l);
+  }
+  cluster_sync();
+  if (threadIdx.x < kFewRows) {
+    float m = kNone, l = 0.f;
+    for (int k = 0; k < C; ++k) {
+      const float2 v = ld_cluster_f2(&s_cta[threadIdx.x], k);
+      const float top = fmaxf(m, v.x);
+      l = l * ex2_approx(m - top) + v.y * ex2_approx(v.x - top);
+      m = top;
+    }
+    s_row[threadIdx.x] = make_float2(m, threadIdx.x < rows ? 1.f / l : 0.f);
+  }
+  cluster_sync();  // (no CTA ends while another may still read its shared memory)
+  float rm[NR], rl[NR];
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    rm[i] = s_row[i].x;
+    rl[i] = s_row[i].y;
+  }
+  const float* const old = p.weights + (size_t)rh * p.weights_stride;
+  float* const out = p.out + (size_t)rh * p.weights_stride;
+  const int k0 = b0 * kBlockSize, k1 = min(sp.L, (b0 + n) * kBlockSize);
+#pragma unroll 2
+  for (int key = k0 + (int)threadIdx.x; key < k1; key += 32 * kClusterWarps) {
+    const float was = key < ctx ? old[key] : 0.f;
+    const float* const s = score_sm + (size_t)(key - k0) * NR;
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+      if (i < rows) a += ex2_approx(s[i] - rm[i]) * rl[i];
+    out[key] = was + a;
+  }
+  if (p.num_slots > 0) griddep_wait();
+  __threadfence();  // performed before the CTA ends: the next grid may be a programmatic one
+}
+
+// Few rows of sequences whose scores outgrow a cluster's shared memory: scores
+// and each 256-key chunk's maximum and sum go through global memory to the
+// finish kernel.
 template <int D, bool F8, int NR>
 __global__ void __launch_bounds__(32 * kScoreWarps) pa_weights_score_kernel(const WeightsParams p) {
-  constexpr int EB = F8 ? 1 : 2;
-  constexpr int VPR = D * EB / 16;  // 16-byte vectors of a key row
-  constexpr int NJ = VPR / 4;       // vectors a lane takes of a row
-  constexpr int NK = D / 16;        // MMAs per block
   griddep_launch_dependents();      // the finish grid waits for this one
+  // (the plan, if any, comes before: this grid completes after it)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (p.num_chunks + kScoreWarps - 1) / kScoreWarps;
   const int rh = (int)(blockIdx.x / (unsigned)per), cc = (int)(blockIdx.x - (unsigned)(rh * per));
   const int r = rh / p.num_kv_heads, h = rh - r * p.num_kv_heads;
   const Span sp = get_span(p, r, cc == 0 && h == 0 && threadIdx.x == 0);
   const int G = p.group, rows = sp.qlen * G;
-  if (!sp.ok || rows == 0 || rows > kFewRows) return;
   const int nb = (sp.L + kBlockSize - 1) / kBlockSize;
   const int chunk = cc * kScoreWarps + warp;
   const int b0 = chunk * kChunkBlocks;
-  if (b0 >= nb) return;
+  if (!sp.ok || rows == 0 || rows > kFewRows || b0 >= nb) {
+    if (p.num_slots > 0) griddep_wait();
+    return;
+  }
   const int n = min(kChunkBlocks, nb - b0);
   int pid = -1;
   if (lane < n) {
@@ -148,154 +451,31 @@ __global__ void __launch_bounds__(32 * kScoreWarps) pa_weights_score_kernel(cons
     }
   }
   const int g = lane >> 2, t = lane & 3;
-
-  // the query operand: row g (token g / G, head g % G), this lane's elements
-  uint32_t bq[NK][2];
-  float unscale = 1.f;  // of row g
-#pragma unroll
-  for (int i = 0; i < NK; ++i) bq[i][0] = bq[i][1] = 0u;
-  {
-    const uint4* const qrow = reinterpret_cast<const uint4*>(
-        p.q + ((size_t)(sp.q0 + g / G) * p.num_q_heads + (size_t)h * G + g % G) * D);
-    if constexpr (F8) {
-      uint4 raw[NJ][2];
-      float mx = 0.f;
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          raw[j][e] = g < rows ? __ldg(qrow + (j * 4 + t) * 2 + e) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t w[4] = {raw[j][e].x, raw[j][e].y, raw[j][e].z, raw[j][e].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 f = bf16x2_to_float2(w[i]);
-            mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
-          }
-        }
-      mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 2));
-      int ex = 0;  // 13 - floor(log2 mx), from the exponent field
-      if (mx > 0.f) {
-        ex = 13 - (((int)(__float_as_uint(mx) >> 23) & 0xff) - 127);
-        ex = ex < -120 ? -120 : (ex > 120 ? 120 : ex);
-      }
-      const float sc = __uint_as_float((uint32_t)(127 + ex) << 23);
-      unscale = __uint_as_float((uint32_t)(127 - ex) << 23);
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const uint32_t w[8] = {raw[j][0].x, raw[j][0].y, raw[j][0].z, raw[j][0].w,
-                               raw[j][1].x, raw[j][1].y, raw[j][1].z, raw[j][1].w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 f = bf16x2_to_float2(w[i]);
-          bq[4 * j + i / 2][i & 1] = float2_to_f16x2(f.x * sc, f.y * sc);
-        }
-      }
-    } else if (g < rows) {
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const uint4 v = __ldg(qrow + j * 4 + t);
-        bq[2 * j][0] = v.x;
-        bq[2 * j][1] = v.y;
-        bq[2 * j + 1][0] = v.z;
-        bq[2 * j + 1][1] = v.w;
-      }
-    }
-  }
-  // the two rows whose scores this lane holds, their scales and last keys
-  const int n0 = 2 * t, n1 = 2 * t + 1;
+  QFrag<D, F8> q;
+  load_query<D, F8>(p, sp, h, rows, lane, q);
+  const int n0 = 2 * t, n1 = 2 * t + 1;  // as in the cluster form
   float sc0 = p.scale_log2, sc1 = p.scale_log2;
   if constexpr (F8) {
-    sc0 *= __shfl_sync(kAll, unscale, n0 * 4);
-    sc1 *= __shfl_sync(kAll, unscale, n1 * 4);
+    sc0 *= __shfl_sync(kAll, q.unscale, n0 * 4);
+    sc1 *= __shfl_sync(kAll, q.unscale, n1 * 4);
   }
   const int ctx = sp.L - sp.qlen;
   const int lim0 = n0 < rows ? ctx + n0 / G : -1, lim1 = n1 < rows ? ctx + n1 / G : -1;
-
-  struct Frag {
-    uint4 a[NJ][2];
-  };
-  const uint4* const kc = static_cast<const uint4*>(p.k_cache);
-  auto load = [&](int i, Frag& f) {
-    const int id = __shfl_sync(kAll, pid, i);
-    const uint4* const src =
-        kc + (((size_t)(id < 0 ? 0 : id) * p.num_kv_heads + h) * kBlockSize + g) * VPR + t;
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      f.a[j][0] = f.a[j][1] = make_uint4(0u, 0u, 0u, 0u);
-      if (id >= 0) {
-        f.a[j][0] = ld_stream(src + 4 * j);
-        f.a[j][1] = ld_stream(src + 8 * VPR + 4 * j);
-      }
-    }
-  };
-  float m0 = kNone, m1 = kNone, l0 = 0.f, l1 = 0.f;
   float* const score = p.scores + ((size_t)rh * p.padded_len + (size_t)b0 * kBlockSize) * NR;
-  auto take = [&](int i, const Frag& f) {
-    float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // two chains of MMAs
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const uint4 u = f.a[j][0], v = f.a[j][1];
-      if constexpr (F8) {
-        const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mma_16x8x16<true>(c[e & 1], e4m3x2_to_f16x2((uint16_t)(uw[e] & 0xffffu)),
-                            e4m3x2_to_f16x2((uint16_t)(vw[e] & 0xffffu)),
-                            e4m3x2_to_f16x2((uint16_t)(uw[e] >> 16)),
-                            e4m3x2_to_f16x2((uint16_t)(vw[e] >> 16)), bq[4 * j + e][0],
-                            bq[4 * j + e][1]);
-      } else {
-        mma_16x8x16<false>(c[0], u.x, v.x, u.y, v.y, bq[2 * j][0], bq[2 * j][1]);
-        mma_16x8x16<false>(c[1], u.z, v.z, u.w, v.w, bq[2 * j + 1][0], bq[2 * j + 1][1]);
-      }
-    }
-    const bool have = __shfl_sync(kAll, pid, i) >= 0;
-    const int key = (b0 + i) * kBlockSize + g;
-    const float x0 = have && key <= lim0 ? (c[0][0] + c[1][0]) * sc0 : -INFINITY;
-    const float x1 = have && key <= lim1 ? (c[0][1] + c[1][1]) * sc1 : -INFINITY;
-    const float y0 = have && key + 8 <= lim0 ? (c[0][2] + c[1][2]) * sc0 : -INFINITY;
-    const float y1 = have && key + 8 <= lim1 ? (c[0][3] + c[1][3]) * sc1 : -INFINITY;
-    float* const at = score + (size_t)(i * kBlockSize + g) * NR + n0;
-    if constexpr (NR == 1) {
-      if (t == 0) {
-        at[0] = x0;
-        at[8] = y0;
-      }
-    } else if (n0 < NR) {
-      *reinterpret_cast<float2*>(at) = make_float2(x0, x1);
-      *reinterpret_cast<float2*>(at + 8 * NR) = make_float2(y0, y1);
-    }
-    const float k0 = fmaxf(m0, fmaxf(x0, y0)), k1 = fmaxf(m1, fmaxf(x1, y1));
-    l0 = l0 * ex2_approx(m0 - k0) + (ex2_approx(x0 - k0) + ex2_approx(y0 - k0));
-    l1 = l1 * ex2_approx(m1 - k1) + (ex2_approx(x1 - k1) + ex2_approx(y1 - k1));
-    m0 = k0;
-    m1 = k1;
+  Run2 run;
+  run.clear();
+  auto take = [&](int i, const KFrag<D, F8>& f) {
+    score_block<D, F8, NR>(f, q, t, __shfl_sync(kAll, pid, i) >= 0, (b0 + i) * kBlockSize + g, lim0,
+                           lim1, sc0, sc1, score + (size_t)(i * kBlockSize + g) * NR + n0, run);
   };
-  Frag fa, fb;
-  load(0, fa);
-#pragma unroll 1
-  for (int i = 0; i < n; i += 2) {
-    if (i + 1 < n) load(i + 1, fb);
-    take(i, fa);
-    if (i + 1 >= n) break;
-    if (i + 2 < n) load(i + 2, fa);
-    take(i + 1, fb);
+  stream_blocks<D, F8>(p, h, lane, n, [&](int j) { return __shfl_sync(kAll, pid, j); }, take);
+  run.over_lanes();
+  if (g == 0) {  // [row][chunk]: the finish kernel reads a row's chunks side by side
+    float2* const st = reinterpret_cast<float2*>(p.stats) + (size_t)rh * kFewRows * p.num_chunks + chunk;
+    st[(size_t)n0 * p.num_chunks] = make_float2(run.m0, run.l0);
+    st[(size_t)n1 * p.num_chunks] = make_float2(run.m1, run.l1);
   }
-  // over the lanes of a row (those of equal t)
-#pragma unroll
-  for (int o = 4; o < 32; o <<= 1) {
-    const float a = __shfl_xor_sync(kAll, m0, o), b = __shfl_xor_sync(kAll, m1, o);
-    const float la = __shfl_xor_sync(kAll, l0, o), lb = __shfl_xor_sync(kAll, l1, o);
-    const float k0 = fmaxf(m0, a), k1 = fmaxf(m1, b);
-    l0 = l0 * ex2_approx(m0 - k0) + la * ex2_approx(a - k0);
-    l1 = l1 * ex2_approx(m1 - k1) + lb * ex2_approx(b - k1);
-    m0 = k0;
-    m1 = k1;
-  }
-  if (g == 0)
-    *reinterpret_cast<float4*>(p.stats + ((size_t)rh * p.num_chunks + chunk) * (2 * kFewRows) +
-                               4 * t) = make_float4(m0, l0, m1, l1);
+  if (p.num_slots > 0) griddep_wait();
 }
 
 template <int NR>
@@ -307,19 +487,63 @@ __global__ void __launch_bounds__(kFinishThreads) pa_weights_finish_kernel(const
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Span sp = get_span(p, r, false);
   const int rows = sp.qlen * p.group;
+  // with prompt chunks in the batch their passes follow; they need nothing of
+  // this grid and wait for it before they complete
+  if (p.num_slots > 0) griddep_launch_dependents();
   griddep_wait();  // the score grid (and, through it, what came before)
   if (!sp.ok || rows == 0 || rows > kFewRows || cc * kFinishKeys >= sp.L) return;
+  const int ctx = sp.L - sp.qlen;
+  const float* const old = p.weights + (size_t)rh * p.weights_stride;
+  float* const out = p.out + (size_t)rh * p.weights_stride;
+  // A thread takes up to four rows of a key (two threads a key of eight rows:
+  // a warp's loads are then one contiguous run). The next round's scores and
+  // sums so far are always on their way: the first round's while the chunks
+  // are joined.
+  constexpr int LPK = NR == 8 ? 2 : 1, RPL = NR / LPK;
+  constexpr int SLOTS = kFinishRound * LPK / kFinishThreads;
+  const int half = LPK == 2 ? (tid & 1) : 0;
+  const int first = cc * kFinishKeys, last = min(sp.L, first + kFinishKeys);
+  struct Round {
+    float x[SLOTS][RPL], was[SLOTS];
+  };
+  auto load = [&](int k0, Round& q) {
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) {
+      const int key = k0 + (i * kFinishThreads + tid) / LPK;
+      const float* const s = p.scores + ((size_t)rh * p.padded_len + key) * NR + half * RPL;
+      q.was[i] = 0.f;
+      if (key < last) {
+        if constexpr (RPL == 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(s));
+          q.x[i][0] = v.x, q.x[i][1] = v.y, q.x[i][2] = v.z, q.x[i][3] = v.w;
+        } else {
+#pragma unroll
+          for (int n = 0; n < RPL; ++n) q.x[i][n] = __ldcg(s + n);
+        }
+        if (key < ctx && half == 0) q.was[i] = old[key];
+      }
+    }
+  };
+  Round ra, rb;
+  load(first, ra);
   // warp n joins row n's chunks
   {
     static_assert(kFinishThreads / 32 == kFewRows, "a warp per row");
     const int chunks = (sp.L + kChunkBlocks * kBlockSize - 1) / (kChunkBlocks * kBlockSize);
     const float2* const st = reinterpret_cast<const float2*>(p.stats) +
-                             (size_t)rh * p.num_chunks * kFewRows + warp;
+                             ((size_t)rh * kFewRows + warp) * p.num_chunks;
     float m = kNone, l = 0.f;
-    for (int c = lane; c < chunks; c += 32) {
-      const float2 v = __ldcg(st + (size_t)c * kFewRows);
-      const float k = fmaxf(m, v.x);
-      l = l * ex2_approx(m - k) + v.y * ex2_approx(v.x - k);
+    for (int c0 = 0; c0 < chunks; c0 += 128) {  // four chunks per lane and round trip
+      float2 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int c = c0 + u * 32 + lane;
+        v[u] = c < chunks ? __ldcg(st + c) : make_float2(kNone, 0.f);
+      }
+      const float k = fmaxf(fmaxf(m, fmaxf(v[0].x, v[1].x)), fmaxf(v[2].x, v[3].x));
+      l *= ex2_approx(m - k);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) l += v[u].y * ex2_approx(v[u].x - k);
       m = k;
     }
 #pragma unroll
@@ -335,36 +559,31 @@ __global__ void __launch_bounds__(kFinishThreads) pa_weights_finish_kernel(const
     }
   }
   __syncthreads();
-  float m[NR], inv[NR];
+  float m[RPL], inv[RPL];
 #pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    m[n] = s_m[n];
-    inv[n] = s_inv[n];
+  for (int n = 0; n < RPL; ++n) {
+    m[n] = s_m[half * RPL + n];
+    inv[n] = s_inv[half * RPL + n];
   }
-  const int ctx = sp.L - sp.qlen;
-  const float* const old = p.weights + (size_t)rh * p.weights_stride;
-  float* const out = p.out + (size_t)rh * p.weights_stride;
+  auto finish = [&](int k0, const Round& q) {
 #pragma unroll
-  for (int i = 0; i < kFinishKeys / kFinishThreads; ++i) {
-    const int key = cc * kFinishKeys + i * kFinishThreads + tid;
-    if (key >= sp.L) break;
-    const float* const s = p.scores + ((size_t)rh * p.padded_len + key) * NR;
-    float x[NR];
-    if constexpr (NR >= 4) {
+    for (int i = 0; i < SLOTS; ++i) {
+      const int key = k0 + (i * kFinishThreads + tid) / LPK;
+      float a = 0.f;
 #pragma unroll
-      for (int n = 0; n < NR; n += 4) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(s + n));
-        x[n] = v.x, x[n + 1] = v.y, x[n + 2] = v.z, x[n + 3] = v.w;
-      }
-    } else {
-#pragma unroll
-      for (int n = 0; n < NR; ++n) x[n] = __ldcg(s + n);
+      for (int n = 0; n < RPL; ++n)
+        if (half * RPL + n < rows && key < last) a += ex2_approx(q.x[i][n] - m[n]) * inv[n];
+      if constexpr (LPK == 2) a += __shfl_xor_sync(kAll, a, 1);
+      if (key < last && half == 0) out[key] = q.was[i] + a;
     }
-    float a = 0.f;
-#pragma unroll
-    for (int n = 0; n < NR; ++n)
-      if (n < rows) a += ex2_approx(x[n] - m[n]) * inv[n];
-    out[key] = key < ctx ? old[key] + a : a;
+  };
+#pragma unroll 1
+  for (int k0 = first; k0 < last; k0 += 2 * kFinishRound) {
+    if (k0 + kFinishRound < last) load(k0 + kFinishRound, rb);
+    finish(k0, ra);
+    if (k0 + kFinishRound >= last) break;
+    if (k0 + 2 * kFinishRound < last) load(k0 + 2 * kFinishRound, ra);
+    finish(k0 + kFinishRound, rb);
   }
   __threadfence();  // performed before the CTA ends: the next grid may be a programmatic one
 }
@@ -372,42 +591,69 @@ __global__ void __launch_bounds__(kFinishThreads) pa_weights_finish_kernel(const
 // ---------------------------------------------------------------------------------------
 // many rows
 // ---------------------------------------------------------------------------------------
+// One work item, all its roles need in 32 bytes.
+struct WItem {
+  int r, h, q0, qlen;
+  int ctx;
+  int x;      // row tile (pass 1) or key tile (pass 2) of X
+  int y0, n;  // Y tiles y0 .. y0 + n - 1
+};
+static_assert(sizeof(WItem) == 32, "two 16-byte loads");
+
 // The work lists of both passes, longest items first (bucket counts), and the
 // number of key parts of every row tile. Row tile rt of request r has slot
 // q0 / TOK + r + rt: consecutive requests' slots never meet, since a span of
-// qlen tokens has at most (q0 + qlen) / TOK - q0 / TOK + 1 tiles.
+// qlen tokens has at most (q0 + qlen) / TOK - q0 / TOK + 1 tiles. A warp takes
+// a request, its lanes the request's tiles.
 __global__ void __launch_bounds__(kPlanThreads) pa_weights_plan_kernel(const WeightsParams p) {
   __shared__ int cnt[2][kBuckets];
   __shared__ int wsum[kPlanThreads / 32], s_fits;
+  griddep_launch_dependents();  // the decodes' grids need no plan and wait for this one at their end
   bool none = false;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int TOK = 128 / p.group;
   for (int b = tid; b < kBuckets; b += kPlanThreads) cnt[0][b] = cnt[1][b] = 0;
+  for (int i = tid; i < p.num_slots; i += kPlanThreads) p.parts[i] = 0;
   __syncthreads();
+  auto put = [&](int k, const WItem& w) -> int {  // a place in the list for every KV head
+    return atomicAdd(&cnt[k][min(w.n, kBuckets - 1)], p.num_kv_heads);
+  };
+  auto write = [&](int k, int at, WItem w) {
+    int4* const dst = p.items[k] + 2 * (size_t)at;
+    for (int h = 0; h < p.num_kv_heads; ++h) {
+      dst[2 * h] = make_int4(w.r, h, w.q0, w.qlen);
+      dst[2 * h + 1] = make_int4(w.ctx, w.x, w.y0, w.n);
+    }
+  };
   // what: 0 counts the items per bucket, 1 writes them
   auto walk = [&](int what) {
-    for (int r = tid; r < p.num_reqs; r += kPlanThreads) {
-      const Span s = get_span(p, r, what == 0);
-      if (!s.ok || s.qlen * p.group <= kFewRows) continue;
-      const int ctx = s.L - s.qlen, nrt = (s.qlen + TOK - 1) / TOK;
-      for (int rt = 0; rt < nrt; ++rt) {
-        const int last = ctx + min(s.qlen, (rt + 1) * TOK) - 1;
-        const int nkt = last / 128 + 1;
-        const int slot = s.q0 / TOK + r + rt;
-        if (what) p.parts[slot] = (nkt + kSplitTiles - 1) / kSplitTiles;
-        for (int i0 = 0; i0 < nkt; i0 += kSplitTiles) {
-          const int len = min(kSplitTiles, nkt - i0);
-          const int at = atomicAdd(&cnt[0][min(len, kBuckets - 1)], p.num_kv_heads);
-          if (what)
-            for (int h = 0; h < p.num_kv_heads; ++h) p.items[0][at + h] = make_int4(r, h, rt, i0);
+    for (int r0 = warp * 32; r0 < p.num_reqs; r0 += kPlanThreads) {
+      // 32 requests' spans in one round trip; then those with many rows in turn
+      Span mine{0, 0, 0, false};
+      if (r0 + lane < p.num_reqs) mine = get_span(p, r0 + lane, what == 0);
+      unsigned todo = __ballot_sync(kAll, mine.ok && mine.qlen * p.group > kFewRows);
+      while (todo) {
+        const int src = __ffs((int)todo) - 1, r = r0 + src;
+        todo &= todo - 1;
+        const int q0 = __shfl_sync(kAll, mine.q0, src), qlen = __shfl_sync(kAll, mine.qlen, src);
+        const int L = __shfl_sync(kAll, mine.L, src), ctx = L - qlen;
+        const int nrt = (qlen + TOK - 1) / TOK;
+        for (int rt = lane; rt < nrt; rt += 32) {
+          const int nkt = (ctx + min(qlen, (rt + 1) * TOK) - 1) / 128 + 1;
+          if (what) p.parts[q0 / TOK + r + rt] = (nkt + kSplitTiles - 1) / kSplitTiles;
+          for (int i0 = 0; i0 < nkt; i0 += kSplitTiles) {
+            const WItem w{r, 0, q0, qlen, ctx, rt, i0, min(kSplitTiles, nkt - i0)};
+            const int at = put(0, w);
+            if (what) write(0, at, w);
+          }
         }
-      }
-      const int nkt = (s.L + 127) / 128;
-      for (int kt = 0; kt < nkt; ++kt) {
-        const int rt0 = max(0, kt * 128 - ctx) / TOK;  // the first row tile that sees the keys
-        const int at = atomicAdd(&cnt[1][min(nrt - rt0, kBuckets - 1)], p.num_kv_heads);
-        if (what)
-          for (int h = 0; h < p.num_kv_heads; ++h) p.items[1][at + h] = make_int4(r, h, kt, rt0);
+        const int nkt = (L + 127) / 128;
+        for (int kt = lane; kt < nkt; kt += 32) {
+          const int rt0 = max(0, kt * 128 - ctx) / TOK;  // the first row tile that sees the keys
+          const WItem w{r, 0, q0, qlen, ctx, kt, rt0, nrt - rt0};
+          const int at = put(1, w);
+          if (what) write(1, at, w);
+        }
       }
     }
   };
@@ -425,8 +671,10 @@ __global__ void __launch_bounds__(kPlanThreads) pa_weights_plan_kernel(const Wei
     }
     if (lane == 31) wsum[warp] = incl;
     __syncthreads();
-    int before = incl - v;
-    for (int w = 0; w < warp; ++w) before += wsum[w];
+    int below = lane < warp ? wsum[lane] : 0;  // the warps before this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) below += __shfl_xor_sync(kAll, below, o);
+    const int before = below + incl - v;
     cnt[k][b] = before;
     // spans that overlap (a query_start_loc that falls) could outgrow the list
     if (tid == kPlanThreads - 1) {
@@ -438,15 +686,11 @@ __global__ void __launch_bounds__(kPlanThreads) pa_weights_plan_kernel(const Wei
     none = none || s_fits == 0;
     __syncthreads();
   }
-  for (int i = tid; i < p.num_slots; i += kPlanThreads) p.parts[i] = 0;
-  __syncthreads();
   if (none) {  // no such request, or spans that cannot be
     if (tid < 2) p.counts[tid] = 0;
   } else {
     walk(1);
   }
-  griddep_launch_dependents();
-  griddep_wait();  // complete only after the grid before: later waits see its work too
 }
 static_assert(kBuckets == kPlanThreads, "one bucket per thread");
 
@@ -466,12 +710,19 @@ __global__ void __launch_bounds__(128) pa_weights_join_kernel(const WeightsParam
     l = l * ex2_approx(m - k) + v.y * ex2_approx(v.x - k);
     m = k;
   }
-  p.lse[at] = l > 0.f ? m + log2f(l) : INFINITY;  // rows past the span: +inf, a weight of zero
+  p.neg_lse[at] = l > 0.f ? -(m + log2f(l)) : -INFINITY;  // rows past the span: a weight of zero
   __threadfence();
 }
 
-template <int D>
+template <int D, bool F8>
 struct WCfg {
+  // Softmax warpgroups. A tile is a chain of TMEM loads, exponentials and sums
+  // in one thread; four tiles in work at once hide it (two: 34 us and 30 us for
+  // the passes over three 512-token chunks, against PASS1 and PASS2). The E4M3
+  // form has converter warps besides, and registers for three.
+  static constexpr int NWG = F8 ? 3 : 4;
+  static constexpr int THREADS = 64 + 128 * NWG;      // producer, MMA issuer, softmax
+  static constexpr int ALL_THREADS = THREADS + (F8 ? 128 : 0);  // + 4 converter warps
   static constexpr int NCH = D / 64;           // 64-element (128-byte) parts of a row
   static constexpr int CHUNK = 128 * 128;
   static constexpr int TILE = NCH * CHUNK;     // a 128-row operand
@@ -482,16 +733,13 @@ struct WCfg {
   static constexpr int OFF_Y = 2 * TILE;
   static constexpr int OFF_LSE = OFF_Y + NY * TILE;
   static constexpr int OFF_XCH = OFF_LSE + NLSE * 512;
-  static constexpr int OFF_BAR = OFF_XCH + 128 * 8;
+  static constexpr int OFF_BAR = OFF_XCH + (NWG - 1) * 128 * 8;
   static constexpr int B_XF = 0, B_XE = 2, B_YF = 4, B_YE = B_YF + NY, B_SF = B_YE + NY,
                        B_SE = B_SF + NS, B_XCHF = B_SE + NS, B_XCHE = B_XCHF + 1,
                        B_DRAIN = B_XCHE + 1, B_COUNT = B_DRAIN + 1;
   static constexpr int SMEM = OFF_BAR + 8 * B_COUNT + 16 + 1024;
   static_assert(SMEM <= 227 * 1024, "one CTA per SM");
 };
-constexpr int kTcThreads = 320;             // producer, MMA issuer, 2 x 4 softmax warps
-constexpr int kTcThreadsF8 = kTcThreads + 128;  // + 4 converter warps
-
 }  // namespace
 
 struct WeightsTcParams {
@@ -502,32 +750,11 @@ struct WeightsTcParams {
 
 namespace {
 
-struct WItem {
-  int r, h, q0, qlen, ctx, L;
-  int x;         // row tile (pass 1) or key tile (pass 2) of X
-  int y0, n;     // Y tiles y0 .. y0 + n - 1
-};
-
 template <int PASS>
 __device__ __forceinline__ WItem get_witem(const WeightsParams& p, int t) {
-  const int4 v = __ldcg(p.items[PASS - 1] + t);
-  const int TOK = 128 / p.group;
-  WItem it;
-  it.r = v.x;
-  it.h = v.y;
-  it.x = v.z;
-  it.y0 = v.w;
-  it.q0 = __ldg(p.qsl + it.r);
-  it.qlen = __ldg(p.qsl + it.r + 1) - it.q0;
-  it.L = __ldg(p.seq_lens + it.r);
-  it.ctx = it.L - it.qlen;
-  if (PASS == 1) {
-    const int last = it.ctx + min(it.qlen, (it.x + 1) * TOK) - 1;
-    it.n = min(kSplitTiles, last / 128 + 1 - it.y0);
-  } else {
-    it.n = (it.qlen + TOK - 1) / TOK - it.y0;
-  }
-  return it;
+  const int4 a = __ldcg(p.items[PASS - 1] + 2 * (size_t)t);
+  const int4 b = __ldcg(p.items[PASS - 1] + 2 * (size_t)t + 1);
+  return WItem{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 
 __device__ __forceinline__ int snake(int i) {  // rounds of items in alternating direction
@@ -536,9 +763,9 @@ __device__ __forceinline__ int snake(int i) {  // rounds of items in alternating
 }
 
 template <int D, int PASS, bool F8>
-__global__ void __launch_bounds__(F8 ? kTcThreadsF8 : kTcThreads, 1)
+__global__ void __launch_bounds__(WCfg<D, F8>::ALL_THREADS, 1)
     pa_weights_tc_kernel(const __grid_constant__ WeightsTcParams tp) {
-  using C = WCfg<D>;
+  using C = WCfg<D, F8>;
   const WeightsParams& p = tp.w;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -558,7 +785,8 @@ __global__ void __launch_bounds__(F8 ? kTcThreadsF8 : kTcThreads, 1)
     for (int i = 0; i < C::B_COUNT; ++i) {
       int n = 1;
       if (i >= C::B_SE && i < C::B_SE + C::NS) n = 128;  // a softmax warpgroup
-      if (i == C::B_XCHF || i == C::B_XCHE) n = 128;
+      if (i == C::B_XCHF) n = 128 * (C::NWG - 1);
+      if (i == C::B_XCHE) n = 128;
       if (kConvY && i >= C::B_YF && i < C::B_YF + C::NY) n = 4;  // the converter warps
       if (kConvX && i >= C::B_XF && i < C::B_XF + 2) n = 4;
       mbar_init(BAR(i), n);
@@ -581,7 +809,7 @@ __global__ void __launch_bounds__(F8 ? kTcThreadsF8 : kTcThreads, 1)
 
   // a request's key tile: 16-key blocks by lanes 0 .. 7, one copy per 64 dims
   auto load_keys = [&](const WItem& it, int kt, uint32_t dst, uint32_t bar) {
-    const int b = kt * 8 + lane, nb = (it.L + kBlockSize - 1) / kBlockSize;
+    const int b = kt * 8 + lane, nb = (it.ctx + it.qlen + kBlockSize - 1) / kBlockSize;
     int pid = -1;
     if (lane < 8 && b < nb) {
       pid = __ldg(p.block_tables + (size_t)it.r * p.bt_stride + b);
@@ -609,7 +837,7 @@ __global__ void __launch_bounds__(F8 ? kTcThreadsF8 : kTcThreads, 1)
       if (PASS == 2) {
         const int slot = it.q0 / TOK + it.r + rt;
         bulk_g2s(base + C::OFF_LSE + lse_slot * 512,
-                 p.lse + ((size_t)it.h * p.num_slots + slot) * 128, 512, bar);
+                 p.neg_lse + ((size_t)it.h * p.num_slots + slot) * 128, 512, bar);
       }
     }
     __syncwarp();
@@ -680,30 +908,35 @@ __global__ void __launch_bounds__(F8 ? kTcThreadsF8 : kTcThreads, 1)
     if (lane == 0) umma_commit(BAR(C::B_DRAIN));
     __syncwarp();
     mbar_wait_bounded(BAR(C::B_DRAIN), 0);
-  } else if (warp < 10) {
-    // ======================= softmax (two warpgroups) =======================
+  } else if (warp < 2 + 4 * C::NWG) {
+    // ======================= softmax =======================
     const int wg = (warp - 2) / 4;
     const int q4 = warp & 3;             // the TMEM lane quarter this warp may access
     const int m = q4 * 32 + lane;        // row of X
     const uint32_t trow = ((uint32_t)(q4 * 32) << 16) + tmem;
     float2* const xch = reinterpret_cast<float2*>(gb + C::OFF_XCH);
     const float sc = p.scale_log2;
+    const float2 sc2 = make_float2(sc, sc), one2 = make_float2(1.f, 1.f);
     int g = 0, it = 0;
     bool ok = true;
     for (int t = snake(it); ok && t < nitems; t = snake(++it)) {
       const WItem w = get_witem<PASS>(p, t);
+      const int L = w.ctx + w.qlen;
       // pass 1: this thread's query row; pass 2: its key
       const int j = w.x * TOK + m / p.group;
-      const int lim = PASS == 1 ? (j < w.qlen ? w.ctx + j : -1) : w.L - 1;
+      const int lim = PASS == 1 ? (j < w.qlen ? w.ctx + j : -1) : L - 1;
       const int key = w.x * 128 + m;
       float mx = kNone, l = 0.f;
+      // pass 2: the key's sum so far, needed at the end
+      const size_t okey = ((size_t)w.r * p.num_kv_heads + w.h) * p.weights_stride + key;
+      const float was = PASS == 2 && wg == 0 && key < w.ctx ? p.weights[okey] : 0.f;
       for (int i = 0; i < w.n; ++i, ++g) {
-        if ((g & 1) != wg) continue;
+        if (g % C::NWG != wg) continue;
         const int sb = g % C::NS;
         if (!wait(C::B_SF + sb, g / C::NS)) { ok = false; break; }
         tc_fence_after();
         const uint32_t s0 = trow + 128 * sb;
-        // columns lo .. hi - 1 of this row count
+        // this thread's columns: lo .. hi - 1
         int lo, hi;
         if (PASS == 1) {
           lo = 0;
@@ -713,117 +946,128 @@ __global__ void __launch_bounds__(F8 ? kTcThreadsF8 : kTcThreads, 1)
           lo = (key - w.ctx - j0) * p.group;
           hi = (w.qlen - j0) * p.group;
         }
-        const bool full = __all_sync(kAll, lo <= 0 && hi >= 128);
-        const float4* const lse =
+        const float4* const nlse =
             reinterpret_cast<const float4*>(gb + C::OFF_LSE + (g % C::NLSE) * 512);
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t rr[32];
-          tmem_ld32(s0 + c * 32, rr);
-          tmem_wait_ld();
-          float x[32];
-          if (PASS == 1) {
+        // 32 columns, the next 32 on their way from TMEM meanwhile
+        auto take = [&](int c, uint32_t (&rr)[32]) {
+          const int lc = lo - c * 32, hc = hi - c * 32;
+          if (__all_sync(kAll, hc <= 0 || lc >= 32)) return;  // no thread sees any of them
+          const bool full = __all_sync(kAll, lc <= 0 && hc >= 32);
+          float2 acc[4];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(rr[e]);
+          for (int e = 0; e < 4; ++e) acc[e] = make_float2(0.f, 0.f);
+          if (PASS == 1) {
+            float2 x[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              x[e] = fmul2(make_float2(__uint_as_float(rr[2 * e]), __uint_as_float(rr[2 * e + 1])),
+                           sc2);
             if (!full) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = c * 32 + e < hi ? x[e] : -INFINITY;
-            }
-            float top = x[0];
-#pragma unroll
-            for (int e = 1; e < 32; ++e) top = fmaxf(top, x[e]);
-            // scale > 0 keeps the order; another one looks at the scaled scores
-            if (!(sc > 0.f)) {
-              top = -INFINITY;
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (full || c * 32 + e < hi) top = fmaxf(top, x[e] * sc);
-            } else {
-              top *= sc;
-            }
-            const float k = fmaxf(mx, top);
-            float a0 = 0.f, a1 = 0.f;
-            if (full) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                a0 += ex2_approx(fmaf(x[e], sc, -k));
-                a1 += ex2_approx(fmaf(x[e + 1], sc, -k));
+              for (int e = 0; e < 16; ++e) {
+                x[e].x = 2 * e < hc ? x[e].x : -INFINITY;
+                x[e].y = 2 * e + 1 < hc ? x[e].y : -INFINITY;
               }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (c * 32 + e < hi) a0 += ex2_approx(fmaf(x[e], sc, -k));
             }
-            l = l * ex2_approx(mx - k) + (a0 + a1);
+            float top[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top[e] = fmaxf(x[e].x, x[e].y);
+#pragma unroll
+            for (int e = 4; e < 16; ++e) top[e & 3] = fmaxf(top[e & 3], fmaxf(x[e].x, x[e].y));
+            const float k = fmaxf(mx, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+            const float2 nk = make_float2(-k, -k);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 d = ffma2(x[e], one2, nk);
+              acc[e & 3] = ffma2(make_float2(ex2_approx(d.x), ex2_approx(d.y)), one2, acc[e & 3]);
+            }
+            l *= ex2_approx(mx - k);
             mx = k;
           } else {
-            float a0 = 0.f, a1 = 0.f;
-            if (full) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float4 v = lse[c * 8 + e];
-                a0 += ex2_approx(fmaf(__uint_as_float(rr[4 * e]), sc, -v.x));
-                a1 += ex2_approx(fmaf(__uint_as_float(rr[4 * e + 1]), sc, -v.y));
-                a0 += ex2_approx(fmaf(__uint_as_float(rr[4 * e + 2]), sc, -v.z));
-                a1 += ex2_approx(fmaf(__uint_as_float(rr[4 * e + 3]), sc, -v.w));
+            for (int e = 0; e < 8; ++e) {
+              const float4 v = nlse[c * 8 + e];
+              float2 d0 = ffma2(make_float2(__uint_as_float(rr[4 * e]), __uint_as_float(rr[4 * e + 1])),
+                                sc2, make_float2(v.x, v.y));
+              float2 d1 =
+                  ffma2(make_float2(__uint_as_float(rr[4 * e + 2]), __uint_as_float(rr[4 * e + 3])),
+                        sc2, make_float2(v.z, v.w));
+              if (!full) {
+                d0.x = 4 * e >= lc && 4 * e < hc ? d0.x : -INFINITY;
+                d0.y = 4 * e + 1 >= lc && 4 * e + 1 < hc ? d0.y : -INFINITY;
+                d1.x = 4 * e + 2 >= lc && 4 * e + 2 < hc ? d1.x : -INFINITY;
+                d1.y = 4 * e + 3 >= lc && 4 * e + 3 < hc ? d1.y : -INFINITY;
               }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float4 v = lse[c * 8 + e];
-                const float ls[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                  const int col = c * 32 + 4 * e + f;
-                  if (col >= lo && col < hi)
-                    a0 += ex2_approx(fmaf(__uint_as_float(rr[4 * e + f]), sc, -ls[f]));
-                }
-              }
+              const int q = (2 * e) & 3;
+              acc[q] = ffma2(make_float2(ex2_approx(d0.x), ex2_approx(d0.y)), one2, acc[q]);
+              acc[q + 1] = ffma2(make_float2(ex2_approx(d1.x), ex2_approx(d1.y)), one2, acc[q + 1]);
             }
-            l += a0 + a1;
           }
-        }
+          l += ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) +
+               ((acc[2].x + acc[2].y) + (acc[3].x + acc[3].y));
+        };
+        uint32_t ra[32], rb[32];
+        tmem_ld32(s0, ra);
+        tmem_wait_ld();
+        tmem_ld32(s0 + 32, rb);
+        take(0, ra);
+        tmem_wait_ld();
+        tmem_ld32(s0 + 64, ra);
+        take(1, rb);
+        tmem_wait_ld();
+        tmem_ld32(s0 + 96, rb);
+        take(2, ra);
+        tmem_wait_ld();
+        // the whole buffer is in registers: the MMAs may have it back
         tc_fence_before();
-        mbar_arrive(BAR(C::B_SE + sb));
+        if (PASS == 1) mbar_arrive(BAR(C::B_SE + sb));
+        take(3, rb);
+        if (PASS == 2) mbar_arrive(BAR(C::B_SE + sb));  // the row statistics are read too
       }
       if (!ok) break;
-      // warpgroup 1's part joins warpgroup 0's
-      if (wg == 1) {
+      // the other warpgroups' parts join warpgroup 0's
+      if (wg > 0) {
         if (it > 0 && !wait(C::B_XCHE, it - 1)) break;
-        xch[m] = make_float2(mx, l);
+        xch[(wg - 1) * 128 + m] = make_float2(mx, l);
         mbar_arrive(BAR(C::B_XCHF));
         continue;
       }
       if (!wait(C::B_XCHF, it)) break;
-      const float2 o = xch[m];
+      float2 o[C::NWG - 1];
+#pragma unroll
+      for (int e = 0; e < C::NWG - 1; ++e) o[e] = xch[e * 128 + m];
       mbar_arrive(BAR(C::B_XCHE));
       if (PASS == 1) {
-        const float k = fmaxf(mx, o.x);
-        l = l * ex2_approx(mx - k) + o.y * ex2_approx(o.x - k);
+        float k = mx;
+#pragma unroll
+        for (int e = 0; e < C::NWG - 1; ++e) k = fmaxf(k, o[e].x);
+        l *= ex2_approx(mx - k);
+#pragma unroll
+        for (int e = 0; e < C::NWG - 1; ++e) l += o[e].y * ex2_approx(o[e].x - k);
         const int slot = w.q0 / TOK + w.r + w.x;
         const size_t at = ((size_t)w.h * p.num_slots + slot) * 128 + m;
         const int nkt = (w.ctx + min(w.qlen, (w.x + 1) * TOK) - 1) / 128 + 1;
         if (nkt <= kSplitTiles)
-          p.lse[at] = l > 0.f ? k + log2f(l) : INFINITY;
+          p.neg_lse[at] = l > 0.f ? -(k + log2f(l)) : -INFINITY;
         else
           __stcg(p.partial + (size_t)(w.y0 / kSplitTiles) * p.num_kv_heads * p.num_slots * 128 + at,
                  make_float2(k, l));
-      } else if (key < w.L) {
-        const size_t at = ((size_t)w.r * p.num_kv_heads + w.h) * p.weights_stride + key;
-        l += o.y;
-        p.out[at] = key < w.ctx ? p.weights[at] + l : l;
+      } else if (key < L) {
+#pragma unroll
+        for (int e = 0; e < C::NWG - 1; ++e) l += o[e].y;
+        p.out[okey] = was + l;
       }
     }
   } else if constexpr (F8) {
     // ======================= E4M3 converters: the key operand =======================
-    const int row = threadIdx.x - kTcThreads;
+    const int row = threadIdx.x - C::THREADS;
     int g = 0, it = 0;
     bool ok = true;
     for (int t = snake(it); ok && t < nitems; t = snake(++it)) {
       const WItem w = get_witem<PASS>(p, t);
       auto convert = [&](int kt, unsigned char* dst) {
         const int key = kt * 128 + row;
-        bool valid = key < w.L;
+        bool valid = key < w.ctx + w.qlen;
         size_t src = 0;
         if (valid) {
           const int pid = __ldg(p.block_tables + (size_t)w.r * p.bt_stride + key / kBlockSize);
@@ -882,15 +1126,55 @@ cudaError_t launch_chained(K kern, const P& p, long long grid, int threads, int 
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+// Bytes of scores of one CTA of a cluster of C over sequences of padded_len keys.
+long long cluster_smem(int padded_len, int C, int rows) {
+  const long long blocks = padded_len / kBlockSize;
+  return (blocks + C - 1) / C * kBlockSize * rows * 4;
+}
+
 template <int D, bool F8, int NR>
 cudaError_t launch_few(const WeightsParams& p, cudaStream_t s) {
   const long long rh = (long long)p.num_reqs * p.num_kv_heads;
+  if (p.cluster > 0) {
+    auto kern = pa_weights_cluster_kernel<D, F8, NR>;
+    static bool attr_set[64] = {false};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kClusterSmem);
+      if (e != cudaSuccess) return e;
+      if (dev >= 0 && dev < 64) attr_set[dev] = true;
+    }
+    if (rh * p.cluster > 0x7fffffffLL) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(rh * p.cluster));
+    cfg.blockDim = dim3(32 * kClusterWarps);
+    cfg.dynamicSmemBytes = (size_t)cluster_smem(p.padded_len, p.cluster, NR);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)p.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    // behind the plan, beside it; without one this is the first grid of the
+    // call and no programmatic dependent
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.num_slots > 0 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+  }
   const long long g1 = rh * ((p.num_chunks + kScoreWarps - 1) / kScoreWarps);
   if (g1 > 0x7fffffffLL) return cudaErrorInvalidValue;
-  // the first grid of the call is no programmatic dependent: everything the
-  // stream did before is complete and visible
-  pa_weights_score_kernel<D, F8, NR><<<(unsigned)g1, 32 * kScoreWarps, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e;
+  if (p.num_slots > 0) {  // behind the plan, beside it
+    e = launch_chained(pa_weights_score_kernel<D, F8, NR>, p, g1, 32 * kScoreWarps, 0, s);
+  } else {
+    // the first grid of the call is no programmatic dependent: everything the
+    // stream did before is complete and visible
+    pa_weights_score_kernel<D, F8, NR><<<(unsigned)g1, 32 * kScoreWarps, 0, s>>>(p);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return e;
   return launch_chained(pa_weights_finish_kernel<NR>, p,
                         rh * ((p.padded_len + kFinishKeys - 1) / kFinishKeys), kFinishThreads, 0, s);
@@ -915,11 +1199,12 @@ cudaError_t launch_pass(const WeightsTcParams& tp, int num_sms, cudaStream_t s) 
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, WCfg<D>::SMEM);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             WCfg<D, F8>::SMEM);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  return launch_chained(kern, tp, num_sms, F8 ? kTcThreadsF8 : kTcThreads, WCfg<D>::SMEM, s);
+  return launch_chained(kern, tp, num_sms, WCfg<D, F8>::ALL_THREADS, WCfg<D, F8>::SMEM, s);
 }
 
 template <int D, bool F8>
@@ -939,8 +1224,7 @@ cudaError_t launch_many(const WeightsParams& p, int num_sms, cudaStream_t s) {
     if (!encode_tmap_bf16_2d(&tp.tm_k, p.k_cache, D, rows, (uint64_t)D * 2, 64, kBlockSize))
       return cudaErrorInvalidValue;
   }
-  cudaError_t e = launch_chained(pa_weights_plan_kernel, p, 1, kPlanThreads, 0, s);
-  if (e == cudaSuccess) e = launch_pass<D, 1, F8>(tp, num_sms, s);
+  cudaError_t e = launch_pass<D, 1, F8>(tp, num_sms, s);
   if (e == cudaSuccess && p.max_seq_len > 128 * kSplitTiles)
     e = launch_chained(pa_weights_join_kernel, p, (long long)p.num_slots * p.num_kv_heads, 128, 0, s);
   if (e == cudaSuccess) e = launch_pass<D, 2, F8>(tp, num_sms, s);
@@ -949,10 +1233,17 @@ cudaError_t launch_many(const WeightsParams& p, int num_sms, cudaStream_t s) {
 
 template <int D, bool F8>
 cudaError_t launch_weights_t(const WeightsParams& p, int num_sms, cudaStream_t s, int* launches) {
-  *launches = 2;
-  cudaError_t e = launch_few_rows<D, F8>(p, s);
-  if (e != cudaSuccess || p.max_query_len * (long long)p.group <= kFewRows) return e;
-  *launches += p.max_seq_len > 128 * kSplitTiles ? 4 : 3;
+  // decodes: score, finish. With chunks: plan, score, finish, pass 1, (join,)
+  // pass 2 - the first two need nothing of one another and run together
+  *launches = p.cluster > 0 ? 1 : 2;
+  cudaError_t e = cudaSuccess;
+  if (p.num_slots > 0) {
+    *launches += p.max_seq_len > 128 * kSplitTiles ? 4 : 3;
+    pa_weights_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess) e = launch_few_rows<D, F8>(p, s);
+  if (e != cudaSuccess || p.num_slots == 0) return e;
   return launch_many<D, F8>(p, num_sms, s);
 }
 
@@ -983,16 +1274,25 @@ WeightsLayout weights_layout(int num_reqs, int num_tokens, int num_q_heads, int 
   l.max_items[1] = (int)(rh * tiles);
   l.parts_off = l.counts_off + 256;
   l.items1_off = l.parts_off + pa_align256(sizeof(int) * slots);
-  l.items2_off = l.items1_off + pa_align256(sizeof(int4) * slots * parts * num_kv_heads);
-  l.lse_off = l.items2_off + pa_align256(sizeof(int4) * rh * tiles);
+  l.items2_off = l.items1_off + pa_align256(2 * sizeof(int4) * slots * parts * num_kv_heads);
+  l.lse_off = l.items2_off + pa_align256(2 * sizeof(int4) * rh * tiles);
   l.partial_off = l.lse_off + pa_align256(sizeof(float) * 128 * slots * num_kv_heads);
   l.total = l.partial_off +
             (parts > 1 ? pa_align256(sizeof(float2) * 128 * slots * num_kv_heads * parts) : 0);
   return l;
 }
 
-cudaError_t launch_weights(const WeightsParams& p, int head_dim, bool f8, int num_sms,
-                           cudaStream_t s, int* launches) {
+cudaError_t launch_weights(WeightsParams p, int head_dim, bool f8, int num_sms, cudaStream_t s,
+                           int* launches) {
+  // CTAs per (request, KV head) of the few-rows form: enough that a CTA's
+  // scores leave room for three CTAs on an SM and the grid has at least two
+  // waves of them; 0: they do not fit even eight CTAs (kClusterSmem each)
+  const long long rh = (long long)p.num_reqs * p.num_kv_heads;
+  p.cluster = 1;
+  while (p.cluster < 8 && (cluster_smem(p.padded_len, p.cluster, p.stored_rows) > kClusterSmem ||
+                           (rh * p.cluster < 6LL * num_sms && p.padded_len > 1024 * p.cluster)))
+    p.cluster *= 2;
+  if (cluster_smem(p.padded_len, p.cluster, p.stored_rows) > kClusterSmem) p.cluster = 0;
   if (head_dim == 128)
     return f8 ? launch_weights_t<128, true>(p, num_sms, s, launches)
               : launch_weights_t<128, false>(p, num_sms, s, launches);

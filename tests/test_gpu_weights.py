@@ -76,6 +76,14 @@ def test_long_context_parts(pa_lib, fp8):
     check(b)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("hq,spans", [(8, [(41500, 1), (300, 1)]), (1, [(50000, 2), (9, 8)]),
+                                      (4, [(41000, 2), (700, 70)])])
+def test_longer_than_a_cluster_holds(pa_lib, hq, spans, fp8):
+    """Scores that outgrow eight CTAs' shared memory go through global memory."""
+    check(ref.Batch(spans, hq, 1, 64, hq, fp8=fp8))
+
+
 def test_in_place_and_sharp(pa_lib):
     """Accumulation in place; queries sharp enough to give one key nearly all."""
     b = ref.Batch([(500, 1), (90, 40), (1, 1)], 8, 2, 128, 6, q_scale=6.0)
