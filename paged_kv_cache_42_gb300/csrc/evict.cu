@@ -11,13 +11,14 @@
 // number of CTAs can move rows with no order between them.
 //
 // Two kernels, chained by programmatic launch:
-//   select  a cluster of 1 to 8 CTAs per (request, KV head), each with its own
-//           contiguous part of the candidates: a radix select over the binary32
-//           weights (11 + 11 + 10 bits; a 2048-bin histogram per CTA, summed
-//           into the first one's shared memory), then an order-preserving
-//           compaction: each warp counts the kept tokens of its own contiguous
-//           part, one scan joins the counts. Bound by its chain of about ten
-//           barriers, so the cluster is sized for a few keys per thread.
+//   select  a cluster of 1 to 4 CTAs per (request, KV head), each with its own
+//           contiguous part of the candidates, a key or more per thread in
+//           registers: a radix select over the binary32 weights (11 + 11 + 10
+//           bits; each CTA counts its keys' digits in shared memory and adds
+//           the few bins in use to every CTA's total, so that each picks the
+//           digit by itself after one cluster barrier), then an
+//           order-preserving compaction by ballots, with the counts of the
+//           warps and CTAs before. Bound by its chain of barriers.
 //   move    the rows, bound by HBM: 2 x keep x D elements in, the same out.
 #include "pa_internal.h"
 #include "ptx.cuh"
@@ -50,22 +51,25 @@ __device__ __forceinline__ int cut_length(const EvictParams& p, int r, bool& bad
   return !bad && L > p.keep ? L : 0;
 }
 
-// Cluster-wide barrier and reads of another CTA's shared memory. Every CTA of
-// a cluster reaches every barrier: the paths depend on the request alone.
+// Cluster-wide barrier; reads of and sums into another CTA's shared memory.
+// Every CTA of a cluster reaches every barrier: the paths depend on the request
+// alone.
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::
+  __syncwarp();  // the aligned form wants the warp together
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
-__device__ __forceinline__ uint32_t ld_cluster(const void* mine, int rank) {
-  uint32_t at, v;
+__device__ __forceinline__ uint32_t cluster_addr(const void* mine, int rank) {
+  uint32_t at;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(mine)), "r"(rank));
+  return at;
+}
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t at) {
+  uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
   return v;
 }
-
-__device__ __forceinline__ void add_cluster(const void* mine, int rank, uint32_t v) {
-  uint32_t at;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(mine)), "r"(rank));
+__device__ __forceinline__ void add_cluster(uint32_t at, uint32_t v) {
   asm volatile("red.shared::cluster.add.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
 
@@ -75,12 +79,15 @@ __device__ __forceinline__ int warp_sum(int v) {
   return v;
 }
 
+// KPT: keys per thread, in registers; 0: parts longer than that, whose weights
+// are read again (from L2) in every pass.
+template <int KPT>
 __global__ void __launch_bounds__(kSelThreads) pa_evict_select_kernel(const EvictParams p) {
-  extern __shared__ uint32_t keys_sm[];  // this CTA's candidates' keys, when they fit
-  __shared__ uint32_t hist[2][kBins];    // counts of this CTA; of the cluster (in its first CTA)
+  __shared__ uint32_t hist[kBins];      // digits of this CTA's keys
+  __shared__ uint32_t total[3][kBins];  // of the cluster's, one per pass
   __shared__ int wsum[kSelWarps], wsum2[kSelWarps];
-  __shared__ uint32_t s_pick[2];         // a pass's bin, and the tokens in the bins above it
-  __shared__ uint32_t s_count[2];        // kept tokens above the threshold, tokens at it
+  __shared__ uint32_t s_pick[2];        // a pass's bin, and the tokens in the bins above it
+  __shared__ uint32_t s_count[2];       // this CTA's tokens above the threshold, and at it
   griddep_launch_dependents();  // the move grid may take its place; it waits for this one
   const int C = p.cluster, rank = (int)(blockIdx.x % (unsigned)C);
   const int rh = (int)(blockIdx.x / (unsigned)C);
@@ -99,10 +106,35 @@ __global__ void __launch_bounds__(kSelThreads) pa_evict_select_kernel(const Evic
   const float* const w = p.weights + (size_t)rh * p.weights_stride;
   int32_t* const kept = p.kept + (size_t)rh * p.keep;
   float* const nw = p.new_weights ? p.new_weights + (size_t)rh * p.new_weights_stride : nullptr;
-  // this CTA's candidates: c0 .. c0 + nc - 1 of the n
+  // this CTA's candidates: c0 .. c0 + nc - 1 of the n; this warp's: lo .. hi - 1 of those
   const int part = ((n + C - 1) / C + 31) & ~31;
   const int c0 = min(n, rank * part), nc = min(n, c0 + part) - c0;
+  const int seg = ((nc + kSelWarps - 1) / kSelWarps + 31) & ~31;
+  const int lo = min(nc, warp * seg), hi = min(nc, lo + seg);
   const float* const wc = w + a + c0;
+  uint32_t key[KPT > 0 ? KPT : 1];
+  if (m > 0 && KPT > 0) {  // on their way while the totals are cleared
+#pragma unroll
+    for (int e = 0; e < KPT; ++e) {
+      const int i = lo + e * 32 + lane;
+      key[e] = i < hi ? __float_as_uint(__ldg(wc + i)) : 0u;
+    }
+  }
+  // fn(i, key, in): the warp's candidates 32 at a time, in order
+  auto each = [&](auto fn) {
+    if constexpr (KPT > 0) {
+#pragma unroll
+      for (int e = 0; e < KPT; ++e) {
+        const int i = lo + e * 32 + lane;
+        fn(i, key[e], i < hi);
+      }
+    } else {
+      for (int i0 = lo; i0 < hi; i0 += 32) {
+        const int i = i0 + lane;
+        fn(i, i < hi ? weight_key(__ldg(wc + i)) : 0u, i < hi);
+      }
+    }
+  };
 
   // the tokens that stay whatever they weigh
   for (int i = rank * kSelThreads + tid; i < a + p.recent; i += C * kSelThreads) {
@@ -113,120 +145,99 @@ __global__ void __launch_bounds__(kSelThreads) pa_evict_select_kernel(const Evic
   }
   if (m == 0) return;
 
-  const bool in_sm = nc <= p.smem_keys;
-  auto key_at = [&](int i) -> uint32_t { return in_sm ? keys_sm[i] : weight_key(__ldg(wc + i)); };
   // radix select: after the passes, prefix is the m-th largest key and `need`
   // the number of tokens of exactly that key that stay (the lowest ones)
   uint32_t prefix = 0;
   int need = m;
   constexpr int kShift[3] = {21, 10, 0};
   constexpr int kWidth[3] = {11, 11, 10};
-  for (int b = tid; b < kBins; b += kSelThreads) hist[0][b] = hist[1][b] = 0u;
-  cluster_sync();
+  for (int b = tid; b < kBins; b += kSelThreads) hist[b] = total[0][b] = total[1][b] = total[2][b] = 0u;
+  if constexpr (KPT > 0) {
+#pragma unroll
+    for (int e = 0; e < KPT; ++e) key[e] = weight_key(__uint_as_float(key[e]));
+  }
+  if (C > 1) cluster_sync(); else __syncthreads();
 #pragma unroll
   for (int ps = 0; ps < 3; ++ps) {
     const int shift = kShift[ps], bins = 1 << kWidth[ps];
-    for (int i = tid; i < nc; i += kSelThreads) {
-      uint32_t k;
-      if (ps == 0) {
-        k = weight_key(__ldg(wc + i));
-        if (in_sm) keys_sm[i] = k;
-      } else {
-        k = key_at(i);
-        if ((k >> (shift + kWidth[ps])) != prefix >> (shift + kWidth[ps])) continue;
-      }
-      atomicAdd(&hist[0][(k >> shift) & (uint32_t)(bins - 1)], 1u);  // a count: its order is nothing
-    }
+    uint32_t* const own = C > 1 ? hist : total[ps];
+    each([&](int, uint32_t k, bool in) {
+      if (in && (ps == 0 || (k >> (shift + kWidth[ps])) == prefix >> (shift + kWidth[ps])))
+        atomicAdd(&own[(k >> shift) & (uint32_t)(bins - 1)], 1u);  // a count: its order is nothing
+    });
     __syncthreads();
-    // into the first CTA's total: few bins are in use, whatever the pass
     if (C > 1) {
       for (int b = tid; b < bins; b += kSelThreads) {
-        const uint32_t v = hist[0][b];
-        if (v) add_cluster(&hist[1][b], 0, v);
-        hist[0][b] = 0u;
+        const uint32_t v = hist[b];
+        if (v) {
+          hist[b] = 0u;
+          for (int k = 0; k < C; ++k) add_cluster(cluster_addr(&total[ps][b], k), v);
+        }
       }
       cluster_sync();
     }
-    if (rank == 0) {
-      // the bin, from the top, in which the need-th token falls: thread t
-      // holds `per` consecutive bins of the descending order
-      uint32_t* const hs = hist[C > 1 ? 1 : 0];
-      constexpr int kPer = kBins / kSelThreads;
-      const int per = bins / kSelThreads;
-      int c[kPer], sum = 0;
+    // the bin, from the top, in which the need-th token falls: thread t holds
+    // `per` consecutive bins of the descending order
+    constexpr int kPer = kBins / kSelThreads;
+    const int per = bins / kSelThreads;
+    int c[kPer], sum = 0;
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        const int b = bins - 1 - (tid * per + e);
-        c[e] = 0;
-        if (e < per) {
-          c[e] = (int)hs[b];
-          hs[b] = 0u;  // for the next pass
-        }
-        sum += c[e];
-      }
-      int incl = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(kAll, incl, o);
-        if (lane >= o) incl += y;
-      }
-      if (lane == 31) wsum[warp] = incl;
-      __syncthreads();
-      int before = incl - sum + warp_sum(lane < warp ? wsum[lane & (kSelWarps - 1)] : 0);
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        if (before < need && need <= before + c[e]) {
-          s_pick[0] = (uint32_t)(bins - 1 - (tid * per + e));
-          s_pick[1] = (uint32_t)before;
-        }
-        before += c[e];
-      }
+    for (int e = 0; e < kPer; ++e) {
+      c[e] = e < per ? (int)total[ps][bins - 1 - (tid * per + e)] : 0;
+      sum += c[e];
     }
-    if (C > 1) {
-      cluster_sync();
-      prefix |= ld_cluster(&s_pick[0], 0) << shift;
-      need -= (int)ld_cluster(&s_pick[1], 0);
-    } else {
-      __syncthreads();
-      prefix |= s_pick[0] << shift;
-      need -= (int)s_pick[1];
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kAll, incl, o);
+      if (lane >= o) incl += y;
     }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    int before = incl - sum + warp_sum(lane < warp ? wsum[lane & (kSelWarps - 1)] : 0);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      if (before < need && need <= before + c[e]) {
+        s_pick[0] = (uint32_t)(bins - 1 - (tid * per + e));
+        s_pick[1] = (uint32_t)before;
+      }
+      before += c[e];
+    }
+    __syncthreads();
+    prefix |= s_pick[0] << shift;
+    need -= (int)s_pick[1];
   }
 
-  // compaction in order: warp v takes candidates [v seg, v seg + seg) of the part
-  const int seg = ((nc + kSelWarps - 1) / kSelWarps + 31) & ~31;
-  const int lo = min(nc, warp * seg), hi = min(nc, lo + seg);
+  // compaction in order
   int gt = 0, eq = 0;
-  for (int i0 = lo; i0 < hi; i0 += 32) {
-    const bool in = i0 + lane < hi;
-    const uint32_t k = in ? key_at(i0 + lane) : 0u;
+  each([&](int, uint32_t k, bool in) {
     gt += __popc(__ballot_sync(kAll, in && k > prefix));
     eq += __popc(__ballot_sync(kAll, in && k == prefix));
-  }
+  });
   if (lane == 0) {
     wsum[warp] = gt;
     wsum2[warp] = eq;
   }
   __syncthreads();
-  const int all_gt = warp_sum(lane < kSelWarps ? wsum[lane] : 0);
-  const int all_eq = warp_sum(lane < kSelWarps ? wsum2[lane] : 0);
-  gt = warp_sum(lane < warp ? wsum[lane & (kSelWarps - 1)] : 0);
-  eq = warp_sum(lane < warp ? wsum2[lane & (kSelWarps - 1)] : 0);
-  if (tid == 0) {
-    s_count[0] = (uint32_t)all_gt;
-    s_count[1] = (uint32_t)all_eq;
+  if (C > 1) {
+    const int all_gt = warp_sum(lane < kSelWarps ? wsum[lane] : 0);
+    const int all_eq = warp_sum(lane < kSelWarps ? wsum2[lane] : 0);
+    if (tid == 0) {
+      s_count[0] = (uint32_t)all_gt;
+      s_count[1] = (uint32_t)all_eq;
+    }
+    cluster_sync();
   }
-  cluster_sync();
-  for (int k = 0; k < rank; ++k) {  // the parts before this one
-    gt += (int)ld_cluster(&s_count[0], k);
-    eq += (int)ld_cluster(&s_count[1], k);
-  }
+  // the warps and the parts before this one
+  const bool part_before = C > 1 && lane < rank;
+  gt = warp_sum((lane < warp ? wsum[lane & (kSelWarps - 1)] : 0) +
+                (part_before ? (int)ld_cluster(cluster_addr(&s_count[0], lane)) : 0));
+  eq = warp_sum((lane < warp ? wsum2[lane & (kSelWarps - 1)] : 0) +
+                (part_before ? (int)ld_cluster(cluster_addr(&s_count[1], lane)) : 0));
   const unsigned below = (1u << lane) - 1u;
-  for (int i0 = lo; i0 < hi; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t k = i < hi ? key_at(i) : 0u;
-    const unsigned bg = __ballot_sync(kAll, i < hi && k > prefix);
-    const unsigned be = __ballot_sync(kAll, i < hi && k == prefix);
+  each([&](int i, uint32_t k, bool in) {
+    const unsigned bg = __ballot_sync(kAll, in && k > prefix);
+    const unsigned be = __ballot_sync(kAll, in && k == prefix);
     const int eb = eq + __popc(be & below);  // equal ones before this one
     const bool stay = (bg >> lane & 1u) || ((be >> lane & 1u) && eb < need);
     if (stay) {
@@ -236,8 +247,24 @@ __global__ void __launch_bounds__(kSelThreads) pa_evict_select_kernel(const Evic
     }
     gt += __popc(bg);
     eq += __popc(be);
-  }
-  cluster_sync();  // no CTA ends while another may still read its shared memory
+  });
+  if (C > 1) cluster_sync();  // no CTA ends while another may still read its shared memory
+}
+
+template <int KPT>
+cudaError_t launch_select(const EvictParams& p, unsigned rows, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(rows * (unsigned)p.cluster);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = 0;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)p.cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, pa_evict_select_kernel<KPT>, p);
 }
 
 // kMoveRows kept rows of one (request, KV head): the source and destination
@@ -310,44 +337,22 @@ cudaError_t launch_evict(EvictParams p, int row_bytes, int num_sms, cudaStream_t
   const long long rows = (long long)p.num_reqs * p.num_kv_heads;
   const long long chunks = (p.keep + kMoveRows - 1) / kMoveRows;
   if (rows > 0x7fffffffLL || rows * chunks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  // a part's keys stay in shared memory up to this many; longer ones are read
-  // again in every pass (from L2)
-  constexpr int kMaxKeys = 40960;
-  static bool attr_set[64] = {false};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    e = cudaFuncSetAttribute(pa_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMaxKeys * 4);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) attr_set[dev] = true;
-  }
-  // CTAs per (request, KV head): parts of about 4096 keys, eight per thread,
-  // as long as the grid leaves SMs idle; beyond that a larger cluster only
-  // repeats the barriers (64 rows of 32768: SELLONG us with eight CTAs, 40 us
-  // with one; 512 rows of up to 4096: one CTA each)
+  // CTAs per (request, KV head): parts of at most 8192 keys, sixteen per thread,
+  // as long as the grid leaves SMs idle (64 rows of 32768 keys, whole call: 43.3
+  // us with four CTAs each, 44.6 with two of 32 keys per thread, 53 with eight
+  // of eight, whose barriers cost more than the shorter parts give; 512 rows of
+  // up to 4096 keys: one CTA each).
   const long long most = (long long)p.max_seq_len - p.sinks - p.recent;
   p.cluster = 1;
-  while (p.cluster < 8 && most > 4096LL * p.cluster && rows * p.cluster < 4LL * num_sms) p.cluster *= 2;
-  const long long part = (most + p.cluster - 1) / p.cluster + 31;
-  p.smem_keys = part < 1 ? 1 : (part < kMaxKeys ? (int)part : kMaxKeys);
+  while (p.cluster < 4 && most > 8192LL * p.cluster && rows * p.cluster < 4LL * num_sms) p.cluster *= 2;
   if (rows * p.cluster > 0x7fffffffLL) return cudaErrorInvalidValue;
-  {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(rows * p.cluster));
-    cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = (size_t)p.smem_keys * 4;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)p.cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, pa_evict_select_kernel, p);
-    if (e != cudaSuccess) return e;
-  }
+  const long long part = (((most > 0 ? most : 1) + p.cluster - 1) / p.cluster + 31) / 32 * 32;
+  cudaError_t e = part <= 4 * kSelThreads    ? launch_select<4>(p, (unsigned)rows, s)
+                  : part <= 8 * kSelThreads  ? launch_select<8>(p, (unsigned)rows, s)
+                  : part <= 16 * kSelThreads ? launch_select<16>(p, (unsigned)rows, s)
+                  : part <= 32 * kSelThreads ? launch_select<32>(p, (unsigned)rows, s)
+                                             : launch_select<0>(p, (unsigned)rows, s);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * chunks));
   cfg.blockDim = dim3(kMoveThreads);

@@ -235,9 +235,6 @@ cudaError_t launch_nr(const NormRopeParams& p, int num_sms, cudaStream_t s) {
     const long long chunks = (rows + HPG * iter - 1) / (HPG * iter);
     return (p.num_tokens * chunks + kThreads / 32 - 1) / (kThreads / 32);
   };
-#ifndef kManyIter
-#define kManyIter 6
-#endif
   // Few tokens: one group of heads per warp, the shortest chain. Once that
   // would be more than the warps an SM holds, kManyIter groups per warp.
   const bool small = blocks(1) <= 8LL * num_sms;

@@ -719,7 +719,7 @@ pa_status weights_impl(const void* q, const void* k_cache, const int32_t* block_
   // grids and work lists are indexed with 32 bits
   const long long rh = (long long)num_reqs * num_kv_heads;
   if (rh * (lay.padded_len / 128 + 1) >= (1LL << 31) ||
-      (long long)lay.num_slots * num_kv_heads * (lay.padded_len / 2048 + 1) >= (1LL << 31))
+      (long long)lay.num_slots * num_kv_heads * 16 >= (1LL << 31))
     return PA_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < lay.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return PA_ERR_WORKSPACE;
@@ -756,11 +756,14 @@ pa_status weights_impl(const void* q, const void* k_cache, const int32_t* block_
   p.stats = reinterpret_cast<float*>(ws + lay.stats_off);
   p.scores = reinterpret_cast<float*>(ws + lay.scores_off);
   p.counts = reinterpret_cast<int*>(ws + lay.counts_off);
-  p.parts = reinterpret_cast<int*>(ws + lay.parts_off);
+  p.num_counters = lay.num_counters;
+  p.num_sms = d->num_sms;
+  p.counters = reinterpret_cast<int*>(ws + lay.counters_off);
   p.items[0] = reinterpret_cast<int4*>(ws + lay.items1_off);
   p.items[1] = reinterpret_cast<int4*>(ws + lay.items2_off);
   p.neg_lse = reinterpret_cast<float*>(ws + lay.lse_off);
   p.partial = reinterpret_cast<float2*>(ws + lay.partial_off);
+  p.sums = reinterpret_cast<float*>(ws + lay.sums_off);
   p.err = d->err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   TimerScope timer(6, s);
@@ -855,7 +858,6 @@ pa_status pa_evict_kv(void* k_cache, void* v_cache, const int32_t* block_tables,
   p.recent = recent;
   p.sinks = sinks;
   p.cluster = 1;
-  p.smem_keys = 0;
   p.err = d->err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   TimerScope timer(7, s);

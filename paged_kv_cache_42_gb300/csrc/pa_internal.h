@@ -384,12 +384,14 @@ struct WeightsLayout {
   // few rows: per (request, kv head, 256-key chunk) 8 x {max, sum}; scaled
   // scores [request][kv head][padded_len][stored_rows]
   size_t stats_off, scores_off;
-  // many rows: item counts, key parts per row tile, the two work lists, row
-  // statistics [kv head][slot][128] and their parts [part][kv head][slot][128]
-  size_t counts_off, parts_off, items1_off, items2_off, lse_off, partial_off;
+  // many rows: item counts, parts done, the two work lists, row statistics
+  // [kv head][slot][128], their parts [part][kv head][slot][128], and the
+  // parts of keys' sums [unit][part][256]
+  size_t counts_off, counters_off, items1_off, items2_off, lse_off, partial_off, sums_off;
   size_t total;
   int num_chunks, padded_len, stored_rows, num_slots;
   int max_items[2];  // entries of the work lists
+  int num_counters;
 };
 WeightsLayout weights_layout(int num_reqs, int num_tokens, int num_q_heads, int num_kv_heads,
                              int max_query_len, int max_seq_len);
@@ -407,14 +409,17 @@ struct WeightsParams {
   int num_reqs, num_tokens, num_q_heads, num_kv_heads, group, num_blocks, bt_stride;
   int max_query_len, max_seq_len;
   int num_chunks, padded_len, stored_rows, num_slots, max_items[2];  // see WeightsLayout
+  int num_counters;
   int cluster;  // CTAs per (request, kv head), set at launch; 0: the two-kernel form
+  int num_sms;  // set at launch
   float* stats;
   float* scores;
   int* counts;
-  int* parts;
+  int* counters;
   int4* items[2];
   float* neg_lse;  // minus the log2-sum-exp of every row, -inf for rows past a span
   float2* partial;
+  float* sums;
   unsigned long long* err;
 };
 
@@ -431,9 +436,7 @@ struct EvictParams {
   int num_reqs, num_kv_heads, num_blocks, max_blocks_per_req, max_new_blocks;
   long long weights_stride, new_weights_stride;
   int max_seq_len, keep, recent, sinks;
-  // set at launch: CTAs per (request, KV head) of the select kernel, and the
-  // keys each keeps in shared memory
-  int cluster, smem_keys;
+  int cluster;  // CTAs per (request, KV head) of the select kernel, set at launch
   unsigned long long* err;
 };
 

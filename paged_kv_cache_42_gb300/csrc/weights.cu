@@ -24,18 +24,30 @@
 // that brings its largest element into [2^13, 2^14).
 //
 // Many rows (prompt chunks): bound by arithmetic, 2 x 2 head_dim flops and two
-// exponentials per (row, key). Two passes of one tcgen05 kernel: a stationary
-// 128-row operand X against a stream of 128-row operands Y, S = X Y^T into
-// TMEM, one thread per row of X with no exchange between threads:
-//   pass 1  X = 128 query rows (G heads x 128 / G tokens), Y = key tiles: the
-//           thread keeps its query's running maximum and sum -> lse. Keys are
-//           cut into parts of 16 tiles, joined by a small kernel.
-//   pass 2  X = 128 keys, Y = the query row tiles that see them: the thread
-//           sums exp2(s - lse) over its key's columns, in a fixed order, and
-//           writes the key's weight. No atomics and no partial sums.
-// The softmax warpgroups take the Y tiles in turn; four S buffers in TMEM let
-// the MMAs run ahead of them. A pass's pace is the exponentials: 128 x 128 of
-// them are 1024 cycles of an SM's special-function unit, the MMA about half.
+// exponentials per (row, key). Two passes of one tcgen05 kernel: a pair of
+// stationary 128-row operands X against a stream of 128-row operands Y, S = X
+// Y^T into TMEM, one thread per row of X with no exchange between threads:
+//   pass 1  X = 2 x 128 query rows (G heads x 128 / G tokens), Y = key tiles:
+//           the thread keeps its query's running maximum and sum -> lse.
+//   pass 2  X = 2 x 128 keys, Y = the query row tiles that see them: the
+//           thread sums exp2(s - lse) over its key's columns and writes the
+//           key's weight.
+// A pair's Y tiles are cut into parts where that evens out the CTAs' shares (a
+// planner kernel decides). A part leaves its 32 rows' results per warp in the
+// workspace and counts itself done; the warp that counts last joins all parts,
+// in their order, so the result does not depend on which that is.
+// X comes in pairs because a Y tile costs more to bring (its copies take the
+// TMA unit some 40 ns each, whatever their size, and a stage about 2 us to turn
+// around) than one 128 x 128 product on it takes. Two warps issue the MMAs:
+// between the products of a step one warp's waits, fences and commits take as
+// long as the products. Warpgroup w takes X tile w % 2 and half
+// w / 2 of the columns; it copies its 64 columns to registers, gives the S
+// buffer back and only then takes exponentials, so that the MMAs of the next
+// step but one run meanwhile. What is left is the exponentials: 128 x 128 of
+// them hold the special-function units for 512 cycles of an SM, the products
+// the tensor pipe for as long, and a step takes about STEP cycles. (Three
+// 512-token chunks on 0, 1024 and 2048 keys, 32 / 8 heads: single X tiles, one
+// issuer and no parts 63 us; pairs 55.5; two issuers 54; halves and parts CHUNKS.)
 #include <cuda.h>
 
 #include "pa_internal.h"
@@ -56,7 +68,9 @@ constexpr int kFinishThreads = 256;
 constexpr int kFinishRound = 1024;   // keys of one round of a finish CTA
 constexpr int kFinishKeys = 4 * kFinishRound;  // keys of one finish CTA (joining the chunks costs
                                                  // each CTA the same, whatever its keys)
-constexpr int kSplitTiles = 32;      // key tiles of one part in pass 1
+constexpr int kMaxParts = 16;        // parts of a pair's Y tiles
+constexpr int kMinPart = 8;          // Y tiles of a part in pass 1, at least (pass 2: 2)
+constexpr int kMaxUnits = 512;       // pairs of pass 2 that may be cut: only few of them are
 constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = 1024;
 constexpr float kNone = -1e30f;      // a running maximum before the first key
@@ -99,7 +113,9 @@ __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
 
 // Cluster-wide barrier, and a read of another CTA's shared memory.
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  __syncwarp();  // the aligned form wants the warp together
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
 }
 __device__ __forceinline__ float2 ld_cluster_f2(const void* mine, int rank) {
   uint32_t at;
@@ -591,73 +607,115 @@ __global__ void __launch_bounds__(kFinishThreads) pa_weights_finish_kernel(const
 // ---------------------------------------------------------------------------------------
 // many rows
 // ---------------------------------------------------------------------------------------
-// One work item, all its roles need in 32 bytes.
+// One work item, all its roles need in 48 bytes.
 struct WItem {
   int r, h, q0, qlen;
   int ctx;
-  int x;      // row tile (pass 1) or key tile (pass 2) of X
-  int y0, n;  // Y tiles y0 .. y0 + n - 1
+  int x;            // first row tile (pass 1) or key tile (pass 2) of the X pair
+  int y0, n;        // Y tiles y0 .. y0 + n - 1
+  int part, parts;  // which part of the pair's Y tiles, of how many
+  int unit;         // pass 2, parts > 1: the pair's place in the partial sums
+  int pad;
 };
-static_assert(sizeof(WItem) == 32, "two 16-byte loads");
+static_assert(sizeof(WItem) == 48, "three 16-byte loads");
 
-// The work lists of both passes, longest items first (bucket counts), and the
-// number of key parts of every row tile. Row tile rt of request r has slot
-// q0 / TOK + r + rt: consecutive requests' slots never meet, since a span of
-// qlen tokens has at most (q0 + qlen) / TOK - q0 / TOK + 1 tiles. A warp takes
-// a request, its lanes the request's tiles.
+// The work lists of both passes, longest items first (bucket counts). Row tile
+// rt of request r has slot q0 / TOK + r + rt: consecutive requests' slots never
+// meet, since a span of qlen tokens has at most (q0 + qlen) / TOK - q0 / TOK + 1
+// tiles. Request r belongs to warp r % 32, whose lanes take its pairs if it has
+// many rows: chunks stand side by side in a batch, and so go to different
+// warps. Pairs are cut into parts (of half a CTA's even share) only where there
+// are fewer of them than half the CTAs: joining costs a warpgroup about 3000
+// cycles per part, two steps' time, and on three 512-token chunks (192 and 144
+// pairs) it took more than the evener shares gave (65.7 us against 52.9).
 __global__ void __launch_bounds__(kPlanThreads) pa_weights_plan_kernel(const WeightsParams p) {
   __shared__ int cnt[2][kBuckets];
   __shared__ int wsum[kPlanThreads / 32], s_fits;
+  __shared__ int s_steps[2], s_pairs[2], s_unit;
   griddep_launch_dependents();  // the decodes' grids need no plan and wait for this one at their end
   bool none = false;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int TOK = 128 / p.group;
+  const int TOK = 128 / p.group, tsh = __ffs(TOK) - 1;  // a power of two
   for (int b = tid; b < kBuckets; b += kPlanThreads) cnt[0][b] = cnt[1][b] = 0;
-  for (int i = tid; i < p.num_slots; i += kPlanThreads) p.parts[i] = 0;
+  for (int i = tid; i < p.num_counters; i += kPlanThreads) p.counters[i] = 0;
+  if (tid < 2) s_steps[tid] = s_pairs[tid] = 0;
+  if (tid == 2) s_unit = 0;
   __syncthreads();
-  auto put = [&](int k, const WItem& w) -> int {  // a place in the list for every KV head
-    return atomicAdd(&cnt[k][min(w.n, kBuckets - 1)], p.num_kv_heads);
+  // the spans; a batch of up to 1024 requests keeps them in registers
+  Span kept{0, 0, 0, false};
+  auto span_of = [&](int r, bool first) {
+    if (r >= p.num_reqs) return Span{0, 0, 0, false};
+    return first || r >= kPlanThreads ? get_span(p, r, first) : kept;
   };
-  auto write = [&](int k, int at, WItem w) {
-    int4* const dst = p.items[k] + 2 * (size_t)at;
+  static_assert(kPlanThreads == 1024, "32 warps of 32 lanes");
+  const int r_of = warp + 32 * lane;  // of each 1024 requests
+  for (int r = r_of; r < p.num_reqs; r += kPlanThreads) {
+    const Span s = span_of(r, true);
+    if (r < kPlanThreads) kept = s;
+    if (!s.ok || s.qlen * p.group <= kFewRows) continue;
+    // pairs, and their Y tiles as if these grew evenly from the first to the last
+    const int ctx = s.L - s.qlen, nrt = (s.qlen + TOK - 1) >> tsh, nkt = (s.L + 127) / 128;
+    const int pairs1 = (nrt + 1) / 2 * p.num_kv_heads, pairs2 = (nkt + 1) / 2 * p.num_kv_heads;
+    const int nk0 = (ctx + min(s.qlen, 2 * TOK) - 1) / 128 + 1;
+    const int rt0 = max(0, (nkt - 1) * 128 - ctx) >> tsh;
+    atomicAdd(&s_pairs[0], pairs1);
+    atomicAdd(&s_pairs[1], pairs2);
+    atomicAdd(&s_steps[0], pairs1 * (nk0 + nkt) / 2);
+    atomicAdd(&s_steps[1], pairs2 * (2 * nrt - rt0) / 2);
+  }
+  __syncthreads();
+  int len1 = 0, len2 = 0;  // Y tiles of a part
+  auto item = [&](int k, bool fill, WItem w) {
+    const int at = atomicAdd(&cnt[k][min(w.n, kBuckets - 1)], p.num_kv_heads);  // every KV head's
+    if (!fill) return;
+    int4* const dst = p.items[k] + 3 * (size_t)at;
     for (int h = 0; h < p.num_kv_heads; ++h) {
-      dst[2 * h] = make_int4(w.r, h, w.q0, w.qlen);
-      dst[2 * h + 1] = make_int4(w.ctx, w.x, w.y0, w.n);
+      dst[3 * h] = make_int4(w.r, h, w.q0, w.qlen);
+      dst[3 * h + 1] = make_int4(w.ctx, w.x, w.y0, w.n);
+      dst[3 * h + 2] = make_int4(w.part, w.parts, w.unit + h, 0);
     }
   };
-  // what: 0 counts the items per bucket, 1 writes them
-  auto walk = [&](int what) {
-    for (int r0 = warp * 32; r0 < p.num_reqs; r0 += kPlanThreads) {
-      // 32 requests' spans in one round trip; then those with many rows in turn
-      Span mine{0, 0, 0, false};
-      if (r0 + lane < p.num_reqs) mine = get_span(p, r0 + lane, what == 0);
+  // fill: write the items, else count them per bucket
+  auto walk = [&](bool fill) {
+    for (int r0 = 0; r0 < p.num_reqs; r0 += kPlanThreads) {
+      const Span mine = span_of(r0 + r_of, false);
       unsigned todo = __ballot_sync(kAll, mine.ok && mine.qlen * p.group > kFewRows);
       while (todo) {
-        const int src = __ffs((int)todo) - 1, r = r0 + src;
+        const int src = __ffs((int)todo) - 1, r = r0 + warp + 32 * src;
         todo &= todo - 1;
         const int q0 = __shfl_sync(kAll, mine.q0, src), qlen = __shfl_sync(kAll, mine.qlen, src);
         const int L = __shfl_sync(kAll, mine.L, src), ctx = L - qlen;
-        const int nrt = (qlen + TOK - 1) / TOK;
-        for (int rt = lane; rt < nrt; rt += 32) {
-          const int nkt = (ctx + min(qlen, (rt + 1) * TOK) - 1) / 128 + 1;
-          if (what) p.parts[q0 / TOK + r + rt] = (nkt + kSplitTiles - 1) / kSplitTiles;
-          for (int i0 = 0; i0 < nkt; i0 += kSplitTiles) {
-            const WItem w{r, 0, q0, qlen, ctx, rt, i0, min(kSplitTiles, nkt - i0)};
-            const int at = put(0, w);
-            if (what) write(0, at, w);
-          }
+        const int nrt = (qlen + TOK - 1) >> tsh;
+        for (int rt = 2 * lane; rt < nrt; rt += 64) {  // pairs of row tiles
+          const int nkt = (ctx + min(qlen, (rt + 2) * TOK) - 1) / 128 + 1;
+          const int parts = (nkt - 1) / len1 + 1, per = (nkt + parts - 1) / parts;
+          for (int i = 0; i < parts; ++i)
+            item(0, fill,
+                 WItem{r, 0, q0, qlen, ctx, rt, i * per, min(per, nkt - i * per), i, parts, 0, 0});
         }
         const int nkt = (L + 127) / 128;
-        for (int kt = lane; kt < nkt; kt += 32) {
-          const int rt0 = max(0, kt * 128 - ctx) / TOK;  // the first row tile that sees the keys
-          const WItem w{r, 0, q0, qlen, ctx, kt, rt0, nrt - rt0};
-          const int at = put(1, w);
-          if (what) write(1, at, w);
+        for (int kt = 2 * lane; kt < nkt; kt += 64) {  // pairs of key tiles
+          const int rt0 = max(0, kt * 128 - ctx) >> tsh;  // the first row tile that sees the keys
+          const int n = nrt - rt0, parts = (n - 1) / len2 + 1, per = (n + parts - 1) / parts;
+          const int unit = parts > 1 && fill ? atomicAdd(&s_unit, p.num_kv_heads) : 0;
+          for (int i = 0; i < parts; ++i)
+            item(1, fill,
+                 WItem{r, 0, q0, qlen, ctx, kt, rt0 + i * per, min(per, n - i * per), i, parts, unit, 0});
         }
       }
     }
   };
-  walk(0);
+  {
+    const int most1 = (p.max_seq_len + 127) / 128, most2 = (p.max_query_len + TOK - 1) >> tsh;
+    len1 = s_pairs[0] >= p.num_sms / 2
+               ? 0x40000000
+               : max(max(kMinPart, s_steps[0] / (2 * p.num_sms) + 1), (most1 + kMaxParts - 1) / kMaxParts);
+    // (fewer pairs than SMs: the units fit)
+    len2 = s_pairs[1] >= p.num_sms / 2 || s_pairs[1] > kMaxUnits
+               ? 0x40000000
+               : max(max(2, s_steps[1] / (2 * p.num_sms) + 1), (most2 + kMaxParts - 1) / kMaxParts);
+  }
+  walk(false);
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < 2; ++k) {  // first places, longest bucket first
@@ -689,54 +747,44 @@ __global__ void __launch_bounds__(kPlanThreads) pa_weights_plan_kernel(const Wei
   if (none) {  // no such request, or spans that cannot be
     if (tid < 2) p.counts[tid] = 0;
   } else {
-    walk(1);
+    walk(true);
   }
 }
 static_assert(kBuckets == kPlanThreads, "one bucket per thread");
 
-// Joins the key parts of the row tiles that have more than one.
-__global__ void __launch_bounds__(128) pa_weights_join_kernel(const WeightsParams p) {
-  griddep_wait();
-  const int slot = (int)(blockIdx.x % (unsigned)p.num_slots);
-  const int h = (int)(blockIdx.x / (unsigned)p.num_slots);
-  const int n = __ldcg(p.parts + slot);
-  if (n <= 1) return;
-  const size_t at = ((size_t)h * p.num_slots + slot) * 128 + threadIdx.x;
-  const size_t step = (size_t)p.num_kv_heads * p.num_slots * 128;
-  float m = kNone, l = 0.f;
-  for (int i = 0; i < n; ++i) {
-    const float2 v = __ldcg(p.partial + (size_t)i * step + at);
-    const float k = fmaxf(m, v.x);
-    l = l * ex2_approx(m - k) + v.y * ex2_approx(v.x - k);
-    m = k;
-  }
-  p.neg_lse[at] = l > 0.f ? -(m + log2f(l)) : -INFINITY;  // rows past the span: a weight of zero
-  __threadfence();
-}
-
 template <int D, bool F8>
 struct WCfg {
-  // Softmax warpgroups. A tile is a chain of TMEM loads, exponentials and sums
-  // in one thread; four tiles in work at once hide it (two: 34 us and 30 us for
-  // the passes over three 512-token chunks, against PASS1 and PASS2). The E4M3
-  // form has converter warps besides, and registers for three.
-  static constexpr int NWG = F8 ? 3 : 4;
-  static constexpr int THREADS = 64 + 128 * NWG;      // producer, MMA issuer, softmax
+  // Softmax warpgroups: warpgroup w works on X tile w % 2 of the pair and on part
+  // w / 2 of the SPLIT its columns are in. The E4M3 form has converter warps
+  // besides.
+  static constexpr int NWG = F8 ? 2 : 4;
+  static constexpr int SPLIT = NWG / 2;
+  static constexpr int SOFT0 = 3;                     // first softmax warp: after the producer
+                                                      // and two MMA issuers
+  static constexpr int THREADS = 32 * SOFT0 + 128 * NWG;
   static constexpr int ALL_THREADS = THREADS + (F8 ? 128 : 0);  // + 4 converter warps
   static constexpr int NCH = D / 64;           // 64-element (128-byte) parts of a row
   static constexpr int CHUNK = 128 * 128;
   static constexpr int TILE = NCH * CHUNK;     // a 128-row operand
   static constexpr int NY = 4, NS = 4;         // Y stages, S buffers
-  static constexpr int NLSE = NY + NS;         // row statistics: a slot is refilled NY + NS tiles
-                                               // later, after the S buffer before it was read
-  static constexpr int OFF_X = 0;              // two X operands
+  // Row statistics (pass 2): slot g % NLSE is refilled for Y tile g + 8, once
+  // every softmax warp has taken the scores of tile g + 4, hence finished tile
+  // g + 3.
+  static constexpr int NLSE = 8;
+  static_assert(NY == 4 && NS == 4, "what the slots' reuse relies on");
+  static constexpr int OFF_X = 0;              // the pair of X operands
+  // layout of the key operand: 8-row groups KSBO apart, 64-element parts KHALF
+  // apart. A 128-dim bf16 block of 16 keys lands by one 4 KB copy as [group]
+  // [part][8 rows][128 B]; otherwise whole parts lie one after the other.
+  static constexpr bool ONE_COPY = D == 128 && !F8;
+  static constexpr int KSBO = ONE_COPY ? 2048 : 1024, KHALF = ONE_COPY ? 1024 : CHUNK;
   static constexpr int OFF_Y = 2 * TILE;
   static constexpr int OFF_LSE = OFF_Y + NY * TILE;
   static constexpr int OFF_XCH = OFF_LSE + NLSE * 512;
-  static constexpr int OFF_BAR = OFF_XCH + (NWG - 1) * 128 * 8;
-  static constexpr int B_XF = 0, B_XE = 2, B_YF = 4, B_YE = B_YF + NY, B_SF = B_YE + NY,
-                       B_SE = B_SF + NS, B_XCHF = B_SE + NS, B_XCHE = B_XCHF + 1,
-                       B_DRAIN = B_XCHE + 1, B_COUNT = B_DRAIN + 1;
+  static constexpr int OFF_BAR = OFF_XCH + 2 * 128 * 8;
+  static constexpr int B_XF = 0, B_XE = 1, B_YF = 2, B_YE = B_YF + NY, B_SF = B_YE + NY,
+                       B_SE = B_SF + NS, B_XCHF = B_SE + NS, B_XCHE = B_XCHF + 2,
+                       B_DRAIN = B_XCHE + 2, B_COUNT = B_DRAIN + 1;
   static constexpr int SMEM = OFF_BAR + 8 * B_COUNT + 16 + 1024;
   static_assert(SMEM <= 227 * 1024, "one CTA per SM");
 };
@@ -744,7 +792,9 @@ struct WCfg {
 
 struct WeightsTcParams {
   CUtensorMap tm_q;  // q as [T][Hq][D], box {64, G, 128 / G}, 128B swizzle
-  CUtensorMap tm_k;  // k_cache as [blocks * Hkv * 16][D], box {64, 16} (bf16 caches)
+  // bf16 caches: k_cache as [blocks * Hkv * 16][64], box {64, 16}; of head_dim
+  // 128 as {64, 8 rows, 2 parts, 8-row groups}, box {64, 8, 2, 2}
+  CUtensorMap tm_k;
   WeightsParams w;
 };
 
@@ -752,9 +802,22 @@ namespace {
 
 template <int PASS>
 __device__ __forceinline__ WItem get_witem(const WeightsParams& p, int t) {
-  const int4 a = __ldcg(p.items[PASS - 1] + 2 * (size_t)t);
-  const int4 b = __ldcg(p.items[PASS - 1] + 2 * (size_t)t + 1);
-  return WItem{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  const int4* const src = p.items[PASS - 1] + 3 * (size_t)t;
+  const int4 a = __ldcg(src), b = __ldcg(src + 1), c = __ldcg(src + 2);
+  return WItem{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, 0};
+}
+
+// Counts a part of `parts` as done for the 32 rows of this warp, whose results
+// are stored; true for the one that counts last, which then sees all of them.
+__device__ __forceinline__ bool last_part(int* counter, int parts, int lane) {
+  __threadfence();
+  __syncwarp();
+  int n = 0;
+  if (lane == 0) n = atomicAdd(counter, 1);
+  n = __shfl_sync(kAll, n, 0);
+  if (n != parts - 1) return false;
+  __threadfence();
+  return true;
 }
 
 __device__ __forceinline__ int snake(int i) {  // rounds of items in alternating direction
@@ -784,11 +847,13 @@ __global__ void __launch_bounds__(WCfg<D, F8>::ALL_THREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::B_COUNT; ++i) {
       int n = 1;
-      if (i >= C::B_SE && i < C::B_SE + C::NS) n = 128;  // a softmax warpgroup
-      if (i == C::B_XCHF) n = 128 * (C::NWG - 1);
-      if (i == C::B_XCHE) n = 128;
+      if (i >= C::B_SE && i < C::B_SE + C::NS) n = 4 * C::SPLIT;  // the warps that share it
+      if (i >= C::B_XCHF && i < C::B_XCHE + 2) n = 128;
       if (kConvY && i >= C::B_YF && i < C::B_YF + C::NY) n = 4;  // the converter warps
-      if (kConvX && i >= C::B_XF && i < C::B_XF + 2) n = 4;
+      if (kConvX && i == C::B_XF) n = 4;
+      // every softmax warp has its scores of a Y tile, whose products are done then
+      if (i >= C::B_YE && i < C::B_YE + C::NY) n = 8 * C::SPLIT;
+      if (i == C::B_XE || i == C::B_DRAIN) n = 2;  // the MMA issuers
       mbar_init(BAR(i), n);
     }
     fence_barrier_init();
@@ -807,8 +872,8 @@ __global__ void __launch_bounds__(WCfg<D, F8>::ALL_THREADS, 1)
   const int nitems = __ldcg(p.counts + (PASS - 1));
   const int TOK = 128 / p.group;
 
-  // a request's key tile: 16-key blocks by lanes 0 .. 7, one copy per 64 dims
-  auto load_keys = [&](const WItem& it, int kt, uint32_t dst, uint32_t bar) {
+  // the block id of this lane's block of a key tile (lanes 0 .. 7), -1: none
+  auto key_block = [&](const WItem& it, int kt) -> int {
     const int b = kt * 8 + lane, nb = (it.ctx + it.qlen + kBlockSize - 1) / kBlockSize;
     int pid = -1;
     if (lane < 8 && b < nb) {
@@ -818,122 +883,155 @@ __global__ void __launch_bounds__(WCfg<D, F8>::ALL_THREADS, 1)
         pid = -1;
       }
     }
-    const int nload = __popc(__ballot_sync(kAll, pid >= 0));
-    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(nload * C::NCH) * 2048u);
-    __syncwarp();
-    if (pid >= 0) {
+    return pid;
+  };
+  auto copy_block = [&](const WItem& it, int pid, uint32_t dst, uint32_t bar) {
+    if (pid < 0) return;
+    if constexpr (C::ONE_COPY) {
+      const int grp = (pid * p.num_kv_heads + it.h) * (kBlockSize / 8);  // the block's first group
+      tma_load_4d(dst + lane * 2 * C::KSBO, &tp.tm_k, 0, 0, 0, grp, bar);
+    } else {
       const int row = (pid * p.num_kv_heads + it.h) * kBlockSize;
 #pragma unroll
       for (int c = 0; c < C::NCH; ++c)
         tma_load_2d(dst + c * C::CHUNK + lane * 2048, &tp.tm_k, c * 64, row, bar);
     }
   };
-  auto load_rows = [&](const WItem& it, int rt, uint32_t dst, uint32_t bar, int lse_slot) {
-    if (lane == 0) {
-      mbar_arrive_expect_tx(bar, C::TILE + (PASS == 2 ? 512u : 0u));
+  auto copy_rows = [&](const WItem& it, int rt, uint32_t dst, uint32_t bar) {  // one thread
 #pragma unroll
-      for (int c = 0; c < C::NCH; ++c)
-        tma_load_3d(dst + c * C::CHUNK, &tp.tm_q, c * 64, it.h * p.group, it.q0 + rt * TOK, bar);
-      if (PASS == 2) {
-        const int slot = it.q0 / TOK + it.r + rt;
-        bulk_g2s(base + C::OFF_LSE + lse_slot * 512,
-                 p.neg_lse + ((size_t)it.h * p.num_slots + slot) * 128, 512, bar);
-      }
-    }
-    __syncwarp();
+    for (int c = 0; c < C::NCH; ++c)
+      tma_load_3d(dst + c * C::CHUNK, &tp.tm_q, c * 64, it.h * p.group, it.q0 + rt * TOK, bar);
   };
+  constexpr uint32_t kBlockBytes = (uint32_t)C::NCH * 2048u;
 
   if (warp == 0) {
     // ======================= TMA producer =======================
-    int g = 0, it = 0, nx = 0;  // Y and X operands copied
+    int g = 0, it = 0, nx = 0;  // Y operands and X pairs copied
     bool ok = true;
     for (int t = snake(it); ok && t < nitems; t = snake(++it)) {
       const WItem w = get_witem<PASS>(p, t);
-      const int xs = it & 1;
-      const uint32_t xdst = base + C::OFF_X + xs * C::TILE;
+      const uint32_t xdst = base + C::OFF_X, xbar = BAR(C::B_XF);
       if (!kConvX) {
-        if (it >= 2 && !wait(C::B_XE + xs, it / 2 - 1)) break;
+        int id0 = -1, id1 = -1;
+        if (PASS == 2) {
+          id0 = key_block(w, w.x);
+          id1 = key_block(w, w.x + 1);
+        }
+        if (it >= 1 && !wait(C::B_XE, it - 1)) break;
         ++nx;
-        if (PASS == 1)
-          load_rows(w, w.x, xdst, BAR(C::B_XF + xs), 0);
-        else
-          load_keys(w, w.x, xdst, BAR(C::B_XF + xs));
-      }
-      for (int i = 0; !kConvY && i < w.n; ++i, ++g) {
-        const int ys = g % C::NY;
-        if (g >= C::NY && !wait(C::B_YE + ys, g / C::NY - 1)) { ok = false; break; }
-        const uint32_t ydst = base + C::OFF_Y + ys * C::TILE;
-        if (PASS == 1)
-          load_keys(w, w.y0 + i, ydst, BAR(C::B_YF + ys));
-        else
-          load_rows(w, w.y0 + i, ydst, BAR(C::B_YF + ys), g % C::NLSE);
-      }
-    }
-    // every copy issued has landed before the CTA may exit
-    for (int j = nx > 2 ? nx - 2 : 0; j < nx; ++j)
-      mbar_wait_bounded(BAR(C::B_XF + (j & 1)), (uint32_t)(j / 2) & 1u);
-    for (int j = g > C::NY ? g - C::NY : 0; j < g; ++j)
-      mbar_wait_bounded(BAR(C::B_YF + j % C::NY), (uint32_t)(j / C::NY) & 1u);
-  } else if (warp == 1) {
-    // ======================= MMA issuer =======================
-    constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false);
-    const uint64_t desc = smem_desc_sw128(base, 16, 1024);  // K-major, 8-row groups 1 KB apart
-    int g = 0, it = 0;
-    bool ok = true;
-    for (int t = snake(it); ok && t < nitems; t = snake(++it)) {
-      const WItem w = get_witem<PASS>(p, t);
-      const int xs = it & 1;
-      if (!wait(C::B_XF + xs, it / 2)) break;
-      for (int i = 0; i < w.n; ++i, ++g) {
-        const int ys = g % C::NY, sb = g % C::NS;
-        if (!wait(C::B_YF + ys, g / C::NY)) { ok = false; break; }
-        if (g >= C::NS && !wait(C::B_SE + sb, g / C::NS - 1)) { ok = false; break; }
-        tc_fence_after();
-        if (lane == 0) {
-          const uint64_t a0 = desc + ((uint64_t)(C::OFF_X + xs * C::TILE) >> 4);
-          const uint64_t b0 = desc + ((uint64_t)(C::OFF_Y + ys * C::TILE) >> 4);
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint64_t off = (uint64_t)((ks / 4) * C::CHUNK + (ks % 4) * 32) >> 4;
-            umma_bf16(tmem + 128 * sb, a0 + off, b0 + off, idesc, ks > 0 ? 1u : 0u);
+        if (PASS == 1) {
+          // a second tile past the span reads rows of other spans (zeros past
+          // the batch): nothing of it is used
+          if (lane == 0) {
+            mbar_arrive_expect_tx(xbar, 2u * C::TILE);
+            copy_rows(w, w.x, xdst, xbar);
+            copy_rows(w, w.x + 1, xdst + C::TILE, xbar);
           }
-          umma_commit(BAR(C::B_SF + sb));
-          umma_commit(BAR(C::B_YE + ys));
-          if (i + 1 == w.n) umma_commit(BAR(C::B_XE + xs));
+        } else {
+          const int nload = __popc(__ballot_sync(kAll, id0 >= 0)) + __popc(__ballot_sync(kAll, id1 >= 0));
+          if (lane == 0) mbar_arrive_expect_tx(xbar, (uint32_t)nload * kBlockBytes);
+          __syncwarp();
+          copy_block(w, id0, xdst, xbar);
+          copy_block(w, id1, xdst + C::TILE, xbar);
         }
         __syncwarp();
       }
+      int id = !kConvY && PASS == 1 ? key_block(w, w.y0) : -1;
+      for (int i = 0; !kConvY && i < w.n; ++i, ++g) {
+        const int ys = g % C::NY;
+        // the next tile's block ids are on their way while this one waits
+        const int next = PASS == 1 && i + 1 < w.n ? key_block(w, w.y0 + i + 1) : -1;
+        if (g >= C::NY && !wait(C::B_YE + ys, g / C::NY - 1)) { ok = false; break; }
+        const uint32_t ydst = base + C::OFF_Y + ys * C::TILE, ybar = BAR(C::B_YF + ys);
+        if (PASS == 1) {
+          const int nload = __popc(__ballot_sync(kAll, id >= 0));
+          if (lane == 0) mbar_arrive_expect_tx(ybar, (uint32_t)nload * kBlockBytes);
+          __syncwarp();
+          copy_block(w, id, ydst, ybar);
+          id = next;
+        } else if (lane == 0) {
+          const int rt = w.y0 + i, slot = w.q0 / TOK + w.r + rt;
+          mbar_arrive_expect_tx(ybar, C::TILE + 512u);
+          copy_rows(w, rt, ydst, ybar);
+          bulk_g2s(base + C::OFF_LSE + (g % C::NLSE) * 512,
+                   p.neg_lse + ((size_t)w.h * p.num_slots + slot) * 128, 512, ybar);
+        }
+        __syncwarp();
+      }
+    }
+    // every copy issued has landed before the CTA may exit
+    if (nx > 0) mbar_wait_bounded(BAR(C::B_XF), (uint32_t)(nx - 1) & 1u);
+    for (int j = g > C::NY ? g - C::NY : 0; j < g; ++j)
+      mbar_wait_bounded(BAR(C::B_YF + j % C::NY), (uint32_t)(j / C::NY) & 1u);
+  } else if (warp < C::SOFT0) {
+    // ======================= MMA issuers =======================
+    // Warp 1 + xi issues the products on X tile xi: one warp's waits, fences and
+    // commits between the products take as long as the products, two overlap them.
+    const int xi = warp - 1;
+    constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false);
+    // K-major operands: rows as TMA lands them, and the key operand
+    const uint64_t qdesc = smem_desc_sw128(base, 16, 1024), kdesc = smem_desc_sw128(base, 16, C::KSBO);
+    const uint64_t a0 = (PASS == 1 ? qdesc : kdesc) + ((uint64_t)(C::OFF_X + xi * C::TILE) >> 4);
+    int g = 0, it = 0;
+    bool ok = true;
+    for (int t = snake(it); ok && t < nitems; t = snake(++it)) {
+      const int n = get_witem<PASS>(p, t).n;
+      if (!wait(C::B_XF, it)) break;
+      for (int i = 0; i < n; ++i, ++g) {
+        const int ys = g % C::NY, gs = 2 * g + xi, sb = gs % C::NS;
+        if (!wait(C::B_YF + ys, g / C::NY)) { ok = false; break; }
+        if (gs >= C::NS && !wait(C::B_SE + sb, gs / C::NS - 1)) { ok = false; break; }
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t b0 = (PASS == 1 ? kdesc : qdesc) + ((uint64_t)(C::OFF_Y + ys * C::TILE) >> 4);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint64_t qo = (uint64_t)((ks / 4) * C::CHUNK + (ks % 4) * 32) >> 4;
+            const uint64_t ko = (uint64_t)((ks / 4) * C::KHALF + (ks % 4) * 32) >> 4;
+            umma_bf16(tmem + 128 * sb, a0 + (PASS == 1 ? qo : ko), b0 + (PASS == 1 ? ko : qo), idesc,
+                      ks > 0 ? 1u : 0u);
+          }
+          umma_commit(BAR(C::B_SF + sb));
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (lane == 0) umma_commit(BAR(C::B_XE));  // once this issuer's products on the pair are done
+      __syncwarp();
     }
     // every MMA issued above has completed before TMEM is released
     if (lane == 0) umma_commit(BAR(C::B_DRAIN));
     __syncwarp();
     mbar_wait_bounded(BAR(C::B_DRAIN), 0);
-  } else if (warp < 2 + 4 * C::NWG) {
+  } else if (warp < C::SOFT0 + 4 * C::NWG) {
     // ======================= softmax =======================
-    const int wg = (warp - 2) / 4;
+    const int wg = (warp - C::SOFT0) / 4;
+    const int xi = wg & 1;               // its X tile of the pair
     const int q4 = warp & 3;             // the TMEM lane quarter this warp may access
     const int m = q4 * 32 + lane;        // row of X
     const uint32_t trow = ((uint32_t)(q4 * 32) << 16) + tmem;
-    float2* const xch = reinterpret_cast<float2*>(gb + C::OFF_XCH);
+    float2* const xch = reinterpret_cast<float2*>(gb + C::OFF_XCH) + xi * 128;
     const float sc = p.scale_log2;
     const float2 sc2 = make_float2(sc, sc), one2 = make_float2(1.f, 1.f);
+    const bool ordered = sc > 0.f;  // the largest raw score is the largest scaled one
+    const float2 msc = ordered ? sc2 : one2;
     int g = 0, it = 0;
     bool ok = true;
     for (int t = snake(it); ok && t < nitems; t = snake(++it)) {
       const WItem w = get_witem<PASS>(p, t);
       const int L = w.ctx + w.qlen;
       // pass 1: this thread's query row; pass 2: its key
-      const int j = w.x * TOK + m / p.group;
+      const int xt = w.x + xi;
+      const int j = xt * TOK + m / p.group;
       const int lim = PASS == 1 ? (j < w.qlen ? w.ctx + j : -1) : L - 1;
-      const int key = w.x * 128 + m;
+      const int key = xt * 128 + m;
       float mx = kNone, l = 0.f;
       // pass 2: the key's sum so far, needed at the end
       const size_t okey = ((size_t)w.r * p.num_kv_heads + w.h) * p.weights_stride + key;
-      const float was = PASS == 2 && wg == 0 && key < w.ctx ? p.weights[okey] : 0.f;
+      const float was = PASS == 2 && wg < 2 && key < w.ctx ? p.weights[okey] : 0.f;
       for (int i = 0; i < w.n; ++i, ++g) {
-        if (g % C::NWG != wg) continue;
-        const int sb = g % C::NS;
-        if (!wait(C::B_SF + sb, g / C::NS)) { ok = false; break; }
+        const int gs = 2 * g + xi, sb = gs % C::NS;
+        if (!wait(C::B_SF + sb, gs / C::NS)) { ok = false; break; }
         tc_fence_after();
         const uint32_t s0 = trow + 128 * sb;
         // this thread's columns: lo .. hi - 1
@@ -946,22 +1044,26 @@ __global__ void __launch_bounds__(WCfg<D, F8>::ALL_THREADS, 1)
           lo = (key - w.ctx - j0) * p.group;
           hi = (w.qlen - j0) * p.group;
         }
+        const bool whole = __all_sync(kAll, lo <= 0 && hi >= 128);
         const float4* const nlse =
             reinterpret_cast<const float4*>(gb + C::OFF_LSE + (g % C::NLSE) * 512);
-        // 32 columns, the next 32 on their way from TMEM meanwhile
+        // 32 columns
         auto take = [&](int c, uint32_t (&rr)[32]) {
           const int lc = lo - c * 32, hc = hi - c * 32;
-          if (__all_sync(kAll, hc <= 0 || lc >= 32)) return;  // no thread sees any of them
-          const bool full = __all_sync(kAll, lc <= 0 && hc >= 32);
+          if (!whole && __all_sync(kAll, hc <= 0 || lc >= 32)) return;  // no thread sees any
+          const bool full = whole || __all_sync(kAll, lc <= 0 && hc >= 32);
           float2 acc[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[e] = make_float2(0.f, 0.f);
           if (PASS == 1) {
-            float2 x[16];
+            float2 x[16];  // raw scores; scaled ones where the scale does not keep their order
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              x[e] = fmul2(make_float2(__uint_as_float(rr[2 * e]), __uint_as_float(rr[2 * e + 1])),
-                           sc2);
+              x[e] = make_float2(__uint_as_float(rr[2 * e]), __uint_as_float(rr[2 * e + 1]));
+            if (!ordered) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) x[e] = fmul2(x[e], sc2);
+            }
             if (!full) {
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
@@ -974,11 +1076,12 @@ __global__ void __launch_bounds__(WCfg<D, F8>::ALL_THREADS, 1)
             for (int e = 0; e < 4; ++e) top[e] = fmaxf(x[e].x, x[e].y);
 #pragma unroll
             for (int e = 4; e < 16; ++e) top[e & 3] = fmaxf(top[e & 3], fmaxf(x[e].x, x[e].y));
-            const float k = fmaxf(mx, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+            const float k =
+                fmaxf(mx, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * msc.x);
             const float2 nk = make_float2(-k, -k);
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float2 d = ffma2(x[e], one2, nk);
+              const float2 d = ffma2(x[e], msc, nk);
               acc[e & 3] = ffma2(make_float2(ex2_approx(d.x), ex2_approx(d.y)), one2, acc[e & 3]);
             }
             l *= ex2_approx(mx - k);
@@ -1007,55 +1110,89 @@ __global__ void __launch_bounds__(WCfg<D, F8>::ALL_THREADS, 1)
                ((acc[2].x + acc[2].y) + (acc[3].x + acc[3].y));
         };
         uint32_t ra[32], rb[32];
-        tmem_ld32(s0, ra);
-        tmem_wait_ld();
-        tmem_ld32(s0 + 32, rb);
-        take(0, ra);
-        tmem_wait_ld();
-        tmem_ld32(s0 + 64, ra);
-        take(1, rb);
-        tmem_wait_ld();
-        tmem_ld32(s0 + 96, rb);
-        take(2, ra);
-        tmem_wait_ld();
-        // the whole buffer is in registers: the MMAs may have it back
-        tc_fence_before();
-        if (PASS == 1) mbar_arrive(BAR(C::B_SE + sb));
-        take(3, rb);
-        if (PASS == 2) mbar_arrive(BAR(C::B_SE + sb));  // the row statistics are read too
+        if constexpr (C::SPLIT == 2) {
+          const int c0 = wg >= 2 ? 2 : 0;
+          tmem_ld32(s0 + c0 * 32, ra);
+          tmem_ld32(s0 + c0 * 32 + 32, rb);
+          tmem_wait_ld();
+          // the columns are in registers: the MMAs may have the buffer back
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(BAR(C::B_SE + sb));
+            mbar_arrive(BAR(C::B_YE + g % C::NY));
+          }
+          take(c0, ra);
+          take(c0 + 1, rb);
+        } else {
+          tmem_ld32(s0, ra);
+          tmem_wait_ld();
+          tmem_ld32(s0 + 32, rb);
+          take(0, ra);
+          tmem_wait_ld();
+          tmem_ld32(s0 + 64, ra);
+          take(1, rb);
+          tmem_wait_ld();
+          tmem_ld32(s0 + 96, rb);
+          take(2, ra);
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(BAR(C::B_SE + sb));
+            mbar_arrive(BAR(C::B_YE + g % C::NY));
+          }
+          take(3, rb);
+        }
       }
       if (!ok) break;
-      // the other warpgroups' parts join warpgroup 0's
-      if (wg > 0) {
-        if (it > 0 && !wait(C::B_XCHE, it - 1)) break;
-        xch[(wg - 1) * 128 + m] = make_float2(mx, l);
-        mbar_arrive(BAR(C::B_XCHF));
-        continue;
+      // the part of the warpgroup that took the other columns
+      float2 o = make_float2(kNone, 0.f);
+      if (C::SPLIT == 2) {
+        if (wg >= 2) {
+          if (it > 0 && !wait(C::B_XCHE + xi, it - 1)) break;
+          xch[m] = make_float2(mx, l);
+          mbar_arrive(BAR(C::B_XCHF + xi));
+          continue;
+        }
+        if (!wait(C::B_XCHF + xi, it)) break;
+        o = xch[m];
+        mbar_arrive(BAR(C::B_XCHE + xi));
       }
-      if (!wait(C::B_XCHF, it)) break;
-      float2 o[C::NWG - 1];
-#pragma unroll
-      for (int e = 0; e < C::NWG - 1; ++e) o[e] = xch[e * 128 + m];
-      mbar_arrive(BAR(C::B_XCHE));
       if (PASS == 1) {
-        float k = mx;
-#pragma unroll
-        for (int e = 0; e < C::NWG - 1; ++e) k = fmaxf(k, o[e].x);
-        l *= ex2_approx(mx - k);
-#pragma unroll
-        for (int e = 0; e < C::NWG - 1; ++e) l += o[e].y * ex2_approx(o[e].x - k);
-        const int slot = w.q0 / TOK + w.r + w.x;
+        const float k = fmaxf(mx, o.x);
+        l = l * ex2_approx(mx - k) + o.y * ex2_approx(o.x - k);
+        if (xt * TOK >= w.qlen) continue;  // the pair's second tile is past the span
+        const int slot = w.q0 / TOK + w.r + xt;
         const size_t at = ((size_t)w.h * p.num_slots + slot) * 128 + m;
-        const int nkt = (w.ctx + min(w.qlen, (w.x + 1) * TOK) - 1) / 128 + 1;
-        if (nkt <= kSplitTiles)
+        if (w.parts > 1) {
+          const size_t step = (size_t)p.num_kv_heads * p.num_slots * 128;
+          __stcg(p.partial + (size_t)w.part * step + at, make_float2(k, l));
+          if (!last_part(p.counters + ((size_t)w.h * p.num_slots + slot) * 4 + q4, w.parts, lane)) continue;
+          float top = kNone, sum = 0.f;
+          for (int i = 0; i < w.parts; ++i) {
+            const float2 v = __ldcg(p.partial + (size_t)i * step + at);
+            const float t2 = fmaxf(top, v.x);
+            sum = sum * ex2_approx(top - t2) + v.y * ex2_approx(v.x - t2);
+            top = t2;
+          }
+          // rows past the span: -inf, a weight of zero
+          p.neg_lse[at] = sum > 0.f ? -(top + log2f(sum)) : -INFINITY;
+        } else {
           p.neg_lse[at] = l > 0.f ? -(k + log2f(l)) : -INFINITY;
-        else
-          __stcg(p.partial + (size_t)(w.y0 / kSplitTiles) * p.num_kv_heads * p.num_slots * 128 + at,
-                 make_float2(k, l));
-      } else if (key < L) {
-#pragma unroll
-        for (int e = 0; e < C::NWG - 1; ++e) l += o[e].y;
-        p.out[okey] = was + l;
+        }
+      } else {
+        l += o.y;
+        if (w.parts > 1) {
+          float* const sums = p.sums + (size_t)w.unit * (kMaxParts * 256) + xi * 128 + m;
+          __stcg(sums + w.part * 256, l);
+          if (!last_part(p.counters + (size_t)p.num_kv_heads * p.num_slots * 4 + w.unit * 8 + xi * 4 + q4,
+                         w.parts, lane))
+            continue;
+          l = 0.f;
+          for (int i = 0; i < w.parts; ++i) l += __ldcg(sums + i * 256);
+        }
+        if (key < L) p.out[okey] = was + l;
       }
     }
   } else if constexpr (F8) {
@@ -1083,10 +1220,10 @@ __global__ void __launch_bounds__(WCfg<D, F8>::ALL_THREADS, 1)
         __syncwarp();
       };
       if (PASS == 2) {
-        const int xs = it & 1;
-        if (it >= 2 && !wait(C::B_XE + xs, it / 2 - 1)) break;
-        convert(w.x, gb + C::OFF_X + xs * C::TILE);
-        if (lane == 0) mbar_arrive(BAR(C::B_XF + xs));
+        if (it >= 1 && !wait(C::B_XE, it - 1)) break;
+        convert(w.x, gb + C::OFF_X);
+        convert(w.x + 1, gb + C::OFF_X + C::TILE);
+        if (lane == 0) mbar_arrive(BAR(C::B_XF));
       } else {
         for (int i = 0; i < w.n; ++i, ++g) {
           const int ys = g % C::NY;
@@ -1221,24 +1358,26 @@ cudaError_t launch_many(const WeightsParams& p, int num_sms, cudaStream_t s) {
     tp.tm_k = tp.tm_q;  // not used: the converter warps load the codes
   } else {
     const uint64_t rows = (uint64_t)p.num_blocks * p.num_kv_heads * kBlockSize;
-    if (!encode_tmap_bf16_2d(&tp.tm_k, p.k_cache, D, rows, (uint64_t)D * 2, 64, kBlockSize))
+    if (D == 128) {
+      const uint64_t cd[4] = {64, 8, 2, rows / 8}, cs[3] = {D * 2, 128, 8 * D * 2};
+      const uint32_t cb[4] = {64, 8, 2, kBlockSize / 8};
+      if (!encode_tmap_bf16(&tp.tm_k, 4, p.k_cache, cd, cs, cb)) return cudaErrorInvalidValue;
+    } else if (!encode_tmap_bf16_2d(&tp.tm_k, p.k_cache, D, rows, (uint64_t)D * 2, 64, kBlockSize))
       return cudaErrorInvalidValue;
   }
   cudaError_t e = launch_pass<D, 1, F8>(tp, num_sms, s);
-  if (e == cudaSuccess && p.max_seq_len > 128 * kSplitTiles)
-    e = launch_chained(pa_weights_join_kernel, p, (long long)p.num_slots * p.num_kv_heads, 128, 0, s);
   if (e == cudaSuccess) e = launch_pass<D, 2, F8>(tp, num_sms, s);
   return e;
 }
 
 template <int D, bool F8>
 cudaError_t launch_weights_t(const WeightsParams& p, int num_sms, cudaStream_t s, int* launches) {
-  // decodes: score, finish. With chunks: plan, score, finish, pass 1, (join,)
-  // pass 2 - the first two need nothing of one another and run together
+  // decodes: one grid, or score and finish. With chunks: the plan before them -
+  // they need nothing of one another and run together - and the passes after
   *launches = p.cluster > 0 ? 1 : 2;
   cudaError_t e = cudaSuccess;
   if (p.num_slots > 0) {
-    *launches += p.max_seq_len > 128 * kSplitTiles ? 4 : 3;
+    *launches += 3;
     pa_weights_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
     e = cudaGetLastError();
   }
@@ -1262,23 +1401,27 @@ WeightsLayout weights_layout(int num_reqs, int num_tokens, int num_q_heads, int 
   l.stats_off = 0;
   l.scores_off = pa_align256(sizeof(float) * 2 * kFewRows * rh * (size_t)l.num_chunks);
   l.total = l.scores_off + pa_align256(sizeof(float) * rh * blocks * kBlockSize * l.stored_rows);
-  l.counts_off = l.parts_off = l.items1_off = l.items2_off = l.lse_off = l.partial_off = l.total;
-  l.num_slots = l.max_items[0] = l.max_items[1] = 0;
+  l.counts_off = l.counters_off = l.items1_off = l.items2_off = l.lse_off = l.partial_off =
+      l.sums_off = l.total;
+  l.num_slots = l.max_items[0] = l.max_items[1] = l.num_counters = 0;
   if (!many) return l;
   const size_t tok = (size_t)(128 / G);
   const size_t slots = (size_t)num_tokens / tok + (size_t)num_reqs + 1;
   const size_t tiles = ((size_t)max_seq_len + 127) / 128;
-  const size_t parts = (tiles + kSplitTiles - 1) / kSplitTiles;
+  size_t parts = (tiles + kMinPart - 1) / kMinPart;
+  if (parts > kMaxParts) parts = kMaxParts;
   l.num_slots = (int)slots;
+  l.num_counters = (int)(4 * slots * num_kv_heads + 8 * kMaxUnits);
   l.max_items[0] = (int)(slots * parts * num_kv_heads);
-  l.max_items[1] = (int)(rh * tiles);
-  l.parts_off = l.counts_off + 256;
-  l.items1_off = l.parts_off + pa_align256(sizeof(int) * slots);
-  l.items2_off = l.items1_off + pa_align256(2 * sizeof(int4) * slots * parts * num_kv_heads);
-  l.lse_off = l.items2_off + pa_align256(2 * sizeof(int4) * rh * tiles);
+  l.max_items[1] = (int)(rh * tiles) + kMaxUnits * kMaxParts;
+  l.counters_off = l.counts_off + 256;
+  l.items1_off = l.counters_off + pa_align256(sizeof(int) * (size_t)l.num_counters);
+  l.items2_off = l.items1_off + pa_align256(sizeof(WItem) * (size_t)l.max_items[0]);
+  l.lse_off = l.items2_off + pa_align256(sizeof(WItem) * (size_t)l.max_items[1]);
   l.partial_off = l.lse_off + pa_align256(sizeof(float) * 128 * slots * num_kv_heads);
-  l.total = l.partial_off +
-            (parts > 1 ? pa_align256(sizeof(float2) * 128 * slots * num_kv_heads * parts) : 0);
+  l.sums_off = l.partial_off +
+               (parts > 1 ? pa_align256(sizeof(float2) * 128 * slots * num_kv_heads * parts) : 0);
+  l.total = l.sums_off + sizeof(float) * 256 * kMaxParts * (size_t)kMaxUnits;
   return l;
 }
 
@@ -1288,6 +1431,7 @@ cudaError_t launch_weights(WeightsParams p, int head_dim, bool f8, int num_sms, 
   // scores leave room for three CTAs on an SM and the grid has at least two
   // waves of them; 0: they do not fit even eight CTAs (kClusterSmem each)
   const long long rh = (long long)p.num_reqs * p.num_kv_heads;
+  p.num_sms = num_sms;
   p.cluster = 1;
   while (p.cluster < 8 && (cluster_smem(p.padded_len, p.cluster, p.stored_rows) > kClusterSmem ||
                            (rh * p.cluster < 6LL * num_sms && p.padded_len > 1024 * p.cluster)))

@@ -77,6 +77,21 @@ def test_long_context_parts(pa_lib, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("hq,hkv,d,spans", [
+    (8, 1, 64, [(0, 700)]), (4, 4, 128, [(1500, 600)]), (16, 2, 128, [(3000, 260), (0, 30)]),
+    (64, 8, 64, [(100, 1000), (700, 333)]), (1, 1, 128, [(0, 3001)])])
+def test_pairs_in_parts(pa_lib, hq, hkv, d, spans, fp8):
+    """Few pairs over many tiles: both passes cut them into parts, joined by the
+    warp that finishes last; repeated, since which one that is may change."""
+    b = ref.Batch(spans, hq, hkv, d, hq + d, fp8=fp8)
+    check(b)
+    w = torch.rand(len(spans), hkv, b.mb * 16)
+    one = run(b, w, torch.zeros_like(w))
+    for _ in range(5):
+        assert torch.equal(one, run(b, w, torch.zeros_like(w)))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("hq,spans", [(8, [(41500, 1), (300, 1)]), (1, [(50000, 2), (9, 8)]),
                                       (4, [(41000, 2), (700, 70)])])
 def test_longer_than_a_cluster_holds(pa_lib, hq, spans, fp8):
