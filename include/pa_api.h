@@ -306,7 +306,8 @@ pa_status pa_attention_cascade(const void* q, const void* k_cache, const void* v
  * table entries are not read, whatever they hold. Of the keys in a block that
  * is read, those that no new token of the request attends to may hold
  * anything; K and V of the others must be finite, as for pa_attention. Time
- * and bytes follow the keys attended to, not the sequence length.
+ * and bytes follow the keys attended to, not the sequence length. num_blocks
+ * >= 1.
  */
 pa_status pa_attention_window(const void* q, const void* k_cache, const void* v_cache,
                               const int32_t* block_tables, const int32_t* seq_lens,
@@ -345,7 +346,7 @@ pa_status pa_attention_window_fp8(const void* q, const void* k_cache, const void
  *                 call at a time. The size grows with num_reqs x max_seq_len:
  *                 4 bytes per (request, query head, key) for a decode batch.
  * The other arguments are pa_attention's, and so are the limits (head_dim 64 or
- * 128, groups of 1, 2, 4 or 8) and the errors. A request longer than
+ * 128, groups of 1, 2, 4 or 8; num_blocks >= 1) and the errors. A request longer than
  * weights_stride sets PA_DEVERR_LENGTHS and is skipped. Scores and sums are
  * binary32; results do not depend on the order in which CTAs run.
  */

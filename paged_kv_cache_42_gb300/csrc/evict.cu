@@ -353,6 +353,7 @@ cudaError_t launch_evict(EvictParams p, int row_bytes, int num_sms, cudaStream_t
                   : part <= 32 * kSelThreads ? launch_select<32>(p, (unsigned)rows, s)
                                              : launch_select<0>(p, (unsigned)rows, s);
   if (e != cudaSuccess) return e;
+  if (p.max_seq_len <= p.keep) return cudaSuccess;  // no request is cut: the lengths were all
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * chunks));
   cfg.blockDim = dim3(kMoveThreads);

@@ -352,15 +352,20 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
                          int sinks, int kv_fp8, float k_scale, float v_scale, void* workspace,
                          size_t workspace_bytes, void* stream) {
   bool nothing = false;
+  const bool windowed = window > 0;
   // a window that holds every key of the batch hides none
   if (window >= max_seq_len) window = sinks = 0;
+  // the most keys a token's blocks can span (it sizes the flattened work)
+  const long long span = (long long)window + sinks + 3 * kBlockSize;
+  const int seen = window > 0 && span < max_seq_len ? (int)span : max_seq_len;
   if (pa_status st = check_attention_args(
           q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale, out, num_reqs,
           num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
-          max_blocks_per_req, max_query_len, max_seq_len, prefix_len, kv_fp8, k_scale, v_scale,
+          max_blocks_per_req, max_query_len, seen, prefix_len, kv_fp8, k_scale, v_scale,
           &nothing))
     return st;
   if (nothing) return PA_OK;
+  if (windowed && num_blocks < 1) return PA_ERR_INVALID_ARG;  // no block to attend to
   const WsLayout lay = ws_layout(num_reqs, num_tokens, num_q_heads, num_kv_heads, head_dim);
   const size_t need =
       lay.total + (prefix_len > 0
@@ -701,14 +706,17 @@ pa_status weights_impl(const void* q, const void* k_cache, const int32_t* block_
                        int max_blocks_per_req, int max_query_len, int max_seq_len,
                        void* workspace, size_t workspace_bytes, void* stream) {
   bool nothing = false;
-  // pa_attention's checks; there is no V here and out is checked below
+  // pa_attention's checks; there is no V here, out is checked below, and no
+  // work is flattened over the keys (so their number does not count here)
   if (pa_status st = check_attention_args(
           q, k_cache, k_cache, block_tables, seq_lens, query_start_loc, scale, q, num_reqs,
           num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
-          max_blocks_per_req, max_query_len, max_seq_len, 0, kv_fp8, k_scale, 1.f, &nothing))
+          max_blocks_per_req, max_query_len, max_seq_len < 1 ? max_seq_len : 1, 0, kv_fp8, k_scale,
+          1.f, &nothing))
     return st;
   if (weights_stride < 0) return PA_ERR_INVALID_ARG;
   if (nothing) return PA_OK;
+  if (num_blocks < 1) return PA_ERR_INVALID_ARG;  // no block to read
   if (!weights || !out || (reinterpret_cast<uintptr_t>(weights) & 3u) ||
       (reinterpret_cast<uintptr_t>(out) & 3u))
     return PA_ERR_INVALID_ARG;
@@ -862,7 +870,7 @@ pa_status pa_evict_kv(void* k_cache, void* v_cache, const int32_t* block_tables,
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   TimerScope timer(7, s);
   const cudaError_t e = launch_evict(p, head_dim * elem_bytes, d->num_sms, s);
-  g_launches.fetch_add(2);
+  g_launches.fetch_add(max_seq_len > keep ? 2 : 1);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

@@ -77,6 +77,10 @@ def test_window(pa_lib, fp8):
     assert f(ws=None) == WS and f(wsb=16) == WS and f(ws=FAKE + 16) == WS
     assert f(R=0, wsb=0) == OK and f(T=0, wsb=0) == OK
     assert f(R=0, w=0, wsb=0) == ARG
+    assert f(nb=0) == ARG and f(nb=0, R=0, wsb=0) == OK
+    # the flattened work follows the window, not the sequence: too long without one
+    assert f(T=4096, hkv=2, ms=2 ** 22, mb=2 ** 18, wsb=16, w=2 ** 22 - 1) == UNSUP
+    assert f(T=4096, hkv=2, ms=2 ** 22, mb=2 ** 18, wsb=16) == WS
     if fp8:
         assert f(ks=0.0) == ARG and f(vs=math.inf) == ARG
 
@@ -108,6 +112,7 @@ def test_weights(pa_lib, fp8):
     assert f(d=96) == UNSUP and f(bs=32) == UNSUP and f(hq=32, hkv=2, wsb=0) == UNSUP
     assert f(ws=None) == WS and f(wsb=16) == WS and f(ws=FAKE + 16) == WS
     assert f(R=0, wsb=0) == OK and f(T=0, wsb=0) == OK
+    assert f(nb=0) == ARG and f(ms=-1, wsb=0) == ARG
     assert f(mq=0, ws=None) == OK and f(ms=0, ws=None) == OK  # no request can have a new token
     assert f(ms=(1 << 30) + 1, R=1, T=1, hkv=1, wsb=0) == UNSUP
     # 2 R x 2^22 key tiles: 8.4e8 for 100 requests, past 2^31 (grids) for 600
