@@ -102,6 +102,10 @@ struct WsHeader {
 // about kPrefillStepUs; the split-KV kernel streams about kDecodeSmBytesPerUs
 // per SM until the copy peak (kHbmBytesPerUs) caps it.
 constexpr float kPrefillStepUs = 2.4f;
+// A windowed item has two masked edges, so more of its steps take the masked
+// softmax (512 decodes and three 512-token chunks at window 1024: 334 us on the
+// 14 SMs that 2.4 us asks for, 302 us on 16 to 24).
+constexpr float kWindowStepUs = 3.2f;
 constexpr float kDecodeSmBytesPerUs = 47.0e3f;
 constexpr float kHbmBytesPerUs = 6.6e6f;
 constexpr float kOverlapMargin = 0.85f;  // prefill share planned to end this early

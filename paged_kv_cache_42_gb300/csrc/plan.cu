@@ -208,7 +208,8 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
     int ctas = p.num_sms, workers = p.num_workers;
     if (p.overlap && p.use_prefill && W > 0 && s_steps > 0) {
       const int S_ = p.num_sms;
-      const float pre = kPrefillStepUs * (float)s_steps;  // SM x us
+      const float step_us = p.window > 0 ? kWindowStepUs : kPrefillStepUs;
+      const float pre = step_us * (float)s_steps;  // SM x us
       const float bytes = (float)W * (float)p.position_bytes;
       auto dec_us = [&](int n) {
         return fmaxf(bytes / ((float)n * kDecodeSmBytesPerUs), bytes / kHbmBytesPerUs);
