@@ -614,6 +614,8 @@ pa_status pa_set_kernel_timer(int kernel_id, void* start_event, void* stop_event
  *     each head's keys in one half-warp). 0: the per-(token, kv head) tiles
  *     of the other groupings. Both are within the attention tolerances of
  *     the exact result on the same codes; they are not bit-identical.
+ *     pa_attention_window_fp8 takes these tiles only for batches with enough
+ *     keys attended to (20 blocks per SM).
  */
 #define PA_OPT_DECODE_TOKEN_MAJOR 5
 /*
@@ -632,7 +634,7 @@ pa_status pa_set_kernel_timer(int kernel_id, void* start_event, void* stop_event
  *     (taken only at G = Hq / Hkv <= 4; G = 8 always runs one) each SM runs
  *     two CTAs of two copy stages each instead of one of four, so twice as
  *     many workers slice the keys; results stay within the attention
- *     tolerances.
+ *     tolerances. A windowed call below 64 blocks per SM runs one.
  */
 #define PA_OPT_DECODE_TM_CTAS_PER_SM 7
 /*

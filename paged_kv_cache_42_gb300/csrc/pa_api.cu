@@ -439,9 +439,18 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
   const int dec_sms = d->num_sms - prefix_ctas;  // SMs the split-KV grid fills
   // An E4M3 cache over eight KV heads takes the token-major tiles (one block
   // of every KV head per tile) on the tensor cores.
-  const int tm_cps = g_tm_ctas.load();
+  // Windowed calls: by the blocks the tokens attend to at most, per SM. Below 20
+  // a token-major worker's start and its many-partial merge outweigh its faster
+  // tiles (eight tokens of 252 blocks at G = 8: 29.9 us with the other tiles,
+  // 34.7 token-major; 64 tokens of 66 blocks: 50.7 and 47.2), and below 64 one
+  // CTA per SM is at least as good as two (64 tokens of 66 blocks at G = 4: 37.6
+  // us against 41.2; 128 of 257: 180 against 176).
+  const long long win_blocks =
+      window > 0 ? (long long)num_tokens * (((long long)window + sinks + kBlockSize - 1) / kBlockSize)
+                 : 0;
+  const int tm_cps = window > 0 && win_blocks < 64LL * d->num_sms ? 1 : g_tm_ctas.load();
   const bool use_tm =
-      use_tc && kv_fp8 && g_token_major.load() &&
+      use_tc && kv_fp8 && g_token_major.load() && !(window > 0 && win_blocks < 20LL * d->num_sms) &&
       decode_tm_supported(head_dim, group, num_kv_heads, decode_tm_workers(group, d->num_sms, tm_cps));
   const int launched = use_tm   ? decode_tm_workers(group, d->num_sms, tm_cps)
                        : use_tc ? decode_tc_workers(d->num_sms)
@@ -455,8 +464,8 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
   pp.sinks = sinks;
   // A window leaves short units, and a batch of a few of them is a chain of
   // blocks in a handful of warps: there the CUDA-core kernel's workers take
-  // single blocks (four tokens of a 16-key window at head_dim 64: MINPOS us
-  // against 15 us with eight blocks each). The tensor-core kernels' workers
+  // single blocks (four tokens of a 16-key window at head_dim 64: 7.3 us per
+  // call against 16 us with eight blocks each). The tensor-core kernels' workers
   // keep a whole tile.
   pp.min_pos = window > 0 && !use_tc ? 1 : PA_DEC_MIN_POS;
   // A mixed batch on the tensor-core split-KV kernel (bf16) may run its
@@ -584,7 +593,7 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
   mp.token_major = pp.token_major;
   // Few tokens over many workers (a window over long sequences): a token's
   // partials are shared by the warps of a CTA per KV head (eight tokens over
-  // 152 workers: MERGE us against 16 us for a warp per KV head).
+  // 152 workers: 35 us per call against 40 with a warp per KV head).
   mp.tm_wide = window > 0 && use_tm && workers > 4 * num_tokens ? 1 : 0;
   mp.min_pos = pp.min_pos;
   mp.num_q_heads = num_q_heads;

@@ -40,14 +40,15 @@
 // TMA unit some 40 ns each, whatever their size, and a stage about 2 us to turn
 // around) than one 128 x 128 product on it takes. Two warps issue the MMAs:
 // between the products of a step one warp's waits, fences and commits take as
-// long as the products. Warpgroup w takes X tile w % 2 and half
-// w / 2 of the columns; it copies its 64 columns to registers, gives the S
-// buffer back and only then takes exponentials, so that the MMAs of the next
-// step but one run meanwhile. What is left is the exponentials: 128 x 128 of
-// them hold the special-function units for 512 cycles of an SM, the products
-// the tensor pipe for as long, and a step takes about STEP cycles. (Three
-// 512-token chunks on 0, 1024 and 2048 keys, 32 / 8 heads: single X tiles, one
-// issuer and no parts 63 us; pairs 55.5; two issuers 54; halves and parts CHUNKS.)
+// long as the products. Warpgroup w takes X tile w % 2 and half w / 2 of the
+// columns; it copies its 64 columns to registers, gives the S buffer back and
+// only then takes exponentials, so that the next steps' MMAs run meanwhile.
+// Three 512-token chunks on 0, 1024 and 2048 keys, 32 / 8 heads: single X tiles
+// and one issuer 63 us per call, pairs 55.5, two issuers 54, halves of the
+// columns 53. A step (two products) then takes about 1900 cycles against 1024 of
+// the tensor pipe and of the special-function units each (per-step clock probe;
+// leaving out every exponential gains 4 us of the 53, so it is neither alone):
+// the products' operands and the copies load shared memory for about 1250.
 #include <cuda.h>
 
 #include "pa_internal.h"

@@ -110,6 +110,15 @@ def test_long_sequences(pa_lib, hq, hkv, d, fp8):
     check(b, 3001, 70)
 
 
+@pytest.mark.parametrize("hq,n,L,window", [(8, 220, 400, 250), (32, 220, 400, 250),
+                                           (64, 220, 400, 250), (32, 300, 900, 700),
+                                           (32, 3, 30000, 20000)])
+def test_token_major_tiles(pa_lib, hq, n, L, window):
+    """E4M3 over eight KV heads with enough blocks for the token-major kernel:
+    one and two CTAs per SM, and few tokens over many workers."""
+    check(ref.Batch([(L + 3 * i, 1) for i in range(n)], hq, 8, 128, hq + n, fp8=True), window, 5)
+
+
 def test_wide_chunk_overlaps_decodes(pa_lib):
     """A batch on the overlapped path: many decodes beside a long chunk."""
     b = ref.Batch([(900 + 7 * i, 1) for i in range(96)] + [(1000, 300)], 16, 4, 128, 3)
