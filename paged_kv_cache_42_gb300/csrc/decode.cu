@@ -229,7 +229,10 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
     W = p.header->num_positions;
     K = p.header->num_units;
   }
-  if (W <= 0) return;
+  if (W <= 0) {  // no work; this grid still completes only after the one before
+    griddep_wait();
+    return;
+  }
   const int launched = (int)gridDim.x * WARPS;
   const int NW = plan_workers(W, launched < p.max_workers ? launched : p.max_workers, p.min_pos);
   const int w = blockIdx.x * WARPS + warp;

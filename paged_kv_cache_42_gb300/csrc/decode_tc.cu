@@ -1077,7 +1077,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // overlapped mixed batch: complete only after the prefill-chunk grid, so
   // that whoever waits for this grid (the merge pass, later work on the
   // stream) sees the whole call
-  if (p.overlap && threadIdx.x == 0) griddep_wait();
+  // (and with no work at all, only after whatever the grid before is)
+  if ((p.overlap || W <= 0) && threadIdx.x == 0) griddep_wait();
 }
 
 // One warp per (token, kv head): each of the G query rows is scaled by the

@@ -762,6 +762,8 @@ __global__ void __launch_bounds__(kTmThreads, CPS)
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmemCols);
   }
+  // no work: this grid still completes only after the one before
+  if (W <= 0 && threadIdx.x == 0) griddep_wait();
 }
 
 // ---------------------------------------------------------------------------------------

@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(kSelThreads) pa_evict_select_kernel(const Evic
   __shared__ int wsum[kSelWarps], wsum2[kSelWarps];
   __shared__ uint32_t s_pick[2];        // a pass's bin, and the tokens in the bins above it
   __shared__ uint32_t s_count[2];       // this CTA's tokens above the threshold, and at it
+  griddep_wait();               // a programmatic dependent of the grid before
   griddep_launch_dependents();  // the move grid may take its place; it waits for this one
   const int C = p.cluster, rank = (int)(blockIdx.x % (unsigned)C);
   const int rh = (int)(blockIdx.x / (unsigned)C);
@@ -258,12 +259,14 @@ cudaError_t launch_select(const EvictParams& p, unsigned rows, cudaStream_t s) {
   cfg.blockDim = dim3(kSelThreads);
   cfg.dynamicSmemBytes = 0;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)p.cluster;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, pa_evict_select_kernel<KPT>, p);
 }
 

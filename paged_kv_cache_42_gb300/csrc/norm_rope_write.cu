@@ -111,6 +111,7 @@ __global__ void __launch_bounds__(kThreads) pa_norm_rope_write_kernel(const Norm
     ea = turned ? sub * 4 : half + sub * 4;
     eb = turned ? ea + half : ea + (D - p.rotary_dim) / 2;
   }
+  griddep_wait();  // a programmatic dependent of the grid before, which made q, k and v
   // every load that needs no position first
   const long long slot = __ldg(p.slot_mapping + t);
   const int pos = p.rotary_dim > 0 ? __ldg(p.positions + t) : 0;
@@ -240,11 +241,17 @@ cudaError_t launch_nr(const NormRopeParams& p, int num_sms, cudaStream_t s) {
   const bool small = blocks(1) <= 8LL * num_sms;
   const long long grid = small ? blocks(1) : blocks(kManyIter);
   if (grid > 0x3fffffffLL) return cudaErrorInvalidValue;  // warps are counted in 32 bits
-  if (small)
-    pa_norm_rope_write_kernel<D, F8, INTER, 1><<<(unsigned)grid, kThreads, 0, s>>>(p);
-  else
-    pa_norm_rope_write_kernel<D, F8, INTER, kManyIter><<<(unsigned)grid, kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return small ? cudaLaunchKernelEx(&cfg, pa_norm_rope_write_kernel<D, F8, INTER, 1>, p)
+               : cudaLaunchKernelEx(&cfg, pa_norm_rope_write_kernel<D, F8, INTER, kManyIter>, p);
 }
 
 template <int D>

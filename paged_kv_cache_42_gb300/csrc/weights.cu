@@ -339,7 +339,13 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 2) pa_weights_cluster_kern
   __shared__ float2 s_run[kClusterWarps][kFewRows];
   __shared__ float2 s_cta[kFewRows];                 // this CTA's {max, sum} of each row
   __shared__ float2 s_row[kFewRows];                 // the request's {max, 1 / sum}
-  if (p.num_slots > 0) griddep_launch_dependents();  // prompt chunks' passes need nothing of this
+  // The first grid of the call waits for the grid before it; behind a plan,
+  // which has waited, this one does so only to complete after it, and lets the
+  // chunks' passes, which need nothing of it, take their places.
+  if (p.num_slots == 0)
+    griddep_wait();
+  else
+    griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int C = p.cluster, rank = (int)(blockIdx.x % (unsigned)C);
   const int rh = (int)(blockIdx.x / (unsigned)C);
@@ -443,7 +449,10 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 2) pa_weights_cluster_kern
 // finish kernel.
 template <int D, bool F8, int NR>
 __global__ void __launch_bounds__(32 * kScoreWarps) pa_weights_score_kernel(const WeightsParams p) {
-  griddep_launch_dependents();      // the finish grid waits for this one
+  // the first grid of the call waits for the grid before it; behind a plan,
+  // which has waited, this one does so only to complete after it
+  if (p.num_slots == 0) griddep_wait();
+  griddep_launch_dependents();  // the finish grid waits for this one
   // (the plan, if any, comes before: this grid completes after it)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (p.num_chunks + kScoreWarps - 1) / kScoreWarps;
@@ -633,6 +642,7 @@ __global__ void __launch_bounds__(kPlanThreads) pa_weights_plan_kernel(const Wei
   __shared__ int cnt[2][kBuckets];
   __shared__ int wsum[kPlanThreads / 32], s_fits;
   __shared__ int s_steps[2], s_pairs[2], s_unit;
+  griddep_wait();               // the first grid of the call waits for the grid before it
   griddep_launch_dependents();  // the decodes' grids need no plan and wait for this one at their end
   bool none = false;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -1294,25 +1304,15 @@ cudaError_t launch_few(const WeightsParams& p, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)p.cluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    // behind the plan, beside it; without one this is the first grid of the
-    // call and no programmatic dependent
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = p.num_slots > 0 ? 2 : 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, p);
   }
   const long long g1 = rh * ((p.num_chunks + kScoreWarps - 1) / kScoreWarps);
   if (g1 > 0x7fffffffLL) return cudaErrorInvalidValue;
-  cudaError_t e;
-  if (p.num_slots > 0) {  // behind the plan, beside it
-    e = launch_chained(pa_weights_score_kernel<D, F8, NR>, p, g1, 32 * kScoreWarps, 0, s);
-  } else {
-    // the first grid of the call is no programmatic dependent: everything the
-    // stream did before is complete and visible
-    pa_weights_score_kernel<D, F8, NR><<<(unsigned)g1, 32 * kScoreWarps, 0, s>>>(p);
-    e = cudaGetLastError();
-  }
+  cudaError_t e = launch_chained(pa_weights_score_kernel<D, F8, NR>, p, g1, 32 * kScoreWarps, 0, s);
   if (e != cudaSuccess) return e;
   return launch_chained(pa_weights_finish_kernel<NR>, p,
                         rh * ((p.padded_len + kFinishKeys - 1) / kFinishKeys), kFinishThreads, 0, s);
@@ -1379,8 +1379,7 @@ cudaError_t launch_weights_t(const WeightsParams& p, int num_sms, cudaStream_t s
   cudaError_t e = cudaSuccess;
   if (p.num_slots > 0) {
     *launches += 3;
-    pa_weights_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
-    e = cudaGetLastError();
+    e = launch_chained(pa_weights_plan_kernel, p, 1, kPlanThreads, 0, s);
   }
   if (e == cudaSuccess) e = launch_few_rows<D, F8>(p, s);
   if (e != cudaSuccess || p.num_slots == 0) return e;
