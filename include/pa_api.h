@@ -223,8 +223,8 @@ pa_status pa_attention_fp8(const void* q, const void* k_cache, const void* v_cac
  *      itself where q is contiguous, and overlaps no other argument.
  *   k_cache, v_cache, slot_mapping  as for pa_write_kv. A negative slot marks
  *      a padding token, of which nothing is written, q_out included.
- * Arithmetic is binary32, each result rounded once. head_dim 64 or 128, any
- * number of heads. A slot outside the pool sets PA_DEVERR_SLOT and a position
+ * Arithmetic is binary32, each result rounded once. head_dim 64 or 128, up to
+ * 65536 heads of a kind. A slot outside the pool sets PA_DEVERR_SLOT and a position
  * outside the table PA_DEVERR_POSITION; such a token is skipped whole.
  */
 pa_status pa_norm_rope_write_kv(const void* q, const void* k, const void* v, long long q_stride,

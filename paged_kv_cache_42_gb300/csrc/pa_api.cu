@@ -24,6 +24,7 @@ __device__ unsigned long long g_device_error[2];
 namespace {
 
 constexpr int kMaxDevices = 64;
+constexpr int kMaxRopeHeads = 65536;  // a token's elements are counted in 32 bits
 
 // Per-device set-up, done once. The cached device address of the error word
 // stays valid for the life of the CUDA context: the library does not support
@@ -220,7 +221,8 @@ pa_status norm_rope_write_impl(const void* q, const void* k, const void* v, long
     return PA_ERR_INVALID_ARG;
   if (kv_fp8 && !(k_scale > 0.f && k_scale < INFINITY && v_scale > 0.f && v_scale < INFINITY))
     return PA_ERR_INVALID_ARG;
-  if (block_size != kBlockSize || (head_dim != 64 && head_dim != 128) || rotary_dim % 16 != 0)
+  if (block_size != kBlockSize || (head_dim != 64 && head_dim != 128) || rotary_dim % 16 != 0 ||
+      num_q_heads > kMaxRopeHeads || num_kv_heads > kMaxRopeHeads)
     return PA_ERR_UNSUPPORTED;
   const NvtxRange range(kv_fp8 ? "pa_norm_rope_write_kv_fp8" : "pa_norm_rope_write_kv");
   if (num_tokens == 0) return PA_OK;

@@ -39,6 +39,8 @@ def test_norm_rope_write(pa_lib, fp8):
     assert f(qw=FAKE + 2) == ARG and f(kw=FAKE + 2) == ARG
     assert f(T=-1) == ARG and f(hq=0) == ARG and f(hkv=-1) == ARG and f(nb=-1) == ARG
     assert f(d=96) == UNSUP and f(d=32, rot=32) == UNSUP and f(bs=32) == UNSUP
+    assert f(hq=65537, qs=65537 * 64) == UNSUP
+    assert f(hkv=65537, ks=65537 * 64, vs=65537 * 64) == UNSUP
     assert f(rot=24) == UNSUP and f(rot=80) == ARG and f(rot=-16) == ARG and f(mp=-1) == ARG
     assert f(eps=-1e-6) == ARG and f(eps=math.nan) == ARG and f(eps=math.inf) == ARG
     assert f(qs=255) == ARG and f(qs=260) == ARG and f(ks=120) == ARG and f(vs=132) == ARG
