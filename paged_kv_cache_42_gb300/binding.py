@@ -237,6 +237,15 @@ def _where(stream) -> tuple[int, int]:
     return dev, int(stream.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory for a call on `stream`, from that stream's own: the allocator may
+    hand memory of another one to later work there while this call still runs."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _heads(t: torch.Tensor, shape: tuple, dev: int, name: str) -> tuple[int, int]:
     """(address, token stride in elements) of [tokens, heads, head_dim] whose
     tokens may lie apart (a part of a wider projection)."""
@@ -282,7 +291,7 @@ def _norm_rope(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_we
         if k_weight.numel() != d:
             raise ValueError("a norm weight must be [head_dim]")
     if out is None:
-        out = torch.empty(qshape, dtype=torch.bfloat16, device=q.device)
+        out = _empty(qshape, torch.bfloat16, q.device, stream)
     elif out.shape != qshape:
         raise ValueError("out must have q's shape")
     qp, qs = _heads(q, qshape, dev, "q")
@@ -472,12 +481,12 @@ def _window(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale,
     if query_start_loc.numel() != R + 1 or mr != R:
         raise ValueError("metadata shapes must be qsl [R+1], block_tables [R, max_blocks]")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(qshape, torch.bfloat16, q.device, stream)
     elif out.shape != qshape:
         raise ValueError("out must have q's shape")
     if workspace is None:
         need = workspace_size(R, T, hq, hkv, d)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(need, 256), torch.uint8, q.device, stream)
     dev, raw_stream = _where(stream)
     out_p = _ptr(out, torch.bfloat16, dev, "out") if out.is_cuda else _out(out)
     cache_dtype = torch.uint8 if fp8 else torch.bfloat16
@@ -544,7 +553,7 @@ def _weights(q, k_cache, block_tables, seq_lens, query_start_loc, scale, weights
         raise ValueError("out must have weights' shape")
     if workspace is None:
         need = weights_workspace_size(R, T, hq, hkv, d, max_query_len, max_seq_len)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(need, 256), torch.uint8, q.device, stream)
     dev, raw_stream = _where(stream)
     st = lib().pa_attention_weights_args(_pack_wts(
         _ptr(q, torch.bfloat16, dev, "q"),
@@ -609,12 +618,11 @@ def evict_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.T
         if t.dim() != 2 or t.shape[0] != R:
             raise ValueError("block tables must be [num_reqs, blocks]")
     if new_seq_lens is None:
-        new_seq_lens = torch.empty(R, dtype=torch.int32, device=k_cache.device)
+        new_seq_lens = _empty(R, torch.int32, k_cache.device, stream)
     if kept is None:
-        kept = torch.empty((R, hkv, max(keep, 0)), dtype=torch.int32, device=k_cache.device)
+        kept = _empty((R, hkv, max(keep, 0)), torch.int32, k_cache.device, stream)
     if new_weights is None:
-        new_weights = torch.empty((R, hkv, max(keep, 0)), dtype=torch.float32,
-                                  device=k_cache.device)
+        new_weights = _empty((R, hkv, max(keep, 0)), torch.float32, k_cache.device, stream)
     if new_seq_lens.shape != (R,) or kept.shape != (R, hkv, keep) or \
             new_weights.dim() != 3 or new_weights.shape[:2] != (R, hkv):
         raise ValueError("new_seq_lens must be [R], kept [R, Hkv, keep], new_weights [R, Hkv, width]")

@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kMoveThreads) pa_evict_move_kernel(const Evict
   constexpr int ITER = kMoveRows * VPR / kMoveThreads;     // vectors per thread and tensor
   static_assert(ITER >= 1, "every thread copies");
   __shared__ long long s_src[kMoveRows], s_dst[kMoveRows];  // row numbers in the caches; -1: none
-  const int chunks = (p.keep + kMoveRows - 1) / kMoveRows;
+  const int chunks = (p.keep - 1) / kMoveRows + 1;
   const long long g = blockIdx.x;
   const int c = (int)(g % chunks);
   const int rh = (int)(g / chunks);
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kMoveThreads) pa_evict_move_kernel(const Evict
 
 cudaError_t launch_evict(EvictParams p, int row_bytes, int num_sms, cudaStream_t s) {
   const long long rows = (long long)p.num_reqs * p.num_kv_heads;
-  const long long chunks = (p.keep + kMoveRows - 1) / kMoveRows;
+  const long long chunks = (p.keep - 1) / kMoveRows + 1;
   if (rows > 0x7fffffffLL || rows * chunks > 0x7fffffffLL) return cudaErrorInvalidValue;
   // CTAs per (request, KV head): parts of at most 8192 keys, sixteen per thread,
   // as long as the grid leaves SMs idle (64 rows of 32768 keys, whole call: 43.3

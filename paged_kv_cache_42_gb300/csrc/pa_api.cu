@@ -735,9 +735,9 @@ pa_status weights_impl(const void* q, const void* k_cache, const int32_t* block_
   if (max_seq_len > (1 << 30)) return PA_ERR_UNSUPPORTED;  // key positions are 32-bit
   const WeightsLayout lay = weights_layout(num_reqs, num_tokens, num_q_heads, num_kv_heads,
                                            max_query_len, max_seq_len);
-  // grids and work lists are indexed with 32 bits
+  // grids and work lists (with some room for parts) are indexed with 32 bits
   const long long rh = (long long)num_reqs * num_kv_heads;
-  if (rh * (lay.padded_len / 128 + 1) >= (1LL << 31) ||
+  if (rh * (lay.padded_len / 128 + 1) >= (1LL << 31) - (1 << 14) ||
       (long long)lay.num_slots * num_kv_heads * 16 >= (1LL << 31))
     return PA_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < lay.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))

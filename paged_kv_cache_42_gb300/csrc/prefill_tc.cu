@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
         const bool unmasked = __all_sync(kAll, kv0 + 127 <= lim);
         // WIN: the row sees lo .. lim and the sinks; whole and empty runs of 32
         // columns are told apart, since a window has two edges to every item
-        const int lo = WIN ? lim - p.window + 1 : 0;
+        const int lo = WIN ? max(0, lim - p.window + 1) : 0;
         uint32_t whole = unmasked ? 15u : 0u, empty = 0u;  // bit c: columns 32 c .. 32 c + 31
         if constexpr (WIN) {
           whole = 0u;

@@ -51,6 +51,8 @@
 // the products' operands and the copies load shared memory for about 1250.
 #include <cuda.h>
 
+#include <cfloat>
+
 #include "pa_internal.h"
 #include "ptx.cuh"
 
@@ -74,7 +76,7 @@ constexpr int kMinPart = 8;          // Y tiles of a part in pass 1, at least (p
 constexpr int kMaxUnits = 512;       // pairs of pass 2 that may be cut: only few of them are
 constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = 1024;
-constexpr float kNone = -1e30f;      // a running maximum before the first key
+constexpr float kNone = -FLT_MAX;    // a running maximum before the first key
 
 struct Span {
   int q0, qlen, L;

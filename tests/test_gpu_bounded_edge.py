@@ -233,3 +233,65 @@ def test_attention_right_behind(pa_lib):
         torch.cuda.synchronize()
         for x, y in zip(got, want):
             assert torch.equal(x, y)
+
+
+def test_memory_of_the_calls_stream(pa_lib, monkeypatch):
+    """What a call on another stream allocates comes from that stream."""
+    from paged_kv_cache_42_gb300 import binding
+    b = ref.Batch([(300, 1), (40, 20)], 8, 2, 64, 11, extra_blocks=6)
+    g = b.gpu()
+    kw = {"max_query_len": b.max_q, "max_seq_len": b.max_len}
+    w = torch.rand(2, 2, b.mb * 16, device="cuda")
+    slots = torch.full((21,), -1, dtype=torch.int64, device="cuda")
+    kv = torch.zeros(21, 2, 64, dtype=torch.bfloat16, device="cuda")
+    new_tables = g["free"].view(2, 3).contiguous()
+    side, at = torch.cuda.Stream(), []
+    torch.cuda.synchronize()
+    empty = torch.empty
+
+    def spy(*args, **kwargs):
+        at.append(torch.cuda.current_stream() == side)
+        return empty(*args, **kwargs)
+    monkeypatch.setattr(torch, "empty", spy)
+    args = (g["q"], g["k"], g["v"], g["tables"], g["seq_lens"], g["qsl"], b.scale)
+    got = binding.attention_window(*args, window=50, sinks=4, **kw, stream=side)
+    binding.norm_rope_write_kv(g["q"], kv, kv, None, None, slots, g["k"], g["v"], stream=side)
+    binding.attention_weights(g["q"], g["k"], g["tables"], g["seq_lens"], g["qsl"], b.scale, w,
+                              **kw, stream=side)
+    binding.evict_kv(g["k"], g["v"], g["tables"], g["seq_lens"], w, new_tables, keep=40, recent=8,
+                     max_seq_len=b.max_len, stream=side)
+    monkeypatch.undo()
+    torch.cuda.synchronize()
+    assert at == [True] * 7
+    want = ref.window_attention(b.q, b.k, b.v, b.tables, b.seq_lens, b.qsl, b.scale, 50, 4)
+    assert (got.cpu().double() - want).abs().max() < 2e-2
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_decodes_with_scores_below_any_sentinel(pa_lib, d):
+    """Scores of -1e31 and less: key i of a request scores i + 1 times the first
+    key's, so the first key the token sees takes the whole weight."""
+    from paged_kv_cache_42_gb300 import binding
+    b = ref.Batch([(0, 1), (4, 1), (100, 1), (700, 1)], 4, 2, d, 3)
+    b.q.fill_(2.0 ** 50)
+    for r, (c, n) in enumerate(b.spans):
+        i = torch.arange(c + n)
+        # one or two bits each: exact in bf16, falling with the position
+        val = -(2.0 ** 50) * (1.0 + (i % 128) / 128.0) * 2.0 ** (i // 128)
+        b.k[b.tables[r].long()[i // 16], :, i % 16] = val.bfloat16()[:, None, None]
+    g = b.gpu()
+    kw = {"max_query_len": 1, "max_seq_len": b.max_len}
+    out = torch.full((4, 2, b.mb * 16), -7.0, device="cuda")
+    zero = torch.zeros_like(out)
+    binding.attention_weights(g["q"], g["k"], g["tables"], g["seq_lens"], g["qsl"], b.scale, zero,
+                              out=out, **kw)
+    got = binding.attention_window(g["q"], g["k"], g["v"], g["tables"], g["seq_lens"], g["qsl"],
+                                   b.scale, window=30, **kw).cpu()
+    for r, (c, n) in enumerate(b.spans):
+        L = c + n
+        want = torch.zeros(2, L)
+        want[:, 0] = 2.0  # both query heads of the KV head
+        assert torch.equal(out[r, :, :L].cpu(), want)
+        first = max(0, L - 30)
+        v = b.v[b.tables[r, first // 16], :, first % 16]
+        assert torch.equal(got[r], v.repeat_interleave(2, 0))
