@@ -88,8 +88,11 @@ __global__ void __launch_bounds__(kSelThreads) pa_evict_select_kernel(const Evic
   __shared__ int wsum[kSelWarps], wsum2[kSelWarps];
   __shared__ uint32_t s_pick[2];        // a pass's bin, and the tokens in the bins above it
   __shared__ uint32_t s_count[2];       // this CTA's tokens above the threshold, and at it
-  griddep_wait();               // a programmatic dependent of the grid before
-  griddep_launch_dependents();  // the move grid may take its place; it waits for this one
+  griddep_wait();  // a programmatic dependent of the grid before
+  // The move grid may take its place; it waits for this one. Without a move grid
+  // (no request is longer than `keep`) nothing may start early: a split-KV grid
+  // reads its lengths without waiting.
+  if (p.max_seq_len > p.keep) griddep_launch_dependents();
   const int C = p.cluster, rank = (int)(blockIdx.x % (unsigned)C);
   const int rh = (int)(blockIdx.x / (unsigned)C);
   const int r = rh / p.num_kv_heads, h = rh - r * p.num_kv_heads;
@@ -101,6 +104,7 @@ __global__ void __launch_bounds__(kSelThreads) pa_evict_select_kernel(const Evic
       report_error(p.err, PA_DEVERR_LENGTHS, r);
     else
       p.new_seq_lens[r] = L ? p.keep : __ldg(p.seq_lens + r);
+    __threadfence();  // as at the move grid's end
   }
   if (L == 0) return;
   const int a = p.sinks, n = L - p.recent - a, m = p.keep - p.sinks - p.recent;  // m of n stay

@@ -295,3 +295,32 @@ def test_decodes_with_scores_below_any_sentinel(pa_lib, d):
         first = max(0, L - 30)
         v = b.v[b.tables[r, first // 16], :, first % 16]
         assert torch.equal(got[r], v.repeat_interleave(2, 0))
+
+
+def test_lengths_of_an_eviction_that_cuts_nothing(pa_lib):
+    """Attention right behind an eviction reads the lengths it wrote, also where
+    no request is longer than `keep` (a single grid then, and no rows moved)."""
+    from paged_kv_cache_42_gb300 import binding
+    b = ref.Batch([(5 + 7 * i % 90, 1) for i in range(500)], 8, 8, 64, 41)
+    g = b.gpu()
+    R, keep = len(b.spans), 128
+    kw = {"max_query_len": 1, "max_seq_len": b.max_len}
+    args = (g["q"], g["k"], g["v"], g["tables"])
+    ws = torch.empty(binding.workspace_size(R, R, 8, 8, 64), dtype=torch.uint8, device="cuda")
+    want = binding.attention(*args, g["seq_lens"], g["qsl"], b.scale, workspace=ws, **kw)
+    w = torch.rand(R, 8, b.mb * 16, device="cuda")
+    new_tables = torch.zeros(R, 8, dtype=torch.int32, device="cuda")
+    new_lens = torch.empty(R, dtype=torch.int32, device="cuda")
+    kept = torch.empty(R, 8, keep, dtype=torch.int32, device="cuda")
+    new_w = torch.empty(R, 8, keep, device="cuda")
+    torch.cuda.synchronize()
+    binding.get_device_error(True)
+    for _ in range(50):
+        out = torch.empty_like(want)
+        new_lens.fill_(1)  # a length that every request may have
+        binding.evict_kv(g["k"], g["v"], g["tables"], g["seq_lens"], w, new_tables, keep=keep,
+                         recent=8, max_seq_len=b.max_len, new_seq_lens=new_lens, kept=kept,
+                         new_weights=new_w)
+        binding.attention(*args, new_lens, g["qsl"], b.scale, workspace=ws, out=out, **kw)
+        assert torch.equal(out, want)
+    assert binding.get_device_error(True)[0] == 0
