@@ -324,3 +324,54 @@ def test_lengths_of_an_eviction_that_cuts_nothing(pa_lib):
         binding.attention(*args, new_lens, g["qsl"], b.scale, workspace=ws, out=out, **kw)
         assert torch.equal(out, want)
     assert binding.get_device_error(True)[0] == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_two_graphs_share_a_workspace(pa_lib, fp8):
+    """Captured windows and weights of two batches, one workspace, replayed in
+    turn: no call depends on what another left there."""
+    from paged_kv_cache_42_gb300 import binding
+    batches = [ref.Batch([(900, 300), (40, 1), (0, 20)], 32, 8, 128, 50, fp8=fp8),
+               ref.Batch([(33, 1), (2100, 1), (5, 130), (16, 0), (700, 3)], 32, 8, 128, 51, fp8=fp8)]
+    size = max(max(binding.workspace_size(len(b.spans), len(b.q), 32, 8, 128),
+                   binding.weights_workspace_size(len(b.spans), len(b.q), 32, 8, 128, b.max_q,
+                                                  b.max_len)) for b in batches)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    steps, alive = [], []
+    for b in batches:
+        g = b.gpu()
+        o = torch.zeros_like(g["q"])
+        w = torch.zeros(len(b.spans), 8, b.mb * 16, device="cuda")
+        wo = torch.zeros_like(w)
+
+        def step(b=b, g=g, o=o, w=w, wo=wo):
+            kw = {"max_query_len": b.max_q, "max_seq_len": b.max_len, "workspace": ws}
+            meta = (g["tables"], g["seq_lens"], g["qsl"], b.scale)
+            if fp8:
+                binding.attention_window_fp8(g["q"], g["k"], g["v"], *meta, b.k_scale, b.v_scale,
+                                             window=200, sinks=4, out=o, **kw)
+                binding.attention_weights_fp8(g["q"], g["k"], *meta, b.k_scale, w, out=wo, **kw)
+            else:
+                binding.attention_window(g["q"], g["k"], g["v"], *meta, window=200, sinks=4, out=o,
+                                         **kw)
+                binding.attention_weights(g["q"], g["k"], *meta, w, out=wo, **kw)
+        step()
+        torch.cuda.synchronize()
+        want = o.clone(), wo.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        steps.append((graph, o, wo, want))
+        alive.append(step)  # the graph's inputs
+    for i in (0, 1, 1, 0, 0, 1):
+        graph, o, wo, want = steps[i]
+        o.zero_()
+        wo.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(wo, want[1])
+    for i in (0, 1) * 4:  # and with nothing between the replays
+        steps[i][0].replay()
+    torch.cuda.synchronize()
+    for _, o, wo, want in steps:
+        assert torch.equal(o, want[0]) and torch.equal(wo, want[1])
