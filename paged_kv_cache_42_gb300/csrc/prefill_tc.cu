@@ -67,6 +67,9 @@ namespace pa {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
+// A softmax reference of more than this (base-2 units) is subtracted before the
+// scale: below it the rounding of its product moves P by a factor of at most 2^(2^-15).
+constexpr float kFar = 1024.f;
 
 // Threads per S row in the softmax (1 or 2). With 2, the two threads of a row
 // take 64 score columns each and combine their row maxima through shared
@@ -224,8 +227,8 @@ __device__ __forceinline__ int snake_item(int r, int g) {
 // sees (win_tiles: the sinks', then the windows'), every row masks its own
 // keys, and a block that no row sees is not read at all - its table entry may
 // be stale - and counts as zeros in V. A row may see no key of its item's
-// first tiles; its running maximum then starts at a finite floor, so that the
-// first tile it does see rescales a zero O by zero.
+// first tiles: it has no reference then, and the first tile it does see
+// rescales a zero O by zero.
 template <int D, int G, bool PREFIX, bool F8, bool WIN>
 __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
     pa_prefill_kernel(const __grid_constant__ PrefillParams p) {
@@ -362,7 +365,10 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
     }
   } else if (warp == 1) {
     // ======================= MMA issuer =======================
-    constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128, false);
+    // a negative scale: S = -Q K^T under its absolute value, so that the largest
+    // raw score is the largest scaled one
+    const uint32_t idesc_qk =
+        idesc_bf16_f32(128, 128, false) | (p.scale_log2 < 0.f ? kIdescNegateA : 0u);
     constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, true);
     // Shared-memory descriptors differ only in their start address field
     // (address >> 4), so each MMA takes a base descriptor plus a constant.
@@ -516,7 +522,14 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
         j = tl.j0 + rt * C::TOK + m / G;  // chunk token of this row
         lim = min(ctx + j, L - 1);        // last key this row may see
       }
-      float m_used = -INFINITY, l = 0.f;
+      // m_raw is the largest raw score so far, m_used that times the scale (-inf:
+      // no key seen). P = exp2(score x scale - m_used) takes one FMA, exact but for
+      // the rounding of m_used: a factor common to all of a row's P. `far`: it
+      // could overflow P (kFar) in some row of the warp; the raw differences are
+      // then taken first, and the largest P is 1 whatever the scores' size.
+      const float sc = fabsf(p.scale_log2);
+      float m_used = -INFINITY, m_raw = -INFINITY, l = 0.f;
+      bool far = false;
       for (int i = 0; i < tl.n; ++i) {
         // S_rt(i) complete implies every earlier MMA is too: O_rt is stable
         // and P_rt(i-1) has been consumed.
@@ -561,36 +574,63 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
         }
         mx = exchange(mx, true, ok);         // the whole row's max
         if (!ok) break;
-        const float mt = mx * p.scale_log2;  // -inf stays -inf
+        // A tile of which the row sees no key (mx = -inf) changes nothing.
+        const bool blind = mx == -INFINITY;
+        const float mt = blind ? mx : mx * sc;
+        const float was = m_used, was_raw = m_raw;
         float alpha = 1.f;
         bool resc = false;
         if (i == 0) {
-          m_used = mt;  // the item's first key is always visible: finite
-          if constexpr (WIN) m_used = fmaxf(mt, -1e30f);
+          m_used = mt;
+          m_raw = mx;
         } else if (mt > m_used + 8.f) {
           alpha = exp2f(m_used - mt);
           m_used = mt;
+          m_raw = mx;
           resc = true;
         }
-        if (__any_sync(kAll, resc)) {
+        const bool now_far = fabsf(mt) > kFar && !blind;
+        if (__any_sync(kAll, resc || now_far)) {
+          far = far || __any_sync(kAll, now_far);
+          if (far && i > 0) {  // the same by the raw scores, whose products may round alike
+            const bool none = was == -INFINITY;
+            resc = !blind && (none || (mx - was_raw) * sc > 8.f);
+            alpha = !resc ? 1.f : none ? 0.f : exp2f((was_raw - mx) * sc);
+            m_used = resc ? mt : was;
+            m_raw = resc ? mx : was_raw;
+          }
+          if (__any_sync(kAll, resc)) {
 #pragma unroll 1
-          for (int oc = 0; oc < OCH; ++oc) {
-            const int c = hf * OCH + oc;
-            uint32_t o[32];
-            tmem_ld32(o_addr + c * 32, o);
+            for (int oc = 0; oc < OCH; ++oc) {
+              const int c = hf * OCH + oc;
+              uint32_t o[32];
+              tmem_ld32(o_addr + c * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st32(o_addr + c * 32, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        l *= alpha;
+        if (far) {  // S - m_raw in the place of S
+#pragma unroll 1
+          for (int cc = 0; cc < C::CPH; ++cc) {
+            const uint32_t at = s_addr + (hf * C::CPH + cc) * 32;
+            uint32_t r[32];
+            tmem_ld32(at, r);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st32(o_addr + c * 32, o);
+            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) - m_raw);
+            tmem_st32(at, r);
           }
           tmem_wait_st();
         }
-        l *= alpha;
         // pass 2: P = exp2(s * scale - m) as bf16 pairs, written over this
         // thread's own S columns: chunk c's 16 P columns start at pcol(c),
         // which only covers S columns this thread has already read.
-        const float nm = -m_used;
-        const float sc = p.scale_log2;
+        const float nm = far ? 0.f : -m_used;
         float l2[2] = {0.f, 0.f};  // two partial sums: shorter dependency chains
 #pragma unroll 1
         for (int cc = 0; cc < C::CPH; ++cc) {

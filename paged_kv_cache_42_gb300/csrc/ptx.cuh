@@ -354,6 +354,9 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo
   return d;
 }
 
+// Instruction descriptor bit: the product takes -A for A.
+constexpr uint32_t kIdescNegateA = 1u << 13;
+
 // Instruction descriptor, kind::f16 with bf16 A/B and fp32 D.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool b_mn_major) {
   return (1u << 4)                      // D format: f32
