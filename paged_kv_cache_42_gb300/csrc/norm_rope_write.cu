@@ -20,8 +20,8 @@
 // Layout of the work. A lane holds 4 pairs of one head: elements 4i .. 4i + 3
 // and their partners R / 2 further on (two 8-byte loads), or 8 consecutive
 // elements when interleaved (one 16-byte load). A rotation is then arithmetic
-// within the lane, on 4 cosines and 4 sines; elements past R pair up the same
-// way under the angle zero. A head is D / 8 lanes, a warp 2 (D = 128) or 4
+// within the lane, on 4 cosines and 4 sines; elements past R go four and four
+// the same way and are left alone. A head is D / 8 lanes, a warp 2 (D = 128) or 4
 // (D = 64) heads, a norm's sum 4 or 3 shuffles. A warp takes ITER such groups
 // of heads of ONE token and ONE kind (queries, K or V): their loads are all in
 // flight together, before anything depends on the position; the token's
@@ -29,6 +29,8 @@
 // V skips the arithmetic. 2048 tokens of 32 + 8 + 8 heads of 128 take 12.5 us,
 // 4.1 TB/s; 2, 6 or 8 groups a warp 13.8, 13.6 and 14.5 us, and units that mix
 // the kinds 13.6 us (more instructions: the choice is made per head).
+#include <type_traits>
+
 #include "pa_internal.h"
 #include "ptx.cuh"
 
@@ -90,8 +92,10 @@ __device__ __forceinline__ uint2 pack_e4m3(const Pairs& v, float scale) {
                     two(v.x[2].x, v.x[2].y) | two(v.x[3].x, v.x[3].y) << 16);
 }
 
+// At least nine CTAs on an SM into a bf16 cache (56 registers): 2048 tokens 12.1
+// us, with 64 registers and eight of them 13.2. The E4M3 form does not fit 56.
 template <int D, bool F8, bool INTER, int ITER>
-__global__ void __launch_bounds__(kThreads) pa_norm_rope_write_kernel(const NormRopeParams p) {
+__global__ void __launch_bounds__(kThreads, F8 ? 8 : 9) pa_norm_rope_write_kernel(const NormRopeParams p) {
   constexpr int LPH = D / 8;     // lanes per head
   constexpr int HPG = 32 / LPH;  // heads per group
   const int lane = threadIdx.x & 31;
@@ -188,8 +192,7 @@ __global__ void __launch_bounds__(kThreads) pa_norm_rope_write_kernel(const Norm
     __threadfence();
     return;
   }
-  float2 c[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)};  // of this lane's pairs
-  float2 s[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  float2 c[2] = {}, s[2] = {};  // of this lane's pairs
   if (turned) {
     const float* const cs = p.cos_sin + (long long)pos * p.rotary_dim + sub * 4;
     const float4 cv = __ldg(reinterpret_cast<const float4*>(cs));
@@ -199,39 +202,47 @@ __global__ void __launch_bounds__(kThreads) pa_norm_rope_write_kernel(const Norm
     s[0] = make_float2(sv.x, sv.y);
     s[1] = make_float2(sv.z, sv.w);
   }
-  const Pairs wv = unpack<INTER>(rw);
+  auto heads = [&](auto normed) {
+    constexpr bool NORM = decltype(normed)::value;
+    const Pairs wv = unpack<INTER>(rw);
 #pragma unroll
-  for (int i = 0; i < ITER; ++i) {
-    const int row = row0 + i * HPG;
-    Pairs v = unpack<INTER>(raw[i]);
-    if (w != nullptr) {
-      // the head's sum of squares (every lane of the warp takes the shuffles)
-      float2 sq = fmul2(v.x[0], v.x[0]);
+    for (int i = 0; i < ITER; ++i) {
+      const int row = row0 + i * HPG;
+      Pairs v = unpack<INTER>(raw[i]);
+      if constexpr (NORM) {
+        // the head's sum of squares (every lane of the warp takes the shuffles)
+        float2 sq = fmul2(v.x[0], v.x[0]);
 #pragma unroll
-      for (int e = 1; e < 4; ++e) sq = ffma2(v.x[e], v.x[e], sq);
-      float ss = sq.x + sq.y;
+        for (int e = 1; e < 4; ++e) sq = ffma2(v.x[e], v.x[e], sq);
+        float ss = sq.x + sq.y;
 #pragma unroll
-      for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(kAll, ss, o);
-      const float r = rsqrtf(ss * (1.f / D) + p.eps);
+        for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(kAll, ss, o);
+        const float r = rsqrtf(ss * (1.f / D) + p.eps);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v.x[e] = fmul2(fmul2(v.x[e], make_float2(r, r)), wv.x[e]);
+        for (int e = 0; e < 4; ++e) v.x[e] = fmul2(fmul2(v.x[e], make_float2(r, r)), wv.x[e]);
+      }
+      if (row >= rows) continue;
+      if (turned) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 a = v.x[e], b = v.x[2 + e];
+          const float2 ns = make_float2(-s[e].x, -s[e].y);
+          v.x[e] = ffma2(b, ns, fmul2(a, c[e]));
+          v.x[2 + e] = ffma2(a, s[e], fmul2(b, c[e]));
+        }
+      }
+      if (F8 && kind == 1) {
+        store8(p.k_cache, row, pack_e4m3<INTER>(v, p.k_scale));
+      } else {
+        // neither normalised nor turned: the bits as they came, a NaN's too
+        store(kind == 0 ? p.q_out : p.k_cache, row, NORM || turned ? pack<INTER>(v) : raw[i]);
+      }
     }
-    if (row >= rows) continue;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float2 a = v.x[e], b = v.x[2 + e];
-      const float2 ns = make_float2(-s[e].x, -s[e].y);
-      v.x[e] = ffma2(b, ns, fmul2(a, c[e]));
-      v.x[2 + e] = ffma2(a, s[e], fmul2(b, c[e]));
-    }
-    if (kind == 0) {
-      store(p.q_out, row, pack<INTER>(v));
-    } else if constexpr (F8) {
-      store8(p.k_cache, row, pack_e4m3<INTER>(v, p.k_scale));
-    } else {
-      store(p.k_cache, row, pack<INTER>(v));
-    }
-  }
+  };
+  if (w != nullptr)
+    heads(std::true_type{});
+  else
+    heads(std::false_type{});
   // The split-KV kernel that follows may be a programmatic dependent that
   // reads q without waiting for this grid's flush. This grid never releases a
   // dependent early (that happens when its last CTA ends), and the fence has
