@@ -348,7 +348,11 @@ pa_status pa_attention_window_fp8(const void* q, const void* k_cache, const void
  * The other arguments are pa_attention's, and so are the limits (head_dim 64 or
  * 128, groups of 1, 2, 4 or 8; num_blocks >= 1) and the errors. A request longer than
  * weights_stride sets PA_DEVERR_LENGTHS and is skipped. Scores and sums are
- * binary32; results do not depend on the order in which CTAs run.
+ * binary32; results do not depend on the order in which CTAs run. In spans of
+ * more than 8 rows (tokens x G) so is a row's log-sum-exp, whose rounding its
+ * weights take over: a relative error of |lse| x 2^-24, so scores there should
+ * stay below some 10^4. A NaN or an infinity in a query or in a key makes NaN
+ * of the weights of every key that the row, or a row that sees the key, sees.
  */
 size_t pa_attention_weights_workspace_size(int num_reqs, int num_tokens, int num_q_heads,
                                            int num_kv_heads, int head_dim, int max_query_len,

@@ -421,7 +421,7 @@ struct WeightsParams {
   int* counts;
   int* counters;
   int4* items[2];
-  float* neg_lse;  // minus the log2-sum-exp of every row, -inf for rows past a span
+  float* neg_lse;  // minus the log2-sum-exp of every row
   float2* partial;
   float* sums;
   unsigned long long* err;

@@ -1175,6 +1175,8 @@ __global__ void __launch_bounds__(WCfg<D, F8>::ALL_THREADS, 1)
       if (PASS == 1) {
         const float k = fmaxf(mx, o.x);
         l = l * ex2_approx(mx - k) + o.y * ex2_approx(o.x - k);
+        // A row past the span leaves anything (no key takes it); one with a NaN or an
+        // infinity among its scores a NaN, which reaches every key that it sees.
         if (xt * TOK >= w.qlen) continue;  // the pair's second tile is past the span
         const int slot = w.q0 / TOK + w.r + xt;
         const size_t at = ((size_t)w.h * p.num_slots + slot) * 128 + m;
@@ -1189,10 +1191,9 @@ __global__ void __launch_bounds__(WCfg<D, F8>::ALL_THREADS, 1)
             sum = sum * ex2_approx(top - t2) + v.y * ex2_approx(v.x - t2);
             top = t2;
           }
-          // rows past the span: -inf, a weight of zero
-          p.neg_lse[at] = sum > 0.f ? -(top + log2f(sum)) : -INFINITY;
+          p.neg_lse[at] = -(top + log2f(sum));
         } else {
-          p.neg_lse[at] = l > 0.f ? -(k + log2f(l)) : -INFINITY;
+          p.neg_lse[at] = -(k + log2f(l));
         }
       } else {
         l += o.y;

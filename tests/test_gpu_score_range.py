@@ -84,3 +84,58 @@ def test_chunks_with_scores_below_any_sentinel(pa_lib, hq, hkv, d, rising):
         for out, key in ((full, p * rising), (got, p if rising else (p - 29).clamp(min=0))):
             v = b.v[b.tables[r].long()[key // 16], :, key % 16]
             assert torch.equal(out[rows], v.repeat_interleave(hq // hkv, 1)), r
+
+
+def add_weights(b, **kw):
+    """One step's weights over zeros, in place: [R, Hkv, width] on the CPU."""
+    from paged_kv_cache_42_gb300 import binding
+    g = b.gpu()
+    w = torch.zeros(len(b.spans), b.hkv, b.mb * 16, device="cuda")
+    args = (g["q"], g["k"], g["tables"], g["seq_lens"], g["qsl"], b.scale)
+    kw = {"max_query_len": b.max_q, "max_seq_len": b.max_len, **kw}
+    got = binding.attention_weights_fp8(*args, b.k_scale, w, **kw) if b.fp8 else \
+        binding.attention_weights(*args, w, **kw)
+    torch.cuda.synchronize()
+    assert binding.get_device_error(True)[0] == 0
+    return got.cpu()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("hq,hkv,d,scale", [(4, 2, 64, -0.1), (8, 2, 128, 0.0), (16, 2, 128, -0.1),
+                                            (16, 2, 64, 0.0), (4, 4, 128, 1.5)])
+def test_weights_with_a_scale_of_any_sign_and_size(pa_lib, hq, hkv, d, scale, fp8):
+    """The relative error of a weight is the absolute one of its exponent: with
+    |score| up to 6 sqrt(d) x 1.5 x log2 e < 150, 2^-23 x 150 for the product and
+    as much for the log-sum-exp, below 2^-14 with the exponentials'."""
+    spans = [(300, 1), (37, 5), (0, 300), (1000, 200), (130, 16)]
+    b = ref.Batch(spans, hq, hkv, d, 31, fp8=fp8)
+    b.scale = scale
+    zero = torch.zeros(len(spans), hkv, b.mb * 16)
+    want = ref.attention_weights(b.q, b.k, b.tables, b.seq_lens, b.qsl, scale, zero, zero, b.k_scale)
+    got = add_weights(b)
+    tiny = 2.0 ** -120  # weights below binary32's range
+    assert ((got.double() - want).abs() <= want * 2.0 ** -14 + tiny).all()
+
+
+@pytest.mark.parametrize("where", ["key", "query"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("hq,hkv,d,c,n", [(4, 2, 64, 100, 1), (8, 2, 128, 100, 2), (8, 2, 128, 100, 300),
+                                          (4, 1, 64, 5, 140), (8, 1, 128, 3000, 200)])
+def test_a_bad_row_spoils_the_keys_it_sees(pa_lib, hq, hkv, d, c, n, value, where):
+    """A NaN or an infinity in a new token's query spoils the weights of all keys
+    the token sees; one in a key those of every key that a row seeing it sees.
+    Other KV heads, and keys seen by good rows only, keep theirs."""
+    b = ref.Batch([(c, n), (50, min(n, 40))], hq, hkv, d, 9)
+    b.q[..., 3] = b.q[..., 3].abs() + 0.5  # an infinite key scores plus infinity
+    clean = add_weights(b)
+    at = c + n // 2  # position of the token, and of the key
+    if where == "query":
+        b.q[n // 2, 0, 3] = value  # a query head of KV head 0
+    else:
+        b.k[b.tables[0, at // 16], 0, at % 16, 3] = value
+    got = add_weights(b)
+    last = at if where == "query" else c + n - 1  # keys up to here are seen by a bad row
+    assert torch.isnan(got[0, 0, :last + 1]).all()
+    want = clean.clone()
+    want[0, 0, :last + 1] = got[0, 0, :last + 1]
+    assert torch.equal(got.view(torch.int32), want.view(torch.int32))
