@@ -569,6 +569,8 @@ def run_ours(args, rank, world, local, dist):
         binding.set_option("decode_tm_ctas_per_sm", args.tm_ctas_per_sm)
     if args.mixed_prefill_ctas:
         binding.set_option("mixed_prefill_ctas", args.mixed_prefill_ctas)
+    # every attention call here directly follows the KV write of its step
+    binding.set_option("write_overlap", 1)
     props = torch.cuda.get_device_properties(local)
     l2 = int(getattr(props, "L2_cache_size", 128 << 20) or (128 << 20))
     flush_buf = torch.empty(2 * l2, dtype=torch.uint8, device="cuda")

@@ -166,11 +166,16 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
 
   // The work list: from the planner (the preceding grid), or - for a
   // decode-only batch (every span at most one token) - built by this CTA from
-  // query_start_loc and seq_lens, without waiting for any earlier grid.
+  // query_start_loc and seq_lens; with early_start before any earlier grid is
+  // waited for, else after.
   const UnitInfo* units = p.units;
   int W, K;
   bool waited = false;  // lane 0: griddepcontrol.wait done (plan, KV write visible)
   if (p.self_plan) {
+    if (!p.early_start) {
+      griddep_wait();
+      waited = true;
+    }
     UnitInfo* const su = reinterpret_cast<UnitInfo*>(smem + WARPS * WS::BYTES);
     __shared__ int s_tot[WARPS];
     const int R = p.num_reqs, T = p.num_tokens, Hkv_ = p.num_kv_heads;

@@ -302,12 +302,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // The work list: from the planner (the preceding grid), or - for a
-  // decode-only batch - built here from query_start_loc and seq_lens without
-  // waiting for any earlier grid. A unit without keys keeps len 0.
+  // decode-only batch - built here from query_start_loc and seq_lens, with
+  // early_start before any earlier grid is waited for, else after. A unit
+  // without keys keeps len 0.
   const UnitInfo* units = p.units;
   int W, K;
   bool waited = false;  // griddepcontrol.wait done (the plan and the KV write are visible)
   if (p.self_plan) {
+    if (!p.early_start) {
+      griddep_wait();
+      waited = true;
+    }
     UnitInfo* const su = reinterpret_cast<UnitInfo*>(gb + M::OFF_UNITS);
     __shared__ int s_tot[kWarps];
     const int R = p.num_reqs, T = p.num_tokens, Hkv_ = p.num_kv_heads;
@@ -1091,6 +1096,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int G>
 __global__ void __launch_bounds__(256) pa_qsplit_kernel(const DecodeParams p) {
   griddep_launch_dependents();  // the split-KV grid may start its prologue
+  if (!p.early_start) griddep_wait();  // the grid before may have made q
   const int grp = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (grp < p.num_tokens * p.num_kv_heads) {
 #pragma unroll

@@ -195,10 +195,12 @@ __global__ void __launch_bounds__(kTmThreads, CPS)
   }
 
   // The work list: the planner's (one unit per token, positions = its
-  // blocks), or built here for a decode-only batch.
+  // blocks), or built here for a decode-only batch (with early_start before any
+  // earlier grid is waited for, else after).
   const UnitInfo* units = p.units;
   int W, K;
   if (p.self_plan) {
+    if (!p.early_start) griddep_wait();
     UnitInfo* const su = reinterpret_cast<UnitInfo*>(gb + L::OFF_UNITS);
     __shared__ int s_tot[kTmThreads / 32];
     const int R = p.num_reqs, T = p.num_tokens;
@@ -316,10 +318,10 @@ __global__ void __launch_bounds__(kTmThreads, CPS)
       }
     }
     // The split query rows and scales, and the K/V write before them, come
-    // from the preceding grids: a planned batch waited for them at the top; a
-    // self-planned one waits below, after the K/V copies of its first two
-    // tiles that the write does not touch.
-    bool waited = !p.self_plan;
+    // from the preceding grids: waited for at the top, or, with early_start in
+    // a self-planned batch, below, after the K/V copies of its first two tiles
+    // that the write does not touch.
+    bool waited = !(p.self_plan && p.early_start);
 
     struct Meta {
       TmRec r;

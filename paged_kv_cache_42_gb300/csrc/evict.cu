@@ -89,10 +89,7 @@ __global__ void __launch_bounds__(kSelThreads) pa_evict_select_kernel(const Evic
   __shared__ uint32_t s_pick[2];        // a pass's bin, and the tokens in the bins above it
   __shared__ uint32_t s_count[2];       // this CTA's tokens above the threshold, and at it
   griddep_wait();  // a programmatic dependent of the grid before
-  // The move grid may take its place; it waits for this one. Without a move grid
-  // (no request is longer than `keep`) nothing may start early: a split-KV grid
-  // reads its lengths without waiting.
-  if (p.max_seq_len > p.keep) griddep_launch_dependents();
+  griddep_launch_dependents();  // the move grid may take its place; it waits for this one
   const int C = p.cluster, rank = (int)(blockIdx.x % (unsigned)C);
   const int rh = (int)(blockIdx.x / (unsigned)C);
   const int r = rh / p.num_kv_heads, h = rh - r * p.num_kv_heads;
@@ -104,7 +101,6 @@ __global__ void __launch_bounds__(kSelThreads) pa_evict_select_kernel(const Evic
       report_error(p.err, PA_DEVERR_LENGTHS, r);
     else
       p.new_seq_lens[r] = L ? p.keep : __ldg(p.seq_lens + r);
-    __threadfence();  // as at the move grid's end
   }
   if (L == 0) return;
   const int a = p.sinks, n = L - p.recent - a, m = p.keep - p.sinks - p.recent;  // m of n stay
@@ -335,7 +331,6 @@ __global__ void __launch_bounds__(kMoveThreads) pa_evict_move_kernel(const Evict
       vc[dst * VPR + e % VPR] = vv[i];
     }
   }
-  __threadfence();  // performed before the CTA ends: the next grid may be a programmatic one
 }
 
 }  // namespace

@@ -189,7 +189,6 @@ __global__ void __launch_bounds__(kThreads, F8 ? 8 : 9) pa_norm_rope_write_kerne
       else
         store(p.v_cache, row, raw[i]);
     }
-    __threadfence();
     return;
   }
   float2 c[2] = {}, s[2] = {};  // of this lane's pairs
@@ -243,11 +242,6 @@ __global__ void __launch_bounds__(kThreads, F8 ? 8 : 9) pa_norm_rope_write_kerne
     heads(std::true_type{});
   else
     heads(std::false_type{});
-  // The split-KV kernel that follows may be a programmatic dependent that
-  // reads q without waiting for this grid's flush. This grid never releases a
-  // dependent early (that happens when its last CTA ends), and the fence has
-  // every store performed at the GPU's scope before its CTA ends.
-  __threadfence();
 }
 
 template <int D, bool F8, bool INTER>

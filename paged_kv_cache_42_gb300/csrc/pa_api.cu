@@ -45,6 +45,7 @@ std::atomic<int> g_mixed_overlap{1};  // pa_set_option(PA_OPT_MIXED_OVERLAP, ...
 std::atomic<int> g_token_major{1};  // pa_set_option(PA_OPT_DECODE_TOKEN_MAJOR, ...)
 std::atomic<int> g_cascade_overlap{1};  // pa_set_option(PA_OPT_CASCADE_OVERLAP, ...)
 std::atomic<int> g_tm_ctas{2};  // pa_set_option(PA_OPT_DECODE_TM_CTAS_PER_SM, ...)
+std::atomic<int> g_write_overlap{0};  // pa_set_option(PA_OPT_WRITE_OVERLAP, ...)
 std::atomic<int> g_mixed_ctas{0};  // pa_set_option(PA_OPT_MIXED_PREFILL_CTAS, ...): 0 = planned
 constexpr int kNumTimers = 8;  // write, plan, decode, prefill, cascade prefix, merge, weights, evict
 cudaEvent_t g_timer_start[kNumTimers] = {};
@@ -402,9 +403,10 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
   pp.block_tables = block_tables;
   pp.prefix_blocks = prefix_len / kBlockSize;
   // a decode-only batch (every span at most one token) plans itself inside
-  // the split-KV kernel: no planner launch, and the kernel overlaps the KV write
+  // the split-KV kernel: no planner launch
   const int self_plan = (g_self_plan.load() && prefix_len == 0 && max_query_len <= 1 &&
                          num_reqs <= kSelfPlanMaxReqs) ? 1 : 0;
+  pp.early_start = g_write_overlap.load();
   pp.early_trigger = prefix_len > 0 ? 1 : 0;
   pp.num_reqs = num_reqs;
   pp.num_tokens = num_tokens;
@@ -549,6 +551,7 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
   dp.prefix_chunks = chunks;
   dp.num_tokens = num_tokens;
   dp.self_plan = self_plan;
+  dp.early_start = pp.early_start;
   dp.num_reqs = num_reqs;
   dp.max_blocks_per_req = max_blocks_per_req;
   dp.max_query_len = max_query_len;
@@ -993,6 +996,10 @@ pa_status pa_set_option(int option, int value) {
     case PA_OPT_MIXED_PREFILL_CTAS:
       if (value < 0) return PA_ERR_INVALID_ARG;
       g_mixed_ctas.store(value);
+      return PA_OK;
+    case PA_OPT_WRITE_OVERLAP:
+      if (value != 0 && value != 1) return PA_ERR_INVALID_ARG;
+      g_write_overlap.store(value);
       return PA_OK;
     case PA_OPT_MIXED_OVERLAP:
       g_mixed_overlap.store(value ? 1 : 0);

@@ -217,6 +217,7 @@ struct PlanParams {
   const int32_t* seq_lens;
   const int32_t* block_tables;  // read only for the cascade prefix check
   int prefix_blocks;            // cascade: blocks of the common prefix; 0 otherwise
+  int early_start;              // PA_OPT_WRITE_OVERLAP: plan before waiting for the grid before
   int early_trigger;            // release the next grid at the top (it needs no plan at first)
   int num_reqs, num_tokens, num_kv_heads, max_blocks_per_req, max_query_len, max_seq_len;
   int group;        // G = Hq / Hkv
@@ -289,6 +290,9 @@ struct DecodeParams {
   // self-planned decode-only batch: the kernel builds its unit table from these
   // and its first CTA publishes the position count (header_out) for the merge pass
   int self_plan, num_reqs, max_blocks_per_req, max_query_len, max_seq_len;
+  // PA_OPT_WRITE_OVERLAP: a self-planned kernel (and the E4M3 query split) reads
+  // all but the newest keys before it waits for the grid before
+  int early_start;
   const int32_t* qsl;
   const int32_t* seq_lens;
   WsHeader* header_out;

@@ -56,6 +56,9 @@ __device__ __forceinline__ long long block_exclusive_scan(long long v, long long
 constexpr int kTileBuckets = 512;  // tiles sorted by key-tile count, longest first
 
 __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
+  // The lengths and tables may come from the grid before, and so may what the
+  // cascade prefix pass reads, which this grid lets start next.
+  if (!p.early_start) griddep_wait();
   // When the next grid has work that needs no plan (the cascade prefix
   // pass), let it start now; a grid that would only wait at its top for the
   // plan is released at the end of this one instead (starting it early
@@ -268,9 +271,9 @@ cudaError_t launch_plan(const PlanParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  // Launched as a programmatic dependent of the previous grid (normally the
-  // KV write): it needs none of its output and overlaps it, and waits for it
-  // before completing.
+  // Launched as a programmatic dependent of the previous grid, which it waits
+  // for at its start; with early_start (the KV write, which makes nothing that
+  // a plan needs) before completing.
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(1);
   // A batch with no tensor-core work needs no bucket sort: a block sized to the

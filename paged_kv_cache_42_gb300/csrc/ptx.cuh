@@ -132,6 +132,9 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 }
 
 // ---- programmatic dependent launch ------------------------------------------
+// What a grid reads before its griddep_wait() must be older than the grid
+// before it, and that grid must have waited for its own predecessors before it
+// released this one: only a wait makes a grid's results visible, not its end.
 __device__ __forceinline__ void griddep_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

@@ -443,7 +443,6 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 2) pa_weights_cluster_kern
     out[key] = was + a;
   }
   if (p.num_slots > 0) griddep_wait();
-  __threadfence();  // performed before the CTA ends: the next grid may be a programmatic one
 }
 
 // Few rows of sequences whose scores outgrow a cluster's shared memory: scores
@@ -613,7 +612,6 @@ __global__ void __launch_bounds__(kFinishThreads) pa_weights_finish_kernel(const
     if (k0 + 2 * kFinishRound < last) load(k0 + 2 * kFinishRound, ra);
     finish(k0 + kFinishRound, rb);
   }
-  __threadfence();  // performed before the CTA ends: the next grid may be a programmatic one
 }
 
 // ---------------------------------------------------------------------------------------
@@ -1248,7 +1246,6 @@ __global__ void __launch_bounds__(WCfg<D, F8>::ALL_THREADS, 1)
       }
     }
   }
-  __threadfence();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
