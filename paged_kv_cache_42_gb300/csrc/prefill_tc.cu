@@ -57,6 +57,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <cfloat>
 #include <mutex>
 
 #include "pa_internal.h"
@@ -144,7 +145,11 @@ struct PrefillParams {
   const WsHeader* header;
   const PrefillTile* tiles;
   int bt_stride, num_q_heads, num_kv_heads, num_blocks;
+  // A negative scale: S = -Q K^T (idesc_qk) under its absolute value, so that the
+  // largest raw score is the largest scaled one. A scale of zero becomes the
+  // smallest number: -inf times it stays -inf.
   float scale_log2;
+  uint32_t idesc_qk;
   // cascade prefix pass
   int num_tokens, prefix_len, prefix_chunks, prefix_pairs, slot_floats;
   float* prefix_partials;
@@ -365,10 +370,6 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
     }
   } else if (warp == 1) {
     // ======================= MMA issuer =======================
-    // a negative scale: S = -Q K^T under its absolute value, so that the largest
-    // raw score is the largest scaled one
-    const uint32_t idesc_qk =
-        idesc_bf16_f32(128, 128, false) | (p.scale_log2 < 0.f ? kIdescNegateA : 0u);
     constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, true);
     // Shared-memory descriptors differ only in their start address field
     // (address >> 4), so each MMA takes a base descriptor plus a constant.
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const int off = ((ks / 4) * C::CHUNK + (ks % 4) * 32) >> 4;
-            umma_bf16(d, a0 + off, b0 + off, idesc_qk, ks > 0 ? 1u : 0u);
+            umma_bf16(d, a0 + off, b0 + off, p.idesc_qk, ks > 0 ? 1u : 0u);
           }
           umma_commit(BAR(B_S_FULL + rt));
           if (rt == 1) {
@@ -527,7 +528,6 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
       // the rounding of m_used: a factor common to all of a row's P. `far`: it
       // could overflow P (kFar) in some row of the warp; the raw differences are
       // then taken first, and the largest P is 1 whatever the scores' size.
-      const float sc = fabsf(p.scale_log2);
       float m_used = -INFINITY, m_raw = -INFINITY, l = 0.f;
       bool far = false;
       for (int i = 0; i < tl.n; ++i) {
@@ -575,8 +575,7 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
         mx = exchange(mx, true, ok);         // the whole row's max
         if (!ok) break;
         // A tile of which the row sees no key (mx = -inf) changes nothing.
-        const bool blind = mx == -INFINITY;
-        const float mt = blind ? mx : mx * sc;
+        const float mt = mx * p.scale_log2;
         const float was = m_used, was_raw = m_raw;
         float alpha = 1.f;
         bool resc = false;
@@ -589,13 +588,13 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
           m_raw = mx;
           resc = true;
         }
-        const bool now_far = fabsf(mt) > kFar && !blind;
-        if (__any_sync(kAll, resc || now_far)) {
-          far = far || __any_sync(kAll, now_far);
+        if (__any_sync(kAll, resc || fabsf(mt) > kFar)) {
+          const bool blind = mx == -INFINITY;
+          far = far || __any_sync(kAll, fabsf(mt) > kFar && !blind);
           if (far && i > 0) {  // the same by the raw scores, whose products may round alike
             const bool none = was == -INFINITY;
-            resc = !blind && (none || (mx - was_raw) * sc > 8.f);
-            alpha = !resc ? 1.f : none ? 0.f : exp2f((was_raw - mx) * sc);
+            resc = !blind && (none || (mx - was_raw) * p.scale_log2 > 8.f);
+            alpha = !resc ? 1.f : none ? 0.f : exp2f((was_raw - mx) * p.scale_log2);
             m_used = resc ? mt : was;
             m_raw = resc ? mx : was_raw;
           }
@@ -631,6 +630,7 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
         // thread's own S columns: chunk c's 16 P columns start at pcol(c),
         // which only covers S columns this thread has already read.
         const float nm = far ? 0.f : -m_used;
+        const float sc = p.scale_log2;
         float l2[2] = {0.f, 0.f};  // two partial sums: shorter dependency chains
 #pragma unroll 1
         for (int cc = 0; cc < C::CPH; ++cc) {
@@ -889,7 +889,8 @@ cudaError_t launch_prefill_t(const PrefillLaunch& a, int num_sms, cudaStream_t s
   p.num_q_heads = a.num_q_heads;
   p.num_kv_heads = a.num_kv_heads;
   p.num_blocks = a.num_blocks;
-  p.scale_log2 = a.scale_log2;
+  p.scale_log2 = fmaxf(fabsf(a.scale_log2), FLT_TRUE_MIN);
+  p.idesc_qk = idesc_bf16_f32(128, 128, false) | (a.scale_log2 < 0.f ? kIdescNegateA : 0u);
   p.err = a.err;
   p.num_tokens = a.num_tokens;
   p.prefix_len = a.prefix_len;
