@@ -616,7 +616,8 @@ pa_status pa_set_kernel_timer(int kernel_id, void* start_event, void* stop_event
  *     of the other groupings. Both are within the attention tolerances of
  *     the exact result on the same codes; they are not bit-identical.
  *     pa_attention_window_fp8 takes these tiles only for batches with enough
- *     keys attended to (20 blocks per SM).
+ *     decodes or keys attended to (G <= 4: a fifth as many decodes as SMs or 30
+ *     blocks per SM; G = 8: three tenths, or 100 blocks per SM).
  */
 #define PA_OPT_DECODE_TOKEN_MAJOR 5
 /*

@@ -51,24 +51,23 @@ __global__ void __launch_bounds__(kMergeWarps * 32) pa_merge_kernel(const MergeP
     wf = worker_of(first, W, NW);
     wl = worker_of(first + nb - 1, W, NW);
   } else {
-    const int w = (int)blockIdx.x / (p.tm_wide ? p.num_kv_heads : 1) + 1;
+    const int w = (int)blockIdx.x + 1;
     const int4 task = __ldcg(p.tasks + w);
     // tasks past this call's worker count are stale
     if (w >= plan_workers(W, nw, p.min_pos) || task.x < 0) return;
     tok = task.x;
     wf = task.z;
     wl = task.w;
-    kv = p.tm_wide ? (int)blockIdx.x % p.num_kv_heads : task.y;
+    kv = task.y;
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
   // The partials: the suffix slots wf .. wl, then (cascade) the prefix chunks.
-  // Worker wf + i's slot: u + wf + i (u = token * Hkv + kv head), or, of
-  // token-major partials, (token + wf + i) * Hkv + kv head.
+  // Worker wf + i's slot: u + wf + i (u = token * Hkv + kv head).
   const int u = tok * p.num_kv_heads + kv;
   const int ns = wl - wf + 1, n = ns + p.prefix_chunks;
   auto slot = [&](int i) -> const float* {
-    const size_t s0 = p.tm_wide ? (size_t)(tok + wf + i) * p.num_kv_heads + kv : (size_t)(u + wf + i);
+    const size_t s0 = (size_t)(u + wf + i);
     return i < ns ? p.partials + s0 * p.slot_floats
                   : p.prefix_partials +
                         (((size_t)(i - ns) * p.num_tokens + tok) * p.num_kv_heads + kv) *
@@ -235,8 +234,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) pa_merge_tm_kernel(const Mer
 template <int D, int G>
 cudaError_t launch_merge_t(const MergeParams& p, cudaStream_t s) {
   // one CTA per slice boundary, or per (token, kv head)
-  const int boundaries = p.all_units ? p.num_tokens * p.num_kv_heads
-                                     : (p.num_workers - 1) * (p.tm_wide ? p.num_kv_heads : 1);
+  const int boundaries = p.all_units ? p.num_tokens * p.num_kv_heads : p.num_workers - 1;
   if (boundaries <= 0) return cudaSuccess;  // one worker: nothing is ever split
   // token-major partials: eight KV heads, no cascade (the split-KV kernel's own limits)
   if (p.token_major && (p.all_units || p.prefix_chunks != 0 || p.num_kv_heads > kMergeWarps))
@@ -253,7 +251,7 @@ cudaError_t launch_merge_t(const MergeParams& p, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (p.token_major && !p.tm_wide) {  // a CTA per boundary, a warp per KV head
+  if (p.token_major) {  // a CTA per boundary, a warp per KV head
     cfg.blockDim = dim3(32 * p.num_kv_heads);
     return cudaLaunchKernelEx(&cfg, pa_merge_tm_kernel<D, G>, p);
   }

@@ -443,18 +443,27 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
   const int dec_sms = d->num_sms - prefix_ctas;  // SMs the split-KV grid fills
   // An E4M3 cache over eight KV heads takes the token-major tiles (one block
   // of every KV head per tile) on the tensor cores.
-  // Windowed calls: by the blocks the tokens attend to at most, per SM. Below 20
-  // a token-major worker's start and its many-partial merge outweigh its faster
-  // tiles (eight tokens of 252 blocks at G = 8: 29.9 us with the other tiles,
-  // 34.7 token-major; 64 tokens of 66 blocks: 50.7 and 47.2), and below 64 one
-  // CTA per SM is at least as good as two (64 tokens of 66 blocks at G = 4: 37.6
-  // us against 41.2; 128 of 257: 180 against 176).
+  // Windowed calls leave little work, where a token-major worker's start and its
+  // many-partial merge can outweigh its faster tiles: by the tokens on this path
+  // and the blocks they attend to at most. G = 4 (us, other tiles / token-major):
+  // 8 tokens of 502 blocks 39.5 / 40.7, 8 of 1001 64.3 / 60.0, 16 of 129 25.3 /
+  // 25.4, 32 of 33 19.5 / 18.3; G = 8: 8 of 1001 69.2 / 77.3, 32 of 129 45.9 /
+  // 49.7, 32 of 502 124.1 / 119.8, 48 of 33 30.5 / 29.9. And below 64 blocks per SM
+  // one CTA per SM is mostly the better (G = 4, one / two: 32 of 129 38.6 / 39.8,
+  // 64 of 66 38.3 / 40.3, 64 of 502 175.5 / 171.1; but 64 of 33 25.9 / 21.5).
+  const long long win_tokens =
+      pp.use_prefill  // spans of one token, if the others have the longest's length
+          ? num_reqs - ((long long)num_tokens - num_reqs) / (max_query_len - 1)
+          : num_tokens;
+  const long long win_keys = (long long)window + sinks;
   const long long win_blocks =
-      window > 0 ? (long long)num_tokens * (((long long)window + sinks + kBlockSize - 1) / kBlockSize)
-                 : 0;
+      win_tokens * (((win_keys < max_seq_len ? win_keys : max_seq_len) + kBlockSize - 1) / kBlockSize);
+  const bool win_tm = group <= 4 ? 5 * win_tokens >= d->num_sms || win_blocks >= 30LL * d->num_sms
+                                 : 10 * win_tokens >= 3LL * d->num_sms ||
+                                       win_blocks >= 100LL * d->num_sms;
   const int tm_cps = window > 0 && win_blocks < 64LL * d->num_sms ? 1 : g_tm_ctas.load();
   const bool use_tm =
-      use_tc && kv_fp8 && g_token_major.load() && !(window > 0 && win_blocks < 20LL * d->num_sms) &&
+      use_tc && kv_fp8 && g_token_major.load() && (window == 0 || win_tm) &&
       decode_tm_supported(head_dim, group, num_kv_heads, decode_tm_workers(group, d->num_sms, tm_cps));
   const int launched = use_tm   ? decode_tm_workers(group, d->num_sms, tm_cps)
                        : use_tc ? decode_tc_workers(d->num_sms)
@@ -596,10 +605,6 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
   mp.num_workers = workers;
   mp.workers_from_header = overlap;
   mp.token_major = pp.token_major;
-  // Few tokens over many workers (a window over long sequences): a token's
-  // partials are shared by the warps of a CTA per KV head (eight tokens over
-  // 152 workers: 35 us per call against 40 with a warp per KV head).
-  mp.tm_wide = window > 0 && use_tm && workers > 4 * num_tokens ? 1 : 0;
   mp.min_pos = pp.min_pos;
   mp.num_q_heads = num_q_heads;
   mp.num_kv_heads = num_kv_heads;

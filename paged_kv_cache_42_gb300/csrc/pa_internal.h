@@ -340,9 +340,6 @@ struct MergeParams {
   int token_major;          // token-major split-KV: a task {token, -, wf, wl} covers every
                             // kv head (a CTA per boundary, a warp per kv head), slot
                             // (token + w) * Hkv + kv head
-  // token-major partials, but a CTA per (boundary, kv head) whose warps share
-  // the head's partials: for few tokens over many workers
-  int tm_wide;
   int min_pos;  // as the split-KV kernel's
   int num_q_heads, num_kv_heads, num_tokens;
   int key_start_blocks;
