@@ -51,35 +51,14 @@ __device__ __forceinline__ int cut_length(const EvictParams& p, int r, bool& bad
   return !bad && L > p.keep ? L : 0;
 }
 
-// Cluster-wide barrier; reads of and sums into another CTA's shared memory.
-// Every CTA of a cluster reaches every barrier: the paths depend on the request
-// alone.
-__device__ __forceinline__ void cluster_sync() {
-  __syncwarp();  // the aligned form wants the warp together
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
-__device__ __forceinline__ uint32_t cluster_addr(const void* mine, int rank) {
-  uint32_t at;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(mine)), "r"(rank));
-  return at;
-}
-__device__ __forceinline__ uint32_t ld_cluster(uint32_t at) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-  return v;
-}
-__device__ __forceinline__ void add_cluster(uint32_t at, uint32_t v) {
-  asm volatile("red.shared::cluster.add.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
-}
-
 __device__ __forceinline__ int warp_sum(int v) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) v += __shfl_xor_sync(kAll, v, o);
   return v;
 }
 
-// KPT: keys per thread, in registers; 0: parts longer than that, whose weights
+// Every CTA of a cluster reaches every cluster barrier: the paths depend on the
+// request alone. KPT: keys per thread, in registers; 0: parts longer than that, whose weights
 // are read again (from L2) in every pass.
 template <int KPT>
 __global__ void __launch_bounds__(kSelThreads) pa_evict_select_kernel(const EvictParams p) {

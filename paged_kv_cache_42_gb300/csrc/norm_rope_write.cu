@@ -253,7 +253,7 @@ cudaError_t launch_nr(const NormRopeParams& p, int num_sms, cudaStream_t s) {
     return (p.num_tokens * chunks + kThreads / 32 - 1) / (kThreads / 32);
   };
   // Few tokens: one group of heads per warp, the shortest chain. Once that
-  // would be more than the warps an SM holds, kManyIter groups per warp.
+  // would be more than eight CTAs (32 warps) per SM, kManyIter groups per warp.
   const bool small = blocks(1) <= 8LL * num_sms;
   const long long grid = small ? blocks(1) : blocks(kManyIter);
   if (grid > 0x3fffffffLL) return cudaErrorInvalidValue;  // warps are counted in 32 bits

@@ -103,8 +103,12 @@ struct WsHeader {
 // per SM until the copy peak (kHbmBytesPerUs) caps it.
 constexpr float kPrefillStepUs = 2.4f;
 // A windowed item has two masked edges, so more of its steps take the masked
-// softmax (512 decodes and three 512-token chunks at window 1024: 334 us on the
-// 14 SMs that 2.4 us asks for, 302 us on 16 to 24).
+// softmax (512 decodes and three 512-token chunks at window 1024: 355 us on the
+// 14 SMs that 2.4 us asks for, 307 us on 20 to 28). With 3.2 the planner's share
+// is within 1% of the best forced one at windows of 128, 256, 512, 1024 and 2000
+// for 512 decodes (chunks of 256 and of 512) and 256 decodes beside one chunk of
+// 1024 (but 8% at window 128); for 128 decodes it keeps the two in turn, up to 12%
+// behind 40 to 48 SMs.
 constexpr float kWindowStepUs = 3.2f;
 constexpr float kDecodeSmBytesPerUs = 47.0e3f;
 constexpr float kHbmBytesPerUs = 6.6e6f;

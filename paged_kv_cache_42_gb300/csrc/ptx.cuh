@@ -142,6 +142,33 @@ __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// ---- thread-block clusters ------------------------------------------------------
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();  // the aligned form wants the warp together
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// CTA `rank`'s counterpart of this CTA's shared memory at `mine`; reads of and
+// sums into it.
+__device__ __forceinline__ uint32_t cluster_addr(const void* mine, int rank) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(mine)), "r"(rank));
+  return at;
+}
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t at) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void add_cluster(uint32_t at, uint32_t v) {
+  asm volatile("red.shared::cluster.add.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+
 // ---- shared memory vector loads ----------------------------------------------
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;

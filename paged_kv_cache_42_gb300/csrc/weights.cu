@@ -65,7 +65,11 @@ constexpr int kFewRows = 8;          // rows the bandwidth-bound form takes (the
 constexpr int kChunkBlocks = 16;     // 16-key blocks per warp
 constexpr int kScoreWarps = 4;
 constexpr int kClusterWarps = 8;
-constexpr int kClusterSmem = 64 * 1024;  // scores of one CTA of a cluster, at most: three CTAs on an SM
+// Scores of one CTA of a cluster, at most. Two CTAs share an SM (their registers),
+// but what 112 KB each would keep on the SM are few CTAs with long parts: 8 x 24576
+// keys at G = 8 59.1 -> 56.1 us, 1 x 28672 18.6 -> 38.4, 8 x 49152 at G = 4 145 ->
+// 163, against the form through global memory.
+constexpr int kClusterSmem = 64 * 1024;
 constexpr int kFinishThreads = 256;
 
 constexpr int kFinishRound = 1024;   // keys of one round of a finish CTA
@@ -111,20 +115,6 @@ __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
-  return v;
-}
-
-// Cluster-wide barrier, and a read of another CTA's shared memory.
-__device__ __forceinline__ void cluster_sync() {
-  __syncwarp();  // the aligned form wants the warp together
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
-__device__ __forceinline__ float2 ld_cluster_f2(const void* mine, int rank) {
-  uint32_t at;
-  float2 v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(mine)), "r"(rank));
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
   return v;
 }
 
@@ -415,7 +405,7 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 2) pa_weights_cluster_kern
   if (threadIdx.x < kFewRows) {
     float m = kNone, l = 0.f;
     for (int k = 0; k < C; ++k) {
-      const float2 v = ld_cluster_f2(&s_cta[threadIdx.x], k);
+      const float2 v = ld_cluster_f2(cluster_addr(&s_cta[threadIdx.x], k));
       const float top = fmaxf(m, v.x);
       l = l * ex2_approx(m - top) + v.y * ex2_approx(v.x - top);
       m = top;
@@ -1427,9 +1417,10 @@ WeightsLayout weights_layout(int num_reqs, int num_tokens, int num_q_heads, int 
 
 cudaError_t launch_weights(WeightsParams p, int head_dim, bool f8, int num_sms, cudaStream_t s,
                            int* launches) {
-  // CTAs per (request, KV head) of the few-rows form: enough that a CTA's
-  // scores leave room for three CTAs on an SM and the grid has at least two
-  // waves of them; 0: they do not fit even eight CTAs (kClusterSmem each)
+  // CTAs per (request, KV head) of the few-rows form: enough that a CTA's scores
+  // fit kClusterSmem and, while parts are longer than 1024 keys, that the grid has
+  // three waves of two CTAs per SM (two waves measure the same over 1 to 256
+  // requests); 0: they do not fit even eight CTAs
   const long long rh = (long long)p.num_reqs * p.num_kv_heads;
   p.num_sms = num_sms;
   p.cluster = 1;
