@@ -307,7 +307,10 @@ pa_status pa_attention_cascade(const void* q, const void* k_cache, const void* v
  * is read, those that no new token of the request attends to may hold
  * anything; K and V of the others must be finite, as for pa_attention. Time
  * and bytes follow the keys attended to, not the sequence length. num_blocks
- * >= 1.
+ * >= 1. Where the tensor cores take the products (prompt chunks; decodes by
+ * PA_OPT_DECODE_TC) the softmax weights are rounded to bf16 for them, or over an
+ * E4M3 cache's decodes to two E4M3 terms each, as in pa_attention: an output is
+ * within 2^-7 of its weights' sum of |V|, and its own rounding.
  */
 pa_status pa_attention_window(const void* q, const void* k_cache, const void* v_cache,
                               const int32_t* block_tables, const int32_t* seq_lens,

@@ -319,10 +319,10 @@ cudaError_t launch_evict(EvictParams p, int row_bytes, int num_sms, cudaStream_t
   const long long chunks = (p.keep - 1) / kMoveRows + 1;
   if (rows > 0x7fffffffLL || rows * chunks > 0x7fffffffLL) return cudaErrorInvalidValue;
   // CTAs per (request, KV head): parts of at most 8192 keys, sixteen per thread,
-  // as long as the grid leaves SMs idle (64 rows of 32768 keys, whole call: 43.3
-  // us with four CTAs each, 44.6 with two of 32 keys per thread, 53 with eight
-  // of eight, whose barriers cost more than the shorter parts give; 512 rows of
-  // up to 4096 keys: one CTA each).
+  // as long as the grid leaves SMs idle (64 rows of 32768 keys, whole call: 41.2
+  // us with four CTAs each, 42.6 with two of 32 keys per thread, 51.4 with eight
+  // of eight, whose barriers cost more than the shorter parts give, 106 with one,
+  // whose keys no longer fit registers; 512 rows of up to 4096 keys: one CTA each).
   const long long most = (long long)p.max_seq_len - p.sinks - p.recent;
   p.cluster = 1;
   while (p.cluster < 4 && most > 8192LL * p.cluster && rows * p.cluster < 4LL * num_sms) p.cluster *= 2;

@@ -26,9 +26,9 @@
 // of heads of ONE token and ONE kind (queries, K or V): their loads are all in
 // flight together, before anything depends on the position; the token's
 // cosines and sines and the kind's weight are loaded once for all of them, and
-// V skips the arithmetic. 2048 tokens of 32 + 8 + 8 heads of 128 take 12.5 us,
-// 4.1 TB/s; 2, 6 or 8 groups a warp 13.8, 13.6 and 14.5 us, and units that mix
-// the kinds 13.6 us (more instructions: the choice is made per head).
+// V skips the arithmetic. 2048 tokens of 32 + 8 + 8 heads of 128 take 10.8 us,
+// 4.8 TB/s (E4M3 12.9); 2, 6 or 8 groups a warp 12.3, 12.0 and 12.8 us (13.4, 14.3,
+// 15.6). Units that mix the kinds were 9% slower: the choice is made per head.
 #include <type_traits>
 
 #include "pa_internal.h"
@@ -92,8 +92,8 @@ __device__ __forceinline__ uint2 pack_e4m3(const Pairs& v, float scale) {
                     two(v.x[2].x, v.x[2].y) | two(v.x[3].x, v.x[3].y) << 16);
 }
 
-// At least nine CTAs on an SM into a bf16 cache (56 registers): 2048 tokens 12.1
-// us, with 64 registers and eight of them 13.2. The E4M3 form does not fit 56.
+// At least nine CTAs on an SM into a bf16 cache (56 registers): with 64 registers
+// and eight of them 2048 tokens took 9% longer. The E4M3 form does not fit 56.
 template <int D, bool F8, bool INTER, int ITER>
 __global__ void __launch_bounds__(kThreads, F8 ? 8 : 9) pa_norm_rope_write_kernel(const NormRopeParams p) {
   constexpr int LPH = D / 8;     // lanes per head

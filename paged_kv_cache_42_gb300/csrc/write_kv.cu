@@ -15,8 +15,8 @@
 namespace pa {
 
 __global__ void __launch_bounds__(256) pa_write_kv_kernel(WriteParams p) {
-  // A planner launched next may start now: it reads only metadata, and
-  // waits for this grid before it completes.
+  // The next grid may be placed now: it waits for this one, at its start or
+  // (PA_OPT_WRITE_OVERLAP) before it reads what this one writes.
   griddep_launch_dependents();
   const int vec_per_row = p.head_dim / 8;  // 16-byte vectors per D-element row
   const long long total = (long long)p.num_tokens * p.num_kv_heads * vec_per_row;

@@ -55,13 +55,11 @@ def rounds(step, n, reps=4):
                 assert torch.equal(x, y)
 
 
-@pytest.mark.parametrize("prefix", [0, 64])
-@pytest.mark.parametrize("name", CASES)
+@pytest.mark.parametrize("name,prefix", [(n, 0) for n in CASES] + [("cuda-core", 64),
+                                                                   ("tensor-core", 64)])
 def test_inputs_made_right_before(pa_lib, name, prefix):
     from paged_kv_cache_42_gb300 import binding
     spans, hq, hkv, d, fp8 = CASES[name]
-    if prefix and (fp8 or any(c < prefix for c, _ in spans)):
-        pytest.skip("no such cascade")
     binding.get_device_error(True)
     b = ref.Batch(spans, hq, hkv, d, 5, fp8=fp8)
     if prefix:
