@@ -530,6 +530,114 @@ pa_status pa_evict_kv_args(const pa_evict_args* args);
 
 size_t pa_args_size(int which);
 
+/*
+ * Row-scaled E4M3 caches: K and V as E4M3 codes with one power of two for every
+ * row (the head_dim elements of one token and KV head), which the write finds.
+ * The pages' FP8 cache has one scale per tensor, to be known before the first
+ * write; they have no counterpart to this one.
+ *   k_cache, v_cache  [num_blocks][num_kv_heads][16][head_dim] codes, as for
+ *                     pa_write_kv_fp8
+ *   scales            [num_blocks][num_kv_heads][2][16] bytes, 16-byte aligned:
+ *                     K's 16 rows of a block, then V's. A byte b stands for
+ *                     2^(b - 127) (the 8-bit format with an exponent only),
+ *                     255 for NaN.
+ * With a the largest |x| of a row, e is the smallest integer of [-100, 119] with
+ * a <= 448 x 2^e, b = e + 127, and an element's code is E4M3(x 2^-e), rounded
+ * once, to nearest even, saturating at +-448 (which only rows past 448 x 2^119
+ * reach). A row's value is code x 2^e, a bf16 number. A row with an infinity or
+ * a NaN gets b = 255 and codes of zero, and reads back as NaN. The calls that
+ * read such a cache take the bytes that these writes make (27 to 246, 255).
+ *
+ * The calls from here on take their arguments in a struct only, laid out like the
+ * structs above; pa_args_size(16 + i) is the size of the i-th. NULL is
+ * PA_ERR_INVALID_ARG.
+ */
+
+/* pa_write_kv into a row-scaled cache. Tokens of k and v are k_stride / v_stride
+ * elements apart (at least one token's heads, a multiple of 8), a token's heads
+ * contiguous. head_dim 64 or 128, up to 65536 KV heads; a negative slot is
+ * skipped, one outside the pool too, with PA_DEVERR_SLOT. */
+typedef struct pa_write_rows_args { /* 16 */
+  const void *k, *v;
+  const int64_t* slot_mapping;
+  void *k_cache, *v_cache;
+  uint8_t* scales;
+  void* stream;
+  long long k_stride, v_stride;
+  int num_tokens, num_kv_heads, head_dim, block_size, num_blocks;
+} pa_write_rows_args;
+pa_status pa_write_kv_rows(const pa_write_rows_args* args);
+
+/* pa_norm_rope_write_kv into a row-scaled cache: each row of K and V from the
+ * binary32 values, its scale from theirs. */
+typedef struct pa_norm_rope_write_rows_args { /* 17 */
+  const void *q, *k, *v;
+  const int32_t* positions;
+  const float* cos_sin;
+  const void *q_weight, *k_weight;
+  const int64_t* slot_mapping;
+  void *q_out, *k_cache, *v_cache;
+  uint8_t* scales;
+  void* stream;
+  long long q_stride, k_stride, v_stride;
+  float eps;
+  int rotary_dim, interleaved, max_position;
+  int num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks;
+} pa_norm_rope_write_rows_args;
+pa_status pa_norm_rope_write_kv_rows(const pa_norm_rope_write_rows_args* args);
+
+/*
+ * pa_attention over a row-scaled cache: keys are code x 2^e of their row, values
+ * alike. Prompt chunks (spans of 16 or more new tokens) run on the tensor-core
+ * kernel over tiles widened to bf16, exactly; every other span on a split-KV
+ * kernel that takes a key's 2^e after the products with its codes and a value's
+ * before. The workspace is pa_attention_workspace_size(...) bytes; limits and
+ * errors are pa_attention's. A row that reads back as NaN makes NaN of the outputs
+ * that attend to it, and in a prompt chunk may make NaN of those of earlier
+ * tokens of the chunk, for the query heads of its KV head. V rows past 448 x 2^100
+ * may lose the smaller keys' part.
+ */
+typedef struct pa_attention_rows_args { /* 18 */
+  const void *q, *k_cache, *v_cache;
+  const uint8_t* scales;
+  const int32_t *block_tables, *seq_lens, *query_start_loc;
+  void *out, *workspace, *stream;
+  size_t workspace_bytes;
+  float scale;
+  int num_reqs, num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks;
+  int max_blocks_per_req, max_query_len, max_seq_len;
+} pa_attention_rows_args;
+pa_status pa_attention_rows(const pa_attention_rows_args* args);
+
+/*
+ * Read ranges of cached keys and values back, dense and in bf16: for another
+ * cache or format, or for code that knows no block tables. The pages have no
+ * counterpart.
+ *   read_start_loc  [num_reqs + 1] int32, non-decreasing: request r's keys go to
+ *                   rows read_start_loc[r] .. read_start_loc[r + 1] - 1 of
+ *                   k_out and v_out; rows of no request are left untouched
+ *   first           [num_reqs] int32: the first key read, or NULL: key 0
+ *   k_out, v_out    [num_tokens][num_kv_heads][head_dim] bf16, 32-byte aligned
+ *   kv_format       0: bf16 caches, copied bit for bit; 1: E4M3 with k_scale and
+ *                   v_scale, the binary32 product rounded once; 2: row-scaled
+ *                   (scales), exact
+ *   num_tokens      rows of k_out and v_out
+ * head_dim 64 or 128, up to 8192 KV heads. Errors: a request whose rows do not lie
+ * in [0, num_tokens] sets PA_DEVERR_QSL, one whose keys its table does not hold
+ * PA_DEVERR_LENGTHS, and is skipped; a key whose block id is outside the pool sets
+ * PA_DEVERR_BLOCK_ID and its row is left untouched.
+ */
+typedef struct pa_read_args { /* 19 */
+  const void *k_cache, *v_cache;
+  const uint8_t* scales;
+  const int32_t *block_tables, *read_start_loc, *first;
+  void *k_out, *v_out, *stream;
+  float k_scale, v_scale;
+  int kv_format, num_reqs, num_tokens, num_kv_heads, head_dim, block_size, num_blocks;
+  int max_blocks_per_req;
+} pa_read_args;
+pa_status pa_read_kv(const pa_read_args* args);
+
 /* Size of the fixed scratch array used by pa_attention_noalloc. */
 size_t pa_noalloc_scratch_bytes(void);
 
@@ -564,8 +672,8 @@ pa_status pa_mapped_pointer(const void* host_ptr, void** device_ptr);
  * created by the caller) around every later launch of the given kernel on its
  * stream; pass NULL events to stop. Kernel ids: 0 write_kv, 1 planner,
  * 2 decode (split-KV), 3 prefill chunk, 4 cascade prefix pass, 5 split-KV
- * merge pass, 6 accumulated weights, 7 eviction (the last two: all launches of
- * the call). Process-wide setting, not thread-safe.
+ * merge pass, 6 accumulated weights, 7 eviction (these two: all launches of
+ * the call), 8 reading back. Process-wide setting, not thread-safe.
  */
 pa_status pa_set_kernel_timer(int kernel_id, void* start_event, void* stop_event);
 

@@ -42,7 +42,7 @@ DEVICE_ERRORS = {0: "none", 1: "slot outside the pool", 2: "block id outside the
                  5: "bounded wait timed out", 6: "table does not start with the common prefix",
                  7: "position outside the rotation table"}
 KERNEL_IDS = {"write_kv": 0, "plan": 1, "decode": 2, "prefill": 3, "prefix": 4, "merge": 5,
-              "weights": 6, "evict": 7}
+              "weights": 6, "evict": 7, "read": 8}
 
 
 class PagedAttentionError(RuntimeError):
@@ -105,6 +105,12 @@ def lib() -> ctypes.CDLL:
             fn.restype = _c_i
             if L.pa_args_size(i) != -(-layout.size // 8) * 8:
                 raise RuntimeError(f"{name}: the library's argument struct has another layout")
+        for i, (name, layout) in enumerate(_ARGS2.items()):
+            fn = getattr(L, name)
+            fn.argtypes = [ctypes.c_char_p]
+            fn.restype = _c_i
+            if L.pa_args_size(16 + i) != -(-layout.size // 8) * 8:
+                raise RuntimeError(f"{name}: the library's argument struct has another layout")
         L.pa_attention_weights_workspace_size.argtypes = [_c_i] * 7
         L.pa_attention_weights_workspace_size.restype = ctypes.c_size_t
         L.pa_attention_weights.argtypes = ([_c_p] * 5 + [_f, _c_p, _c_p, _ll] + [_c_i] * 10 +
@@ -139,6 +145,12 @@ _ARGS = {"pa_norm_rope_write_kv_args": struct.Struct("@12P3q3f10i"),
          "pa_attention_weights_args": struct.Struct("@9PNq2f11i"),
          "pa_evict_kv_args": struct.Struct("@10P2q12i")}
 _pack_nr, _pack_win, _pack_wts, _pack_evict = (s.pack for s in _ARGS.values())
+# The calls that take a struct only.
+_ARGS2 = {"pa_write_kv_rows": struct.Struct("@7P2q5i"),
+          "pa_norm_rope_write_kv_rows": struct.Struct("@13P3qf9i"),
+          "pa_attention_rows": struct.Struct("@10PNf10i"),
+          "pa_read_kv": struct.Struct("@9P2f8i")}
+_pack_wr, _pack_nrr, _pack_ar, _pack_read = (s.pack for s in _ARGS2.values())
 
 
 def _check(status: int, what: str) -> None:
@@ -263,8 +275,17 @@ def _heads(t: torch.Tensor, shape: tuple, dev: int, name: str) -> tuple[int, int
     return t.data_ptr(), (s0 if shape[0] > 1 else shape[1] * shape[2])
 
 
+def _scales(t: torch.Tensor, cache_shape, dev: int) -> int:
+    """Address of a row-scaled cache's scale bytes."""
+    at = _ptr(t, torch.uint8, dev, "scales")
+    nb, hkv = cache_shape[:2]
+    if t.shape != (nb, hkv, 2, 16):
+        raise ValueError("scales must be [num_blocks, Hkv, 2, 16]")
+    return at
+
+
 def _norm_rope(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight,
-               eps, interleaved, out, fp8, k_scale, v_scale, stream):
+               eps, interleaved, out, fp8, k_scale, v_scale, stream, scales=None):
     T, hq, d = qshape = q.shape
     cshape = k_cache.shape
     nb, hkv, bs, d2 = cshape
@@ -302,6 +323,15 @@ def _norm_rope(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_we
     if slot_mapping.numel() != T:
         raise ValueError("slot_mapping must be [num_tokens]")
     cache_dtype = torch.uint8 if fp8 else torch.bfloat16
+    if fp8 == 2:
+        st = lib().pa_norm_rope_write_kv_rows(_pack_nrr(
+            qp, kp, vp, pos_p, cs_p, qw_p, kw_p, sp, _ptr(out, torch.bfloat16, dev, "out"),
+            _ptr(k_cache, cache_dtype, dev, "k_cache"), _ptr(v_cache, cache_dtype, dev, "v_cache"),
+            _scales(scales, cshape, dev), raw_stream, qs, ks, vs, eps, rot,
+            1 if interleaved else 0, max_pos, T, hq, hkv, d, bs, nb))
+        if st:
+            _check(st, "pa_norm_rope_write_kv_rows")
+        return out
     st = lib().pa_norm_rope_write_kv_args(_pack_nr(
         qp, kp, vp, pos_p, cs_p, qw_p, kw_p, sp, _ptr(out, torch.bfloat16, dev, "out"),
         _ptr(k_cache, cache_dtype, dev, "k_cache"), _ptr(v_cache, cache_dtype, dev, "v_cache"),
@@ -639,6 +669,157 @@ def evict_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.T
     if st:
         _check(st, "pa_evict_kv")
     return new_seq_lens, kept, new_weights
+
+
+def _like_cache(k_cache, v_cache, d: int | None = None):
+    """The common shape of two caches [num_blocks, Hkv, 16, D]."""
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape or (d is not None and shape[3] != d):
+        raise ValueError("shape mismatch between the caches" + ("" if d is None else " and q"))
+    return shape
+
+
+def write_kv_rows(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
+                  k_cache: torch.Tensor, v_cache: torch.Tensor, scales: torch.Tensor, *,
+                  stream=None) -> None:
+    """pa_write_kv_rows: scatter k/v [T, Hkv, D] bf16 into a row-scaled cache: E4M3
+    codes (uint8 [num_blocks, Hkv, 16, D]) and a power of two for every row, which
+    the call finds (uint8 ``scales`` [num_blocks, Hkv, 2, 16]: K's, then V's; b
+    stands for 2^(b - 127)). k and v may be views into one projection's output.
+    """
+    cshape = _like_cache(k_cache, v_cache)
+    nb, hkv, bs, d = cshape
+    T = k.shape[0]
+    dev, raw_stream = _where(stream)
+    kp, ks = _heads(k, (T, hkv, d), dev, "k")
+    vp, vs = _heads(v, (T, hkv, d), dev, "v")
+    sp = _ptr(slot_mapping, torch.int64, dev, "slot_mapping")
+    if slot_mapping.numel() != T:
+        raise ValueError("slot_mapping must be [num_tokens]")
+    st = lib().pa_write_kv_rows(_pack_wr(
+        kp, vp, sp, _ptr(k_cache, torch.uint8, dev, "k_cache"),
+        _ptr(v_cache, torch.uint8, dev, "v_cache"), _scales(scales, cshape, dev), raw_stream, ks, vs,
+        T, hkv, d, bs, nb))
+    if st:
+        _check(st, "pa_write_kv_rows")
+
+
+def norm_rope_write_kv_rows(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                            positions: torch.Tensor | None, cos_sin: torch.Tensor | None,
+                            slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                            v_cache: torch.Tensor, scales: torch.Tensor, *,
+                            q_weight: torch.Tensor | None = None,
+                            k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                            interleaved: bool = False, out: torch.Tensor | None = None,
+                            stream=None) -> torch.Tensor:
+    """pa_norm_rope_write_kv_rows: :func:`norm_rope_write_kv` into a row-scaled cache
+    (see :func:`write_kv_rows`)."""
+    return _norm_rope(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight,
+                      k_weight, eps, interleaved, out, 2, 1.0, 1.0, stream, scales)
+
+
+def attention_rows(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   scales: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                   query_start_loc: torch.Tensor, scale: float, *, max_query_len: int,
+                   max_seq_len: int, out: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """pa_attention_rows: :func:`attention` over a row-scaled cache (see
+    :func:`write_kv_rows`). The workspace is ``workspace_size(...)`` bytes."""
+    T, hq, d = qshape = q.shape
+    cshape = _like_cache(k_cache, v_cache, d)
+    nb, hkv, bs, _ = cshape
+    R = seq_lens.shape[0]
+    mr, mb = block_tables.shape
+    if query_start_loc.numel() != R + 1 or mr != R:
+        raise ValueError("metadata shapes must be qsl [R+1], block_tables [R, max_blocks]")
+    if out is None:
+        out = _empty(qshape, torch.bfloat16, q.device, stream)
+    elif out.shape != qshape:
+        raise ValueError("out must have q's shape")
+    if workspace is None:
+        need = workspace_size(R, T, hq, hkv, d)
+        workspace = _empty(max(need, 256), torch.uint8, q.device, stream)
+    dev, raw_stream = _where(stream)
+    out_p = _ptr(out, torch.bfloat16, dev, "out") if out.is_cuda else _out(out)
+    st = lib().pa_attention_rows(_pack_ar(
+        _ptr(q, torch.bfloat16, dev, "q"), _ptr(k_cache, torch.uint8, dev, "k_cache"),
+        _ptr(v_cache, torch.uint8, dev, "v_cache"), _scales(scales, cshape, dev),
+        _ptr(block_tables, torch.int32, dev, "block_tables"),
+        _ptr(seq_lens, torch.int32, dev, "seq_lens"),
+        _ptr(query_start_loc, torch.int32, dev, "query_start_loc"), out_p,
+        _ptr(workspace, torch.uint8, dev, "workspace"), raw_stream, workspace.numel(), scale, R, T,
+        hq, hkv, d, bs, nb, mb, max_query_len, max_seq_len))
+    if st:
+        _check(st, "pa_attention_rows")
+    return out
+
+
+def _read(k_cache, v_cache, scales, block_tables, read_start_loc, first, num_tokens, k_out, v_out,
+          fmt, k_scale, v_scale, stream):
+    cshape = _like_cache(k_cache, v_cache)
+    nb, hkv, bs, d = cshape
+    R, mb = block_tables.shape
+    if read_start_loc.numel() != R + 1:
+        raise ValueError("read_start_loc must be [num_reqs + 1]")
+    if num_tokens is None:
+        if k_out is None and v_out is None:
+            raise ValueError("give num_tokens, or k_out and v_out")
+        num_tokens = (v_out if k_out is None else k_out).shape[0]
+    shape = (num_tokens, hkv, d)
+    if k_out is None:
+        k_out = _empty(shape, torch.bfloat16, k_cache.device, stream)
+    if v_out is None:
+        v_out = _empty(shape, torch.bfloat16, k_cache.device, stream)
+    if k_out.shape != shape or v_out.shape != shape:
+        raise ValueError("k_out and v_out must be [num_tokens, Hkv, D]")
+    dev, raw_stream = _where(stream)
+    first_p = 0
+    if first is not None:
+        first_p = _ptr(first, torch.int32, dev, "first")
+        if first.numel() != R:
+            raise ValueError("first must be [num_reqs]")
+    cache_dtype = torch.uint8 if fmt else torch.bfloat16
+    st = lib().pa_read_kv(_pack_read(
+        _ptr(k_cache, cache_dtype, dev, "k_cache"), _ptr(v_cache, cache_dtype, dev, "v_cache"),
+        _scales(scales, cshape, dev) if fmt == 2 else 0,
+        _ptr(block_tables, torch.int32, dev, "block_tables"),
+        _ptr(read_start_loc, torch.int32, dev, "read_start_loc"), first_p,
+        _ptr(k_out, torch.bfloat16, dev, "k_out"), _ptr(v_out, torch.bfloat16, dev, "v_out"),
+        raw_stream, k_scale, v_scale, fmt, R, num_tokens, hkv, d, bs, nb, mb))
+    if st:
+        _check(st, "pa_read_kv")
+    return k_out, v_out
+
+
+def read_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+            read_start_loc: torch.Tensor, *, first: torch.Tensor | None = None,
+            num_tokens: int | None = None, k_out: torch.Tensor | None = None,
+            v_out: torch.Tensor | None = None, stream=None):
+    """pa_read_kv over a bf16 cache: dense copies [num_tokens, Hkv, D] of cached keys
+    and values. Rows ``read_start_loc[r]`` .. ``read_start_loc[r + 1] - 1`` (int32
+    [R + 1]) get request r's keys from ``first[r]`` (int32 [R]; None: 0) on. Returns
+    ``(k_out, v_out)``; given buffers are filled, missing ones allocated.
+    """
+    return _read(k_cache, v_cache, None, block_tables, read_start_loc, first, num_tokens, k_out,
+                 v_out, 0, 1.0, 1.0, stream)
+
+
+def read_kv_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                read_start_loc: torch.Tensor, k_scale: float, v_scale: float, *,
+                first: torch.Tensor | None = None, num_tokens: int | None = None,
+                k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None, stream=None):
+    """pa_read_kv over an E4M3 cache (uint8) with one scale per tensor."""
+    return _read(k_cache, v_cache, None, block_tables, read_start_loc, first, num_tokens, k_out,
+                 v_out, 1, k_scale, v_scale, stream)
+
+
+def read_kv_rows(k_cache: torch.Tensor, v_cache: torch.Tensor, scales: torch.Tensor,
+                 block_tables: torch.Tensor, read_start_loc: torch.Tensor, *,
+                 first: torch.Tensor | None = None, num_tokens: int | None = None,
+                 k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None, stream=None):
+    """pa_read_kv over a row-scaled cache (see :func:`write_kv_rows`)."""
+    return _read(k_cache, v_cache, scales, block_tables, read_start_loc, first, num_tokens, k_out,
+                 v_out, 2, 1.0, 1.0, stream)
 
 
 def get_device_error(clear: bool = True) -> tuple[int, int]:

@@ -38,6 +38,7 @@
 
 #include "pa_internal.h"
 #include "ptx.cuh"
+#include "rows.cuh"
 
 namespace pa {
 
@@ -63,8 +64,12 @@ constexpr unsigned kFull = 0xffffffffu;
 #define PA_DEC_VD8_MAXG 4
 #endif
 
-template <int D, int G, bool F8>
+// KV: the caches, 0 bf16, 1 E4M3 with one scale per tensor, 2 row-scaled E4M3
+// (rows.cuh): a block's 32 scale bytes ride along with its tile, a score takes
+// its key's 2^e after the dot product and a p its row's before the P.V pass.
+template <int D, int G, int KV>
 struct Cfg {
+  static constexpr bool F8 = KV != 0;
   static constexpr int EB = F8 ? 1 : 2;          // bytes per cached K/V element
   static constexpr int DPT = (G <= 4) ? 16 : 8;  // q.k dims per lane
   static constexpr int TPT = D / DPT;            // lanes per token in q.k
@@ -76,16 +81,17 @@ struct Cfg {
   static constexpr int RPS = 32 / LPR;  // V rows per step
   static constexpr int KV_BYTES = kBlockSize * D * EB;
   static constexpr int Q_BYTES = G * D * 2;
-  static constexpr int STAGE_BYTES = 2 * KV_BYTES + Q_BYTES;
+  static constexpr int S_BYTES = KV == 2 ? kScaleBytes : 0;
+  static constexpr int STAGE_BYTES = 2 * KV_BYTES + Q_BYTES + S_BYTES;
   static constexpr int P_BYTES = kBlockSize * G * 4 + 64;  // p[16][G], alpha[G]
   static_assert(TPT >= G, "a token's lane group must hold one value per head");
   static_assert(DPT == 8 || DPT == 16, "one or two 16-byte chunks per lane");
   static_assert(RPS >= 1 && kBlockSize % RPS == 0, "whole V rows per step");
 };
 
-template <int D, int G, int NSTAGE, bool F8>
+template <int D, int G, int NSTAGE, int KV>
 struct WarpSmem {
-  using C = Cfg<D, G, F8>;
+  using C = Cfg<D, G, KV>;
   static constexpr int RAW = NSTAGE * C::STAGE_BYTES + C::P_BYTES + NSTAGE * 8;
   static constexpr int BYTES = (RAW + 127) / 128 * 128;
 };
@@ -143,10 +149,11 @@ struct Loc {
 // WIN: windowed attention (win_span): a unit's positions are the blocks its
 // token attends to, and a key of such a block outside the window is treated
 // as one past the sequence end.
-template <int D, int G, int WARPS, int NSTAGE, bool F8, bool WIN>
+template <int D, int G, int WARPS, int NSTAGE, int KV, bool WIN>
 __device__ __forceinline__ void decode_body(const DecodeParams& p) {
-  using C = Cfg<D, G, F8>;
-  using WS = WarpSmem<D, G, NSTAGE, F8>;
+  constexpr bool F8 = KV != 0;
+  using C = Cfg<D, G, KV>;
+  using WS = WarpSmem<D, G, NSTAGE, KV>;
   extern __shared__ __align__(128) unsigned char smem[];
   // The merge pass may be placed as soon as CTAs of this persistent grid
   // retire (it waits for the whole grid before reading).
@@ -350,13 +357,17 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
       const uint32_t bar = bars + 8 * stage;
       const size_t off = ((size_t)pid * Hkv + kv) * (kBlockSize * D) * C::EB;  // bytes
       fence_proxy_async_smem();
-      mbar_arrive_expect_tx(bar, 2 * C::KV_BYTES + (with_q ? C::Q_BYTES : 0) + PA_TEST_EXTRA_TX);
+      mbar_arrive_expect_tx(bar, 2 * C::KV_BYTES + (with_q ? C::Q_BYTES : 0) + C::S_BYTES +
+                                     PA_TEST_EXTRA_TX);
       bulk_g2s(dst, static_cast<const unsigned char*>(p.k_cache) + off, C::KV_BYTES, bar);
       bulk_g2s(dst + C::KV_BYTES, static_cast<const unsigned char*>(p.v_cache) + off, C::KV_BYTES,
                bar);
       if (with_q)
         bulk_g2s(dst + 2 * C::KV_BYTES, p.q + ((size_t)tok * Hq + (size_t)kv * G) * D, C::Q_BYTES,
                  bar);
+      if constexpr (KV == 2)
+        bulk_g2s(dst + 2 * C::KV_BYTES + C::Q_BYTES, p.scales + ((size_t)pid * Hkv + kv) * kScaleBytes,
+                 kScaleBytes, bar);
     }
   };
 
@@ -524,6 +535,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
         part[h] = a2.x + a2.y;
       }
       sc[ps] = reduce_heads<G, C::TPT>(part, lane);
+      if constexpr (KV == 2) sc[ps] *= row_size(st_ptr[2 * C::KV_BYTES + C::Q_BYTES + t]);
     }
     if constexpr (WIN) {
 #pragma unroll
@@ -548,7 +560,13 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
     for (int ps = 0; ps < C::NPASS; ++ps) {
       const float pr = exp2f(sc[ps] - m_new);
       psum += pr;
-      p_s[(ps * C::TPP + tg) * G + hsel] = pr;
+      if constexpr (KV == 2) {  // past the sequence end the byte may be anything
+        const int t = ps * C::TPP + tg;
+        const float size = row_size(st_ptr[2 * C::KV_BYTES + C::Q_BYTES + kBlockSize + t]);
+        p_s[t * G + hsel] = t < nvalid ? pr * size : 0.f;
+      } else {
+        p_s[(ps * C::TPP + tg) * G + hsel] = pr;
+      }
     }
     l_run = l_run * alpha + psum;
     m_run = m_new;
@@ -784,9 +802,9 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
   }
 }
 
-template <int D, int G, int WARPS, int NSTAGE, bool F8, bool WIN>
+template <int D, int G, int WARPS, int NSTAGE, int KV, bool WIN>
 __global__ void __launch_bounds__(WARPS * 32) pa_decode_kernel(const DecodeParams p) {
-  decode_body<D, G, WARPS, NSTAGE, F8, WIN>(p);
+  decode_body<D, G, WARPS, NSTAGE, KV, WIN>(p);
   // overlapped cascade: complete only after the prefix pass's grid, so that
   // the merge pass after this grid sees the prefix partials too
   if (p.overlap && threadIdx.x == 0) griddep_wait();
@@ -798,16 +816,16 @@ __global__ void __launch_bounds__(WARPS * 32) pa_decode_kernel(const DecodeParam
 // occupancy, capped so the workers fit the workspace's partial slots.
 // Dynamic shared memory of a launch: the warps' rings, plus the unit table of
 // a self-planned launch.
-template <int D, int G, int WARPS, int NSTAGE, bool F8>
+template <int D, int G, int WARPS, int NSTAGE, int KV>
 constexpr int decode_smem(bool self_plan) {
-  return WARPS * WarpSmem<D, G, NSTAGE, F8>::BYTES +
+  return WARPS * WarpSmem<D, G, NSTAGE, KV>::BYTES +
          (self_plan ? (int)sizeof(UnitInfo) * (kSelfPlanMaxReqs + 1) : 0);
 }
 
-template <int D, int G, int WARPS, int NSTAGE, bool F8, bool WIN>
+template <int D, int G, int WARPS, int NSTAGE, int KV, bool WIN>
 cudaError_t decode_grid(int num_sms, int occ_cap, bool self_plan, int* grid_out) {
-  auto kern = pa_decode_kernel<D, G, WARPS, NSTAGE, F8, WIN>;
-  const int smem = decode_smem<D, G, WARPS, NSTAGE, F8>(self_plan);
+  auto kern = pa_decode_kernel<D, G, WARPS, NSTAGE, KV, WIN>;
+  const int smem = decode_smem<D, G, WARPS, NSTAGE, KV>(self_plan);
   static int occ_cache[64][2] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -815,7 +833,7 @@ cudaError_t decode_grid(int num_sms, int occ_cap, bool self_plan, int* grid_out)
   int occ = (dev >= 0 && dev < 64) ? occ_cache[dev][self_plan] : 0;
   if (occ == 0) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             decode_smem<D, G, WARPS, NSTAGE, F8>(true));
+                             decode_smem<D, G, WARPS, NSTAGE, KV>(true));
     if (e != cudaSuccess) return e;
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, WARPS * 32, smem);
     if (e != cudaSuccess) return e;
@@ -829,13 +847,13 @@ cudaError_t decode_grid(int num_sms, int occ_cap, bool self_plan, int* grid_out)
   return cudaSuccess;
 }
 
-template <int D, int G, int WARPS, int NSTAGE, bool F8, bool WIN>
+template <int D, int G, int WARPS, int NSTAGE, int KV, bool WIN>
 cudaError_t launch_decode_t(const DecodeParams& p, int num_sms, int occ_cap, cudaStream_t s,
                             int* workers_out) {
-  auto kern = pa_decode_kernel<D, G, WARPS, NSTAGE, F8, WIN>;
-  const int smem = decode_smem<D, G, WARPS, NSTAGE, F8>(p.self_plan != 0);
+  auto kern = pa_decode_kernel<D, G, WARPS, NSTAGE, KV, WIN>;
+  const int smem = decode_smem<D, G, WARPS, NSTAGE, KV>(p.self_plan != 0);
   int grid = 0;
-  cudaError_t e = decode_grid<D, G, WARPS, NSTAGE, F8, WIN>(num_sms, occ_cap, p.self_plan != 0, &grid);
+  cudaError_t e = decode_grid<D, G, WARPS, NSTAGE, KV, WIN>(num_sms, occ_cap, p.self_plan != 0, &grid);
   if (e != cudaSuccess) return e;
   *workers_out = grid * WARPS;
   cudaLaunchConfig_t cfg = {};
@@ -886,8 +904,9 @@ cudaError_t launch_decode_t(const DecodeParams& p, int num_sms, int occ_cap, cud
 // Warps per CTA and ring stages per warp of each instantiation. An E4M3 tile
 // is half the bytes of a bf16 one: three-stage FP8 rings still leave room for
 // a third CTA per SM where registers allow it (groups of up to two heads).
-template <int D, int G, bool F8>
+template <int D, int G, int KV>
 struct Tuning {
+  static constexpr bool F8 = KV != 0;
   static constexpr int WARPS =
       D == 128 ? (G == 8 ? PA_DEC128G8_WARPS : PA_DEC128_WARPS) : PA_DEC64_WARPS;
   static constexpr int STAGES =
@@ -895,54 +914,62 @@ struct Tuning {
          : (D == 128 ? (G == 8 ? PA_DEC128G8_STAGES : PA_DEC128_STAGES) : PA_DEC64_STAGES);
 };
 
-template <int D, int G, bool F8>
+// Windows have no row-scaled form (the caller sees to it).
+template <int D, int G, int KV>
 cudaError_t launch_one(const DecodeParams& p, int num_sms, int occ_cap, cudaStream_t s,
                        int* workers_out) {
-  using T = Tuning<D, G, F8>;
-  return p.window > 0
-             ? launch_decode_t<D, G, T::WARPS, T::STAGES, F8, true>(p, num_sms, occ_cap, s, workers_out)
-             : launch_decode_t<D, G, T::WARPS, T::STAGES, F8, false>(p, num_sms, occ_cap, s,
-                                                                     workers_out);
+  using T = Tuning<D, G, KV>;
+  if constexpr (KV != 2)
+    if (p.window > 0)
+      return launch_decode_t<D, G, T::WARPS, T::STAGES, KV, true>(p, num_sms, occ_cap, s, workers_out);
+  return launch_decode_t<D, G, T::WARPS, T::STAGES, KV, false>(p, num_sms, occ_cap, s, workers_out);
 }
 
-template <int D, int G, bool F8>
+template <int D, int G, int KV>
 int workers_one(bool windowed, int num_sms, int occ_cap) {
-  using T = Tuning<D, G, F8>;
+  using T = Tuning<D, G, KV>;
   int grid = 0;
-  const cudaError_t e =
-      windowed ? decode_grid<D, G, T::WARPS, T::STAGES, F8, true>(num_sms, occ_cap, false, &grid)
-               : decode_grid<D, G, T::WARPS, T::STAGES, F8, false>(num_sms, occ_cap, false, &grid);
+  cudaError_t e;
+  if constexpr (KV != 2)
+    e = windowed ? decode_grid<D, G, T::WARPS, T::STAGES, KV, true>(num_sms, occ_cap, false, &grid)
+                 : decode_grid<D, G, T::WARPS, T::STAGES, KV, false>(num_sms, occ_cap, false, &grid);
+  else
+    e = decode_grid<D, G, T::WARPS, T::STAGES, KV, false>(num_sms, occ_cap, false, &grid);
   if (e != cudaSuccess) return 0;
   return grid * T::WARPS;
 }
 
-// Calls FN<D, G, F8>(args...) for the runtime (head_dim, group, f8).
-#define PA_DECODE_DISPATCH(FN, FAIL, ...)                                             \
-  do {                                                                                \
-    if (head_dim == 128) {                                                            \
-      switch (group) {                                                                \
-        case 1: return f8 ? FN<128, 1, true>(__VA_ARGS__) : FN<128, 1, false>(__VA_ARGS__); \
-        case 2: return f8 ? FN<128, 2, true>(__VA_ARGS__) : FN<128, 2, false>(__VA_ARGS__); \
-        case 4: return f8 ? FN<128, 4, true>(__VA_ARGS__) : FN<128, 4, false>(__VA_ARGS__); \
-        case 8: return f8 ? FN<128, 8, true>(__VA_ARGS__) : FN<128, 8, false>(__VA_ARGS__); \
-      }                                                                               \
-    } else if (head_dim == 64) {                                                      \
-      switch (group) {                                                                \
-        case 1: return f8 ? FN<64, 1, true>(__VA_ARGS__) : FN<64, 1, false>(__VA_ARGS__);   \
-        case 2: return f8 ? FN<64, 2, true>(__VA_ARGS__) : FN<64, 2, false>(__VA_ARGS__);   \
-        case 4: return f8 ? FN<64, 4, true>(__VA_ARGS__) : FN<64, 4, false>(__VA_ARGS__);   \
-        case 8: return f8 ? FN<64, 8, true>(__VA_ARGS__) : FN<64, 8, false>(__VA_ARGS__);   \
-      }                                                                               \
-    }                                                                                 \
-    return FAIL;                                                                      \
+// Calls FN<D, G, KV>(args...) for the runtime (head_dim, group, kv).
+#define PA_DECODE_KV(FN, D, G, ...)              \
+  (kv == 2   ? FN<D, G, 2>(__VA_ARGS__)          \
+   : kv == 1 ? FN<D, G, 1>(__VA_ARGS__)          \
+             : FN<D, G, 0>(__VA_ARGS__))
+#define PA_DECODE_DISPATCH(FN, FAIL, ...)                       \
+  do {                                                          \
+    if (head_dim == 128) {                                      \
+      switch (group) {                                          \
+        case 1: return PA_DECODE_KV(FN, 128, 1, __VA_ARGS__);   \
+        case 2: return PA_DECODE_KV(FN, 128, 2, __VA_ARGS__);   \
+        case 4: return PA_DECODE_KV(FN, 128, 4, __VA_ARGS__);   \
+        case 8: return PA_DECODE_KV(FN, 128, 8, __VA_ARGS__);   \
+      }                                                         \
+    } else if (head_dim == 64) {                                \
+      switch (group) {                                          \
+        case 1: return PA_DECODE_KV(FN, 64, 1, __VA_ARGS__);    \
+        case 2: return PA_DECODE_KV(FN, 64, 2, __VA_ARGS__);    \
+        case 4: return PA_DECODE_KV(FN, 64, 4, __VA_ARGS__);    \
+        case 8: return PA_DECODE_KV(FN, 64, 8, __VA_ARGS__);    \
+      }                                                         \
+    }                                                           \
+    return FAIL;                                                \
   } while (0)
 
-cudaError_t launch_decode(const DecodeParams& p, int head_dim, int group, bool f8, int num_sms,
+cudaError_t launch_decode(const DecodeParams& p, int head_dim, int group, int kv, int num_sms,
                           int occ_cap, cudaStream_t s, int* workers_out) {
   PA_DECODE_DISPATCH(launch_one, cudaErrorInvalidValue, p, num_sms, occ_cap, s, workers_out);
 }
 
-int decode_workers(int head_dim, int group, bool f8, bool windowed, int num_sms, int occ_cap) {
+int decode_workers(int head_dim, int group, int kv, bool windowed, int num_sms, int occ_cap) {
   PA_DECODE_DISPATCH(workers_one, 0, windowed, num_sms, occ_cap);
 }
 

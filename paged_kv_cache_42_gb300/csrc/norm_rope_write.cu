@@ -11,7 +11,8 @@
 // pa_write_kv does ("vLLM v1 Deep Dive: How LLM(...) and the Server Boot and
 // Generate", Part 3, "Aside - KV cache and prefix caching"). Everything
 // between the load and the store is binary32 and each result is rounded once
-// (for an E4M3 cache straight from binary32: E4M3(y / scale)).
+// (for an E4M3 cache straight from binary32: E4M3(y / scale), or with a
+// row-scaled one E4M3(y 2^-e), rows.cuh, from the row's largest |y|).
 //
 // What bounds it: bytes, each element once in and once out, with arithmetic
 // close behind; for a few tokens the launch and two dependent loads (position,
@@ -33,6 +34,7 @@
 
 #include "pa_internal.h"
 #include "ptx.cuh"
+#include "rows.cuh"
 
 namespace pa {
 
@@ -92,10 +94,29 @@ __device__ __forceinline__ uint2 pack_e4m3(const Pairs& v, float scale) {
                     two(v.x[2].x, v.x[2].y) | two(v.x[3].x, v.x[3].y) << 16);
 }
 
+// The same for a row of a row-scaled cache; *b: its scale's byte.
+template <bool INTER, int LPH>
+__device__ __forceinline__ uint2 pack_row(const Pairs& v, int lane, int* b) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) top = row_top(row_top(top, v.x[e].x), v.x[e].y);
+  *b = row_scale_byte(row_top_all<LPH>(top, lane));
+  const float inv = row_inverse(*b);
+  if constexpr (INTER)
+    return make_uint2(
+        row_codes(v.x[0].x, v.x[2].x, inv) | row_codes(v.x[0].y, v.x[2].y, inv) << 16,
+        row_codes(v.x[1].x, v.x[3].x, inv) | row_codes(v.x[1].y, v.x[3].y, inv) << 16);
+  return make_uint2(
+      row_codes(v.x[0].x, v.x[0].y, inv) | row_codes(v.x[1].x, v.x[1].y, inv) << 16,
+      row_codes(v.x[2].x, v.x[2].y, inv) | row_codes(v.x[3].x, v.x[3].y, inv) << 16);
+}
+
 // At least nine CTAs on an SM into a bf16 cache (56 registers): with 64 registers
-// and eight of them 2048 tokens took 9% longer. The E4M3 form does not fit 56.
-template <int D, bool F8, bool INTER, int ITER>
-__global__ void __launch_bounds__(kThreads, F8 ? 8 : 9) pa_norm_rope_write_kernel(const NormRopeParams p) {
+// and eight of them 2048 tokens took 9% longer. The E4M3 forms do not fit 56.
+// KV: what the caches hold, 0 bf16, 1 E4M3 with one scale per tensor, 2 row-scaled.
+template <int D, int KV, bool INTER, int ITER>
+__global__ void __launch_bounds__(kThreads, KV ? 8 : 9) pa_norm_rope_write_kernel(const NormRopeParams p) {
+  constexpr bool F8 = KV != 0;
   constexpr int LPH = D / 8;     // lanes per head
   constexpr int HPG = 32 / LPH;  // heads per group
   const int lane = threadIdx.x & 31;
@@ -179,12 +200,22 @@ __global__ void __launch_bounds__(kThreads, F8 ? 8 : 9) pa_norm_rope_write_kerne
       *reinterpret_cast<uint32_t*>(at + eb) = o.y;
     }
   };
+  // a row-scaled cache's row: its codes, and one lane its scale
+  auto store_row = [&](void* base, int row, const Pairs& v, int which) {
+    int b;
+    store8(base, row, pack_row<INTER, LPH>(v, lane, &b));
+    if (sub == 0)
+      p.scales[((slot >> 4) * nk + row) * kScaleBytes + which * kBlockSize + (slot & 15)] =
+          (unsigned char)b;
+  };
   if (kind == 2) {
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
       const int row = row0 + i * HPG;
       if (row >= rows) break;
-      if constexpr (F8)
+      if constexpr (KV == 2)
+        store_row(p.v_cache, row, unpack<INTER>(raw[i]), 1);
+      else if constexpr (F8)
         store8(p.v_cache, row, pack_e4m3<INTER>(unpack<INTER>(raw[i]), p.v_scale));
       else
         store(p.v_cache, row, raw[i]);
@@ -230,7 +261,9 @@ __global__ void __launch_bounds__(kThreads, F8 ? 8 : 9) pa_norm_rope_write_kerne
           v.x[2 + e] = ffma2(a, s[e], fmul2(b, c[e]));
         }
       }
-      if (F8 && kind == 1) {
+      if (KV == 2 && kind == 1) {
+        store_row(p.k_cache, row, v, 0);
+      } else if (F8 && kind == 1) {
         store8(p.k_cache, row, pack_e4m3<INTER>(v, p.k_scale));
       } else {
         // neither normalised nor turned: the bits as they came, a NaN's too
@@ -244,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, F8 ? 8 : 9) pa_norm_rope_write_kerne
     heads(std::false_type{});
 }
 
-template <int D, bool F8, bool INTER>
+template <int D, int KV, bool INTER>
 cudaError_t launch_nr(const NormRopeParams& p, int num_sms, cudaStream_t s) {
   constexpr int HPG = 32 / (D / 8);
   auto blocks = [&](int iter) {
@@ -266,17 +299,22 @@ cudaError_t launch_nr(const NormRopeParams& p, int num_sms, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return small ? cudaLaunchKernelEx(&cfg, pa_norm_rope_write_kernel<D, F8, INTER, 1>, p)
-               : cudaLaunchKernelEx(&cfg, pa_norm_rope_write_kernel<D, F8, INTER, kManyIter>, p);
+  return small ? cudaLaunchKernelEx(&cfg, pa_norm_rope_write_kernel<D, KV, INTER, 1>, p)
+               : cudaLaunchKernelEx(&cfg, pa_norm_rope_write_kernel<D, KV, INTER, kManyIter>, p);
 }
 
 template <int D>
 cudaError_t launch_nr_d(const NormRopeParams& p, int num_sms, cudaStream_t s) {
-  if (p.kv_fp8)
-    return p.interleaved ? launch_nr<D, true, true>(p, num_sms, s)
-                         : launch_nr<D, true, false>(p, num_sms, s);
-  return p.interleaved ? launch_nr<D, false, true>(p, num_sms, s)
-                       : launch_nr<D, false, false>(p, num_sms, s);
+  switch (p.kv_fp8) {
+    case 2:
+      return p.interleaved ? launch_nr<D, 2, true>(p, num_sms, s)
+                           : launch_nr<D, 2, false>(p, num_sms, s);
+    case 1:
+      return p.interleaved ? launch_nr<D, 1, true>(p, num_sms, s)
+                           : launch_nr<D, 1, false>(p, num_sms, s);
+  }
+  return p.interleaved ? launch_nr<D, 0, true>(p, num_sms, s)
+                       : launch_nr<D, 0, false>(p, num_sms, s);
 }
 
 }  // namespace

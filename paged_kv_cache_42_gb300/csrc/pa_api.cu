@@ -47,7 +47,8 @@ std::atomic<int> g_cascade_overlap{1};  // pa_set_option(PA_OPT_CASCADE_OVERLAP,
 std::atomic<int> g_tm_ctas{2};  // pa_set_option(PA_OPT_DECODE_TM_CTAS_PER_SM, ...)
 std::atomic<int> g_write_overlap{0};  // pa_set_option(PA_OPT_WRITE_OVERLAP, ...)
 std::atomic<int> g_mixed_ctas{0};  // pa_set_option(PA_OPT_MIXED_PREFILL_CTAS, ...): 0 = planned
-constexpr int kNumTimers = 8;  // write, plan, decode, prefill, cascade prefix, merge, weights, evict
+// write, plan, decode, prefill, cascade prefix, merge, weights, evict, read
+constexpr int kNumTimers = 9;
 cudaEvent_t g_timer_start[kNumTimers] = {};
 cudaEvent_t g_timer_stop[kNumTimers] = {};
 
@@ -216,7 +217,8 @@ pa_status norm_rope_write_impl(const void* q, const void* k, const void* v, long
                                const int64_t* slot_mapping, void* q_out, void* k_cache,
                                void* v_cache, int kv_fp8, float k_scale, float v_scale,
                                int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
-                               int block_size, int num_blocks, void* stream) {
+                               int block_size, int num_blocks, void* stream,
+                               unsigned char* scales = nullptr) {  // kv_fp8 2: row-scaled
   if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || num_blocks < 0 ||
       rotary_dim < 0 || rotary_dim > head_dim || max_position < 0 || !(eps >= 0.f && eps < INFINITY))
     return PA_ERR_INVALID_ARG;
@@ -225,8 +227,11 @@ pa_status norm_rope_write_impl(const void* q, const void* k, const void* v, long
   if (block_size != kBlockSize || (head_dim != 64 && head_dim != 128) || rotary_dim % 16 != 0 ||
       num_q_heads > kMaxRopeHeads || num_kv_heads > kMaxRopeHeads)
     return PA_ERR_UNSUPPORTED;
-  const NvtxRange range(kv_fp8 ? "pa_norm_rope_write_kv_fp8" : "pa_norm_rope_write_kv");
+  const NvtxRange range(kv_fp8 == 2 ? "pa_norm_rope_write_kv_rows"
+                        : kv_fp8    ? "pa_norm_rope_write_kv_fp8"
+                                    : "pa_norm_rope_write_kv");
   if (num_tokens == 0) return PA_OK;
+  if (kv_fp8 == 2 && (!scales || !aligned16(scales))) return PA_ERR_INVALID_ARG;
   if (!q || !k || !v || !slot_mapping || !q_out || !k_cache || !v_cache ||
       (rotary_dim > 0 && (!positions || !cos_sin)))
     return PA_ERR_INVALID_ARG;
@@ -266,6 +271,7 @@ pa_status norm_rope_write_impl(const void* q, const void* k, const void* v, long
   p.kv_fp8 = kv_fp8;
   p.k_scale = k_scale;
   p.v_scale = v_scale;
+  p.scales = scales;
   p.num_tokens = num_tokens;
   p.num_q_heads = num_q_heads;
   p.num_kv_heads = num_kv_heads;
@@ -353,7 +359,8 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
                          int block_size, int num_blocks, int max_blocks_per_req,
                          int max_query_len, int max_seq_len, int prefix_len, int window,
                          int sinks, int kv_fp8, float k_scale, float v_scale, void* workspace,
-                         size_t workspace_bytes, void* stream) {
+                         size_t workspace_bytes, void* stream,
+                         const unsigned char* scales = nullptr) {  // kv_fp8 2: row-scaled
   bool nothing = false;
   const bool windowed = window > 0;
   // a window that holds every key of the batch hides none
@@ -368,7 +375,8 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
           &nothing))
     return st;
   if (nothing) return PA_OK;
-  if (windowed && num_blocks < 1) return PA_ERR_INVALID_ARG;  // no block to attend to
+  if (kv_fp8 == 2 && (!scales || !aligned16(scales))) return PA_ERR_INVALID_ARG;
+  if ((windowed || kv_fp8 == 2) && num_blocks < 1) return PA_ERR_INVALID_ARG;  // none to attend to
   const WsLayout lay = ws_layout(num_reqs, num_tokens, num_q_heads, num_kv_heads, head_dim);
   const size_t need =
       lay.total + (prefix_len > 0
@@ -380,6 +388,7 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
   DeviceState* d = nullptr;
   if (pa_status st = device_state(&d)) return st;
   const NvtxRange range(prefix_len > 0 ? "pa_attention_cascade"
+                        : kv_fp8 == 2  ? "pa_attention_rows"
                         : window > 0   ? (kv_fp8 ? "pa_attention_window_fp8" : "pa_attention_window")
                                        : (kv_fp8 ? "pa_attention_fp8" : "pa_attention"));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -426,7 +435,7 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
   // the per-(token, kv head) epilogue better (measured 39 vs 76 us on the
   // prefix-sharing batch).
   const int tc_mode = g_decode_tc.load();
-  const bool use_tc = tc_mode != 0 &&
+  const bool use_tc = tc_mode != 0 && kv_fp8 != 2 &&
                       decode_tc_supported(head_dim, group, kv_fp8 != 0, prefix_len / kBlockSize) &&
                       (tc_mode == 2 || (group >= PA_DECODE_TC_MIN_GROUP && prefix_len == 0));
   // A cascade on the CUDA-core suffix pass may run its prefix pass on a few
@@ -467,7 +476,7 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
       decode_tm_supported(head_dim, group, num_kv_heads, decode_tm_workers(group, d->num_sms, tm_cps));
   const int launched = use_tm   ? decode_tm_workers(group, d->num_sms, tm_cps)
                        : use_tc ? decode_tc_workers(d->num_sms)
-                                : decode_workers(head_dim, pp.group, kv_fp8 != 0, window > 0, dec_sms,
+                                : decode_workers(head_dim, pp.group, kv_fp8, window > 0, dec_sms,
                                                 occ_cap);
   if (launched <= 0) return PA_ERR_CUDA;
   const int cap = g_max_workers.load();
@@ -510,6 +519,7 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
     pl.prefix_partials = prefix_partials;
     pl.kv_fp8 = kv_fp8;
     pl.v_scale = kv_fp8 ? v_scale : 1.f;
+    pl.scales = scales;
     pl.q = q;
     pl.k_cache = k_cache;
     pl.v_cache = v_cache;
@@ -542,6 +552,7 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
   dp.k_cache = k_cache;
   dp.v_cache = v_cache;
   dp.v_scale = kv_fp8 ? v_scale : 1.f;
+  dp.scales = scales;
   dp.block_tables = block_tables;
   dp.out = static_cast<uint16_t*>(out);
   dp.bt_stride = max_blocks_per_req;
@@ -589,7 +600,7 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
     const cudaError_t e =
         use_tm   ? launch_decode_tm(dp, group, d->num_sms, tm_cps, s, &launched_workers)
         : use_tc ? launch_decode_tc(dp, group, kv_fp8 != 0, d->num_sms, s, &launched_workers)
-                 : launch_decode(dp, head_dim, group, kv_fp8 != 0, dec_sms, occ_cap, s,
+                 : launch_decode(dp, head_dim, group, kv_fp8, dec_sms, occ_cap, s,
                                  &launched_workers);
     g_launches.fetch_add(1);
     if (e != cudaSuccess) return PA_ERR_CUDA;
@@ -901,6 +912,12 @@ size_t pa_args_size(int which) {
     case 2: return sizeof(pa_weights_args);
     case 3: return sizeof(pa_evict_args);
   }
+  switch (which - 16) {  // the calls that take a struct only
+    case 0: return sizeof(pa_write_rows_args);
+    case 1: return sizeof(pa_norm_rope_write_rows_args);
+    case 2: return sizeof(pa_attention_rows_args);
+    case 3: return sizeof(pa_read_args);
+  }
   return 0;
 }
 
@@ -946,6 +963,115 @@ pa_status pa_evict_kv_args(const pa_evict_args* a) {
                      a->num_kv_heads, a->head_dim, a->elem_bytes, a->block_size, a->num_blocks,
                      a->max_blocks_per_req, a->max_new_blocks, a->weights_stride,
                      a->new_weights_stride, a->max_seq_len, a->keep, a->recent, a->sinks, a->stream);
+}
+
+// Row-scaled caches, and reading back.
+pa_status pa_write_kv_rows(const pa_write_rows_args* a) {
+  if (!a) return PA_ERR_INVALID_ARG;
+  if (a->num_tokens < 0 || a->num_kv_heads <= 0 || a->head_dim <= 0 || a->num_blocks < 0)
+    return PA_ERR_INVALID_ARG;
+  if (a->block_size != kBlockSize || (a->head_dim != 64 && a->head_dim != 128) ||
+      a->num_kv_heads > kMaxRopeHeads)
+    return PA_ERR_UNSUPPORTED;
+  const NvtxRange range("pa_write_kv_rows");
+  if (a->num_tokens == 0) return PA_OK;
+  if (!a->k || !a->v || !a->slot_mapping || !a->k_cache || !a->v_cache || !a->scales)
+    return PA_ERR_INVALID_ARG;
+  if (!aligned16(a->k) || !aligned16(a->v) || !aligned16(a->k_cache) || !aligned16(a->v_cache) ||
+      !aligned16(a->scales) || (reinterpret_cast<uintptr_t>(a->slot_mapping) & 7u))
+    return PA_ERR_INVALID_ARG;
+  const long long kv_row = (long long)a->num_kv_heads * a->head_dim;
+  if (a->k_stride < kv_row || a->v_stride < kv_row || a->k_stride % 8 != 0 || a->v_stride % 8 != 0)
+    return PA_ERR_INVALID_ARG;
+  DeviceState* d = nullptr;
+  if (pa_status st = device_state(&d)) return st;
+  WriteRowsParams p;
+  p.k = static_cast<const uint16_t*>(a->k);
+  p.v = static_cast<const uint16_t*>(a->v);
+  p.k_stride = a->k_stride;
+  p.v_stride = a->v_stride;
+  p.slot_mapping = a->slot_mapping;
+  p.k_cache = static_cast<unsigned char*>(a->k_cache);
+  p.v_cache = static_cast<unsigned char*>(a->v_cache);
+  p.scales = a->scales;
+  p.num_tokens = a->num_tokens;
+  p.num_kv_heads = a->num_kv_heads;
+  p.num_slots = (long long)a->num_blocks * kBlockSize;
+  p.err = d->err;
+  cudaStream_t s = static_cast<cudaStream_t>(a->stream);
+  TimerScope timer(0, s);
+  const cudaError_t e = launch_write_rows(p, a->head_dim, s);
+  g_launches.fetch_add(1);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_norm_rope_write_kv_rows(const pa_norm_rope_write_rows_args* a) {
+  if (!a) return PA_ERR_INVALID_ARG;
+  return norm_rope_write_impl(a->q, a->k, a->v, a->q_stride, a->k_stride, a->v_stride, a->positions,
+                              a->cos_sin, a->q_weight, a->k_weight, a->eps, a->rotary_dim,
+                              a->interleaved, a->max_position, a->slot_mapping, a->q_out,
+                              a->k_cache, a->v_cache, 2, 1.f, 1.f, a->num_tokens, a->num_q_heads,
+                              a->num_kv_heads, a->head_dim, a->block_size, a->num_blocks, a->stream,
+                              a->scales);
+}
+
+pa_status pa_attention_rows(const pa_attention_rows_args* a) {
+  if (!a) return PA_ERR_INVALID_ARG;
+  return attention_impl(a->q, a->k_cache, a->v_cache, a->block_tables, a->seq_lens,
+                        a->query_start_loc, a->scale, a->out, a->num_reqs, a->num_tokens,
+                        a->num_q_heads, a->num_kv_heads, a->head_dim, a->block_size, a->num_blocks,
+                        a->max_blocks_per_req, a->max_query_len, a->max_seq_len, 0, 0, 0, 2, 1.f,
+                        1.f, a->workspace, a->workspace_bytes, a->stream, a->scales);
+}
+
+pa_status pa_read_kv(const pa_read_args* a) {
+  if (!a) return PA_ERR_INVALID_ARG;
+  if (a->num_reqs < 0 || a->num_tokens < 0 || a->num_kv_heads <= 0 || a->head_dim <= 0 ||
+      a->num_blocks < 0 || a->max_blocks_per_req < 0 || a->kv_format < 0 || a->kv_format > 2)
+    return PA_ERR_INVALID_ARG;
+  if (a->kv_format == 1 && !(a->k_scale > 0.f && a->k_scale < INFINITY && a->v_scale > 0.f &&
+                             a->v_scale < INFINITY))
+    return PA_ERR_INVALID_ARG;
+  if (a->block_size != kBlockSize || (a->head_dim != 64 && a->head_dim != 128) ||
+      a->num_kv_heads > kMaxRopeHeads / 8)
+    return PA_ERR_UNSUPPORTED;
+  const NvtxRange range("pa_read_kv");
+  if (a->num_reqs == 0 || a->num_tokens == 0) return PA_OK;
+  if (a->num_blocks < 1) return PA_ERR_INVALID_ARG;  // no block to read
+  if (!a->k_cache || !a->v_cache || !a->block_tables || !a->read_start_loc || !a->k_out ||
+      !a->v_out || (a->kv_format == 2 && !a->scales))
+    return PA_ERR_INVALID_ARG;
+  if (!aligned16(a->k_cache) || !aligned16(a->v_cache) || !aligned16(a->scales) ||
+      (reinterpret_cast<uintptr_t>(a->k_out) & 31u) || (reinterpret_cast<uintptr_t>(a->v_out) & 31u))
+    return PA_ERR_INVALID_ARG;
+  const void* words[] = {a->block_tables, a->read_start_loc, a->first};
+  for (const void* w : words)
+    if (reinterpret_cast<uintptr_t>(w) & 3u) return PA_ERR_INVALID_ARG;
+  DeviceState* d = nullptr;
+  if (pa_status st = device_state(&d)) return st;
+  ReadParams p;
+  p.k_cache = a->k_cache;
+  p.v_cache = a->v_cache;
+  p.scales = a->scales;
+  p.k_scale = a->k_scale;
+  p.v_scale = a->v_scale;
+  p.block_tables = a->block_tables;
+  p.read_start_loc = a->read_start_loc;
+  p.first = a->first;
+  p.k_out = static_cast<uint16_t*>(a->k_out);
+  p.v_out = static_cast<uint16_t*>(a->v_out);
+  p.num_reqs = a->num_reqs;
+  p.num_tokens = a->num_tokens;
+  p.num_kv_heads = a->num_kv_heads;
+  p.num_blocks = a->num_blocks;
+  p.max_blocks_per_req = a->max_blocks_per_req;
+  p.tokens_per_cta = 0;
+  p.err = d->err;
+  cudaStream_t s = static_cast<cudaStream_t>(a->stream);
+  TimerScope timer(8, s);
+  const cudaError_t e = launch_read(p, a->head_dim, a->kv_format, d->num_sms, s);
+  g_launches.fetch_add(1);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 pa_status pa_mapped_pointer(const void* host_ptr, void** device_ptr) {

@@ -251,8 +251,9 @@ struct PrefillLaunch {
   float* prefix_partials;
   // E4M3 caches: k_cache / v_cache hold codes; k_scale is already folded into
   // scale_log2, v_scale multiplies the output
-  int kv_fp8;
+  int kv_fp8;  // 2: row-scaled (scales)
   float v_scale;
+  const unsigned char* scales;
   const void* q;
   const void* k_cache;
   const void* v_cache;
@@ -277,6 +278,7 @@ struct DecodeParams {
   const uint16_t* q;
   const void* k_cache;  // bf16, or E4M3 codes in the f8 instantiation
   const void* v_cache;
+  const unsigned char* scales;  // row-scaled caches: [num_blocks][num_kv_heads][2][16]
   float v_scale;        // output multiplier: the E4M3 V scale, 1 for bf16
   const int32_t* block_tables;
   uint16_t* out;
@@ -381,10 +383,39 @@ struct NormRopeParams {
   uint16_t* q_out;
   void* k_cache;  // bf16, or E4M3 codes when kv_fp8
   void* v_cache;
-  int kv_fp8;
+  int kv_fp8;     // 2: row-scaled, into `scales`
   float k_scale, v_scale;
+  unsigned char* scales;
   int num_tokens, num_q_heads, num_kv_heads;
   long long num_slots;
+  unsigned long long* err;
+};
+
+struct WriteRowsParams {  // row-scaled E4M3 cache (rows.cuh)
+  const uint16_t* k;
+  const uint16_t* v;
+  long long k_stride, v_stride;  // elements from one token to the next
+  const int64_t* slot_mapping;
+  unsigned char* k_cache;
+  unsigned char* v_cache;
+  unsigned char* scales;
+  int num_tokens, num_kv_heads;
+  long long num_slots;
+  unsigned long long* err;
+};
+
+struct ReadParams {
+  const void* k_cache;
+  const void* v_cache;
+  const unsigned char* scales;  // row-scaled caches
+  float k_scale, v_scale;       // E4M3 caches with one scale per tensor
+  const int32_t* block_tables;
+  const int32_t* read_start_loc;
+  const int32_t* first;  // null: key 0 of every request
+  uint16_t* k_out;
+  uint16_t* v_out;
+  int num_reqs, num_tokens, num_kv_heads, num_blocks, max_blocks_per_req;
+  int tokens_per_cta;  // set at launch
   unsigned long long* err;
 };
 
@@ -472,6 +503,9 @@ pa_status check_attention_args(const void* q, const void* k_cache, const void* v
 cudaError_t launch_write_kv(const WriteParams& p, cudaStream_t s);
 cudaError_t launch_norm_rope_write(const NormRopeParams& p, int head_dim, int num_sms,
                                    cudaStream_t s);
+cudaError_t launch_write_rows(const WriteRowsParams& p, int head_dim, cudaStream_t s);
+// format: 0 bf16, 1 E4M3 with one scale per tensor, 2 row-scaled E4M3.
+cudaError_t launch_read(ReadParams p, int head_dim, int format, int num_sms, cudaStream_t s);
 // The accumulated-weight kernels, in order; *launches: how many.
 cudaError_t launch_weights(WeightsParams p, int head_dim, bool f8, int num_sms, cudaStream_t s,
                            int* launches);
@@ -481,13 +515,13 @@ cudaError_t launch_plan(const PlanParams& p, cudaStream_t s);
 // head_dim / G select the instantiation; unsupported combinations return
 // cudaErrorInvalidValue. occ_cap bounds the resident CTAs per SM (the grid is
 // SMs x min(occupancy, occ_cap)).
-// f8 selects the E4M3-cache instantiation.
-cudaError_t launch_decode(const DecodeParams& p, int head_dim, int group, bool f8, int num_sms,
+// kv: the caches, 0 bf16, 1 E4M3 with one scale per tensor, 2 row-scaled E4M3.
+cudaError_t launch_decode(const DecodeParams& p, int head_dim, int group, int kv, int num_sms,
                           int occ_cap, cudaStream_t s, int* workers_out);
 // The merge pass after a split-KV launch of num_workers workers (p.num_workers).
 cudaError_t launch_merge(const MergeParams& p, int head_dim, int group, cudaStream_t s);
 // Split-KV workers launch_decode will use on this device (0 on error).
-int decode_workers(int head_dim, int group, bool f8, bool windowed, int num_sms, int occ_cap);
+int decode_workers(int head_dim, int group, int kv, bool windowed, int num_sms, int occ_cap);
 
 // Tensor-core split-KV decode (decode_tc.cu): one CTA per SM is one worker.
 // Supported for head_dim 128, over a bf16 cache (a cascade's suffix pass

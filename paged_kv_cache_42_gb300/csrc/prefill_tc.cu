@@ -44,7 +44,9 @@
 // coalesced loads (one thread per key row) and widen them to bf16 - exactly,
 // every E4M3 value being a bf16 - straight into the 128B-swizzled operand
 // layout the MMA reads, then arrive on the stage's full barrier. k_scale is
-// folded into the softmax scale and v_scale into the epilogue.
+// folded into the softmax scale and v_scale into the epilogue. Over row-scaled
+// caches (KV 2, rows.cuh) the converters multiply each row by its 2^e, which is
+// exact in bf16 too, and nothing else differs.
 //
 // Warp roles (320 threads): warp 0 issues TMA loads (both Q tiles per work
 // item, K into a 3-stage ring released right after both S MMAs of a key tile,
@@ -62,6 +64,7 @@
 
 #include "pa_internal.h"
 #include "ptx.cuh"
+#include "rows.cuh"
 
 namespace pa {
 
@@ -156,6 +159,7 @@ struct PrefillParams {
   // E4M3 caches (F8): raw codes and the output multiplier (1 for bf16)
   const unsigned char* k_cache8;
   const unsigned char* v_cache8;
+  const unsigned char* scales;  // KV 2
   float v_scale;
   int overlap;  // PrefillLaunch::overlap
   int window, sinks;  // WIN
@@ -234,9 +238,11 @@ __device__ __forceinline__ int snake_item(int r, int g) {
 // be stale - and counts as zeros in V. A row may see no key of its item's
 // first tiles: it has no reference then, and the first tile it does see
 // rescales a zero O by zero.
-template <int D, int G, bool PREFIX, bool F8, bool WIN>
-__global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
+// KV: the caches, 0 bf16, 1 E4M3 with one scale per tensor, 2 row-scaled E4M3.
+template <int D, int G, bool PREFIX, int KV, bool WIN>
+__global__ void __launch_bounds__(KV ? kThreadsF8 : kThreads, 1)
     pa_prefill_kernel(const __grid_constant__ PrefillParams p) {
+  constexpr bool F8 = KV != 0;
   using C = PCfg<D, G>;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -747,23 +753,30 @@ __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreads, 1)
         const int key = key_tile<WIN>(tl, i) * 128 + r;
         bool valid = WIN ? item_sees(tl, key, 1, p.sinks) : key < tl.L;
         size_t src = 0;
+        float ksz = 1.f, vsz = 1.f;  // KV 2: the row's sizes
         if (valid) {
           const int pid = __ldg(bt_row + key / kBlockSize);
           if (pid < 0 || pid >= p.num_blocks) {
             report_error(p.err, PA_DEVERR_BLOCK_ID, key / kBlockSize);
             valid = false;
           } else {
-            src = (((size_t)pid * p.num_kv_heads + tl.kv) * kBlockSize + (key % kBlockSize)) * D;
+            const size_t tile = (size_t)pid * p.num_kv_heads + tl.kv;
+            src = (tile * kBlockSize + (key % kBlockSize)) * D;
+            if constexpr (KV == 2) {
+              const unsigned char* const sc = p.scales + tile * kScaleBytes + key % kBlockSize;
+              ksz = row_size(__ldg(sc));
+              vsz = row_size(__ldg(sc + kBlockSize));
+            }
           }
         }
         const int ks = g % C::KSTAGES, vs = g % C::VSTAGES;
         if (g >= C::KSTAGES && !wait(B_K_EMPTY + ks, ((g / C::KSTAGES) - 1) & 1)) { ok = false; break; }
-        widen_e4m3_row<D>(p.k_cache8 + src, valid, gbase + C::OFF_K + ks * C::KV_BYTES, r);
+        widen_e4m3_row<D, KV == 2>(p.k_cache8 + src, valid, gbase + C::OFF_K + ks * C::KV_BYTES, r, ksz);
         fence_proxy_async_smem();  // generic-proxy stores -> visible to the tensor core
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(B_K_FULL + ks));
         if (g >= C::VSTAGES && !wait(B_V_EMPTY + vs, ((g / C::VSTAGES) - 1) & 1)) { ok = false; break; }
-        widen_e4m3_row<D>(p.v_cache8 + src, valid, gbase + C::OFF_V + vs * C::KV_BYTES, r);
+        widen_e4m3_row<D, KV == 2>(p.v_cache8 + src, valid, gbase + C::OFF_V + vs * C::KV_BYTES, r, vsz);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(B_V_FULL + vs));
@@ -861,9 +874,10 @@ bool encode_tmap_u8(void* tmap, int rank, const void* ptr, const uint64_t* dims,
 
 namespace {
 
-template <int D, int G, bool PREFIX, bool F8, bool WIN>
+template <int D, int G, bool PREFIX, int KV, bool WIN>
 cudaError_t launch_prefill_t(const PrefillLaunch& a, int num_sms, cudaStream_t s) {
   using C = PCfg<D, G>;
+  constexpr bool F8 = KV != 0;
   PrefillParams p;
   {
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.num_q_heads, (cuuint64_t)a.num_tokens};
@@ -900,6 +914,7 @@ cudaError_t launch_prefill_t(const PrefillLaunch& a, int num_sms, cudaStream_t s
   p.prefix_partials = a.prefix_partials;
   p.k_cache8 = F8 ? static_cast<const unsigned char*>(a.k_cache) : nullptr;
   p.v_cache8 = F8 ? static_cast<const unsigned char*>(a.v_cache) : nullptr;
+  p.scales = a.scales;
   p.v_scale = F8 ? a.v_scale : 1.f;
   p.overlap = a.overlap;
   p.window = a.window;
@@ -912,7 +927,7 @@ cudaError_t launch_prefill_t(const PrefillLaunch& a, int num_sms, cudaStream_t s
     if (a.overlap && a.prefix_ctas > 0 && a.prefix_ctas < grid) grid = a.prefix_ctas;
   }
 
-  auto kern = pa_prefill_kernel<D, G, PREFIX, F8, WIN>;
+  auto kern = pa_prefill_kernel<D, G, PREFIX, KV, WIN>;
   static bool attr_set[64] = {false};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -937,22 +952,22 @@ cudaError_t launch_prefill_t(const PrefillLaunch& a, int num_sms, cudaStream_t s
 
 }  // namespace
 
-template <bool PREFIX, bool F8, bool WIN>
+template <bool PREFIX, int KV, bool WIN>
 cudaError_t launch_prefill_mode(const PrefillLaunch& a, int num_sms, cudaStream_t s) {
   const int G = a.num_q_heads / a.num_kv_heads;
   if (a.head_dim == 128) {
     switch (G) {
-      case 1: return launch_prefill_t<128, 1, PREFIX, F8, WIN>(a, num_sms, s);
-      case 2: return launch_prefill_t<128, 2, PREFIX, F8, WIN>(a, num_sms, s);
-      case 4: return launch_prefill_t<128, 4, PREFIX, F8, WIN>(a, num_sms, s);
-      case 8: return launch_prefill_t<128, 8, PREFIX, F8, WIN>(a, num_sms, s);
+      case 1: return launch_prefill_t<128, 1, PREFIX, KV, WIN>(a, num_sms, s);
+      case 2: return launch_prefill_t<128, 2, PREFIX, KV, WIN>(a, num_sms, s);
+      case 4: return launch_prefill_t<128, 4, PREFIX, KV, WIN>(a, num_sms, s);
+      case 8: return launch_prefill_t<128, 8, PREFIX, KV, WIN>(a, num_sms, s);
     }
   } else if (a.head_dim == 64) {
     switch (G) {
-      case 1: return launch_prefill_t<64, 1, PREFIX, F8, WIN>(a, num_sms, s);
-      case 2: return launch_prefill_t<64, 2, PREFIX, F8, WIN>(a, num_sms, s);
-      case 4: return launch_prefill_t<64, 4, PREFIX, F8, WIN>(a, num_sms, s);
-      case 8: return launch_prefill_t<64, 8, PREFIX, F8, WIN>(a, num_sms, s);
+      case 1: return launch_prefill_t<64, 1, PREFIX, KV, WIN>(a, num_sms, s);
+      case 2: return launch_prefill_t<64, 2, PREFIX, KV, WIN>(a, num_sms, s);
+      case 4: return launch_prefill_t<64, 4, PREFIX, KV, WIN>(a, num_sms, s);
+      case 8: return launch_prefill_t<64, 8, PREFIX, KV, WIN>(a, num_sms, s);
     }
   }
   return cudaErrorInvalidValue;
@@ -962,13 +977,15 @@ cudaError_t launch_prefill(const PrefillLaunch& a, int num_sms, cudaStream_t s) 
   if (!get_encoder()) return cudaErrorNotSupported;
   if (a.kv_fp8) {
     if (a.prefix_len > 0) return cudaErrorNotSupported;  // no FP8 cascade
-    return a.window > 0 ? launch_prefill_mode<false, true, true>(a, num_sms, s)
-                        : launch_prefill_mode<false, true, false>(a, num_sms, s);
+    if (a.kv_fp8 == 2)  // windows have no row-scaled form
+      return a.window > 0 ? cudaErrorNotSupported : launch_prefill_mode<false, 2, false>(a, num_sms, s);
+    return a.window > 0 ? launch_prefill_mode<false, 1, true>(a, num_sms, s)
+                        : launch_prefill_mode<false, 1, false>(a, num_sms, s);
   }
   if (a.window > 0)  // never with a prefix
-    return launch_prefill_mode<false, false, true>(a, num_sms, s);
-  return a.prefix_len > 0 ? launch_prefill_mode<true, false, false>(a, num_sms, s)
-                          : launch_prefill_mode<false, false, false>(a, num_sms, s);
+    return launch_prefill_mode<false, 0, true>(a, num_sms, s);
+  return a.prefix_len > 0 ? launch_prefill_mode<true, 0, false>(a, num_sms, s)
+                          : launch_prefill_mode<false, 0, false>(a, num_sms, s);
 }
 
 }  // namespace pa
