@@ -10,8 +10,9 @@
 // the place of its subnormals (below 2^-14 of that element). It makes the value
 // code x 2^e a bf16 number, so the tensor cores take widened rows exactly and
 // reading back rounds nothing, and it is a quarter of an fp32 scale's bytes.
-// A row with an infinity or a NaN gets b = 255 and codes of zero: 255 << 23 is
-// the binary32 infinity, and 0 x inf the NaN that the row then stands for.
+// A row with an infinity or a NaN gets b = 255, which stands for NaN, and codes
+// of zero (an E4M3 NaN among the codes of a tile would spread further than its
+// row: 0 x NaN in the products of other rows).
 #pragma once
 
 #include "ptx.cuh"
@@ -33,8 +34,10 @@ __device__ __forceinline__ int row_scale_byte(uint32_t top) {
 __device__ __forceinline__ float row_inverse(int b) {
   return b == kRowPoison ? 0.f : __uint_as_float((uint32_t)(254 - b) << 23);
 }
-// 2^e; infinity for a poisoned row.
-__device__ __forceinline__ float row_size(int b) { return __uint_as_float((uint32_t)b << 23); }
+// 2^e; NaN for a poisoned row.
+__device__ __forceinline__ float row_size(int b) {
+  return __uint_as_float(b == kRowPoison ? 0x7fc00000u : (uint32_t)b << 23);
+}
 
 // Largest |x| so far, as binary32 bits.
 __device__ __forceinline__ uint32_t row_top(uint32_t top, float x) {
