@@ -83,7 +83,9 @@ typedef enum pa_status {
 #define PA_DEVERR_QSL 4          /* pa_attention: query_start_loc not within [0, num_tokens] */
 #define PA_DEVERR_WAIT_TIMEOUT 5 /* a kernel's bounded wait on a copy gave up */
 #define PA_DEVERR_PREFIX 6       /* pa_attention_cascade: a request's table does not start
-                                    with request 0's common-prefix blocks */
+                                    with request 0's common-prefix blocks;
+                                    pa_attention_shared: with its group's, or a
+                                    group's prefix length is not one */
 #define PA_DEVERR_POSITION 7     /* pa_norm_rope_write_kv: a position outside the table */
 
 /*
@@ -637,6 +639,53 @@ typedef struct pa_read_args { /* 19 */
   int max_blocks_per_req;
 } pa_read_args;
 pa_status pa_read_kv(const pa_read_args* args);
+
+/*
+ * Attention for a batch whose requests share prefixes in groups, over any cache
+ * format: pa_attention's result (up to the order of sums and the tolerances of
+ * the kernels), with every group's prefix attended to once for all of its tokens.
+ * The pages describe one prefix common to the whole batch ("vLLM: An Exhaustive
+ * Technical Study for Kernel Engineers", 2.3, cascade attention; here
+ * pa_attention_cascade) and fall back to plain attention for a forest of them.
+ *   group_start_loc  [num_groups + 1] int32, non-decreasing: requests
+ *                    group_start_loc[g] .. group_start_loc[g + 1] - 1 are group g;
+ *                    requests before the first and behind the last share nothing
+ *   prefix_lens      [num_groups] int32: tokens of the group's prefix, a multiple
+ *                    of 16, at most max_prefix_len; 0: the group shares nothing.
+ *                    The prefix's blocks start the tables of all of its requests.
+ *   max_prefix_len   host-side upper bound; sizes the workspace
+ *   kv_format, scales, k_scale, v_scale  as for pa_read_kv
+ *   workspace        at least pa_attention_shared_workspace_size(...) bytes
+ * The other arguments are pa_attention's. Sharing follows the lengths: a request
+ * that does not see its whole prefix (a context shorter than it), that brings 16 or
+ * more new tokens (a prompt chunk, whose rows share K and V already) or that is
+ * left alone with one token attends on its own, with the same result.
+ * The prefixes run on the tensor cores as a cascade's does, in pairs of 128-row
+ * tiles of a group's queries and chunks of keys, into fp32 partials; each token's
+ * own keys on the split-KV kernels; a merge pass folds both. At most 1024 groups,
+ * num_reqs x max_blocks_per_req below 2^31 (PA_ERR_UNSUPPORTED); num_blocks >= 1.
+ * Errors: host-side as pa_attention. On the device, beside pa_attention's: a group
+ * whose requests are not of the batch sets PA_DEVERR_QSL, one whose prefix is
+ * negative, no multiple of 16 or longer than max_prefix_len PA_DEVERR_PREFIX (its
+ * requests then attend on their own); a sharing request whose table does not start
+ * with the blocks of the group's first sharing request sets PA_DEVERR_PREFIX, and
+ * is computed with that one's prefix (the result is wrong; the error word says so).
+ */
+size_t pa_attention_shared_workspace_size(int num_reqs, int num_tokens, int num_q_heads,
+                                          int num_kv_heads, int head_dim, int num_groups,
+                                          int max_prefix_len);
+
+typedef struct pa_shared_args { /* 20 */
+  const void *q, *k_cache, *v_cache;
+  const uint8_t* scales;
+  const int32_t *block_tables, *seq_lens, *query_start_loc, *group_start_loc, *prefix_lens;
+  void *out, *workspace, *stream;
+  size_t workspace_bytes;
+  float scale, k_scale, v_scale;
+  int kv_format, num_reqs, num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks;
+  int max_blocks_per_req, max_query_len, max_seq_len, num_groups, max_prefix_len;
+} pa_shared_args;
+pa_status pa_attention_shared(const pa_shared_args* args);
 
 /* Size of the fixed scratch array used by pa_attention_noalloc. */
 size_t pa_noalloc_scratch_bytes(void);

@@ -111,6 +111,8 @@ def lib() -> ctypes.CDLL:
             fn.restype = _c_i
             if L.pa_args_size(16 + i) != -(-layout.size // 8) * 8:
                 raise RuntimeError(f"{name}: the library's argument struct has another layout")
+        L.pa_attention_shared_workspace_size.argtypes = [_c_i] * 7
+        L.pa_attention_shared_workspace_size.restype = ctypes.c_size_t
         L.pa_attention_weights_workspace_size.argtypes = [_c_i] * 7
         L.pa_attention_weights_workspace_size.restype = ctypes.c_size_t
         L.pa_attention_weights.argtypes = ([_c_p] * 5 + [_f, _c_p, _c_p, _ll] + [_c_i] * 10 +
@@ -149,8 +151,9 @@ _pack_nr, _pack_win, _pack_wts, _pack_evict = (s.pack for s in _ARGS.values())
 _ARGS2 = {"pa_write_kv_rows": struct.Struct("@7P2q5i"),
           "pa_norm_rope_write_kv_rows": struct.Struct("@13P3qf9i"),
           "pa_attention_rows": struct.Struct("@10PNf10i"),
-          "pa_read_kv": struct.Struct("@9P2f8i")}
-_pack_wr, _pack_nrr, _pack_ar, _pack_read = (s.pack for s in _ARGS2.values())
+          "pa_read_kv": struct.Struct("@9P2f8i"),
+          "pa_attention_shared": struct.Struct("@12PN3f13i")}
+_pack_wr, _pack_nrr, _pack_ar, _pack_read, _pack_sh = (s.pack for s in _ARGS2.values())
 
 
 def _check(status: int, what: str) -> None:
@@ -820,6 +823,93 @@ def read_kv_rows(k_cache: torch.Tensor, v_cache: torch.Tensor, scales: torch.Ten
     """pa_read_kv over a row-scaled cache (see :func:`write_kv_rows`)."""
     return _read(k_cache, v_cache, scales, block_tables, read_start_loc, first, num_tokens, k_out,
                  v_out, 2, 1.0, 1.0, stream)
+
+
+def shared_workspace_size(num_reqs: int, num_tokens: int, num_q_heads: int, num_kv_heads: int,
+                          head_dim: int, num_groups: int, max_prefix_len: int) -> int:
+    return int(lib().pa_attention_shared_workspace_size(num_reqs, num_tokens, num_q_heads,
+                                                        num_kv_heads, head_dim, num_groups,
+                                                        max_prefix_len))
+
+
+def _shared(q, k_cache, v_cache, scales, block_tables, seq_lens, query_start_loc, group_start_loc,
+            prefix_lens, scale, max_prefix_len, max_query_len, max_seq_len, out, workspace, fmt,
+            k_scale, v_scale, stream):
+    T, hq, d = qshape = q.shape
+    cshape = _like_cache(k_cache, v_cache, d)
+    nb, hkv, bs, _ = cshape
+    R = seq_lens.shape[0]
+    mr, mb = block_tables.shape
+    if query_start_loc.numel() != R + 1 or mr != R:
+        raise ValueError("metadata shapes must be qsl [R+1], block_tables [R, max_blocks]")
+    G = prefix_lens.numel()
+    if group_start_loc.numel() != G + 1:
+        raise ValueError("group_start_loc must be [num_groups + 1], prefix_lens [num_groups]")
+    if out is None:
+        out = _empty(qshape, torch.bfloat16, q.device, stream)
+    elif out.shape != qshape:
+        raise ValueError("out must have q's shape")
+    if workspace is None:
+        need = shared_workspace_size(R, T, hq, hkv, d, G, max_prefix_len)
+        workspace = _empty(max(need, 256), torch.uint8, q.device, stream)
+    dev, raw_stream = _where(stream)
+    out_p = _ptr(out, torch.bfloat16, dev, "out") if out.is_cuda else _out(out)
+    cache_dtype = torch.uint8 if fmt else torch.bfloat16
+    st = lib().pa_attention_shared(_pack_sh(
+        _ptr(q, torch.bfloat16, dev, "q"), _ptr(k_cache, cache_dtype, dev, "k_cache"),
+        _ptr(v_cache, cache_dtype, dev, "v_cache"),
+        _scales(scales, cshape, dev) if fmt == 2 else 0,
+        _ptr(block_tables, torch.int32, dev, "block_tables"),
+        _ptr(seq_lens, torch.int32, dev, "seq_lens"),
+        _ptr(query_start_loc, torch.int32, dev, "query_start_loc"),
+        _ptr(group_start_loc, torch.int32, dev, "group_start_loc"),
+        _ptr(prefix_lens, torch.int32, dev, "prefix_lens"), out_p,
+        _ptr(workspace, torch.uint8, dev, "workspace"), raw_stream, workspace.numel(), scale, k_scale,
+        v_scale, fmt, R, T, hq, hkv, d, bs, nb, mb, max_query_len, max_seq_len, G, max_prefix_len))
+    if st:
+        _check(st, "pa_attention_shared")
+    return out
+
+
+def attention_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                     block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                     query_start_loc: torch.Tensor, group_start_loc: torch.Tensor,
+                     prefix_lens: torch.Tensor, scale: float, *, max_prefix_len: int,
+                     max_query_len: int, max_seq_len: int, out: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """pa_attention_shared: :func:`attention` where requests ``group_start_loc[g]`` ..
+    ``group_start_loc[g + 1] - 1`` (int32 [groups + 1]) share their first
+    ``prefix_lens[g]`` keys (int32 [groups], multiples of 16, 0: none), the same blocks
+    at the start of their tables; a prefix is attended to once for its group. The
+    workspace is ``shared_workspace_size(...)`` bytes."""
+    return _shared(q, k_cache, v_cache, None, block_tables, seq_lens, query_start_loc,
+                   group_start_loc, prefix_lens, scale, max_prefix_len, max_query_len, max_seq_len,
+                   out, workspace, 0, 1.0, 1.0, stream)
+
+
+def attention_shared_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                         block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                         query_start_loc: torch.Tensor, group_start_loc: torch.Tensor,
+                         prefix_lens: torch.Tensor, scale: float, k_scale: float, v_scale: float,
+                         *, max_prefix_len: int, max_query_len: int, max_seq_len: int,
+                         out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor:
+    """pa_attention_shared over E4M3 caches (uint8) with one scale per tensor."""
+    return _shared(q, k_cache, v_cache, None, block_tables, seq_lens, query_start_loc,
+                   group_start_loc, prefix_lens, scale, max_prefix_len, max_query_len, max_seq_len,
+                   out, workspace, 1, k_scale, v_scale, stream)
+
+
+def attention_shared_rows(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                          scales: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                          query_start_loc: torch.Tensor, group_start_loc: torch.Tensor,
+                          prefix_lens: torch.Tensor, scale: float, *, max_prefix_len: int,
+                          max_query_len: int, max_seq_len: int, out: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """pa_attention_shared over a row-scaled cache (see :func:`write_kv_rows`)."""
+    return _shared(q, k_cache, v_cache, scales, block_tables, seq_lens, query_start_loc,
+                   group_start_loc, prefix_lens, scale, max_prefix_len, max_query_len, max_seq_len,
+                   out, workspace, 2, 1.0, 1.0, stream)
 
 
 def get_device_error(clear: bool = True) -> tuple[int, int]:

@@ -50,6 +50,15 @@
 // rescales O^T through TMEM first. Sums stay per thread until the token's
 // epilogue (one exchange per token for the heads' sums and maxima).
 //
+// Row-scaled caches (RS, rows.cuh): a third copy lands the block's 256 scale
+// bytes. A key's 2^ek multiplies its score after the product with its codes; its
+// value's 2^ev must go into P', since the codes alone are multiplied by it:
+//   P' = 256 2^(t + ev - r), l = sum 2^(t - r), out = O / l
+// with the references r taken from u = t + ev, so that P' keeps its place below
+// 448 whatever the rows' sizes: E4M3's smallest step is then relative to the
+// largest weight x size, which is what the output is made of. l's terms reach
+// 2^(100 + 3) (ev >= -100), its sum stays in range.
+//
 // Roles (192 threads per CTA): warps 0-3 softmax and epilogue, warp 4
 // the producer (walks the work list, one record per tile, two or three tensor
 // copies), warp 5 allocates TMEM and one thread issues the MMAs. Every wait
@@ -59,6 +68,7 @@
 
 #include "pa_internal.h"
 #include "ptx.cuh"
+#include "rows.cuh"
 
 namespace pa {
 
@@ -83,7 +93,7 @@ constexpr int kTmD = 128;    // head dim
 constexpr int kTmHkv = 8;    // KV heads: 8 x 16 keys = the MMA's 128 rows
 constexpr int kTmThreads = 192;
 
-template <int G, int CPS>
+template <int G, int CPS, bool RS>
 struct TmL {
   static constexpr int HQ = kTmHkv * G;          // query heads of a token
   static constexpr int N = 2 * HQ;               // MMA N: hi rows, then lo rows
@@ -99,9 +109,12 @@ struct TmL {
   static constexpr int OFF_REC = OFF_P + 2 * kPBytes;  // a 32-byte record per stage
   static constexpr int OFF_INV = OFF_REC + kStages * 32;   // per stage: 2^-e of the HQ rows
   static constexpr int OFF_QTAG = OFF_INV + kStages * HQ * 4;  // token whose q' a stage holds
+  // RS: per stage the block's scale bytes, [8 KV heads][K, V][16]
+  static constexpr int kScaleStage = RS ? kTmHkv * kScaleBytes : 0;
+  static constexpr int OFF_SC = (OFF_QTAG + kStages * 4 + 15) / 16 * 16;
   // exchange, two buffers: [4 warp flags][HQ alphas][HQ sums][HQ maxima] floats
   static constexpr int XCH_FLOATS = 4 + 3 * HQ;
-  static constexpr int OFF_XCH = (OFF_QTAG + kStages * 4 + 15) / 16 * 16;
+  static constexpr int OFF_XCH = OFF_SC + kStages * kScaleStage;
   static constexpr int OFF_BAR = (OFF_XCH + 2 * XCH_FLOATS * 4 + 7) / 8 * 8;
   // barriers: FULL[stages], EMPTY[stages], S[2], P_READY[2], P_FREE[2], XCH[2], DRAIN
   static constexpr int B_FULL = 0, B_EMPTY = kStages, B_S = 2 * kStages, B_PREADY = B_S + 2,
@@ -124,6 +137,7 @@ struct TmL {
 constexpr int T_FIRST = 1;  // the token's first tile in this CTA
 constexpr int T_LAST = 2;   // the token's last tile in this CTA
 constexpr int T_WHOLE = 4;  // the CTA holds all of the token's blocks: store bf16 output
+                            // (never with fold_later: the merge pass folds more in)
 constexpr int T_PAR = 8;    // O^T buffer 1 (else 0)
 constexpr int T_END = 16;   // no more tiles
 struct TmRec {
@@ -155,10 +169,10 @@ struct TmDecodeParams {
   DecodeParams d;
 };
 
-template <int G, int CPS, bool WIN>
+template <int G, int CPS, bool WIN, bool RS>
 __global__ void __launch_bounds__(kTmThreads, CPS)
     pa_decode_tm_kernel(const __grid_constant__ TmDecodeParams tp) {
-  using L = TmL<G, CPS>;
+  using L = TmL<G, CPS, RS>;
   constexpr int HQ = L::HQ, N = L::N, kStages = L::kStages;
   const DecodeParams& p = tp.d;
   extern __shared__ unsigned char smem_raw[];
@@ -347,7 +361,7 @@ __global__ void __launch_bounds__(kTmThreads, CPS)
       const int b = WIN ? win_block(ws, blk) : blk;  // the logical block
       t.r = TmRec{U.tok, U.len, b * kBlockSize,
                   (pfirst ? T_FIRST : 0) | (last ? T_LAST : 0) |
-                      ((last && blk + 1 == nb && pstart == 0) ? T_WHOLE : 0) |
+                      ((last && blk + 1 == nb && pstart == 0 && !p.fold_later) ? T_WHOLE : 0) |
                       ((np & 1) ? T_PAR : 0),
                   {0, 0, 0, 0}};
       t.live = 1;
@@ -384,6 +398,11 @@ __global__ void __launch_bounds__(kTmThreads, CPS)
       }
       return pid;
     };
+    auto load_scales = [&](int st, int pid, uint32_t full) {
+      if constexpr (RS)
+        bulk_g2s(base + L::OFF_SC + st * L::kScaleStage, p.scales + (size_t)pid * L::kScaleStage,
+                 L::kScaleStage, full);
+    };
     bool pre0 = false, pre1 = false;  // tiles 0 and 1: K/V copies already issued
     auto issue = [&](const Meta& cur, Meta& nxt2) -> bool {  // false: stop
       nxt2 = next_tile();
@@ -407,13 +426,14 @@ __global__ void __launch_bounds__(kTmThreads, CPS)
         recs[st] = cur.r;
         if (needq) qtag[st] = cur.r.tok;
         const bool kv_done = (i == 0 && pre0) || (i == 1 && pre1);
-        mbar_arrive_expect_tx(full, (kv_done ? 0u : 2u * L::kKvTile) +
+        mbar_arrive_expect_tx(full, (kv_done ? 0u : 2u * L::kKvTile + L::kScaleStage) +
                                         (needq ? (uint32_t)L::kQBytes : 0u));
         const uint32_t sbase = base + L::OFF_STAGE + st * L::kStageBytes;
         if (!kv_done) {
           const int pid = block_id(cur);
           tma_load_2d(sbase, &tp.tm_k, 0, pid * kTmHkv * kBlockSize, full);
           tma_load_2d(sbase + L::kKvTile, &tp.tm_v, 0, pid * kTmHkv * kBlockSize, full);
+          load_scales(st, pid, full);
         }
         if (needq) tma_load_3d(sbase + 2 * L::kKvTile, &tp.tm_q, 0, cur.r.tok * HQ, 0, full);
       }
@@ -432,9 +452,10 @@ __global__ void __launch_bounds__(kTmThreads, CPS)
           const uint32_t full = BAR(L::B_FULL + j);
           const uint32_t sbase = base + L::OFF_STAGE + j * L::kStageBytes;
           const int pid = block_id(t);
-          mbar_expect_tx(full, 2u * L::kKvTile);
+          mbar_expect_tx(full, 2u * L::kKvTile + L::kScaleStage);
           tma_load_2d(sbase, &tp.tm_k, 0, pid * kTmHkv * kBlockSize, full);
           tma_load_2d(sbase + L::kKvTile, &tp.tm_v, 0, pid * kTmHkv * kBlockSize, full);
+          load_scales(j, pid, full);
         }
         return true;
       };
@@ -629,6 +650,15 @@ __global__ void __launch_bounds__(kTmThreads, CPS)
       // scores of this thread's key for its KV head's G query rows (hi + lo,
       // each row's 2^-e undone), in log2 units
       float t[G];
+      // RS: this key's 2^ek, and its value's 2^ev and ev
+      float ksize = 1.f, vsize = 1.f, ev = 0.f;
+      if constexpr (RS) {
+        const unsigned char* const sc = gb + L::OFF_SC + st * L::kScaleStage + hm * kScaleBytes;
+        const int bv = valid ? sc[kBlockSize + kk] : 127;
+        ksize = row_size(sc[kk]);
+        vsize = row_size(bv);
+        ev = bv == kRowPoison ? vsize : (float)(bv - 127);
+      }
       {
         uint32_t shi[2 * G], slo[2 * G];
         const uint32_t scol = (uint32_t)(N * b + 2 * warp * G);
@@ -641,9 +671,14 @@ __global__ void __launch_bounds__(kTmThreads, CPS)
         for (int g = 0; g < G; ++g) {
           const float s = __uint_as_float(hf ? shi[G + g] : shi[g]) +
                           __uint_as_float(hf ? slo[G + g] : slo[g]);
-          t[g] = valid ? s * (inv[g] * p.scale_log2) : -INFINITY;
+          t[g] = valid ? s * (inv[g] * p.scale_log2) * ksize : -INFINITY;
         }
       }
+      // what the references follow: the score, RS: and the value's ev
+      auto ref_of = [&](int g) -> float {
+        if constexpr (RS) return t[g] + ev;
+        return t[g];
+      };
       // references: the token's first tile sets them from its maxima; later
       // tiles move one only for a score above it by more than kSlack
       float alpha[G];
@@ -653,17 +688,17 @@ __global__ void __launch_bounds__(kTmThreads, CPS)
       if (rec.flags & T_FIRST) {
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          mr[g] = half_max(t[g]) + kHeadFirst;
+          mr[g] = half_max(ref_of(g)) + kHeadFirst;
           lt[g] = 0.f;
         }
       } else {
         bool over = false;
 #pragma unroll
-        for (int g = 0; g < G; ++g) over |= t[g] > mr[g] + kSlack;
+        for (int g = 0; g < G; ++g) over |= ref_of(g) > mr[g] + kSlack;
         if (__any_sync(kLanes, over)) {  // warp-uniform: both halves take their maxima
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            const float tmx = half_max(t[g]);
+            const float tmx = half_max(ref_of(g));
             if (tmx > mr[g] + kSlack) {
               alpha[g] = exp2f(mr[g] - (tmx + kHead));
               mr[g] = tmx + kHead;
@@ -691,7 +726,7 @@ __global__ void __launch_bounds__(kTmThreads, CPS)
       }
 #pragma unroll
       for (int g = 0; g < G; g += 2) {
-        const float x0 = 256.f * pr[g], x1 = g + 1 < G ? 256.f * pr[g + 1] : 0.f;
+        const float x0 = 256.f * vsize * pr[g], x1 = g + 1 < G ? 256.f * vsize * pr[g + 1] : 0.f;
         const uint16_t hi = float2_to_e4m3x2(x0, x1);
         const float2 hv = e4m3x2_to_float2(hi);
         const uint16_t lo = float2_to_e4m3x2(x0 - hv.x, x1 - hv.y);
@@ -773,9 +808,9 @@ __global__ void __launch_bounds__(kTmThreads, CPS)
 // ---------------------------------------------------------------------------------------
 namespace {
 
-template <int G, int CPS, bool WIN>
+template <int G, int CPS, bool WIN, bool RS>
 cudaError_t launch_tm_w(const DecodeParams& d, int grid, cudaStream_t s) {
-  using L = TmL<G, CPS>;
+  using L = TmL<G, CPS, RS>;
   TmDecodeParams tp;
   tp.d = d;
   const uint64_t qrows = (uint64_t)d.num_tokens * (uint64_t)d.num_q_heads;
@@ -792,7 +827,7 @@ cudaError_t launch_tm_w(const DecodeParams& d, int grid, cudaStream_t s) {
       !encode_tmap_u8(&tp.tm_k, 2, d.k_cache, cd, cs, cb) ||
       !encode_tmap_u8(&tp.tm_v, 2, d.v_cache, cd, cs, cb))
     return cudaErrorInvalidValue;
-  auto kern = pa_decode_tm_kernel<G, CPS, WIN>;
+  auto kern = pa_decode_tm_kernel<G, CPS, WIN, RS>;
   static bool attr_set[64] = {false};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -823,8 +858,10 @@ cudaError_t launch_tm_w(const DecodeParams& d, int grid, cudaStream_t s) {
 
 template <int G, int CPS>
 cudaError_t launch_tm_t(const DecodeParams& d, int grid, cudaStream_t s) {
-  return d.window > 0 ? launch_tm_w<G, CPS, true>(d, grid, s)
-                      : launch_tm_w<G, CPS, false>(d, grid, s);
+  if (d.scales != nullptr)  // windows have no row-scaled form (the caller sees to it)
+    return launch_tm_w<G, CPS, false, true>(d, grid, s);
+  return d.window > 0 ? launch_tm_w<G, CPS, true, false>(d, grid, s)
+                      : launch_tm_w<G, CPS, false, false>(d, grid, s);
 }
 
 }  // namespace

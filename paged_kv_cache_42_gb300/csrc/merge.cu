@@ -10,7 +10,9 @@
 // ("vLLM: An Exhaustive Technical Study for Kernel Engineers", 2.3, the merge
 // of partial attention states) in a fixed order of operations, so the result
 // does not depend on which warp finished first. In a cascade call the prefix
-// partials of the same (token, kv head) are merged in with the suffix slots.
+// partials of the same (token, kv head) are merged in with the suffix slots; in a
+// shared call (SHARED) those of the token's own group, as many chunks as its
+// prefix has, or none.
 //
 // One CTA per slice boundary, reading the task the split-KV worker after the
 // boundary left for it. Its warps split the partials between them, each
@@ -26,7 +28,7 @@ namespace {
 
 constexpr int kMergeWarps = 8;
 
-template <int D, int G>
+template <int D, int G, bool SHARED>
 __global__ void __launch_bounds__(kMergeWarps * 32) pa_merge_kernel(const MergeParams p) {
   constexpr int V = D / 32;  // output dims per lane
   static_assert(V == 2 || V == 4, "head dim 64 or 128");
@@ -46,7 +48,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) pa_merge_kernel(const MergeP
     if (k >= __ldcg(&p.header->num_units)) return;
     const int4 u = __ldcg(reinterpret_cast<const int4*>(p.units + k));
     const int nb = max(1, (u.z + kBlockSize - 1) / kBlockSize - p.key_start_blocks);
-    const int first = u.w + kv * nb, NW = plan_workers(W, nw, p.min_pos);
+    const int first = u.w + (SHARED && p.token_major ? 0 : kv * nb);
+    const int NW = plan_workers(W, nw, p.min_pos);
     tok = u.x;
     wf = worker_of(first, W, NW);
     wl = worker_of(first + nb - 1, W, NW);
@@ -65,9 +68,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) pa_merge_kernel(const MergeP
   // The partials: the suffix slots wf .. wl, then (cascade) the prefix chunks.
   // Worker wf + i's slot: u + wf + i (u = token * Hkv + kv head).
   const int u = tok * p.num_kv_heads + kv;
-  const int ns = wl - wf + 1, n = ns + p.prefix_chunks;
+  const int ns = wl - wf + 1, n = ns + (SHARED ? __ldcg(p.tok_chunks + tok) : p.prefix_chunks);
   auto slot = [&](int i) -> const float* {
-    const size_t s0 = (size_t)(u + wf + i);
+    const size_t s0 = SHARED && p.token_major ? (size_t)(tok + wf + i) * p.num_kv_heads + kv
+                                              : (size_t)(u + wf + i);
     return i < ns ? p.partials + s0 * p.slot_floats
                   : p.prefix_partials +
                         (((size_t)(i - ns) * p.num_tokens + tok) * p.num_kv_heads + kv) *
@@ -237,7 +241,9 @@ cudaError_t launch_merge_t(const MergeParams& p, cudaStream_t s) {
   const int boundaries = p.all_units ? p.num_tokens * p.num_kv_heads : p.num_workers - 1;
   if (boundaries <= 0) return cudaSuccess;  // one worker: nothing is ever split
   // token-major partials: eight KV heads, no cascade (the split-KV kernel's own limits)
-  if (p.token_major && (p.all_units || p.prefix_chunks != 0 || p.num_kv_heads > kMergeWarps))
+  if (p.tok_chunks != nullptr) {
+    if (!p.all_units) return cudaErrorInvalidValue;
+  } else if (p.token_major && (p.all_units || p.prefix_chunks != 0 || p.num_kv_heads > kMergeWarps))
     return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)boundaries);
@@ -251,11 +257,12 @@ cudaError_t launch_merge_t(const MergeParams& p, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (p.tok_chunks != nullptr) return cudaLaunchKernelEx(&cfg, pa_merge_kernel<D, G, true>, p);
   if (p.token_major) {  // a CTA per boundary, a warp per KV head
     cfg.blockDim = dim3(32 * p.num_kv_heads);
     return cudaLaunchKernelEx(&cfg, pa_merge_tm_kernel<D, G>, p);
   }
-  return cudaLaunchKernelEx(&cfg, pa_merge_kernel<D, G>, p);
+  return cudaLaunchKernelEx(&cfg, pa_merge_kernel<D, G, false>, p);
 }
 
 }  // namespace

@@ -406,7 +406,7 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
   float* const prefix_partials =
       prefix_len > 0 ? reinterpret_cast<float*>(ws + lay.total) : nullptr;
 
-  PlanParams pp;
+  PlanParams pp = {};
   pp.qsl = query_start_loc;
   pp.seq_lens = seq_lens;
   pp.block_tables = block_tables;
@@ -435,9 +435,9 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
   // the per-(token, kv head) epilogue better (measured 39 vs 76 us on the
   // prefix-sharing batch).
   const int tc_mode = g_decode_tc.load();
-  const bool use_tc = tc_mode != 0 && kv_fp8 != 2 &&
-                      decode_tc_supported(head_dim, group, kv_fp8 != 0, prefix_len / kBlockSize) &&
-                      (tc_mode == 2 || (group >= PA_DECODE_TC_MIN_GROUP && prefix_len == 0));
+  bool use_tc = tc_mode != 0 &&
+                decode_tc_supported(head_dim, group, kv_fp8 != 0, prefix_len / kBlockSize) &&
+                (tc_mode == 2 || (group >= PA_DECODE_TC_MIN_GROUP && prefix_len == 0));
   // A cascade on the CUDA-core suffix pass may run its prefix pass on a few
   // SMs (about two prefix items each) beside the suffix pass on the rest; the
   // merge pass then folds every (token, kv head).
@@ -474,6 +474,7 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
   const bool use_tm =
       use_tc && kv_fp8 && g_token_major.load() && (window == 0 || win_tm) &&
       decode_tm_supported(head_dim, group, num_kv_heads, decode_tm_workers(group, d->num_sms, tm_cps));
+  if (kv_fp8 == 2) use_tc = use_tm;  // the other tensor-core tiles have no row-scaled form
   const int launched = use_tm   ? decode_tm_workers(group, d->num_sms, tm_cps)
                        : use_tc ? decode_tc_workers(d->num_sms)
                                 : decode_workers(head_dim, pp.group, kv_fp8, window > 0, dec_sms,
@@ -512,7 +513,7 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
   }
 
   if (pp.use_prefill || prefix_len > 0) {
-    PrefillLaunch pl;
+    PrefillLaunch pl = {};
     pl.prefix_len = prefix_len;
     pl.prefix_chunks = chunks;
     pl.slot_floats = lay.slot_floats;
@@ -608,7 +609,7 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
   // the slicing's worker count, as the split-KV kernel computes it
   const int workers = (cap > 0 && cap < launched_workers) ? cap : launched_workers;
 
-  MergeParams mp;
+  MergeParams mp = {};
   mp.header = pp.header;
   mp.tasks = dp.merge_tasks;
   mp.partials = dp.partials;
@@ -634,6 +635,214 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
     if (e != cudaSuccess) return PA_ERR_CUDA;
   }
   return PA_OK;
+}
+
+// pa_attention_shared. The split-KV kernels see each token's own keys only, as a
+// batch of its own: units whose `req` is an offset into the tables (row stride 1).
+pa_status shared_impl(const pa_shared_args& a) {
+  const int fmt = a.kv_format, group = a.num_kv_heads > 0 ? a.num_q_heads / a.num_kv_heads : 0;
+  const float k_scale = fmt == 1 ? a.k_scale : 1.f, v_scale = fmt == 1 ? a.v_scale : 1.f;
+  if (fmt < 0 || fmt > 2 || a.num_groups < 0 || a.max_prefix_len < 0) return PA_ERR_INVALID_ARG;
+  bool nothing = false;
+  if (pa_status st = check_attention_args(
+          a.q, a.k_cache, a.v_cache, a.block_tables, a.seq_lens, a.query_start_loc, a.scale, a.out,
+          a.num_reqs, a.num_tokens, a.num_q_heads, a.num_kv_heads, a.head_dim, a.block_size,
+          a.num_blocks, a.max_blocks_per_req, a.max_query_len, a.max_seq_len, 0, fmt, k_scale, v_scale,
+          &nothing))
+    return st;
+  if (a.num_groups > kMaxSharedGroups) return PA_ERR_UNSUPPORTED;
+  if (nothing) return PA_OK;
+  if (fmt == 2 && (!a.scales || !aligned16(a.scales))) return PA_ERR_INVALID_ARG;
+  if (a.num_blocks < 1) return PA_ERR_INVALID_ARG;  // no block to attend to
+  if (a.num_groups > 0 && (!a.group_start_loc || !a.prefix_lens ||
+                           (reinterpret_cast<uintptr_t>(a.group_start_loc) & 3u) ||
+                           (reinterpret_cast<uintptr_t>(a.prefix_lens) & 3u)))
+    return PA_ERR_INVALID_ARG;
+  // a unit's place in the tables is a 32-bit offset, and so is a partial's item
+  if ((long long)a.num_reqs * a.max_blocks_per_req >= (1LL << 31)) return PA_ERR_UNSUPPORTED;
+  const SharedLayout sh = shared_layout(a.num_reqs, a.num_tokens, a.num_q_heads, a.num_kv_heads,
+                                        a.head_dim, a.num_groups, a.max_prefix_len);
+  if (!a.workspace || a.workspace_bytes < sh.total ||
+      (reinterpret_cast<uintptr_t>(a.workspace) & 255u))
+    return PA_ERR_WORKSPACE;
+  // nothing shared: the plain call (its workspace comes first in this one's)
+  if (a.num_groups == 0 || a.max_prefix_len < kBlockSize)
+    return attention_impl(a.q, a.k_cache, a.v_cache, a.block_tables, a.seq_lens, a.query_start_loc,
+                          a.scale, a.out, a.num_reqs, a.num_tokens, a.num_q_heads, a.num_kv_heads,
+                          a.head_dim, a.block_size, a.num_blocks, a.max_blocks_per_req,
+                          a.max_query_len, a.max_seq_len, 0, 0, 0, fmt, k_scale, v_scale, a.workspace,
+                          a.workspace_bytes, a.stream, a.scales);
+  const WsLayout lay =
+      ws_layout(a.num_reqs, a.num_tokens, a.num_q_heads, a.num_kv_heads, a.head_dim);
+  DeviceState* d = nullptr;
+  if (pa_status st = device_state(&d)) return st;
+  const NvtxRange range("pa_attention_shared");
+  cudaStream_t s = static_cast<cudaStream_t>(a.stream);
+  unsigned char* const ws = static_cast<unsigned char*>(a.workspace);
+  float* const prefix_partials = reinterpret_cast<float*>(ws + sh.partials_off);
+  int* const tok_chunks = reinterpret_cast<int*>(ws + sh.chunks_off);
+  const float scale_log2 = a.scale * 1.4426950408889634f * k_scale;
+
+  // The suffixes: the token-major tensor-core kernel where pa_attention takes it;
+  // else the CUDA-core kernel, whose many warps hide a short unit's ends (a cascade's
+  // choice).
+  const int tc_mode = g_decode_tc.load(), tm_cps = g_tm_ctas.load();
+  const bool use_tm =
+      fmt != 0 && tc_mode != 0 && (tc_mode == 2 || group >= PA_DECODE_TC_MIN_GROUP) &&
+      g_token_major.load() &&
+      decode_tm_supported(a.head_dim, group, a.num_kv_heads,
+                          decode_tm_workers(group, d->num_sms, tm_cps));
+  const int occ_cap = fmt == 0 ? PA_DEC_OCC_CAP_CASCADE : PA_DEC_OCC_CAP_FP8;
+  const int launched = use_tm ? decode_tm_workers(group, d->num_sms, tm_cps)
+                              : decode_workers(a.head_dim, group, fmt, false, d->num_sms, occ_cap);
+  if (launched <= 0) return PA_ERR_CUDA;
+  const int cap = g_max_workers.load();
+
+  PlanParams pp = {};
+  pp.qsl = a.query_start_loc;
+  pp.seq_lens = a.seq_lens;
+  pp.block_tables = a.block_tables;
+  pp.early_start = g_write_overlap.load();
+  pp.num_reqs = a.num_reqs;
+  pp.num_tokens = a.num_tokens;
+  pp.num_kv_heads = a.num_kv_heads;
+  pp.max_blocks_per_req = a.max_blocks_per_req;
+  pp.max_query_len = a.max_query_len;
+  pp.max_seq_len = a.max_seq_len;
+  pp.group = group;
+  pp.use_prefill = a.max_query_len >= kPrefillMinQlen ? 1 : 0;
+  pp.num_workers = (cap > 0 && cap < launched) ? cap : launched;
+  pp.num_sms = d->num_sms;
+  pp.token_major = use_tm ? 1 : 0;
+  pp.min_pos = PA_DEC_MIN_POS;
+  pp.group_start = a.group_start_loc;
+  pp.prefix_lens = a.prefix_lens;
+  pp.num_groups = a.num_groups;
+  pp.max_prefix_len = a.max_prefix_len;
+  pp.chunk_tiles = sh.chunk_tiles;
+  pp.max_items = sh.max_items;
+  pp.shared_items = reinterpret_cast<SharedItem*>(ws + sh.items_off);
+  pp.tok_chunks = tok_chunks;
+  pp.header = reinterpret_cast<WsHeader*>(ws + lay.header_off);
+  pp.units = reinterpret_cast<UnitInfo*>(ws + lay.units_off);
+  pp.tiles = reinterpret_cast<PrefillTile*>(ws + lay.tiles_off);
+  pp.raw = reinterpret_cast<int2*>(ws + lay.raw_off);
+  pp.worker_unit = reinterpret_cast<int*>(ws + lay.workers_off);
+  pp.err = d->err;
+  {
+    TimerScope timer(1, s);
+    const cudaError_t e = launch_plan(pp, s);
+    g_launches.fetch_add(1);
+    if (e != cudaSuccess) return PA_ERR_CUDA;
+  }
+
+  PrefillLaunch pl = {};
+  pl.slot_floats = lay.slot_floats;
+  pl.prefix_partials = prefix_partials;
+  pl.kv_fp8 = fmt;
+  pl.v_scale = v_scale;
+  pl.scales = a.scales;
+  pl.q = a.q;
+  pl.k_cache = a.k_cache;
+  pl.v_cache = a.v_cache;
+  pl.qsl = a.query_start_loc;
+  pl.seq_lens = a.seq_lens;
+  pl.block_tables = a.block_tables;
+  pl.out = static_cast<uint16_t*>(a.out);
+  pl.header = pp.header;
+  pl.tiles = pp.tiles;
+  pl.num_tokens = a.num_tokens;
+  pl.num_q_heads = a.num_q_heads;
+  pl.num_kv_heads = a.num_kv_heads;
+  pl.head_dim = a.head_dim;
+  pl.num_blocks = a.num_blocks;
+  pl.bt_stride = a.max_blocks_per_req;
+  pl.scale_log2 = scale_log2;
+  pl.err = d->err;
+  if (pp.use_prefill) {  // prompt chunks: their rows share K and V already
+    TimerScope timer(3, s);
+    const cudaError_t e = launch_prefill(pl, d->num_sms, s);
+    g_launches.fetch_add(1);
+    if (e != cudaSuccess) return PA_ERR_CUDA;
+  }
+  pl.shared_items = pp.shared_items;
+  {
+    TimerScope timer(4, s);
+    const cudaError_t e = launch_prefill(pl, d->num_sms, s);
+    g_launches.fetch_add(1);
+    if (e != cudaSuccess) return PA_ERR_CUDA;
+  }
+
+  DecodeParams dp = {};
+  dp.q = static_cast<const uint16_t*>(a.q);
+  dp.k_cache = a.k_cache;
+  dp.v_cache = a.v_cache;
+  dp.scales = a.scales;
+  dp.v_scale = v_scale;
+  dp.block_tables = a.block_tables;
+  dp.out = static_cast<uint16_t*>(a.out);
+  dp.bt_stride = 1;  // units hold offsets
+  dp.num_q_heads = a.num_q_heads;
+  dp.num_kv_heads = a.num_kv_heads;
+  dp.num_blocks = a.num_blocks;
+  dp.scale_log2 = scale_log2;
+  dp.header = pp.header;
+  dp.units = pp.units;
+  dp.worker_unit = a.num_tokens <= kPlanSmemTokens ? pp.worker_unit : nullptr;
+  dp.partials = reinterpret_cast<float*>(ws + lay.partials_off);
+  dp.slot_floats = lay.slot_floats;
+  dp.num_tokens = a.num_tokens;
+  dp.early_start = pp.early_start;
+  dp.num_reqs = a.num_reqs;
+  dp.max_blocks_per_req = a.max_blocks_per_req;
+  dp.max_query_len = a.max_query_len;
+  dp.max_seq_len = a.max_seq_len;
+  dp.qsl = a.query_start_loc;
+  dp.seq_lens = a.seq_lens;
+  dp.header_out = pp.header;
+  dp.merge_tasks = reinterpret_cast<int4*>(ws + lay.tasks_off);
+  dp.max_workers = cap > 0 ? cap : kMaxDecodeWorkers;
+  dp.qsplit = ws + lay.qsplit_off;
+  dp.qinv = reinterpret_cast<const float*>(ws + lay.qinv_off);
+  dp.fold_later = 1;
+  dp.min_pos = pp.min_pos;
+  dp.err = d->err;
+  if (use_tm) {
+    const cudaError_t e = launch_qsplit(dp, group, s);
+    g_launches.fetch_add(1);
+    if (e != cudaSuccess) return PA_ERR_CUDA;
+  }
+  int launched_workers = 0;
+  {
+    TimerScope timer(2, s);
+    const cudaError_t e =
+        use_tm ? launch_decode_tm(dp, group, d->num_sms, tm_cps, s, &launched_workers)
+               : launch_decode(dp, a.head_dim, group, fmt, d->num_sms, occ_cap, s, &launched_workers);
+    g_launches.fetch_add(1);
+    if (e != cudaSuccess) return PA_ERR_CUDA;
+  }
+
+  MergeParams mp = {};
+  mp.header = pp.header;
+  mp.tasks = dp.merge_tasks;
+  mp.partials = dp.partials;
+  mp.slot_floats = lay.slot_floats;
+  mp.num_workers = (cap > 0 && cap < launched_workers) ? cap : launched_workers;
+  mp.token_major = pp.token_major;
+  mp.min_pos = pp.min_pos;
+  mp.num_q_heads = a.num_q_heads;
+  mp.num_kv_heads = a.num_kv_heads;
+  mp.num_tokens = a.num_tokens;
+  mp.prefix_partials = prefix_partials;
+  mp.tok_chunks = tok_chunks;
+  mp.v_scale = v_scale;
+  mp.out = dp.out;
+  mp.all_units = 1;
+  mp.units = pp.units;
+  TimerScope timer(5, s);
+  const cudaError_t e = launch_merge(mp, a.head_dim, group, s);
+  g_launches.fetch_add(1);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace
@@ -917,6 +1126,7 @@ size_t pa_args_size(int which) {
     case 1: return sizeof(pa_norm_rope_write_rows_args);
     case 2: return sizeof(pa_attention_rows_args);
     case 3: return sizeof(pa_read_args);
+    case 4: return sizeof(pa_shared_args);
   }
   return 0;
 }
@@ -1022,6 +1232,21 @@ pa_status pa_attention_rows(const pa_attention_rows_args* a) {
                         a->num_q_heads, a->num_kv_heads, a->head_dim, a->block_size, a->num_blocks,
                         a->max_blocks_per_req, a->max_query_len, a->max_seq_len, 0, 0, 0, 2, 1.f,
                         1.f, a->workspace, a->workspace_bytes, a->stream, a->scales);
+}
+
+size_t pa_attention_shared_workspace_size(int num_reqs, int num_tokens, int num_q_heads,
+                                          int num_kv_heads, int head_dim, int num_groups,
+                                          int max_prefix_len) {
+  if (pa_attention_workspace_size(num_reqs, num_tokens, num_q_heads, num_kv_heads, head_dim) == 0 ||
+      !supported_group(num_q_heads / num_kv_heads) || num_groups < 0 ||
+      num_groups > kMaxSharedGroups || max_prefix_len < 0)
+    return 0;
+  return shared_layout(num_reqs, num_tokens, num_q_heads, num_kv_heads, head_dim, num_groups,
+                       max_prefix_len).total;
+}
+
+pa_status pa_attention_shared(const pa_shared_args* a) {
+  return a ? shared_impl(*a) : PA_ERR_INVALID_ARG;
 }
 
 pa_status pa_read_kv(const pa_read_args* a) {

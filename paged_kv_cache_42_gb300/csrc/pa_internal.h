@@ -92,7 +92,8 @@ struct WsHeader {
   // launch's worker count.
   int prefill_ctas;
   int decode_workers;
-  int pad[59];
+  int num_prefix_items;  // pa_attention_shared: entries of its prefix work list
+  int pad[58];
 };
 
 // Overlapped mixed batch: the planner gives the prefill-chunk items P SMs
@@ -216,6 +217,59 @@ __host__ __device__ inline size_t prefix_partials_bytes(int num_tokens, int num_
                      (size_t)num_tokens * (size_t)num_kv_heads);
 }
 
+// pa_attention_shared: groups of requests, each with its own prefix.
+constexpr int kMaxSharedGroups = 1024;  // the planner keeps them in shared memory
+// A group of fewer tokens than this on the split-KV path attends on its own: one
+// token reads its prefix once either way.
+constexpr int kSharedMinTokens = 2;
+// Prefix work items aimed at (an item holds an SM alone; GB300 has 152).
+constexpr int kSharedTargetItems = 152;
+
+// One prefix work item: two 128-row tiles of kv head `kv`, batch tokens tok0 up
+// to tok_end - 1 at most, against key tiles i0 .. i0 + n - 1 of the L prefix keys
+// in request req's table; chunk: which of the prefix's key chunks that is.
+struct SharedItem {
+  int req, kv, tok0, tok_end, chunk, i0, n, L;
+};
+static_assert(sizeof(SharedItem) == 32, "items are two 16-byte vectors");
+
+// What pa_attention_shared's workspace holds behind ws_layout's.
+struct SharedLayout {
+  size_t items_off, chunks_off, partials_off, total;
+  int chunk_tiles;  // 128-key tiles of a key chunk
+  int max_chunks;   // of any group's prefix
+  int max_items;
+};
+
+inline SharedLayout shared_layout(int num_reqs, int num_tokens, int num_q_heads, int num_kv_heads,
+                                  int head_dim, int num_groups, int max_prefix_len) {
+  const WsLayout base = ws_layout(num_reqs, num_tokens, num_q_heads, num_kv_heads, head_dim);
+  SharedLayout l;
+  const int group = num_q_heads / num_kv_heads;
+  const long long tok_per_pair = 2 * (128 / group);
+  // a group's tokens are neighbours, and the groups' tokens disjoint
+  long long pairs = num_tokens / tok_per_pair + num_groups;
+  if (pairs < 1) pairs = 1;
+  const long long tiles = ((long long)max_prefix_len + 127) / 128;
+  long long chunks = (kSharedTargetItems + pairs * num_kv_heads - 1) / (pairs * num_kv_heads);
+  if (chunks > kMaxPrefixChunks) chunks = kMaxPrefixChunks;
+  if (chunks > tiles) chunks = tiles;
+  if (chunks < 1) chunks = 1;
+  l.chunk_tiles = (int)((tiles + chunks - 1) / chunks);
+  if (l.chunk_tiles < 1) l.chunk_tiles = 1;
+  l.max_chunks = (int)((tiles + l.chunk_tiles - 1) / l.chunk_tiles);
+  if (l.max_chunks < 1) l.max_chunks = 1;
+  const long long items = pairs * num_kv_heads * l.max_chunks;
+  l.max_items = items < (1LL << 30) ? (int)items : (1 << 30);
+  l.items_off = base.total;
+  l.chunks_off = l.items_off + pa_align256(sizeof(SharedItem) * (size_t)l.max_items);
+  l.partials_off = l.chunks_off + pa_align256(sizeof(int) * (size_t)num_tokens);
+  l.total = l.partials_off + pa_align256(sizeof(float) * (size_t)base.slot_floats *
+                                         (size_t)l.max_chunks * (size_t)num_tokens *
+                                         (size_t)num_kv_heads);
+  return l;
+}
+
 struct PlanParams {
   const int32_t* qsl;
   const int32_t* seq_lens;
@@ -238,6 +292,12 @@ struct PlanParams {
   WsHeader* header;
   UnitInfo* units;
   PrefillTile* tiles;
+  // pa_attention_shared (num_groups > 0): see SharedLayout
+  const int32_t* group_start;
+  const int32_t* prefix_lens;
+  int num_groups, max_prefix_len, chunk_tiles, max_items;
+  SharedItem* shared_items;
+  int* tok_chunks;  // of every token: key chunks of its prefix; 0: it attends on its own
   int2* raw;        // per-token scratch when the batch is too large for shared memory
   int* worker_unit; // first unit of each split-KV worker (only when the batch fits)
   unsigned long long* err;
@@ -249,6 +309,7 @@ struct PrefillLaunch {
   // output is fp32 partials, one slot per (chunk, token, kv head)
   int prefix_len, prefix_chunks, slot_floats;
   float* prefix_partials;
+  const SharedItem* shared_items;  // pa_attention_shared's prefix pass; else null
   // E4M3 caches: k_cache / v_cache hold codes; k_scale is already folded into
   // scale_log2, v_scale multiplies the output
   int kv_fp8;  // 2: row-scaled (scales)
@@ -343,6 +404,7 @@ struct MergeParams {
   // prefix chunks; grid units * Hkv
   int all_units;
   const UnitInfo* units;
+  const int* tok_chunks;    // pa_attention_shared (all_units): prefix chunks of each token
   int token_major;          // token-major split-KV: a task {token, -, wf, wl} covers every
                             // kv head (a CTA per boundary, a warp per kv head), slot
                             // (token + w) * Hkv + kv head
@@ -582,5 +644,7 @@ bool encode_tmap_u8(void* tmap, int rank, const void* ptr, const uint64_t* dims,
 #define PA_DEC_OCC_CAP_FP8 3  // E4M3 calls: smaller rings, a third CTA where registers allow
 #endif
 cudaError_t launch_prefill(const PrefillLaunch& a, int num_sms, cudaStream_t s);
+// launch_prefill of a.shared_items (prefill_groups.cu).
+cudaError_t launch_prefill_groups(const PrefillLaunch& a, int num_sms, cudaStream_t s);
 
 }  // namespace pa

@@ -12,6 +12,13 @@
 //    to the split-KV path with the prefix blocks left out of its positions;
 //    requests must see the whole prefix and start with request 0's prefix
 //    blocks, which is checked here.
+//  - Shared calls (groups of requests, each with its own prefix): the tokens of a
+//    group that share its prefix become units over their own keys only - the
+//    unit's `req` is then the offset of its first own block in the tables (the
+//    split-KV kernels run with a row stride of 1), its `len` the keys from there
+//    on - and every (pair of row tiles, kv head, key chunk) of a prefix a work
+//    item of the prefix pass. More CTAs check the tables' prefix blocks, a group
+//    each.
 // Invalid spans or lengths are skipped and reported on the device error word.
 //  - Windowed calls count only the blocks (tiles) that hold a key the token
 //    (an item's rows) attends to.
@@ -55,6 +62,94 @@ __device__ __forceinline__ long long block_exclusive_scan(long long v, long long
 
 constexpr int kTileBuckets = 512;  // tiles sorted by key-tile count, longest first
 
+// ---- shared calls -----------------------------------------------------------------
+// The group of request r, or -1: its prefix in blocks goes to *blocks (0: none, or
+// not one that this call takes).
+__device__ __forceinline__ int shared_group(const PlanParams& p, int r, int* blocks) {
+  int lo = 0, hi = p.num_groups;  // the last group that starts at or before r
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(p.group_start + mid) <= r) lo = mid; else hi = mid;
+  }
+  const int a = __ldg(p.group_start + lo), b = __ldg(p.group_start + lo + 1);
+  const int len = __ldg(p.prefix_lens + lo);
+  *blocks = 0;
+  if (r < a || r >= b || a < 0 || b > p.num_reqs) return -1;
+  if (len > 0 && len % kBlockSize == 0 && len <= p.max_prefix_len) *blocks = len / kBlockSize;
+  return lo;
+}
+
+// Request r's span and length, false if they do not agree (reported if asked).
+__device__ __forceinline__ bool check_request(const PlanParams& p, int r, int& q0, int& qlen, int& L,
+                                              bool report) {
+  // the three loads are issued together: one DRAM round trip, not two
+  q0 = __ldg(p.qsl + r);
+  const int q1 = __ldg(p.qsl + r + 1);
+  L = __ldg(p.seq_lens + r);
+  if (q0 < 0 || q1 < q0 || q1 > p.num_tokens) {
+    if (report) report_error(p.err, PA_DEVERR_QSL, r);
+    return false;
+  }
+  qlen = q1 - q0;
+  if (L < qlen || (L + kBlockSize - 1) / kBlockSize > p.max_blocks_per_req ||
+      qlen > p.max_query_len || L > p.max_seq_len || L - qlen < p.prefix_blocks * kBlockSize) {
+    if (report) report_error(p.err, PA_DEVERR_LENGTHS, r);
+    return false;
+  }
+  return true;
+}
+
+// Whether request r shares a prefix of `blocks` blocks: it has tokens on the
+// split-KV path, and they see all of it.
+__device__ __forceinline__ bool shares(const PlanParams& p, int qlen, int L, int blocks) {
+  return blocks > 0 && qlen > 0 && !(p.use_prefill && qlen >= kPrefillMinQlen) &&
+         L - qlen >= blocks * kBlockSize;
+}
+
+// CTAs 1 .. of a shared call's plan: every request that shares its group's prefix
+// starts with the same blocks as the first one that does.
+__device__ void check_shared_tables(const PlanParams& p) {
+  __shared__ int s_leader;
+  for (int g = (int)blockIdx.x - 1; g < p.num_groups; g += (int)gridDim.x - 1) {
+    const int a = __ldg(p.group_start + g), b = __ldg(p.group_start + g + 1);
+    const int len = __ldg(p.prefix_lens + g);
+    if (threadIdx.x == 0) {
+      if (a < 0 || b < a || b > p.num_reqs) report_error(p.err, PA_DEVERR_QSL, g);
+      else if (len < 0 || len % kBlockSize != 0 || len > p.max_prefix_len)
+        report_error(p.err, PA_DEVERR_PREFIX, g);
+      s_leader = 0x7fffffff;
+    }
+    if (a < 0 || b <= a || b > p.num_reqs || len <= 0 || len % kBlockSize != 0 ||
+        len > p.max_prefix_len)
+      continue;  // the same for every thread
+    const int blocks = len / kBlockSize;
+    __syncthreads();
+    int q0, qlen, L;
+    for (int r = a + (int)threadIdx.x; r < b; r += blockDim.x)
+      if (check_request(p, r, q0, qlen, L, false) && shares(p, qlen, L, blocks)) {
+        atomicMin(&s_leader, r);
+        break;  // a thread's later requests have larger numbers
+      }
+    __syncthreads();
+    const int leader = s_leader;
+    if (leader < b) {
+      const int32_t* const want = p.block_tables + (size_t)leader * p.max_blocks_per_req;
+      // a warp takes a request at a time, with several loads in flight per lane
+      for (int r = leader + 1 + (int)(threadIdx.x >> 5); r < b; r += blockDim.x >> 5) {
+        if (!check_request(p, r, q0, qlen, L, false) || !shares(p, qlen, L, blocks)) continue;
+        const int32_t* const got = p.block_tables + (size_t)r * p.max_blocks_per_req;
+        bool same = true;
+#pragma unroll 8
+        for (int i = (int)(threadIdx.x & 31); i < blocks; i += 32)
+          same &= __ldg(got + i) == __ldg(want + i);
+        if (!same) report_error(p.err, PA_DEVERR_PREFIX, r);
+      }
+    }
+    __syncthreads();  // s_leader is read before the next group's
+  }
+}
+
+template <bool SHARED>
 __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
   // The lengths and tables may come from the grid before, and so may what the
   // cascade prefix pass reads, which this grid lets start next.
@@ -64,6 +159,12 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
   // plan is released at the end of this one instead (starting it early
   // measured slower).
   if (p.early_trigger) griddep_launch_dependents();
+  if constexpr (SHARED) {
+    if (blockIdx.x > 0) {
+      check_shared_tables(p);
+      return;
+    }
+  }
   __shared__ long long scan_sm[32];
   __shared__ int bucket_cnt[kTileBuckets];
   __shared__ int bucket_pos[kTileBuckets];
@@ -86,23 +187,8 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
   __syncthreads();
 
   // a request is valid when its span lies in [0, T] and its lengths agree
-  // (the three loads are issued together: one DRAM round trip, not two)
   auto check = [&](int r, int& q0, int& qlen, int& L, bool report) -> bool {
-    q0 = __ldg(p.qsl + r);
-    const int q1 = __ldg(p.qsl + r + 1);
-    L = __ldg(p.seq_lens + r);
-    if (q0 < 0 || q1 < q0 || q1 > T) {
-      if (report) report_error(p.err, PA_DEVERR_QSL, r);
-      return false;
-    }
-    qlen = q1 - q0;
-    if (L < qlen || (L + kBlockSize - 1) / kBlockSize > p.max_blocks_per_req ||
-        qlen > p.max_query_len || L > p.max_seq_len ||
-        L - qlen < p.prefix_blocks * kBlockSize) {
-      if (report) report_error(p.err, PA_DEVERR_LENGTHS, r);
-      return false;
-    }
-    return true;
+    return check_request(p, r, q0, qlen, L, report);
   };
   auto tile_nkv = [&](int L, int ctx, int j0) -> int {  // 128-key tiles the item needs
     const int last = min(L - 1, ctx + j0 + tok_per_item - 1);  // last key of the item's rows
@@ -134,6 +220,29 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
                        1 + (int)((i0 + (long long)k * blockDim.x) / p.prefix_blocks));
     }
   }
+  // shared: of every group, its tokens that share the prefix (how many, the first
+  // and behind the last) and the first request of theirs
+  __shared__ int s_first[SHARED ? kMaxSharedGroups : 1], s_count[SHARED ? kMaxSharedGroups : 1];
+  __shared__ int s_lo[SHARED ? kMaxSharedGroups : 1], s_hi[SHARED ? kMaxSharedGroups : 1];
+  if constexpr (SHARED) {
+    for (int g = threadIdx.x; g < p.num_groups; g += blockDim.x) {
+      s_first[g] = s_lo[g] = 0x7fffffff;
+      s_count[g] = s_hi[g] = 0;
+    }
+    for (int t = threadIdx.x; t < T; t += blockDim.x) p.tok_chunks[t] = 0;
+    __syncthreads();
+    for (int r = threadIdx.x; r < p.num_reqs; r += blockDim.x) {
+      int q0, qlen, L, blocks;
+      if (!check(r, q0, qlen, L, false)) continue;
+      const int g = shared_group(p, r, &blocks);
+      if (g < 0 || !shares(p, qlen, L, blocks)) continue;
+      atomicMin(&s_first[g], r);
+      atomicAdd(&s_count[g], qlen);
+      atomicMin(&s_lo[g], q0);
+      atomicMax(&s_hi[g], q0 + qlen);
+    }
+    __syncthreads();
+  }
   for (int r = threadIdx.x; r < p.num_reqs; r += blockDim.x) {
     int q0, qlen, L;
     if (!check(r, q0, qlen, L, true)) continue;
@@ -148,7 +257,19 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
       if (p.overlap) atomicAdd(&s_steps, steps * p.num_kv_heads);
       continue;  // these tokens are not on the split-KV path
     }
-    for (int j = 0; j < qlen; ++j) raw[q0 + j] = make_int2(r, ctx + j + 1);
+    if constexpr (SHARED) {
+      int blocks;
+      const int g = shared_group(p, r, &blocks);
+      if (g < 0 || !shares(p, qlen, L, blocks) || s_count[g] < kSharedMinTokens) blocks = 0;
+      const int at = r * p.max_blocks_per_req + blocks, tiles = (blocks + 7) / 8;
+      const int chunks = (tiles + p.chunk_tiles - 1) / p.chunk_tiles;
+      for (int j = 0; j < qlen; ++j) {
+        raw[q0 + j] = make_int2(at, ctx + j + 1 - blocks * kBlockSize);
+        if (chunks > 0) p.tok_chunks[q0 + j] = chunks;
+      }
+    } else {
+      for (int j = 0; j < qlen; ++j) raw[q0 + j] = make_int2(r, ctx + j + 1);
+    }
   }
   __syncthreads();
   if (p.use_prefill) {  // positions of the buckets, longest tiles first (exclusive scan, descending)
@@ -173,6 +294,55 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
         for (int kv = 0; kv < p.num_kv_heads; ++kv) p.tiles[at + kv] = PrefillTile{r, kv, j0, nkv};
       }
     }
+  }
+  if constexpr (SHARED) {  // the prefix pass's items, group after group
+    __shared__ int s_at[kMaxSharedGroups + 1];
+    long long run = 0;
+    for (int c0 = 0; c0 < p.num_groups; c0 += blockDim.x) {
+      const int g = c0 + threadIdx.x;
+      long long n = 0;
+      if (g < p.num_groups && s_count[g] >= kSharedMinTokens) {
+        const int tiles = (__ldg(p.prefix_lens + g) / kBlockSize + 7) / 8;
+        n = (long long)((s_hi[g] - s_lo[g] + tok_per_item - 1) / tok_per_item) *
+            ((tiles + p.chunk_tiles - 1) / p.chunk_tiles) * p.num_kv_heads;
+      }
+      long long total;
+      const long long ex = block_exclusive_scan(n, &total, scan_sm);
+      // (an overfull list, which spans that overlap can make, is cut below)
+      if (g < p.num_groups) s_at[g] = (int)min(run + ex, (long long)p.max_items + 1);
+      run += total;
+    }
+    const int n = (int)min(run, (long long)p.max_items);
+    if (threadIdx.x == 0) {
+      s_at[p.num_groups] = n;
+      p.header->num_prefix_items = n;
+      if (run > n) report_error(p.err, PA_DEVERR_QSL, p.num_reqs);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+      int lo = 0, hi = p.num_groups;  // s_at[lo] <= i < s_at[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_at[mid] <= i) lo = mid; else hi = mid;
+      }
+      const int len = __ldg(p.prefix_lens + lo), tiles = (len + 127) / 128;
+      const int chunks = (tiles + p.chunk_tiles - 1) / p.chunk_tiles;
+      // kv heads innermost, then chunks: neighbouring items read neighbouring keys
+      int k = i - s_at[lo];
+      SharedItem it;
+      it.kv = k % p.num_kv_heads;
+      k /= p.num_kv_heads;
+      it.chunk = k % chunks;
+      k /= chunks;
+      it.req = s_first[lo];
+      it.tok0 = s_lo[lo] + k * tok_per_item;
+      it.tok_end = s_hi[lo];
+      it.i0 = it.chunk * p.chunk_tiles;
+      it.n = min(p.chunk_tiles, tiles - it.i0);
+      it.L = len;
+      p.shared_items[i] = it;
+    }
+    __syncthreads();  // scan_sm is used again
   }
   // compaction: tokens with keys become units with their first flattened position
   constexpr long long kLow = (1LL << 40) - 1;
@@ -257,7 +427,10 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
   griddep_wait();
 }
 
-cudaError_t launch_plan(const PlanParams& p, cudaStream_t s) {
+namespace {
+template <bool SHARED>
+cudaError_t launch_plan_t(const PlanParams& p, cudaStream_t s) {
+  auto kern = pa_plan_kernel<SHARED>;
   const int smem = p.num_tokens <= kPlanSmemTokens
                        ? (int)(sizeof(int2) * p.num_tokens + sizeof(int) * (p.num_tokens + 1))
                        : 0;
@@ -266,7 +439,7 @@ cudaError_t launch_plan(const PlanParams& p, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    e = cudaFuncSetAttribute(pa_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)(sizeof(int2) * kPlanSmemTokens + sizeof(int) * (kPlanSmemTokens + 1)));
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
@@ -275,11 +448,12 @@ cudaError_t launch_plan(const PlanParams& p, cudaStream_t s) {
   // for at its start; with early_start (the KV write, which makes nothing that
   // a plan needs) before completing.
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1);
+  // shared calls: CTAs of their own check the groups' tables
+  cfg.gridDim = dim3(SHARED ? 1 + (p.num_groups < 64 ? p.num_groups : 64) : 1);
   // A batch with no tensor-core work needs no bucket sort: a block sized to the
   // batch (fewer warps per barrier) plans it faster.
   int threads = kPlanThreads;
-  if (!p.use_prefill) {
+  if (!SHARED && !p.use_prefill) {
     int need = p.num_tokens > p.num_reqs ? p.num_tokens : p.num_reqs;
     // a cascade's prefix check reads (requests - 1) x prefix blocks entries
     if (p.prefix_blocks > 0 && (long long)(p.num_reqs - 1) * p.prefix_blocks > need)
@@ -294,7 +468,12 @@ cudaError_t launch_plan(const PlanParams& p, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, pa_plan_kernel, p);
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+}  // namespace
+
+cudaError_t launch_plan(const PlanParams& p, cudaStream_t s) {
+  return p.num_groups > 0 ? launch_plan_t<true>(p, s) : launch_plan_t<false>(p, s);
 }
 
 }  // namespace pa

@@ -109,6 +109,44 @@ def test_read(pa_lib):
     assert pa_lib.pa_read_kv(None) == ARG
 
 
+def shared(**kw):
+    a = dict(q=FAKE, kc=FAKE, vc=FAKE, sc=FAKE, bt=FAKE, sl=FAKE, qsl=FAKE, gl=FAKE, pl=FAKE,
+             out=FAKE, ws=FAKE, wsb=None, scale=0.125, ks=0.5, vs=0.5, fmt=2, R=4, T=4, hq=4, hkv=2,
+             d=64, bs=16, nb=32, mb=4, mq=1, ms=56, G=2, mp=32)
+    a.update(kw)
+    L = binding.lib()
+    if a["wsb"] is None:
+        a["wsb"] = L.pa_attention_shared_workspace_size(a["R"], a["T"], a["hq"], a["hkv"], a["d"],
+                                                        a["G"], a["mp"])
+    p = [a[n] or 0 for n in ("q", "kc", "vc", "sc", "bt", "sl", "qsl", "gl", "pl", "out", "ws")]
+    return L.pa_attention_shared(binding._pack_sh(
+        *p, 0, a["wsb"], a["scale"], a["ks"], a["vs"], a["fmt"], a["R"], a["T"], a["hq"], a["hkv"],
+        a["d"], a["bs"], a["nb"], a["mb"], a["mq"], a["ms"], a["G"], a["mp"]))
+
+
+def test_shared(pa_lib):
+    for name in ("q", "kc", "vc", "sc", "bt", "sl", "qsl", "out", "gl", "pl"):
+        assert shared(**{name: None}) == ARG, name
+    for name in ("q", "kc", "vc", "sc", "out"):
+        assert shared(**{name: FAKE + 8}) == ARG, name
+    assert shared(gl=FAKE + 2) == ARG and shared(pl=FAKE + 1) == ARG
+    assert shared(R=-1, wsb=0) == ARG and shared(G=-1, wsb=0) == ARG and shared(mp=-1, wsb=0) == ARG
+    assert shared(fmt=3) == ARG and shared(fmt=-1) == ARG and shared(scale=math.nan) == ARG
+    assert shared(nb=0) == ARG
+    assert shared(fmt=1, ks=0.0) == ARG and shared(fmt=1, vs=math.inf) == ARG
+    assert shared(d=96) == UNSUP and shared(bs=32) == UNSUP and shared(hq=32, wsb=0) == UNSUP
+    assert shared(G=1025, wsb=0) == UNSUP
+    assert shared(R=2 ** 20, mb=2 ** 11, wsb=2 ** 62) == UNSUP  # table offsets past 32 bits
+    assert shared(ws=None) == WS and shared(wsb=16) == WS and shared(ws=FAKE + 16) == WS
+    assert shared(R=0, wsb=0) == OK and shared(T=0, wsb=0) == OK
+    assert pa_lib.pa_attention_shared(None) == ARG
+    size = pa_lib.pa_attention_shared_workspace_size
+    plain = pa_lib.pa_attention_workspace_size(4, 4, 4, 2, 64)
+    assert size(4, 4, 4, 2, 64, 2, 32) > plain and size(4, 4, 4, 2, 64, 0, 0) > plain
+    assert size(4, 4, 4, 2, 64, 1025, 32) == 0 and size(4, 4, 4, 2, 64, 2, -1) == 0
+    assert size(4, 4, 6, 2, 64, 2, 32) == 0
+
+
 def test_struct_sizes(pa_lib):
     binding.lib()  # checks pa_args_size against every layout
     assert pa_lib.pa_args_size(15) == 0 and pa_lib.pa_args_size(16) > 0
