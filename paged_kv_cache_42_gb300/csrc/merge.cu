@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) pa_merge_kernel(const MergeP
   // The partials: the suffix slots wf .. wl, then (cascade) the prefix chunks.
   // Worker wf + i's slot: u + wf + i (u = token * Hkv + kv head).
   const int u = tok * p.num_kv_heads + kv;
-  const int ns = wl - wf + 1, n = ns + (SHARED ? __ldcg(p.tok_chunks + tok) : p.prefix_chunks);
+  const int ns = wl - wf + 1, n = ns + (SHARED ? __ldcg(p.tok_parts + tok) : p.prefix_chunks);
   auto slot = [&](int i) -> const float* {
     const size_t s0 = SHARED && p.token_major ? (size_t)(tok + wf + i) * p.num_kv_heads + kv
                                               : (size_t)(u + wf + i);
@@ -241,7 +241,7 @@ cudaError_t launch_merge_t(const MergeParams& p, cudaStream_t s) {
   const int boundaries = p.all_units ? p.num_tokens * p.num_kv_heads : p.num_workers - 1;
   if (boundaries <= 0) return cudaSuccess;  // one worker: nothing is ever split
   // token-major partials: eight KV heads, no cascade (the split-KV kernel's own limits)
-  if (p.tok_chunks != nullptr) {
+  if (p.tok_parts != nullptr) {
     if (!p.all_units) return cudaErrorInvalidValue;
   } else if (p.token_major && (p.all_units || p.prefix_chunks != 0 || p.num_kv_heads > kMergeWarps))
     return cudaErrorInvalidValue;
@@ -257,7 +257,7 @@ cudaError_t launch_merge_t(const MergeParams& p, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (p.tok_chunks != nullptr) return cudaLaunchKernelEx(&cfg, pa_merge_kernel<D, G, true>, p);
+  if (p.tok_parts != nullptr) return cudaLaunchKernelEx(&cfg, pa_merge_kernel<D, G, true>, p);
   if (p.token_major) {  // a CTA per boundary, a warp per KV head
     cfg.blockDim = dim3(32 * p.num_kv_heads);
     return cudaLaunchKernelEx(&cfg, pa_merge_tm_kernel<D, G>, p);

@@ -490,7 +490,9 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
   // single blocks (four tokens of a 16-key window at head_dim 64: 7.3 us per
   // call against 16 us with eight blocks each). The tensor-core kernels' workers
   // keep a whole tile.
-  pp.min_pos = window > 0 && !use_tc ? 1 : PA_DEC_MIN_POS;
+  // (Over row-scaled caches the CUDA-core workers do too: four short decodes at
+  // head_dim 64 17.4 -> 8.1 us.)
+  pp.min_pos = (window > 0 || kv_fp8 == 2) && !use_tc ? 1 : PA_DEC_MIN_POS;
   // A mixed batch on the tensor-core split-KV kernel (bf16) may run its
   // prefill chunks on a few SMs beside the split-KV work (the planner decides
   // how many, or none); the E4M3 path keeps its query-split pass between them.
@@ -680,7 +682,7 @@ pa_status shared_impl(const pa_shared_args& a) {
   cudaStream_t s = static_cast<cudaStream_t>(a.stream);
   unsigned char* const ws = static_cast<unsigned char*>(a.workspace);
   float* const prefix_partials = reinterpret_cast<float*>(ws + sh.partials_off);
-  int* const tok_chunks = reinterpret_cast<int*>(ws + sh.chunks_off);
+  int* const tok_parts = reinterpret_cast<int*>(ws + sh.parts_off);
   const float scale_log2 = a.scale * 1.4426950408889634f * k_scale;
 
   // The suffixes: the token-major tensor-core kernel where pa_attention takes it;
@@ -714,7 +716,7 @@ pa_status shared_impl(const pa_shared_args& a) {
   pp.num_workers = (cap > 0 && cap < launched) ? cap : launched;
   pp.num_sms = d->num_sms;
   pp.token_major = use_tm ? 1 : 0;
-  pp.min_pos = PA_DEC_MIN_POS;
+  pp.min_pos = use_tm ? PA_DEC_MIN_POS : 1;  // suffixes are short: as in a windowed call
   pp.group_start = a.group_start_loc;
   pp.prefix_lens = a.prefix_lens;
   pp.num_groups = a.num_groups;
@@ -722,7 +724,7 @@ pa_status shared_impl(const pa_shared_args& a) {
   pp.chunk_tiles = sh.chunk_tiles;
   pp.max_items = sh.max_items;
   pp.shared_items = reinterpret_cast<SharedItem*>(ws + sh.items_off);
-  pp.tok_chunks = tok_chunks;
+  pp.tok_parts = tok_parts;
   pp.header = reinterpret_cast<WsHeader*>(ws + lay.header_off);
   pp.units = reinterpret_cast<UnitInfo*>(ws + lay.units_off);
   pp.tiles = reinterpret_cast<PrefillTile*>(ws + lay.tiles_off);
@@ -834,7 +836,7 @@ pa_status shared_impl(const pa_shared_args& a) {
   mp.num_kv_heads = a.num_kv_heads;
   mp.num_tokens = a.num_tokens;
   mp.prefix_partials = prefix_partials;
-  mp.tok_chunks = tok_chunks;
+  mp.tok_parts = tok_parts;
   mp.v_scale = v_scale;
   mp.out = dp.out;
   mp.all_units = 1;

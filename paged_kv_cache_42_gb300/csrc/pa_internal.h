@@ -222,22 +222,28 @@ constexpr int kMaxSharedGroups = 1024;  // the planner keeps them in shared memo
 // A group of fewer tokens than this on the split-KV path attends on its own: one
 // token reads its prefix once either way.
 constexpr int kSharedMinTokens = 2;
-// Prefix work items aimed at (an item holds an SM alone; GB300 has 152).
-constexpr int kSharedTargetItems = 152;
+// Prefix work items that the workspace leaves room for at least (an item holds an
+// SM alone; GB300 has 152): the planner picks the length of the key chunks.
+constexpr int kSharedMostItems = 2 * 152;
+// Steps (an item's key tile, both row tiles) that starting and ending an item costs.
+constexpr int kSharedItemSteps = 2;
 
 // One prefix work item: two 128-row tiles of kv head `kv`, batch tokens tok0 up
 // to tok_end - 1 at most, against key tiles i0 .. i0 + n - 1 of the L prefix keys
-// in request req's table; chunk: which of the prefix's key chunks that is.
+// in request req's table; its partials are number `part` of its tokens. Split
+// (kSharedSplit set in kv): the rows fit one tile, and the two take them both,
+// one the even key tiles and the other the odd ones, into partials part and
+// part + 1.
 struct SharedItem {
-  int req, kv, tok0, tok_end, chunk, i0, n, L;
+  int req, kv, tok0, tok_end, part, i0, n, L;
 };
 static_assert(sizeof(SharedItem) == 32, "items are two 16-byte vectors");
+constexpr int kSharedSplit = 1 << 30;
 
 // What pa_attention_shared's workspace holds behind ws_layout's.
 struct SharedLayout {
-  size_t items_off, chunks_off, partials_off, total;
-  int chunk_tiles;  // 128-key tiles of a key chunk
-  int max_chunks;   // of any group's prefix
+  size_t items_off, parts_off, partials_off, total;
+  int chunk_tiles;  // 128-key tiles of a key chunk at least
   int max_items;
 };
 
@@ -251,22 +257,22 @@ inline SharedLayout shared_layout(int num_reqs, int num_tokens, int num_q_heads,
   long long pairs = num_tokens / tok_per_pair + num_groups;
   if (pairs < 1) pairs = 1;
   const long long tiles = ((long long)max_prefix_len + 127) / 128;
-  long long chunks = (kSharedTargetItems + pairs * num_kv_heads - 1) / (pairs * num_kv_heads);
+  long long chunks = (kSharedMostItems + pairs * num_kv_heads - 1) / (pairs * num_kv_heads);
   if (chunks > kMaxPrefixChunks) chunks = kMaxPrefixChunks;
   if (chunks > tiles) chunks = tiles;
   if (chunks < 1) chunks = 1;
   l.chunk_tiles = (int)((tiles + chunks - 1) / chunks);
   if (l.chunk_tiles < 1) l.chunk_tiles = 1;
-  l.max_chunks = (int)((tiles + l.chunk_tiles - 1) / l.chunk_tiles);
-  if (l.max_chunks < 1) l.max_chunks = 1;
-  const long long items = pairs * num_kv_heads * l.max_chunks;
+  chunks = (tiles + l.chunk_tiles - 1) / l.chunk_tiles;
+  if (chunks < 1) chunks = 1;
+  const long long items = pairs * num_kv_heads * chunks;
   l.max_items = items < (1LL << 30) ? (int)items : (1 << 30);
   l.items_off = base.total;
-  l.chunks_off = l.items_off + pa_align256(sizeof(SharedItem) * (size_t)l.max_items);
-  l.partials_off = l.chunks_off + pa_align256(sizeof(int) * (size_t)num_tokens);
-  l.total = l.partials_off + pa_align256(sizeof(float) * (size_t)base.slot_floats *
-                                         (size_t)l.max_chunks * (size_t)num_tokens *
-                                         (size_t)num_kv_heads);
+  l.parts_off = l.items_off + pa_align256(sizeof(SharedItem) * (size_t)l.max_items);
+  l.partials_off = l.parts_off + pa_align256(sizeof(int) * (size_t)num_tokens);
+  // two partials of a (token, kv head) per chunk at most
+  l.total = l.partials_off + pa_align256(sizeof(float) * (size_t)base.slot_floats * 2 *
+                                         (size_t)chunks * (size_t)num_tokens * (size_t)num_kv_heads);
   return l;
 }
 
@@ -297,7 +303,7 @@ struct PlanParams {
   const int32_t* prefix_lens;
   int num_groups, max_prefix_len, chunk_tiles, max_items;
   SharedItem* shared_items;
-  int* tok_chunks;  // of every token: key chunks of its prefix; 0: it attends on its own
+  int* tok_parts;  // of every token: partials of its prefix; 0: it attends on its own
   int2* raw;        // per-token scratch when the batch is too large for shared memory
   int* worker_unit; // first unit of each split-KV worker (only when the batch fits)
   unsigned long long* err;
@@ -404,7 +410,7 @@ struct MergeParams {
   // prefix chunks; grid units * Hkv
   int all_units;
   const UnitInfo* units;
-  const int* tok_chunks;    // pa_attention_shared (all_units): prefix chunks of each token
+  const int* tok_parts;     // pa_attention_shared (all_units): prefix partials of each token
   int token_major;          // token-major split-KV: a task {token, -, wf, wl} covers every
                             // kv head (a CTA per boundary, a warp per kv head), slot
                             // (token + w) * Hkv + kv head

@@ -60,6 +60,7 @@ __device__ __forceinline__ long long block_exclusive_scan(long long v, long long
   return before + x - v;
 }
 
+constexpr int kSharedCandidates = 256;  // lengths of a shared call's key chunks looked at
 constexpr int kTileBuckets = 512;  // tiles sorted by key-tile count, longest first
 
 // ---- shared calls -----------------------------------------------------------------
@@ -104,6 +105,17 @@ __device__ __forceinline__ bool check_request(const PlanParams& p, int r, int& q
 __device__ __forceinline__ bool shares(const PlanParams& p, int qlen, int L, int blocks) {
   return blocks > 0 && qlen > 0 && !(p.use_prefill && qlen >= kPrefillMinQlen) &&
          L - qlen >= blocks * kBlockSize;
+}
+
+// A prefix of `tiles` key tiles in chunks of ct: the partials that a pair of row
+// tiles with `left` tokens (its own and the group's behind it) leaves of it. Rows
+// that fit one tile are split over the two by key tiles (SharedItem), where a chunk
+// has two of them.
+__device__ __forceinline__ bool shared_split(int left, int group) { return left * group <= 128; }
+__device__ __forceinline__ int shared_parts(int tiles, int ct, bool split) {
+  const int chunks = (tiles + ct - 1) / ct;
+  if (!split || ct == 1) return chunks;
+  return 2 * chunks - (tiles - (chunks - 1) * ct == 1 ? 1 : 0);
 }
 
 // CTAs 1 .. of a shared call's plan: every request that shares its group's prefix
@@ -224,12 +236,14 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
   // and behind the last) and the first request of theirs
   __shared__ int s_first[SHARED ? kMaxSharedGroups : 1], s_count[SHARED ? kMaxSharedGroups : 1];
   __shared__ int s_lo[SHARED ? kMaxSharedGroups : 1], s_hi[SHARED ? kMaxSharedGroups : 1];
+  __shared__ int s_tiles[SHARED ? kMaxSharedGroups : 1];  // key tiles of its prefix; 0: not shared
+  __shared__ unsigned long long s_best;
   if constexpr (SHARED) {
     for (int g = threadIdx.x; g < p.num_groups; g += blockDim.x) {
       s_first[g] = s_lo[g] = 0x7fffffff;
       s_count[g] = s_hi[g] = 0;
     }
-    for (int t = threadIdx.x; t < T; t += blockDim.x) p.tok_chunks[t] = 0;
+    for (int t = threadIdx.x; t < T; t += blockDim.x) p.tok_parts[t] = 0;
     __syncthreads();
     for (int r = threadIdx.x; r < p.num_reqs; r += blockDim.x) {
       int q0, qlen, L, blocks;
@@ -241,8 +255,35 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
       atomicMin(&s_lo[g], q0);
       atomicMax(&s_hi[g], q0 + qlen);
     }
+    if (threadIdx.x == 0) s_best = ~0ull;
+    __syncthreads();
+    for (int g = threadIdx.x; g < p.num_groups; g += blockDim.x)
+      s_tiles[g] = s_count[g] >= kSharedMinTokens ? (__ldg(p.prefix_lens + g) + 127) / 128 : 0;
+    __syncthreads();
+    // The key chunks' length: of a thread's candidate, the time of the rounds that its
+    // items take on the SMs, in steps (split items half of one per tile).
+    const int ct = p.chunk_tiles + (int)threadIdx.x;
+    if (threadIdx.x < kSharedCandidates) {
+      long long items = 0, halves = 0, tiles_all = 0;
+      for (int g = 0; g < p.num_groups; ++g) {
+        const int tiles = s_tiles[g];
+        if (tiles == 0) continue;
+        const int n = s_hi[g] - s_lo[g], pairs = (n + tok_per_item - 1) / tok_per_item;
+        const int split = shared_split(n - (pairs - 1) * tok_per_item, p.group) ? 1 : 0;
+        items += (long long)pairs * ((tiles + ct - 1) / ct);
+        halves += (long long)(2 * pairs - split) * tiles;
+        tiles_all += (long long)pairs * tiles;
+      }
+      if (items > 0) {
+        const long long rounds = (items * p.num_kv_heads + p.num_sms - 1) / p.num_sms;
+        const float steps = (float)ct * (float)halves / (float)(2 * tiles_all);
+        const float cost = (float)rounds * (steps + kSharedItemSteps);
+        atomicMin(&s_best, (unsigned long long)__float_as_uint(cost) << 32 | (unsigned)ct);
+      }
+    }
     __syncthreads();
   }
+  const int chunk_tiles = SHARED && s_best != ~0ull ? (int)(unsigned)s_best : 1;
   for (int r = threadIdx.x; r < p.num_reqs; r += blockDim.x) {
     int q0, qlen, L;
     if (!check(r, q0, qlen, L, true)) continue;
@@ -261,11 +302,13 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
       int blocks;
       const int g = shared_group(p, r, &blocks);
       if (g < 0 || !shares(p, qlen, L, blocks) || s_count[g] < kSharedMinTokens) blocks = 0;
-      const int at = r * p.max_blocks_per_req + blocks, tiles = (blocks + 7) / 8;
-      const int chunks = (tiles + p.chunk_tiles - 1) / p.chunk_tiles;
+      const int at = r * p.max_blocks_per_req + blocks;
       for (int j = 0; j < qlen; ++j) {
         raw[q0 + j] = make_int2(at, ctx + j + 1 - blocks * kBlockSize);
-        if (chunks > 0) p.tok_chunks[q0 + j] = chunks;
+        if (blocks > 0) {
+          const int left = s_hi[g] - (q0 + j - (q0 + j - s_lo[g]) % tok_per_item);
+          p.tok_parts[q0 + j] = shared_parts((blocks + 7) / 8, chunk_tiles, shared_split(left, p.group));
+        }
       }
     } else {
       for (int j = 0; j < qlen; ++j) raw[q0 + j] = make_int2(r, ctx + j + 1);
@@ -301,11 +344,9 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
     for (int c0 = 0; c0 < p.num_groups; c0 += blockDim.x) {
       const int g = c0 + threadIdx.x;
       long long n = 0;
-      if (g < p.num_groups && s_count[g] >= kSharedMinTokens) {
-        const int tiles = (__ldg(p.prefix_lens + g) / kBlockSize + 7) / 8;
+      if (g < p.num_groups && s_tiles[g] > 0)
         n = (long long)((s_hi[g] - s_lo[g] + tok_per_item - 1) / tok_per_item) *
-            ((tiles + p.chunk_tiles - 1) / p.chunk_tiles) * p.num_kv_heads;
-      }
+            ((s_tiles[g] + chunk_tiles - 1) / chunk_tiles) * p.num_kv_heads;
       long long total;
       const long long ex = block_exclusive_scan(n, &total, scan_sm);
       // (an overfull list, which spans that overlap can make, is cut below)
@@ -325,21 +366,23 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
         const int mid = (lo + hi) >> 1;
         if (s_at[mid] <= i) lo = mid; else hi = mid;
       }
-      const int len = __ldg(p.prefix_lens + lo), tiles = (len + 127) / 128;
-      const int chunks = (tiles + p.chunk_tiles - 1) / p.chunk_tiles;
+      const int tiles = s_tiles[lo], chunks = (tiles + chunk_tiles - 1) / chunk_tiles;
       // kv heads innermost, then chunks: neighbouring items read neighbouring keys
       int k = i - s_at[lo];
       SharedItem it;
       it.kv = k % p.num_kv_heads;
       k /= p.num_kv_heads;
-      it.chunk = k % chunks;
+      const int chunk = k % chunks;
       k /= chunks;
       it.req = s_first[lo];
       it.tok0 = s_lo[lo] + k * tok_per_item;
       it.tok_end = s_hi[lo];
-      it.i0 = it.chunk * p.chunk_tiles;
-      it.n = min(p.chunk_tiles, tiles - it.i0);
-      it.L = len;
+      it.i0 = chunk * chunk_tiles;
+      it.n = min(chunk_tiles, tiles - it.i0);
+      it.L = __ldg(p.prefix_lens + lo);
+      const bool split = shared_split(it.tok_end - it.tok0, p.group);
+      it.part = shared_parts(it.i0, chunk_tiles, split);  // of the chunks before, all whole
+      if (split && it.n > 1) it.kv |= kSharedSplit;
       p.shared_items[i] = it;
     }
     __syncthreads();  // scan_sm is used again

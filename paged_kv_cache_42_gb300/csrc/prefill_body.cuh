@@ -38,7 +38,11 @@
 // max, sum, unnormalised output) per (chunk, token, kv head) for the split-KV
 // kernel to merge, instead of bf16 rows. Groups of requests with a prefix each
 // (MODE kGroups, pa_attention_shared) run the same pass over the planner's list of
-// items.
+// items. A group of few requests has few rows: those that fit one tile are given to
+// both, one warpgroup taking the even key tiles and the other the odd ones, each
+// into a partial of its own. That keeps the two-tile pipeline as it is - per tile
+// of keys, half the products - where an empty second tile would double the work
+// and a lone first one would leave nothing to run beside its softmax.
 //
 // FP8 caches (the F8 instantiation; "vLLM: An Exhaustive Technical Study for
 // Kernel Engineers", 2.8: E4M3 codes with per-tensor k_scale / v_scale): four
@@ -181,7 +185,8 @@ struct Item {
   int i0, n;  // key tiles i0 .. i0 + n - 1
   int L;      // keys that exist (sequence length; prefix length)
   int tok0;   // batch token of the pair's first row
-  int chunk;  // key chunk (prefix pass)
+  int chunk;  // which of its tokens' partials it makes (prefix pass)
+  bool split; // kGroups: both row tiles hold the same rows, one takes the even key tiles
   int tok_end;  // batch tokens from here on are not the item's (prefix pass)
   WinTiles wt;  // WIN: the key tiles of the item's rows
 };
@@ -205,7 +210,8 @@ __device__ __forceinline__ Item get_item(const PrefillParams& p, int t) {
     const int4* const at = reinterpret_cast<const int4*>(p.shared_items + t);
     const int4 a = __ldcg(at), b = __ldcg(at + 1);
     it.req = a.x;
-    it.kv = a.y;
+    it.kv = a.y & ~kSharedSplit;
+    it.split = (a.y & kSharedSplit) != 0;
     it.j0 = 0;
     it.tok0 = a.z;
     it.tok_end = a.w;
@@ -359,13 +365,16 @@ __global__ void __launch_bounds__(KV ? kThreadsF8 : kThreads, 1)
       int pid_nxt = tl.n > 4 ? load_group(1) : -1;
       if (it > 0 && !wait(B_Q_EMPTY, (it - 1) & 1)) { ok = false; break; }
       if (lane == 0) {
-        mbar_arrive_expect_tx(BAR(B_Q_FULL), 2 * C::Q_BYTES);
+        const int tiles = MODE == kGroups && tl.split ? 1 : 2;
+        mbar_arrive_expect_tx(BAR(B_Q_FULL), tiles * C::Q_BYTES);
 #pragma unroll
         for (int rt = 0; rt < 2; ++rt)
+          if (rt < tiles) {
 #pragma unroll
-          for (int c = 0; c < C::NCH; ++c)
-            tma_load_3d(base + C::OFF_Q + rt * C::Q_BYTES + c * C::CHUNK, &p.tm_q, c * 64,
-                        tl.kv * G, tl.tok0 + rt * C::TOK, BAR(B_Q_FULL));
+            for (int c = 0; c < C::NCH; ++c)
+              tma_load_3d(base + C::OFF_Q + rt * C::Q_BYTES + c * C::CHUNK, &p.tm_q, c * 64,
+                          tl.kv * G, tl.tok0 + rt * C::TOK, BAR(B_Q_FULL));
+          }
       }
       for (int i = 0; !F8 && i < tl.n; ++i, ++g) {  // E4M3: the converter warps load K/V
         if (i > 0 && (i & 3) == 0) {
@@ -414,14 +423,15 @@ __global__ void __launch_bounds__(KV ? kThreadsF8 : kThreads, 1)
       const int L = tl.L;
       if (!wait(B_Q_FULL, it & 1)) { ok = false; break; }
 
+      const bool split = MODE == kGroups && tl.split;
       // S_rt(key tile of counter gk) for row tile rt
       auto issue_s = [&](int rt, bool last_of_item) -> bool {
         const int kst = gk % C::KSTAGES;
-        if (rt == 0 && !wait(B_K_FULL + kst, (gk / C::KSTAGES) & 1)) return false;
+        if ((rt == 0 || split) && !wait(B_K_FULL + kst, (gk / C::KSTAGES) & 1)) return false;
         tc_fence_after();
         if (lane == 0) {
           const uint32_t d = tmem + C::TM_S + 128 * rt;
-          const uint64_t a0 = kmaj_base + ((C::OFF_Q + rt * C::Q_BYTES) >> 4);
+          const uint64_t a0 = kmaj_base + ((C::OFF_Q + (split ? 0 : rt * C::Q_BYTES)) >> 4);
           const uint64_t b0 = kmaj_base + ((C::OFF_K + kst * C::KV_BYTES) >> 4);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
@@ -429,23 +439,23 @@ __global__ void __launch_bounds__(KV ? kThreadsF8 : kThreads, 1)
             umma_bf16(d, a0 + off, b0 + off, p.idesc_qk, ks > 0 ? 1u : 0u);
           }
           umma_commit(BAR(B_S_FULL + rt));
-          if (rt == 1) {
+          if (rt == 1 || split) {
             umma_commit(BAR(B_K_EMPTY + kst));
             if (last_of_item) umma_commit(BAR(B_Q_EMPTY));
           }
         }
         __syncwarp();
-        if (rt == 1) ++gk;
+        if (rt == 1 || split) ++gk;
         return true;
       };
-      // P_rt(key tile i) * V for row tile rt
+      // P_rt(key tile i) * V for row tile rt (split: key tile 2 i + rt)
       auto issue_pv = [&](int rt, int i) -> bool {
         const int vst = gv % C::VSTAGES;
         if (!wait(B_P_FULL + rt, np[rt] & 1)) return false;
         ++np[rt];
-        if (rt == 0) {
+        if (rt == 0 || split) {
           if (!wait(B_V_FULL + vst, (gv / C::VSTAGES) & 1)) return false;
-          const int kv0 = key_tile<WIN>(tl, i) * 128;
+          const int kv0 = key_tile<WIN>(tl, split ? 2 * i + rt : i) * 128;
           if (WIN && !F8 && (kv0 + 128 > L || (kv0 < tl.wt.lo && kv0 + 128 > p.sinks))) {
             // rows of keys no row of the item sees, whose blocks were not read
             for (int idx = lane; idx < 128 * 8 * C::NCH; idx += 32) {
@@ -482,13 +492,24 @@ __global__ void __launch_bounds__(KV ? kThreadsF8 : kThreads, 1)
             umma_bf16_ta(d, a_tm + C::pcol(ks >> 1) + 8 * (ks & 1), b0 + ((ks * 2048) >> 4),
                          idesc_pv, (i > 0 || ks > 0) ? 1u : 0u);
           umma_commit(BAR(B_PV_DONE + rt));
-          if (rt == 1) umma_commit(BAR(B_V_EMPTY + vst));
+          if (rt == 1 || split) umma_commit(BAR(B_V_EMPTY + vst));
         }
         __syncwarp();
-        if (rt == 1) ++gv;
+        if (rt == 1 || split) ++gv;
         return true;
       };
 
+      if (split) {  // the same order, each row tile over its own half of the key tiles
+        const int n0 = (tl.n + 1) / 2, n1 = tl.n / 2;  // n1 >= 1
+        ok = issue_s(0, false) && issue_s(1, tl.n == 2);
+        for (int i = 0; ok && i < n0; ++i) {
+          ok = issue_pv(0, i);
+          if (ok && i + 1 < n0) ok = issue_s(0, 2 * i + 3 == tl.n);
+          if (ok && i < n1) ok = issue_pv(1, i);
+          if (ok && i + 1 < n1) ok = issue_s(1, 2 * i + 4 == tl.n);
+        }
+        continue;
+      }
       ok = issue_s(0, tl.n == 1) && issue_s(1, tl.n == 1);
       for (int i = 0; ok && i < tl.n; ++i) {
         const bool more = i + 1 < tl.n;
@@ -559,13 +580,15 @@ __global__ void __launch_bounds__(KV ? kThreadsF8 : kThreads, 1)
       // then taken first, and the largest P is 1 whatever the scores' size.
       float m_used = -INFINITY, m_raw = -INFINITY, l = 0.f;
       bool far = false;
-      for (int i = 0; i < tl.n; ++i) {
+      const bool split = MODE == kGroups && tl.split;
+      const int n = split ? (tl.n + 1 - rt) / 2 : tl.n;
+      for (int i = 0; i < n; ++i) {
         // S_rt(i) complete implies every earlier MMA is too: O_rt is stable
         // and P_rt(i-1) has been consumed.
         if (!wait(B_S_FULL + rt, ns & 1)) { ok = false; break; }
         ++ns;
         tc_fence_after();
-        const int kv0 = key_tile<WIN>(tl, i) * 128;
+        const int kv0 = key_tile<WIN>(tl, split ? 2 * i + rt : i) * 128;
         const bool unmasked = __all_sync(kAll, kv0 + 127 <= lim);
         // WIN: the row sees lo .. lim and the sinks; whole and empty runs of 32
         // columns are told apart, since a window has two edges to every item
@@ -710,11 +733,12 @@ __global__ void __launch_bounds__(KV ? kThreadsF8 : kThreads, 1)
       if (!ok) break;
       if constexpr (PREFIX) {
         // fp32 partial of (chunk, token, kv head), head m % G of the slot
-        const int tok = tl.tok0 + rt * C::TOK + m / G;
+        const int tok = tl.tok0 + (split ? 0 : rt * C::TOK) + m / G;
         const int h = m % G;
         const bool store = tok < tl.tok_end;
         float* const slot = p.prefix_partials +
-                            (((size_t)tl.chunk * p.num_tokens + (store ? tok : 0)) *
+                            (((size_t)(tl.chunk + (split ? rt : 0)) * p.num_tokens +
+                              (store ? tok : 0)) *
                                  p.num_kv_heads + tl.kv) * p.slot_floats;
         if (store && hf == 0) {
           __stcg(slot + h, m_used);
