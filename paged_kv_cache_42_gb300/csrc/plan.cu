@@ -107,15 +107,18 @@ __device__ __forceinline__ bool shares(const PlanParams& p, int qlen, int L, int
          L - qlen >= blocks * kBlockSize;
 }
 
-// A prefix of `tiles` key tiles in chunks of ct: the partials that a pair of row
-// tiles with `left` tokens (its own and the group's behind it) leaves of it. Rows
-// that fit one tile are split over the two by key tiles (SharedItem), where a chunk
-// has two of them.
+// A pair of row tiles with `left` tokens (its own and the group's behind it): rows
+// that fit one tile are split over the two by key tiles (SharedItem). Their key
+// chunks are twice as long (ct tiles otherwise), for as many steps.
 __device__ __forceinline__ bool shared_split(int left, int group) { return left * group <= 128; }
+__device__ __forceinline__ int shared_chunks(int tiles, int ct, bool split) {
+  return split ? (tiles + 2 * ct - 1) / (2 * ct) : (tiles + ct - 1) / ct;
+}
+// The partials that such a pair leaves of a prefix: two of a split chunk, unless it has
+// one tile only.
 __device__ __forceinline__ int shared_parts(int tiles, int ct, bool split) {
-  const int chunks = (tiles + ct - 1) / ct;
-  if (!split || ct == 1) return chunks;
-  return 2 * chunks - (tiles - (chunks - 1) * ct == 1 ? 1 : 0);
+  const int chunks = shared_chunks(tiles, ct, split);
+  return split ? 2 * chunks - (tiles - (chunks - 1) * 2 * ct == 1 ? 1 : 0) : chunks;
 }
 
 // CTAs 1 .. of a shared call's plan: every request that shares its group's prefix
@@ -261,23 +264,23 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
       s_tiles[g] = s_count[g] >= kSharedMinTokens ? (__ldg(p.prefix_lens + g) + 127) / 128 : 0;
     __syncthreads();
     // The key chunks' length: of a thread's candidate, the time of the rounds that its
-    // items take on the SMs, in steps (split items half of one per tile).
+    // items take on the SMs, in steps.
     const int ct = p.chunk_tiles + (int)threadIdx.x;
     if (threadIdx.x < kSharedCandidates) {
-      long long items = 0, halves = 0, tiles_all = 0;
+      long long items = 0;
+      int longest = 0;  // steps
       for (int g = 0; g < p.num_groups; ++g) {
         const int tiles = s_tiles[g];
         if (tiles == 0) continue;
         const int n = s_hi[g] - s_lo[g], pairs = (n + tok_per_item - 1) / tok_per_item;
         const int split = shared_split(n - (pairs - 1) * tok_per_item, p.group) ? 1 : 0;
-        items += (long long)pairs * ((tiles + ct - 1) / ct);
-        halves += (long long)(2 * pairs - split) * tiles;
-        tiles_all += (long long)pairs * tiles;
+        items += (long long)(pairs - split) * shared_chunks(tiles, ct, false) +
+                 split * shared_chunks(tiles, ct, true);
+        longest = max(longest, min(ct, pairs > split ? tiles : (tiles + 1) / 2));
       }
       if (items > 0) {
         const long long rounds = (items * p.num_kv_heads + p.num_sms - 1) / p.num_sms;
-        const float steps = (float)ct * (float)halves / (float)(2 * tiles_all);
-        const float cost = (float)rounds * (steps + kSharedItemSteps);
+        const float cost = (float)rounds * (float)(longest + kSharedItemSteps);
         atomicMin(&s_best, (unsigned long long)__float_as_uint(cost) << 32 | (unsigned)ct);
       }
     }
@@ -344,9 +347,12 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
     for (int c0 = 0; c0 < p.num_groups; c0 += blockDim.x) {
       const int g = c0 + threadIdx.x;
       long long n = 0;
-      if (g < p.num_groups && s_tiles[g] > 0)
-        n = (long long)((s_hi[g] - s_lo[g] + tok_per_item - 1) / tok_per_item) *
-            ((s_tiles[g] + chunk_tiles - 1) / chunk_tiles) * p.num_kv_heads;
+      if (g < p.num_groups && s_tiles[g] > 0) {
+        const int toks = s_hi[g] - s_lo[g], pairs = (toks + tok_per_item - 1) / tok_per_item;
+        const int split = shared_split(toks - (pairs - 1) * tok_per_item, p.group) ? 1 : 0;
+        n = ((long long)(pairs - split) * shared_chunks(s_tiles[g], chunk_tiles, false) +
+             split * shared_chunks(s_tiles[g], chunk_tiles, true)) * p.num_kv_heads;
+      }
       long long total;
       const long long ex = block_exclusive_scan(n, &total, scan_sm);
       // (an overfull list, which spans that overlap can make, is cut below)
@@ -366,22 +372,24 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
         const int mid = (lo + hi) >> 1;
         if (s_at[mid] <= i) lo = mid; else hi = mid;
       }
-      const int tiles = s_tiles[lo], chunks = (tiles + chunk_tiles - 1) / chunk_tiles;
+      const int tiles = s_tiles[lo], chunks = shared_chunks(tiles, chunk_tiles, false);
       // kv heads innermost, then chunks: neighbouring items read neighbouring keys
       int k = i - s_at[lo];
       SharedItem it;
       it.kv = k % p.num_kv_heads;
       k /= p.num_kv_heads;
-      const int chunk = k % chunks;
-      k /= chunks;
       it.req = s_first[lo];
-      it.tok0 = s_lo[lo] + k * tok_per_item;
       it.tok_end = s_hi[lo];
-      it.i0 = chunk * chunk_tiles;
-      it.n = min(chunk_tiles, tiles - it.i0);
-      it.L = __ldg(p.prefix_lens + lo);
+      // only the group's last pair can be split, with fewer chunks than the others
+      const int last = (it.tok_end - s_lo[lo] - 1) / tok_per_item;
+      const int pair = min(k / chunks, last), chunk = k - pair * chunks;
+      it.tok0 = s_lo[lo] + pair * tok_per_item;
       const bool split = shared_split(it.tok_end - it.tok0, p.group);
-      it.part = shared_parts(it.i0, chunk_tiles, split);  // of the chunks before, all whole
+      const int len = split ? 2 * chunk_tiles : chunk_tiles;
+      it.i0 = chunk * len;
+      it.n = min(len, tiles - it.i0);
+      it.L = __ldg(p.prefix_lens + lo);
+      it.part = split ? 2 * chunk : chunk;  // (the chunks before are whole)
       if (split && it.n > 1) it.kv |= kSharedSplit;
       p.shared_items[i] = it;
     }

@@ -45,11 +45,16 @@
 // and a lone first one would leave nothing to run beside its softmax.
 //
 // FP8 caches (the F8 instantiation; "vLLM: An Exhaustive Technical Study for
-// Kernel Engineers", 2.8: E4M3 codes with per-tensor k_scale / v_scale): four
-// more warps (448 threads) load each key tile's E4M3 rows with plain
-// coalesced loads (one thread per key row) and widen them to bf16 - exactly,
-// every E4M3 value being a bf16 - straight into the 128B-swizzled operand
-// layout the MMA reads, then arrive on the stage's full barrier. k_scale is
+// Kernel Engineers", 2.8: E4M3 codes with per-tensor k_scale / v_scale): a block's
+// codes are copied into the stage that their bf16 values will fill - over the
+// rows of their own (a block's 16 rows, at head dim 128 their second halves) - and
+// eight more warps (576 threads), four for K and four for V, widen them in place:
+// a warp takes 32 key rows into registers and writes them back as the
+// 128B-swizzled operand that the MMA reads - exactly, every E4M3 value being a
+// bf16 - and arrives on the stage's full barrier. So a ring of E4M3 tiles has all of
+// its stages in flight, as one of bf16 tiles has. (Loads into registers, two tiles
+// ahead, were limited to what the SM's remaining 28 KB of L1 can await: 4.3 us per
+// key tile of a long prefix against PREFSTEP.) k_scale is
 // folded into the softmax scale and v_scale into the epilogue. Over row-scaled
 // caches (KV 2, rows.cuh) the converters multiply each row by its 2^e, which is
 // exact in bf16 too, and nothing else differs.
@@ -111,6 +116,8 @@ struct PCfg {
   static constexpr int KSTAGES = kSplit == 2 ? 2 : 3;
 #endif
   static constexpr int VSTAGES = 2;
+  // E4M3: where in a stage block b's codes land (+ 2048 b), within the block's own rows
+  static constexpr int OFF_RAW = (NCH - 1) * CHUNK;
   static constexpr int OFF_Q = 0;  // two row tiles
   static constexpr int OFF_K = OFF_Q + 2 * Q_BYTES;
   static constexpr int OFF_V = OFF_K + KSTAGES * KV_BYTES;
@@ -118,7 +125,9 @@ struct PCfg {
   // row-max / row-sum exchange of the split softmax: [row tile][parity][half][128 rows]
   static constexpr int OFF_XCH = OFF_BAR + 256;
   static constexpr int XCH_BYTES = kSplit == 2 ? 2 * 2 * 2 * 128 * 4 : 0;
-  static constexpr int SMEM = OFF_XCH + XCH_BYTES + 1024;  // + 1 KB alignment slack
+  // KV 2: the scale bytes of each stage's rows, K's stages, then V's
+  static constexpr int OFF_SC = OFF_XCH + XCH_BYTES;
+  static constexpr int SMEM = OFF_SC + (KSTAGES + VSTAGES) * 128 + 1024;  // + 1 KB alignment slack
   static constexpr uint32_t TMEM_COLS = 512;
   // S_t (fp32, 128 columns) at 128*t; P_t (bf16 pairs, 64 columns) is written
   // over S_t, each thread's part over its own S columns (P column of key k:
@@ -138,12 +147,13 @@ enum : int {
   B_V_FULL = 8 /* x2 */, B_V_EMPTY = 10 /* x2 */, B_S_FULL = 12 /* x2: per row tile */,
   B_P_FULL = 14 /* x2 */, B_PV_DONE = 16 /* x2 */, B_O_EMPTY = 18 /* x2 */, B_DRAIN = 20,
   B_XCH = 21 /* x4: [row tile][parity], the split softmax's row exchange */,
-  B_COUNT = 25
+  B_K_RAW = 25 /* x3 */, B_V_RAW = 28 /* x2 */, /* E4M3: the codes have landed */
+  B_COUNT = 30
 };
 
 constexpr int kSoftWarps = 8 * kSplit;            // 4 * split per row tile
 constexpr int kThreads = 32 * (2 + kSoftWarps);   // bf16 caches
-constexpr int kThreadsF8 = kThreads + 128;        // E4M3 caches: + 4 converter warps
+constexpr int kThreadsF8 = kThreads + 256;        // E4M3 caches: + 4 converter warps each for K, V
 
 }  // namespace
 
@@ -248,6 +258,57 @@ __device__ __forceinline__ Item get_item(const PrefillParams& p, int t) {
     }
   }
   return it;
+}
+
+// A converter warp's 32 key rows of a stage (rows 32 cw ..): E4M3 codes at raw, a
+// block's 16 rows 2048 bytes from the next's, widened in place to bf16 in the
+// swizzled operand layout. Rows that are no keys (bit n of `rows`: the lane's n-th,
+// row n RPI + lane / LPR of the 32) become zeros. SCALED: times 2^e, sc the rows'
+// bytes. (By conversion instructions: moving the bits of four codes to two bf16
+// pairs with a byte permute, a shift and two masks and multiplying by 2^120 takes
+// as many instructions, on the pipe that the softmax needs most.)
+template <int D, bool SCALED>
+__device__ __forceinline__ void widen_rows(unsigned char* stage, const unsigned char* raw,
+                                           const unsigned char* sc, uint32_t rows, int cw, int lane) {
+  constexpr int LPR = D / 16, RPI = 32 / LPR, NI = LPR;
+  constexpr int CHUNK = 128 * 128;
+  const int sub = lane % LPR, rsub = lane / LPR;
+  uint4 in[NI];
+#pragma unroll
+  for (int n = 0; n < NI; ++n) {
+    const int r = n * RPI + rsub;
+    in[n] = rows >> n & 1u ? *reinterpret_cast<const uint4*>(
+                                 raw + (2 * cw + r / kBlockSize) * 2048 + (r % kBlockSize) * D + sub * 16)
+                           : make_uint4(0u, 0u, 0u, 0u);
+  }
+  __syncwarp();  // every code of the 32 rows is read before the first value is written
+#pragma unroll
+  for (int n = 0; n < NI; ++n) {
+    const int r = cw * 32 + n * RPI + rsub;
+    uint32_t size = 0;
+    if constexpr (SCALED) {
+      const uint32_t b = rows >> n & 1u ? sc[r] : 127u;
+      size = b == kRowPoison ? 0x7fc07fc0u : b << 7 | b << 23;  // 2^e as a pair of bf16
+    }
+    const uint32_t w4[4] = {in[n].x, in[n].y, in[n].z, in[n].w};
+    uint32_t o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float2 a = e4m3x2_to_float2((uint16_t)(w4[e / 2] >> (16 * (e & 1))));
+      o[e] = float2_to_bf16x2(a.x, a.y);
+      if constexpr (SCALED) o[e] = bf16x2_mul(o[e], size);
+    }
+    // elements 16 sub .. + 15: chunk sub / 4, units 2 (sub % 4) and the next. The
+    // chunks are a multiple of all banks apart, so lanes of the second one store
+    // their second unit first.
+    unsigned char* const rowp = stage + (sub / 4) * CHUNK + r * 128;
+    const int u = 2 * (sub % 4), f = sub / 4;
+    const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+    *reinterpret_cast<uint4*>(rowp + (((u + f) ^ (r & 7)) << 4)) = f ? hi : lo;
+    *reinterpret_cast<uint4*>(rowp + (((u + 1 - f) ^ (r & 7)) << 4)) = f ? lo : hi;
+  }
+  fence_proxy_async_smem();  // generic-proxy stores -> visible to the tensor core
+  __syncwarp();
 }
 
 // The r-th work item of CTA blockIdx.x among the g CTAs that take items.
@@ -376,35 +437,53 @@ __global__ void __launch_bounds__(KV ? kThreadsF8 : kThreads, 1)
                           tl.kv * G, tl.tok0 + rt * C::TOK, BAR(B_Q_FULL));
           }
       }
-      for (int i = 0; !F8 && i < tl.n; ++i, ++g) {  // E4M3: the converter warps load K/V
-        if (i > 0 && (i & 3) == 0) {
-          pid_cur = pid_nxt;
-          pid_nxt = (i + 4 < tl.n) ? load_group((i >> 2) + 1) : -1;
-        }
-        const int ks = g % C::KSTAGES, vs = g % C::VSTAGES;
-        const int pid = __shfl_sync(kAll, pid_cur, ((i & 3) << 3) + (lane & 7));
-        const int nload = __popc(__ballot_sync(kAll, lane < 8 && pid >= 0));
-        const int row = (pid * p.num_kv_heads + tl.kv) * kBlockSize;
+      // copies this lane's block of key tile gt into stage st: bf16 as the operand, E4M3
+      // codes (and scales) to be widened there
+      auto copy = [&](int pid, bool is_v, int st) {
         const bool mine = lane < 8 && pid >= 0;
-        if (g >= C::KSTAGES && !wait(B_K_EMPTY + ks, ((g / C::KSTAGES) - 1) & 1)) { ok = false; break; }
-        if (lane == 0) mbar_arrive_expect_tx(BAR(B_K_FULL + ks), nload * C::NCH * 2048);
+        const int nload = __popc(__ballot_sync(kAll, mine));
+        const uint32_t stage = base + (is_v ? C::OFF_V : C::OFF_K) + st * C::KV_BYTES;
+        const uint32_t bar = BAR((F8 ? (is_v ? B_V_RAW : B_K_RAW) : (is_v ? B_V_FULL : B_K_FULL)) + st);
+        constexpr int kBytes = F8 ? kBlockSize * D + (KV == 2 ? kBlockSize : 0) : C::NCH * 2048;
+        if (lane == 0) mbar_arrive_expect_tx(bar, nload * kBytes);
         __syncwarp();
-        if (mine) {
+        if (!mine) return;
+        if constexpr (F8) {  // a block's rows of one head, one behind the other
+          const size_t tile = (size_t)pid * p.num_kv_heads + tl.kv;
+          bulk_g2s(stage + C::OFF_RAW + lane * 2048,
+                   (is_v ? p.v_cache8 : p.k_cache8) + tile * (kBlockSize * D), kBlockSize * D, bar);
+          if constexpr (KV == 2)
+            bulk_g2s(base + C::OFF_SC + ((is_v ? C::KSTAGES : 0) + st) * 128 + lane * kBlockSize,
+                     p.scales + tile * kScaleBytes + (is_v ? kBlockSize : 0), kBlockSize, bar);
+        } else {
+          const int row = (pid * p.num_kv_heads + tl.kv) * kBlockSize;
 #pragma unroll
           for (int c = 0; c < C::NCH; ++c)
-            tma_load_2d(base + C::OFF_K + ks * C::KV_BYTES + c * C::CHUNK + lane * 2048, &p.tm_k,
-                        c * 64, row, BAR(B_K_FULL + ks));
+            tma_load_2d(stage + c * C::CHUNK + lane * 2048, is_v ? &p.tm_v : &p.tm_k, c * 64, row, bar);
         }
-        if (g >= C::VSTAGES && !wait(B_V_EMPTY + vs, ((g / C::VSTAGES) - 1) & 1)) { ok = false; break; }
-        if (lane == 0) mbar_arrive_expect_tx(BAR(B_V_FULL + vs), nload * C::NCH * 2048);
-        __syncwarp();
-        if (mine) {
-#pragma unroll
-          for (int c = 0; c < C::NCH; ++c)
-            tma_load_2d(base + C::OFF_V + vs * C::KV_BYTES + c * C::CHUNK + lane * 2048, &p.tm_v,
-                        c * 64, row, BAR(B_V_FULL + vs));
+      };
+      // K a tile ahead of V: its stages are free once S is done, V's only behind P V
+      int before = -1;  // the block of the tile before
+      for (int i = 0; i <= tl.n; ++i) {
+        int pid = -1;
+        if (i < tl.n) {
+          if (i > 0 && (i & 3) == 0) {
+            pid_cur = pid_nxt;
+            pid_nxt = (i + 4 < tl.n) ? load_group((i >> 2) + 1) : -1;
+          }
+          pid = __shfl_sync(kAll, pid_cur, ((i & 3) << 3) + (lane & 7));
+          const int gk = g + i, ks = gk % C::KSTAGES;
+          if (gk >= C::KSTAGES && !wait(B_K_EMPTY + ks, ((gk / C::KSTAGES) - 1) & 1)) { ok = false; break; }
+          copy(pid, false, ks);
         }
+        if (i > 0) {
+          const int gv = g + i - 1, vs = gv % C::VSTAGES;
+          if (gv >= C::VSTAGES && !wait(B_V_EMPTY + vs, ((gv / C::VSTAGES) - 1) & 1)) { ok = false; break; }
+          copy(before, true, vs);
+        }
+        before = pid;
       }
+      g += tl.n;
     }
   } else if (warp == 1) {
     // ======================= MMA issuer =======================
@@ -789,44 +868,34 @@ __global__ void __launch_bounds__(KV ? kThreadsF8 : kThreads, 1)
       mbar_arrive(BAR(B_O_EMPTY + rt));
     }
   } else if constexpr (F8) {
-    // ======================= E4M3 converters (warps 10-13) =======================
-    const int r = threadIdx.x - kThreads;  // key row of the tile, 0..127 (converter warps)
-    int g = 0, it = 0;
+    // ======================= E4M3 converters (warps 10-13: K, 14-17: V) ==================
+    constexpr int LPR = D / 16, RPI = 32 / LPR, NI = LPR;  // lanes a row, rows and parts a warp
+    const bool is_v = warp >= 2 + kSoftWarps + 4;
+    const int cw = (warp - (2 + kSoftWarps)) & 3;  // key rows 32 cw .. + 31 of a tile: two blocks
+    const int nst = is_v ? C::VSTAGES : C::KSTAGES;
+    const int full = is_v ? B_V_FULL : B_K_FULL, landed = is_v ? B_V_RAW : B_K_RAW;
+    unsigned char* const ring = gbase + (is_v ? C::OFF_V : C::OFF_K);
+    const unsigned char* const scs = gbase + C::OFF_SC + (is_v ? C::KSTAGES * 128 : 0);
+    int st = 0, parity = 0, it = 0;
     bool ok = true;
     for (int t = snake_item(it, ctas); ok && t < ntiles; t = snake_item(++it, ctas)) {
       const Item tl = get_item<D, G, MODE, WIN>(p, t);
-      const int32_t* const bt_row = p.block_tables + (size_t)tl.req * p.bt_stride;
-      for (int i = 0; i < tl.n; ++i, ++g) {
-        const int key = key_tile<WIN>(tl, i) * 128 + r;
-        bool valid = WIN ? item_sees(tl, key, 1, p.sinks) : key < tl.L;
-        size_t src = 0;
-        float ksz = 1.f, vsz = 1.f;  // KV 2: the row's sizes
-        if (valid) {
-          const int pid = __ldg(bt_row + key / kBlockSize);
-          if (pid < 0 || pid >= p.num_blocks) {
-            report_error(p.err, PA_DEVERR_BLOCK_ID, key / kBlockSize);
-            valid = false;
-          } else {
-            const size_t tile = (size_t)pid * p.num_kv_heads + tl.kv;
-            src = (tile * kBlockSize + (key % kBlockSize)) * D;
-            if constexpr (KV == 2) {
-              const unsigned char* const sc = p.scales + tile * kScaleBytes + key % kBlockSize;
-              ksz = row_size(__ldg(sc));
-              vsz = row_size(__ldg(sc + kBlockSize));
-            }
-          }
+      for (int i = 0; i < tl.n; ++i) {
+        const int key0 = key_tile<WIN>(tl, i) * 128 + cw * 32 + lane / LPR;
+        uint32_t rows = 0;  // which of this lane's rows are keys
+#pragma unroll
+        for (int n = 0; n < NI; ++n) {
+          const int key = key0 + n * RPI;
+          if (WIN ? item_sees(tl, key, 1, p.sinks) : key < tl.L) rows |= 1u << n;
         }
-        const int ks = g % C::KSTAGES, vs = g % C::VSTAGES;
-        if (g >= C::KSTAGES && !wait(B_K_EMPTY + ks, ((g / C::KSTAGES) - 1) & 1)) { ok = false; break; }
-        widen_e4m3_row<D, KV == 2>(p.k_cache8 + src, valid, gbase + C::OFF_K + ks * C::KV_BYTES, r, ksz);
-        fence_proxy_async_smem();  // generic-proxy stores -> visible to the tensor core
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(B_K_FULL + ks));
-        if (g >= C::VSTAGES && !wait(B_V_EMPTY + vs, ((g / C::VSTAGES) - 1) & 1)) { ok = false; break; }
-        widen_e4m3_row<D, KV == 2>(p.v_cache8 + src, valid, gbase + C::OFF_V + vs * C::KV_BYTES, r, vsz);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(B_V_FULL + vs));
+        if (!wait(landed + st, parity)) { ok = false; break; }
+        unsigned char* const stage = ring + st * C::KV_BYTES;
+        widen_rows<D, KV == 2>(stage, stage + C::OFF_RAW, scs + st * 128, rows, cw, lane);
+        if (lane == 0) mbar_arrive(BAR(full + st));
+        if (++st == nst) {
+          st = 0;
+          parity ^= 1;
+        }
       }
     }
   }

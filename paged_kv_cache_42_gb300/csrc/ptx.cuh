@@ -216,6 +216,12 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t w) {
   return make_float2(lo, hi);
 }
 
+// Packed bf16 product.
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 // 2^x with the hardware approximation (PTX ex2.approx.ftz.f32): one MUFU op,
 // relative error ~2^-22, results below 2^-126 flushed to zero.
 __device__ __forceinline__ float ex2_approx(float x) {
@@ -471,11 +477,10 @@ __device__ __forceinline__ void tm_st(uint32_t taddr, const uint32_t (&r)[N]) {
 // One key row of an E4M3 tile widened to bf16 into a 128B-swizzled operand
 // tile (row r: 16-byte unit u of 64-element chunk c lives at
 // c * CHUNK + r * 128 + (u ^ (r & 7)) * 16). A row that is not a key of the
-// sequence is written as zeros. SCALED: every element times `size`, a power of
-// two that keeps it a bf16 number.
-template <int D, bool SCALED = false>
+// sequence is written as zeros.
+template <int D>
 __device__ __forceinline__ void widen_e4m3_row(const unsigned char* src, bool valid,
-                                               unsigned char* tile, int r, float size = 1.f) {
+                                               unsigned char* tile, int r) {
   constexpr int CHUNK = 128 * 128;
   uint4 raw[D / 16];
 #pragma unroll
@@ -487,12 +492,8 @@ __device__ __forceinline__ void widen_e4m3_row(const unsigned char* src, bool va
     uint32_t o[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float2 a = e4m3x2_to_float2((uint16_t)(w4[i] & 0xffffu));
-      float2 b = e4m3x2_to_float2((uint16_t)(w4[i] >> 16));
-      if constexpr (SCALED) {
-        a = fmul2(a, make_float2(size, size));
-        b = fmul2(b, make_float2(size, size));
-      }
+      const float2 a = e4m3x2_to_float2((uint16_t)(w4[i] & 0xffffu));
+      const float2 b = e4m3x2_to_float2((uint16_t)(w4[i] >> 16));
       o[2 * i] = float2_to_bf16x2(a.x, a.y);
       o[2 * i + 1] = float2_to_bf16x2(b.x, b.y);
     }
