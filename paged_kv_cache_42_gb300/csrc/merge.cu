@@ -27,6 +27,10 @@ namespace pa {
 namespace {
 
 constexpr int kMergeWarps = 8;
+// Pairs of (unit, kv head) from which a shared call's merge gives each a warp, not a
+// CTA: 4864 pairs of 3 to 5 partials at G = 8 44 -> 9 us, 1088 pairs of a few at G = 4
+// 10 us either way, but 400 pairs of a dozen at G = 8 15 -> 21 us.
+constexpr int kMergeWarpPairs = 1024;
 
 template <int D, int G, bool SHARED>
 __global__ void __launch_bounds__(kMergeWarps * 32) pa_merge_kernel(const MergeParams p) {
@@ -235,6 +239,90 @@ __global__ void __launch_bounds__(kMergeWarps * 32) pa_merge_tm_kernel(const Mer
   }
 }
 
+// Shared calls with many (unit, kv head) pairs: a warp each, which merges the few
+// partials of its pair - the split-KV workers' that hold its own keys, then its
+// prefix's - on its own, a group of them loaded at a time.
+template <int D, int G>
+__global__ void __launch_bounds__(kMergeWarps * 32) pa_merge_shared_kernel(const MergeParams p) {
+  constexpr int V = D / 32;  // output dims per lane
+  griddep_wait();
+  const int W = __ldcg(&p.header->num_positions);
+  const long long item = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+  const int k = (int)(item / p.num_kv_heads), kv = (int)(item % p.num_kv_heads);
+  const int lane = threadIdx.x & 31;
+  if (W <= 0 || k >= __ldcg(&p.header->num_units)) return;
+  const int4 u = __ldcg(reinterpret_cast<const int4*>(p.units + k));
+  const int tok = u.x, parts = __ldcg(p.tok_parts + tok);
+  const int nb = max(1, (u.z + kBlockSize - 1) / kBlockSize);
+  const int first = u.w + (p.token_major ? 0 : kv * nb);
+  const int NW = plan_workers(W, p.num_workers, p.min_pos);
+  const int wf = worker_of(first, W, NW), ns = worker_of(first + nb - 1, W, NW) - wf + 1;
+  const int n = ns + parts;
+  auto slot = [&](int i) -> const float* {
+    const size_t s0 = p.token_major ? (size_t)(tok + wf + i) * p.num_kv_heads + kv
+                                    : (size_t)tok * p.num_kv_heads + kv + wf + i;
+    return i < ns ? p.partials + s0 * p.slot_floats
+                  : p.prefix_partials +
+                        (((size_t)(i - ns) * p.num_tokens + tok) * p.num_kv_heads + kv) *
+                            p.slot_floats;
+  };
+  constexpr int K = G <= 4 ? 4 : 2;
+  float am[G], al[G], ao[G][V], qm[K][G], ql[K][G], qo[K][G][V];
+#pragma unroll
+  for (int h = 0; h < G; ++h) {
+    am[h] = -INFINITY;
+    al[h] = 0.f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) ao[h][e] = 0.f;
+  }
+  for (int i0 = 0; i0 < n; i0 += K) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      const float* const sl = slot(min(i0 + j, n - 1));
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        qm[j][h] = __ldcg(sl + h);
+        ql[j][h] = __ldcg(sl + G + h);
+        if constexpr (V == 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(sl + 16 + h * D) + lane);
+          qo[j][h][0] = v.x;
+          qo[j][h][1] = v.y;
+          qo[j][h][2] = v.z;
+          qo[j][h][3] = v.w;
+        } else {
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(sl + 16 + h * D) + lane);
+          qo[j][h][0] = v.x;
+          qo[j][h][1] = v.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      if (i0 + j >= n) break;
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        const float mn = fmaxf(am[h], qm[j][h]);
+        const float a = exp2f(am[h] - mn), b = exp2f(qm[j][h] - mn);  // am = -inf: a = 0
+        al[h] = al[h] * a + ql[j][h] * b;
+#pragma unroll
+        for (int e = 0; e < V; ++e) ao[h][e] = ao[h][e] * a + qo[j][h][e] * b;
+        am[h] = mn;
+      }
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < G; ++h) {
+    const float sc = p.v_scale / al[h];
+    uint16_t* const orow = p.out + ((size_t)tok * p.num_q_heads + (size_t)kv * G + h) * D;
+    if constexpr (V == 4)
+      *reinterpret_cast<uint2*>(orow + lane * V) =
+          make_uint2(float2_to_bf16x2(ao[h][0] * sc, ao[h][1] * sc),
+                     float2_to_bf16x2(ao[h][2] * sc, ao[h][3] * sc));
+    else
+      *reinterpret_cast<uint32_t*>(orow + lane * V) = float2_to_bf16x2(ao[h][0] * sc, ao[h][1] * sc);
+  }
+}
+
 template <int D, int G>
 cudaError_t launch_merge_t(const MergeParams& p, cudaStream_t s) {
   // one CTA per slice boundary, or per (token, kv head)
@@ -257,7 +345,11 @@ cudaError_t launch_merge_t(const MergeParams& p, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (p.tok_parts != nullptr) return cudaLaunchKernelEx(&cfg, pa_merge_kernel<D, G, true>, p);
+  if (p.tok_parts != nullptr) {
+    if (boundaries < kMergeWarpPairs) return cudaLaunchKernelEx(&cfg, pa_merge_kernel<D, G, true>, p);
+    cfg.gridDim = dim3((unsigned)((boundaries + kMergeWarps - 1) / kMergeWarps));
+    return cudaLaunchKernelEx(&cfg, pa_merge_shared_kernel<D, G>, p);
+  }
   if (p.token_major) {  // a CTA per boundary, a warp per KV head
     cfg.blockDim = dim3(32 * p.num_kv_heads);
     return cudaLaunchKernelEx(&cfg, pa_merge_tm_kernel<D, G>, p);

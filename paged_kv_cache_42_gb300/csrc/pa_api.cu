@@ -716,7 +716,7 @@ pa_status shared_impl(const pa_shared_args& a) {
   pp.num_workers = (cap > 0 && cap < launched) ? cap : launched;
   pp.num_sms = d->num_sms;
   pp.token_major = use_tm ? 1 : 0;
-  pp.min_pos = use_tm ? PA_DEC_MIN_POS : 1;  // suffixes are short: as in a windowed call
+  pp.min_pos = 1;  // suffixes are short: as in a windowed call
   pp.group_start = a.group_start_loc;
   pp.prefix_lens = a.prefix_lens;
   pp.num_groups = a.num_groups;

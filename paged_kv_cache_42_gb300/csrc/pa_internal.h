@@ -225,7 +225,7 @@ constexpr int kSharedMinTokens = 2;
 // Prefix work items that the workspace leaves room for at least (an item holds an
 // SM alone; GB300 has 152): the planner picks the length of the key chunks.
 constexpr int kSharedMostItems = 4 * 152;
-// Steps (an item's key tile, both row tiles) that starting and ending an item costs.
+// Steps (a key tile against a pair of row tiles) that starting and ending an item costs.
 constexpr int kSharedItemSteps = 2;
 
 // One prefix work item: two 128-row tiles of kv head `kv`, batch tokens tok0 up
@@ -270,9 +270,9 @@ inline SharedLayout shared_layout(int num_reqs, int num_tokens, int num_q_heads,
   l.items_off = base.total;
   l.parts_off = l.items_off + pa_align256(sizeof(SharedItem) * (size_t)l.max_items);
   l.partials_off = l.parts_off + pa_align256(sizeof(int) * (size_t)num_tokens);
-  // a partial of a (token, kv head) per chunk, or two per chunk of twice the length
+  // a partial of a (token, kv head) per chunk, or two per chunk of half as much again
   l.total = l.partials_off + pa_align256(sizeof(float) * (size_t)base.slot_floats *
-                                         (size_t)(chunks + 1) * (size_t)num_tokens *
+                                         (size_t)(4 * chunks / 3 + 2) * (size_t)num_tokens *
                                          (size_t)num_kv_heads);
   return l;
 }

@@ -65,15 +65,15 @@ constexpr int kTileBuckets = 512;  // tiles sorted by key-tile count, longest fi
 
 // ---- shared calls -----------------------------------------------------------------
 // The group of request r, or -1: its prefix in blocks goes to *blocks (0: none, or
-// not one that this call takes).
-__device__ __forceinline__ int shared_group(const PlanParams& p, int r, int* blocks) {
+// not one that this call takes). start, lens: group_start_loc and prefix_lens.
+__device__ __forceinline__ int shared_group(const PlanParams& p, const int* start, const int* lens,
+                                            int r, int* blocks) {
   int lo = 0, hi = p.num_groups;  // the last group that starts at or before r
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (__ldg(p.group_start + mid) <= r) lo = mid; else hi = mid;
+    if (start[mid] <= r) lo = mid; else hi = mid;
   }
-  const int a = __ldg(p.group_start + lo), b = __ldg(p.group_start + lo + 1);
-  const int len = __ldg(p.prefix_lens + lo);
+  const int a = start[lo], b = start[lo + 1], len = lens[lo];
   *blocks = 0;
   if (r < a || r >= b || a < 0 || b > p.num_reqs) return -1;
   if (len > 0 && len % kBlockSize == 0 && len <= p.max_prefix_len) *blocks = len / kBlockSize;
@@ -108,17 +108,21 @@ __device__ __forceinline__ bool shares(const PlanParams& p, int qlen, int L, int
 }
 
 // A pair of row tiles with `left` tokens (its own and the group's behind it): rows
-// that fit one tile are split over the two by key tiles (SharedItem). Their key
-// chunks are twice as long (ct tiles otherwise), for as many steps.
+// that fit one tile are split over the two by key tiles (SharedItem). Two tiles of
+// keys take them 4/3 of the time that one takes a pair of full tiles (1.6 and 2.4 us
+// a tile of a long prefix), so that their key chunks are half as long again (ct tiles
+// otherwise).
 __device__ __forceinline__ bool shared_split(int left, int group) { return left * group <= 128; }
+__device__ __forceinline__ int shared_len(int ct, bool split) { return split ? ct + (ct + 1) / 2 : ct; }
 __device__ __forceinline__ int shared_chunks(int tiles, int ct, bool split) {
-  return split ? (tiles + 2 * ct - 1) / (2 * ct) : (tiles + ct - 1) / ct;
+  const int len = shared_len(ct, split);
+  return (tiles + len - 1) / len;
 }
 // The partials that such a pair leaves of a prefix: two of a split chunk, unless it has
 // one tile only.
 __device__ __forceinline__ int shared_parts(int tiles, int ct, bool split) {
   const int chunks = shared_chunks(tiles, ct, split);
-  return split ? 2 * chunks - (tiles - (chunks - 1) * 2 * ct == 1 ? 1 : 0) : chunks;
+  return split ? 2 * chunks - (tiles - (chunks - 1) * shared_len(ct, true) == 1 ? 1 : 0) : chunks;
 }
 
 // CTAs 1 .. of a shared call's plan: every request that shares its group's prefix
@@ -240,19 +244,36 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
   __shared__ int s_first[SHARED ? kMaxSharedGroups : 1], s_count[SHARED ? kMaxSharedGroups : 1];
   __shared__ int s_lo[SHARED ? kMaxSharedGroups : 1], s_hi[SHARED ? kMaxSharedGroups : 1];
   __shared__ int s_tiles[SHARED ? kMaxSharedGroups : 1];  // key tiles of its prefix; 0: not shared
+  // its pairs of row tiles: full ones, and a split one or none
+  __shared__ int s_full[SHARED ? kMaxSharedGroups : 1], s_split[SHARED ? kMaxSharedGroups : 1];
+  __shared__ int s_start[SHARED ? kMaxSharedGroups + 1 : 1], s_len[SHARED ? kMaxSharedGroups : 1];
   __shared__ unsigned long long s_best;
+  // what this thread's (first) request is, kept from one pass over them to the next
+  int my_q0 = 0, my_qlen = 0, my_L = 0, my_group = -1, my_blocks = 0;
+  bool my_valid = false;
   if constexpr (SHARED) {
+    if (threadIdx.x < p.num_reqs)
+      my_valid = check(threadIdx.x, my_q0, my_qlen, my_L, true);
     for (int g = threadIdx.x; g < p.num_groups; g += blockDim.x) {
+      s_start[g] = __ldg(p.group_start + g);
+      s_len[g] = __ldg(p.prefix_lens + g);
       s_first[g] = s_lo[g] = 0x7fffffff;
       s_count[g] = s_hi[g] = 0;
     }
+    if (threadIdx.x == 0) s_start[p.num_groups] = __ldg(p.group_start + p.num_groups);
     for (int t = threadIdx.x; t < T; t += blockDim.x) p.tok_parts[t] = 0;
     __syncthreads();
     for (int r = threadIdx.x; r < p.num_reqs; r += blockDim.x) {
-      int q0, qlen, L, blocks;
-      if (!check(r, q0, qlen, L, false)) continue;
-      const int g = shared_group(p, r, &blocks);
-      if (g < 0 || !shares(p, qlen, L, blocks)) continue;
+      int q0 = my_q0, qlen = my_qlen, L = my_L, blocks;
+      const bool mine = r == (int)threadIdx.x;
+      if (mine ? !my_valid : !check(r, q0, qlen, L, true)) continue;
+      int g = shared_group(p, s_start, s_len, r, &blocks);
+      if (g >= 0 && !shares(p, qlen, L, blocks)) g = -1;
+      if (mine) {
+        my_group = g;
+        my_blocks = blocks;
+      }
+      if (g < 0) continue;
       atomicMin(&s_first[g], r);
       atomicAdd(&s_count[g], qlen);
       atomicMin(&s_lo[g], q0);
@@ -260,27 +281,32 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
     }
     if (threadIdx.x == 0) s_best = ~0ull;
     __syncthreads();
-    for (int g = threadIdx.x; g < p.num_groups; g += blockDim.x)
-      s_tiles[g] = s_count[g] >= kSharedMinTokens ? (__ldg(p.prefix_lens + g) + 127) / 128 : 0;
+    for (int g = threadIdx.x; g < p.num_groups; g += blockDim.x) {
+      s_tiles[g] = s_count[g] >= kSharedMinTokens ? (s_len[g] + 127) / 128 : 0;
+      const int n = s_tiles[g] > 0 ? s_hi[g] - s_lo[g] : 1;
+      const int pairs = (n + tok_per_item - 1) / tok_per_item;
+      s_full[g] = pairs - (shared_split(n - (pairs - 1) * tok_per_item, p.group) ? 1 : 0);
+      s_split[g] = pairs - s_full[g];
+    }
     __syncthreads();
     // The key chunks' length: of a thread's candidate, the time of the rounds that its
     // items take on the SMs, in steps.
     const int ct = p.chunk_tiles + (int)threadIdx.x;
     if (threadIdx.x < kSharedCandidates) {
-      long long items = 0;
+      float items = 0.f;
       int longest = 0;  // steps
+      // (an estimate: the divisions need not be exact)
+      const float by = 1.f / (float)ct, by_split = 1.f / (float)shared_len(ct, true);
       for (int g = 0; g < p.num_groups; ++g) {
         const int tiles = s_tiles[g];
         if (tiles == 0) continue;
-        const int n = s_hi[g] - s_lo[g], pairs = (n + tok_per_item - 1) / tok_per_item;
-        const int split = shared_split(n - (pairs - 1) * tok_per_item, p.group) ? 1 : 0;
-        items += (long long)(pairs - split) * shared_chunks(tiles, ct, false) +
-                 split * shared_chunks(tiles, ct, true);
-        longest = max(longest, min(ct, pairs > split ? tiles : (tiles + 1) / 2));
+        const int full = s_full[g], split = s_split[g];
+        items += (float)full * ceilf((float)tiles * by) + (float)split * ceilf((float)tiles * by_split);
+        longest = max(longest, min(ct, full > 0 ? tiles : (2 * tiles + 2) / 3));
       }
-      if (items > 0) {
-        const long long rounds = (items * p.num_kv_heads + p.num_sms - 1) / p.num_sms;
-        const float cost = (float)rounds * (float)(longest + kSharedItemSteps);
+      if (items > 0.f) {
+        const float rounds = ceilf(items * (float)p.num_kv_heads / (float)p.num_sms);
+        const float cost = rounds * (float)(longest + kSharedItemSteps);
         atomicMin(&s_best, (unsigned long long)__float_as_uint(cost) << 32 | (unsigned)ct);
       }
     }
@@ -288,8 +314,9 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
   }
   const int chunk_tiles = SHARED && s_best != ~0ull ? (int)(unsigned)s_best : 1;
   for (int r = threadIdx.x; r < p.num_reqs; r += blockDim.x) {
-    int q0, qlen, L;
-    if (!check(r, q0, qlen, L, true)) continue;
+    int q0 = my_q0, qlen = my_qlen, L = my_L;
+    const bool mine = SHARED && r == (int)threadIdx.x;
+    if (mine ? !my_valid : !check(r, q0, qlen, L, !SHARED)) continue;
     const int ctx = L - qlen;
     if (p.use_prefill && qlen >= kPrefillMinQlen) {
       int steps = 0;
@@ -302,9 +329,12 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
       continue;  // these tokens are not on the split-KV path
     }
     if constexpr (SHARED) {
-      int blocks;
-      const int g = shared_group(p, r, &blocks);
-      if (g < 0 || !shares(p, qlen, L, blocks) || s_count[g] < kSharedMinTokens) blocks = 0;
+      int g = my_group, blocks = my_blocks;
+      if (!mine) {
+        g = shared_group(p, s_start, s_len, r, &blocks);
+        if (g >= 0 && !shares(p, qlen, L, blocks)) g = -1;
+      }
+      if (g < 0 || s_count[g] < kSharedMinTokens) blocks = 0;
       const int at = r * p.max_blocks_per_req + blocks;
       for (int j = 0; j < qlen; ++j) {
         raw[q0 + j] = make_int2(at, ctx + j + 1 - blocks * kBlockSize);
@@ -347,12 +377,9 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
     for (int c0 = 0; c0 < p.num_groups; c0 += blockDim.x) {
       const int g = c0 + threadIdx.x;
       long long n = 0;
-      if (g < p.num_groups && s_tiles[g] > 0) {
-        const int toks = s_hi[g] - s_lo[g], pairs = (toks + tok_per_item - 1) / tok_per_item;
-        const int split = shared_split(toks - (pairs - 1) * tok_per_item, p.group) ? 1 : 0;
-        n = ((long long)(pairs - split) * shared_chunks(s_tiles[g], chunk_tiles, false) +
-             split * shared_chunks(s_tiles[g], chunk_tiles, true)) * p.num_kv_heads;
-      }
+      if (g < p.num_groups && s_tiles[g] > 0)
+        n = ((long long)s_full[g] * shared_chunks(s_tiles[g], chunk_tiles, false) +
+             s_split[g] * shared_chunks(s_tiles[g], chunk_tiles, true)) * p.num_kv_heads;
       long long total;
       const long long ex = block_exclusive_scan(n, &total, scan_sm);
       // (an overfull list, which spans that overlap can make, is cut below)
@@ -381,14 +408,13 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
       it.req = s_first[lo];
       it.tok_end = s_hi[lo];
       // only the group's last pair can be split, with fewer chunks than the others
-      const int last = (it.tok_end - s_lo[lo] - 1) / tok_per_item;
-      const int pair = min(k / chunks, last), chunk = k - pair * chunks;
+      const int pair = min(k / chunks, s_full[lo] + s_split[lo] - 1), chunk = k - pair * chunks;
       it.tok0 = s_lo[lo] + pair * tok_per_item;
-      const bool split = shared_split(it.tok_end - it.tok0, p.group);
-      const int len = split ? 2 * chunk_tiles : chunk_tiles;
+      const bool split = pair == s_full[lo];
+      const int len = shared_len(chunk_tiles, split);
       it.i0 = chunk * len;
       it.n = min(len, tiles - it.i0);
-      it.L = __ldg(p.prefix_lens + lo);
+      it.L = s_len[lo];
       it.part = split ? 2 * chunk : chunk;  // (the chunks before are whole)
       if (split && it.n > 1) it.kv |= kSharedSplit;
       p.shared_items[i] = it;

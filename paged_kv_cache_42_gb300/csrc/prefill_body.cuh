@@ -54,7 +54,7 @@
 // bf16 - and arrives on the stage's full barrier. So a ring of E4M3 tiles has all of
 // its stages in flight, as one of bf16 tiles has. (Loads into registers, two tiles
 // ahead, were limited to what the SM's remaining 28 KB of L1 can await: 4.3 us per
-// key tile of a long prefix against PREFSTEP.) k_scale is
+// key tile of a long prefix against 1.9.) k_scale is
 // folded into the softmax scale and v_scale into the epilogue. Over row-scaled
 // caches (KV 2, rows.cuh) the converters multiply each row by its 2^e, which is
 // exact in bf16 too, and nothing else differs.
@@ -115,7 +115,10 @@ struct PCfg {
 #else
   static constexpr int KSTAGES = kSplit == 2 ? 2 : 3;
 #endif
-  static constexpr int VSTAGES = 2;
+#ifndef PA_PREFILL_VSTAGES
+#define PA_PREFILL_VSTAGES 2
+#endif
+  static constexpr int VSTAGES = PA_PREFILL_VSTAGES;
   // E4M3: where in a stage block b's codes land (+ 2048 b), within the block's own rows
   static constexpr int OFF_RAW = (NCH - 1) * CHUNK;
   static constexpr int OFF_Q = 0;  // two row tiles
@@ -123,7 +126,7 @@ struct PCfg {
   static constexpr int OFF_V = OFF_K + KSTAGES * KV_BYTES;
   static constexpr int OFF_BAR = OFF_V + VSTAGES * KV_BYTES;
   // row-max / row-sum exchange of the split softmax: [row tile][parity][half][128 rows]
-  static constexpr int OFF_XCH = OFF_BAR + 256;
+  static constexpr int OFF_XCH = OFF_BAR + 320;
   static constexpr int XCH_BYTES = kSplit == 2 ? 2 * 2 * 2 * 128 * 4 : 0;
   // KV 2: the scale bytes of each stage's rows, K's stages, then V's
   static constexpr int OFF_SC = OFF_XCH + XCH_BYTES;
@@ -144,11 +147,11 @@ struct PCfg {
 // barrier slots
 enum : int {
   B_Q_FULL = 0, B_Q_EMPTY = 1, B_K_FULL = 2 /* x3 */, B_K_EMPTY = 5 /* x3 */,
-  B_V_FULL = 8 /* x2 */, B_V_EMPTY = 10 /* x2 */, B_S_FULL = 12 /* x2: per row tile */,
-  B_P_FULL = 14 /* x2 */, B_PV_DONE = 16 /* x2 */, B_O_EMPTY = 18 /* x2 */, B_DRAIN = 20,
-  B_XCH = 21 /* x4: [row tile][parity], the split softmax's row exchange */,
-  B_K_RAW = 25 /* x3 */, B_V_RAW = 28 /* x2 */, /* E4M3: the codes have landed */
-  B_COUNT = 30
+  B_V_FULL = 8 /* x3 */, B_V_EMPTY = 11 /* x3 */, B_S_FULL = 14 /* x2: per row tile */,
+  B_P_FULL = 16 /* x2 */, B_PV_DONE = 18 /* x2 */, B_O_EMPTY = 20 /* x2 */, B_DRAIN = 22,
+  B_XCH = 23 /* x4: [row tile][parity], the split softmax's row exchange */,
+  B_K_RAW = 27 /* x3 */, B_V_RAW = 30 /* x3 */, /* E4M3: the codes have landed */
+  B_COUNT = 33
 };
 
 constexpr int kSoftWarps = 8 * kSplit;            // 4 * split per row tile
@@ -366,6 +369,9 @@ __global__ void __launch_bounds__(KV ? kThreadsF8 : kThreads, 1)
   // The work list comes from the preceding (planner) grid. The prefix pass
   // of a cascade needs none of it and waits only before it completes (see the end).
   if constexpr (MODE != kOnePrefix) griddep_wait();
+  // (A shared call's grids release their dependents on completion only: with the plan
+  // or this one doing so at the top, the next grid's CTAs take their places too early;
+  // documents 133 -> 139 and 151 us.)
   int ntiles = MODE == kGroups      ? p.header->num_prefix_items
                : MODE == kOnePrefix ? p.prefix_pairs * p.num_kv_heads * p.prefix_chunks
                                     : p.header->num_tiles;
@@ -508,15 +514,14 @@ __global__ void __launch_bounds__(KV ? kThreadsF8 : kThreads, 1)
         const int kst = gk % C::KSTAGES;
         if ((rt == 0 || split) && !wait(B_K_FULL + kst, (gk / C::KSTAGES) & 1)) return false;
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
           const uint32_t d = tmem + C::TM_S + 128 * rt;
           const uint64_t a0 = kmaj_base + ((C::OFF_Q + (split ? 0 : rt * C::Q_BYTES)) >> 4);
           const uint64_t b0 = kmaj_base + ((C::OFF_K + kst * C::KV_BYTES) >> 4);
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const int off = ((ks / 4) * C::CHUNK + (ks % 4) * 32) >> 4;
-            umma_bf16(d, a0 + off, b0 + off, p.idesc_qk, ks > 0 ? 1u : 0u);
-          }
+          for (int c = 0; c < C::NCH; ++c)
+            umma_bf16_x4<2>(d, a0 + c * (C::CHUNK >> 4), b0 + c * (C::CHUNK >> 4), p.idesc_qk,
+                            c > 0 ? 1u : 0u);
           umma_commit(BAR(B_S_FULL + rt));
           if (rt == 1 || split) {
             umma_commit(BAR(B_K_EMPTY + kst));
@@ -562,14 +567,14 @@ __global__ void __launch_bounds__(KV ? kThreadsF8 : kThreads, 1)
         }
         if (i == 0 && it > 0 && !wait(B_O_EMPTY + rt, (it - 1) & 1)) return false;
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
           const uint32_t d = tmem + C::TM_O + 128 * rt;
           const uint32_t a_tm = tmem + C::TM_S + 128 * rt;  // P_rt: 64 columns of bf16 pairs
           const uint64_t b0 = vmaj_base + ((C::OFF_V + vst * C::KV_BYTES) >> 4);
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)  // keys 16 ks .. 16 ks + 15: 8 P columns
-            umma_bf16_ta(d, a_tm + C::pcol(ks >> 1) + 8 * (ks & 1), b0 + ((ks * 2048) >> 4),
-                         idesc_pv, (i > 0 || ks > 0) ? 1u : 0u);
+          for (int c = 0; c < 4; ++c)  // keys 32 c .. 32 c + 31: 16 P columns
+            umma_bf16_ta_x2<(2048 >> 4)>(d, a_tm + C::pcol(c), b0 + ((c * 4096) >> 4), idesc_pv,
+                                         (i > 0 || c > 0) ? 1u : 0u);
           umma_commit(BAR(B_PV_DONE + rt));
           if (rt == 1 || split) umma_commit(BAR(B_V_EMPTY + vst));
         }
@@ -600,7 +605,7 @@ __global__ void __launch_bounds__(KV ? kThreadsF8 : kThreads, 1)
       }
     }
     // every MMA issued above has completed before TMEM is released
-    if (lane == 0) umma_commit(BAR(B_DRAIN));
+    if (elect_one()) umma_commit(BAR(B_DRAIN));
     __syncwarp();
     mbar_wait_bounded(BAR(B_DRAIN), 0);
   } else if (warp < 2 + kSoftWarps) {
