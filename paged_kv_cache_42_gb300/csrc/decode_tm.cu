@@ -57,7 +57,11 @@
 // with the references r taken from u = t + ev, so that P' keeps its place below
 // 448 whatever the rows' sizes: E4M3's smallest step is then relative to the
 // largest weight x size, which is what the output is made of. l's terms reach
-// 2^(100 + 3) (ev >= -100), its sum stays in range.
+// 2^(100 + 3) (ev >= -100), its sum stays in range. A long flat tail behind one large
+// weight lies below that step (32768 keys of 2^-15 of it: as much as it together),
+// and alike weights would all round the same way. So the second term is rounded
+// after a shift by a fraction of the step that goes through (-1/2, 1/2) evenly from
+// key to key (multiples of the golden ratio): what the keys lose and gain cancels.
 //
 // Roles (192 threads per CTA): warps 0-3 softmax and epilogue, warp 4
 // the producer (walks the work list, one record per tile, two or three tensor
@@ -729,7 +733,10 @@ __global__ void __launch_bounds__(kTmThreads, CPS)
         const float x0 = 256.f * vsize * pr[g], x1 = g + 1 < G ? 256.f * vsize * pr[g + 1] : 0.f;
         const uint16_t hi = float2_to_e4m3x2(x0, x1);
         const float2 hv = e4m3x2_to_float2(hi);
-        const uint16_t lo = float2_to_e4m3x2(x0 - hv.x, x1 - hv.y);
+        float shift = 0.f;  // RS: within half of E4M3's smallest step, 2^-9
+        if constexpr (RS)
+          shift = (float)(int)((uint32_t)(rec.key0 + kk) * 0x9e3779b1u) * 0x1p-41f;
+        const uint16_t lo = float2_to_e4m3x2(x0 - hv.x + shift, x1 - hv.y + shift);
         const int r = hm * G + g;
         *prow(b, r) = (unsigned char)(hi & 0xffu);
         *prow(b, HQ + r) = (unsigned char)(lo & 0xffu);

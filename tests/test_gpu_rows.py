@@ -355,3 +355,33 @@ def test_attention_over_zero_and_poisoned_rows(pa_lib, hq, hkv, d):
     assert torch.equal(torch.isnan(got), bad)
     assert (got[0] == 0).all()
     assert ((got - want).abs() <= tol)[~bad].all()
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (16, 8, 128), (32, 8, 128), (64, 8, 128)])
+@pytest.mark.parametrize("octaves", [13.0, 15.0, 15.6])
+def test_a_flat_tail_behind_one_large_weight(pa_lib, hq, hkv, d, octaves):
+    """One key of 2^octaves times the weight of each of the others, which together weigh
+    about as much: their values must count, although each is small. Outputs are 64-bit
+    ones to half a bf16 step and 2^-6 of the weights' sum of |V|."""
+    from paged_kv_cache_42_gb300 import binding
+    n = int(2.0 ** octaves)
+    b = rr.Batch([(n, 1)], hq, hkv, d, 3, spread=0.0)
+    g = torch.Generator().manual_seed(2)
+    k = torch.zeros(len(b.k), hkv, 16, d)
+    v = 1 + 0.25 * torch.randn(len(b.k), hkv, 16, d, generator=g)
+    where = b.tables[0, 3].long(), 5  # key 53
+    k[where[0], :, where[1], 0] = 16.0
+    v[where[0], :, where[1]] = -1.0
+    b.k, b.scales[:, :, 0] = rr.quantise_fast(k)
+    b.v, b.scales[:, :, 1] = rr.quantise_fast(v)
+    b.q.zero_()
+    b.q[:, :, 0] = 2.0
+    b.scale = octaves * math.log(2) / 32
+    k64, v64 = rr.values(b.k, b.scales[:, :, 0]), rr.values(b.v, b.scales[:, :, 1])
+    want, _ = rr.attention(b, k64, v64)
+    size, _ = rr.attention(b, k64, v64.abs())
+    t = b.gpu()
+    got = binding.attention_rows(t["q"], t["k"], t["v"], t["scales"], t["tables"], t["seq_lens"],
+                                 t["qsl"], b.scale, max_query_len=1, max_seq_len=b.max_len)
+    err = (got.cpu().double() - want).abs()
+    assert (err <= want.abs() * 2.0 ** -8 + size * 2.0 ** -6).all(), float((err / size).max())
