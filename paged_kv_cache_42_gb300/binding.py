@@ -34,6 +34,7 @@ _LIB = None
 _c_p = ctypes.c_void_p
 _c_i = ctypes.c_int
 _INT_MAX = 2 ** 31 - 1  # counts beyond it mean the same as it
+_BF16, _U8, _I32, _I64 = torch.bfloat16, torch.uint8, torch.int32, torch.int64
 
 STATUS = {0: "PA_OK", -1: "PA_ERR_INVALID_ARG", -2: "PA_ERR_UNSUPPORTED",
           -3: "PA_ERR_WORKSPACE", -4: "PA_ERR_CUDA", -5: "PA_ERR_BOUNDS", -6: "PA_ERR_TIMEOUT"}
@@ -264,6 +265,13 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
 def _heads(t: torch.Tensor, shape: tuple, dev: int, name: str) -> tuple[int, int]:
     """(address, token stride in elements) of [tokens, heads, head_dim] whose
     tokens may lie apart (a part of a wider projection)."""
+    try:
+        if t.dtype is _BF16 and t.shape == shape and t.get_device() == dev:
+            s0, s1, s2 = t.stride()
+            if s2 == 1 and (s1 == shape[2] or shape[1] == 1):
+                return t.data_ptr(), (s0 if shape[0] > 1 else shape[1] * shape[2])
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not torch.bfloat16:
@@ -272,17 +280,13 @@ def _heads(t: torch.Tensor, shape: tuple, dev: int, name: str) -> tuple[int, int
         raise ValueError(f"shape mismatch: {name} is {tuple(t.shape)}, not {shape}")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on the current device cuda:{dev}")
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or (s1 != shape[2] and shape[1] > 1):
-        raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return t.data_ptr(), (s0 if shape[0] > 1 else shape[1] * shape[2])
+    raise ValueError(f"the heads of a token of {name} must be contiguous")
 
 
 def _scales(t: torch.Tensor, cache_shape, dev: int) -> int:
     """Address of a row-scaled cache's scale bytes."""
-    at = _ptr(t, torch.uint8, dev, "scales")
-    nb, hkv = cache_shape[:2]
-    if t.shape != (nb, hkv, 2, 16):
+    at = _ptr(t, _U8, dev, "scales")
+    if t.shape != (cache_shape[0], cache_shape[1], 2, 16):
         raise ValueError("scales must be [num_blocks, Hkv, 2, 16]")
     return at
 
@@ -690,19 +694,18 @@ def write_kv_rows(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
     the call finds (uint8 ``scales`` [num_blocks, Hkv, 2, 16]: K's, then V's; b
     stands for 2^(b - 127)). k and v may be views into one projection's output.
     """
-    cshape = _like_cache(k_cache, v_cache)
-    nb, hkv, bs, d = cshape
+    nb, hkv, bs, d = cshape = _like_cache(k_cache, v_cache)
     T = k.shape[0]
     dev, raw_stream = _where(stream)
-    kp, ks = _heads(k, (T, hkv, d), dev, "k")
-    vp, vs = _heads(v, (T, hkv, d), dev, "v")
-    sp = _ptr(slot_mapping, torch.int64, dev, "slot_mapping")
+    shape = (T, hkv, d)
+    kp, ks = _heads(k, shape, dev, "k")
+    vp, vs = _heads(v, shape, dev, "v")
+    sp = _ptr(slot_mapping, _I64, dev, "slot_mapping")
     if slot_mapping.numel() != T:
         raise ValueError("slot_mapping must be [num_tokens]")
     st = lib().pa_write_kv_rows(_pack_wr(
-        kp, vp, sp, _ptr(k_cache, torch.uint8, dev, "k_cache"),
-        _ptr(v_cache, torch.uint8, dev, "v_cache"), _scales(scales, cshape, dev), raw_stream, ks, vs,
-        T, hkv, d, bs, nb))
+        kp, vp, sp, _ptr(k_cache, _U8, dev, "k_cache"), _ptr(v_cache, _U8, dev, "v_cache"),
+        _scales(scales, cshape, dev), raw_stream, ks, vs, T, hkv, d, bs, nb))
     if st:
         _check(st, "pa_write_kv_rows")
 
