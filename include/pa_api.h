@@ -659,7 +659,8 @@ pa_status pa_read_kv(const pa_read_args* args);
  * The other arguments are pa_attention's. Sharing follows the lengths: a request
  * that does not see its whole prefix (a context shorter than it), that brings 16 or
  * more new tokens (a prompt chunk, whose rows share K and V already) or that is
- * left alone with one token attends on its own, with the same result.
+ * left alone with one token attends on its own, with the same result; and so does the
+ * whole batch where sharing would not pay (PA_OPT_SHARED_MIN_KB).
  * The prefixes run on the tensor cores as a cascade's does, in pairs of 128-row
  * tiles of a group's queries and chunks of keys, into fp32 partials; each token's
  * own keys on the split-KV kernels; a merge pass folds both. At most 1024 groups,
@@ -816,14 +817,22 @@ pa_status pa_set_kernel_timer(int kernel_id, void* start_event, void* stop_event
  *     newest token lies; a planner, a cascade's prefix pass and the splitting
  *     of the queries over an E4M3 cache start at once too. The caller promises
  *     that the work enqueued right before every attention call writes nothing
- *     that the call reads but the new tokens' K and V rows: pa_write_kv[_fp8]
- *     is such work, pa_norm_rope_write_kv (it makes q), pa_evict_kv and a
+ *     that the call reads but the new tokens' K and V rows (and scales):
+ *     pa_write_kv[_fp8, _rows] is such work, pa_norm_rope_write_kv (it makes q), pa_evict_kv and a
  *     kernel that makes q, lengths or tables are not. With 0 every call reads
  *     what the stream's work before it has written, whatever that is. Results
  *     are bit-identical. Llama-8B decode step: 99.6 us with 0, 98.0 with 1;
  *     over an E4M3 cache 68.8 and 64.8.
  */
 #define PA_OPT_WRITE_OVERLAP 9
+/*
+ *   PA_OPT_SHARED_MIN_KB (default 24576; negative is PA_ERR_INVALID_ARG): a
+ *     pa_attention_shared call whose groups would save less reading of K and V
+ *     than this many KB, and hold no shared prefix of 4096 keys or more, attends
+ *     without sharing: the prefix pass would cost more than it saves. 0: every
+ *     group of two tokens shares. Results stay within the attention tolerances.
+ */
+#define PA_OPT_SHARED_MIN_KB 10
 pa_status pa_set_option(int option, int value);
 
 /* Number of kernel launches the library has issued in this process. */

@@ -934,7 +934,7 @@ def set_kernel_timer(kernel: str, start: torch.cuda.Event | None,
 
 OPTIONS = {"decode_self_plan": 1, "decode_tc": 2, "decode_max_workers": 3, "mixed_overlap": 4,
            "decode_token_major": 5, "cascade_overlap": 6, "decode_tm_ctas_per_sm": 7,
-           "mixed_prefill_ctas": 8, "write_overlap": 9}
+           "mixed_prefill_ctas": 8, "write_overlap": 9, "shared_min_kb": 10}
 
 
 def set_option(name: str, value: int) -> None:

@@ -46,6 +46,7 @@ std::atomic<int> g_token_major{1};  // pa_set_option(PA_OPT_DECODE_TOKEN_MAJOR, 
 std::atomic<int> g_cascade_overlap{1};  // pa_set_option(PA_OPT_CASCADE_OVERLAP, ...)
 std::atomic<int> g_tm_ctas{2};  // pa_set_option(PA_OPT_DECODE_TM_CTAS_PER_SM, ...)
 std::atomic<int> g_write_overlap{0};  // pa_set_option(PA_OPT_WRITE_OVERLAP, ...)
+std::atomic<int> g_shared_min{kSharedMinKb};  // pa_set_option(PA_OPT_SHARED_MIN_KB, ...)
 std::atomic<int> g_mixed_ctas{0};  // pa_set_option(PA_OPT_MIXED_PREFILL_CTAS, ...): 0 = planned
 // write, plan, decode, prefill, cascade prefix, merge, weights, evict, read
 constexpr int kNumTimers = 9;
@@ -715,6 +716,8 @@ pa_status shared_impl(const pa_shared_args& a) {
   pp.use_prefill = a.max_query_len >= kPrefillMinQlen ? 1 : 0;
   pp.num_workers = (cap > 0 && cap < launched) ? cap : launched;
   pp.num_sms = d->num_sms;
+  // K and V of one 16-key block, all KV heads
+  pp.position_bytes = 2 * kBlockSize * a.num_kv_heads * a.head_dim * (fmt == 0 ? 2 : 1);
   pp.token_major = use_tm ? 1 : 0;
   pp.min_pos = 1;  // suffixes are short: as in a windowed call
   pp.group_start = a.group_start_loc;
@@ -723,6 +726,7 @@ pa_status shared_impl(const pa_shared_args& a) {
   pp.max_prefix_len = a.max_prefix_len;
   pp.chunk_tiles = sh.chunk_tiles;
   pp.max_items = sh.max_items;
+  pp.shared_min_bytes = (unsigned long long)g_shared_min.load() << 10;
   pp.shared_items = reinterpret_cast<SharedItem*>(ws + sh.items_off);
   pp.tok_parts = tok_parts;
   pp.header = reinterpret_cast<WsHeader*>(ws + lay.header_off);
@@ -1358,6 +1362,10 @@ pa_status pa_set_option(int option, int value) {
     case PA_OPT_WRITE_OVERLAP:
       if (value != 0 && value != 1) return PA_ERR_INVALID_ARG;
       g_write_overlap.store(value);
+      return PA_OK;
+    case PA_OPT_SHARED_MIN_KB:
+      if (value < 0) return PA_ERR_INVALID_ARG;
+      g_shared_min.store(value);
       return PA_OK;
     case PA_OPT_MIXED_OVERLAP:
       g_mixed_overlap.store(value ? 1 : 0);

@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
   // its pairs of row tiles: full ones, and a split one or none
   __shared__ int s_full[SHARED ? kMaxSharedGroups : 1], s_split[SHARED ? kMaxSharedGroups : 1];
   __shared__ int s_start[SHARED ? kMaxSharedGroups + 1 : 1], s_len[SHARED ? kMaxSharedGroups : 1];
-  __shared__ unsigned long long s_best;
+  __shared__ unsigned long long s_best, s_saved;
   // what this thread's (first) request is, kept from one pass over them to the next
   int my_q0 = 0, my_qlen = 0, my_L = 0, my_group = -1, my_blocks = 0;
   bool my_valid = false;
@@ -279,8 +279,23 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
       atomicMin(&s_lo[g], q0);
       atomicMax(&s_hi[g], q0 + qlen);
     }
-    if (threadIdx.x == 0) s_best = ~0ull;
+    if (threadIdx.x == 0) {
+      s_best = ~0ull;
+      s_saved = 0ull;
+    }
     __syncthreads();
+    // what sharing saves of reading, and whether that pays for the prefix pass
+    for (int g = threadIdx.x; g < p.num_groups; g += blockDim.x)
+      if (s_count[g] >= kSharedMinTokens)
+        atomicAdd(&s_saved, s_len[g] >= kSharedLong
+                                ? p.shared_min_bytes
+                                : (unsigned long long)(s_count[g] - 1) *
+                                      (unsigned)(s_len[g] / kBlockSize) * (unsigned)p.position_bytes);
+    __syncthreads();
+    if (s_saved < p.shared_min_bytes) {
+      for (int g = threadIdx.x; g < p.num_groups; g += blockDim.x) s_count[g] = 0;
+      __syncthreads();
+    }
     for (int g = threadIdx.x; g < p.num_groups; g += blockDim.x) {
       s_tiles[g] = s_count[g] >= kSharedMinTokens ? (s_len[g] + 127) / 128 : 0;
       const int n = s_tiles[g] > 0 ? s_hi[g] - s_lo[g] : 1;

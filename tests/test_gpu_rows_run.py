@@ -27,6 +27,7 @@ def table(n, d):
 def test_serving_loop(pa_lib, hq, hkv, d):
     from paged_kv_cache_42_gb300 import binding, host
     binding.get_device_error(True)
+    binding.set_option("shared_min_kb", 0)  # share, however little it saves
     g = torch.Generator().manual_seed(5)
     blocks, prefix = 96, 48
     pool = host.BlockPool(blocks)
@@ -123,6 +124,7 @@ def test_serving_loop(pa_lib, hq, hkv, d):
                                   torch.tensor([0, n], dtype=torch.int32).cuda(), num_tokens=n)
     assert torch.equal(k3, k) and torch.equal(v3, v)
     pool.release(own[1])
+    binding.set_option("shared_min_kb", 24576)
     assert binding.get_device_error(True)[0] == 0
 
 

@@ -10,6 +10,15 @@ from tests import shared_ref as sr
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True)
+def sharing_whatever_it_saves(pa_lib):
+    """These batches are small: by default they would attend without sharing."""
+    from paged_kv_cache_42_gb300 import binding
+    binding.set_option("shared_min_kb", 0)
+    yield
+    binding.set_option("shared_min_kb", 24576)
+
+
 def close(got, b):
     want, tol = b.want()
     mine = ~torch.isnan(want)
@@ -247,3 +256,25 @@ def test_offsets_past_32_bits(pa_lib, fmt):
     assert binding.get_device_error(True)[0] == 0
     del g
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "rows"])
+def test_batches_that_do_not_share(pa_lib, fmt):
+    """Below the limit the call attends without sharing, above it with: the same result."""
+    from paged_kv_cache_42_gb300 import binding
+    b = sr.Batch([(256, [(9, 1), (40, 1), (0, 3)]), (1040, [(3, 1), (4, 1)])], 32, 8, 128, 7, fmt=fmt,
+                 before=[(30, 1)], after=[(5, 20)])
+    g = b.gpu()
+    outs = []
+    for kb in (24576, 0, 2 ** 31 - 1):
+        binding.set_option("shared_min_kb", kb)
+        outs.append(b.run(g).clone())
+        close(outs[-1], b)
+    assert torch.equal(outs[0], outs[2])
+    # a long prefix is shared whatever the tokens save
+    b = sr.Batch([(4096, [(9, 1), (40, 1)])], 8, 2, 64, 7, fmt=fmt)
+    g = b.gpu()
+    for kb in (2 ** 31 - 1, 0):
+        binding.set_option("shared_min_kb", kb)
+        close(b.run(g), b)
+    assert binding.get_device_error(True)[0] == 0

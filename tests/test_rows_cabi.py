@@ -172,3 +172,8 @@ def test_binding_refuses_cpu_tensors_and_shapes(pa_lib, monkeypatch):
         binding.read_kv(kc, kc, bt, torch.zeros(2, dtype=torch.int32), num_tokens=4)
     with pytest.raises(ValueError, match="num_tokens"):
         binding.read_kv(kc, kc, bt, torch.zeros(3, dtype=torch.int32))
+
+
+def test_shared_min_kb_option(pa_lib):
+    assert pa_lib.pa_set_option(10, -1) == ARG
+    assert pa_lib.pa_set_option(10, 0) == OK and pa_lib.pa_set_option(10, 24576) == OK
