@@ -399,7 +399,8 @@ pa_status pa_attention_weights_fp8(const void* q, const void* k_cache,
  * as they are: a rotation by position stays the one they were written with.
  * Requests with seq_lens[r] <= keep are left as they are: only new_seq_lens[r]
  * is written for them.
- *   k_cache, v_cache  the pool, elem_bytes (2: bf16, 1: E4M3 codes) per element
+ *   k_cache, v_cache  the pool, elem_bytes (2: bf16, 1: E4M3 codes with a scale per
+ *                     tensor) per element; a row-scaled cache's scales are not moved
  *   weights           [num_reqs][num_kv_heads][weights_stride] fp32, entries
  *                     past a request's length not read (pa_attention_weights
  *                     makes them)
@@ -558,7 +559,9 @@ size_t pa_args_size(int which);
 /* pa_write_kv into a row-scaled cache. Tokens of k and v are k_stride / v_stride
  * elements apart (at least one token's heads, a multiple of 8), a token's heads
  * contiguous. head_dim 64 or 128, up to 65536 KV heads; a negative slot is
- * skipped, one outside the pool too, with PA_DEVERR_SLOT. */
+ * skipped, one outside the pool too, with PA_DEVERR_SLOT. The other slots of a call
+ * are distinct: of tokens with the same one, a row may keep one's codes and another's
+ * scale. */
 typedef struct pa_write_rows_args { /* 16 */
   const void *k, *v;
   const int64_t* slot_mapping;
@@ -670,7 +673,9 @@ pa_status pa_read_kv(const pa_read_args* args);
  * negative, no multiple of 16 or longer than max_prefix_len PA_DEVERR_PREFIX (its
  * requests then attend on their own); a sharing request whose table does not start
  * with the blocks of the group's first sharing request sets PA_DEVERR_PREFIX, and
- * is computed with that one's prefix (the result is wrong; the error word says so).
+ * is computed with that one's prefix where the batch shares (the result is wrong; the
+ * error word says so). With no groups, or max_prefix_len below 16, the call is
+ * pa_attention's and reads neither group_start_loc nor prefix_lens.
  */
 size_t pa_attention_shared_workspace_size(int num_reqs, int num_tokens, int num_q_heads,
                                           int num_kv_heads, int head_dim, int num_groups,

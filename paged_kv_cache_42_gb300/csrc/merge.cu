@@ -27,30 +27,36 @@ namespace pa {
 namespace {
 
 constexpr int kMergeWarps = 8;
-// Pairs of (unit, kv head) from which a shared call's merge gives each a warp, not a
-// CTA: 4864 pairs of 3 to 5 partials at G = 8 44 -> 9 us, 1088 pairs of a few at G = 4
-// 10 us either way, but 400 pairs of a dozen at G = 8 15 -> 21 us.
-constexpr int kMergeWarpPairs = 1024;
+// A shared call's merge takes the query heads of a (unit, kv head) pair four at a time:
+// G = 8, 400 pairs of a dozen partials 13 -> 8 us (two at a time 10: more CTAs than fit).
+constexpr int kMergeHeads = 4;
+// Such shares of a pair from which each gets a warp, not a CTA. Measured (us, CTA / warp):
+// 2048 shares of 7 partials 18 / 9, 1856 of 3 to 5 11 / 5, 928 of them 5 / 5, but 544 5 / 8
+// and 800 of a dozen 8 / 10.
+constexpr int kMergeWarpShares = 1024;
 
-template <int D, int G, bool SHARED>
+// H: query heads of a CTA (SHARED; else all G).
+template <int D, int G, bool SHARED, int H = G>
 __global__ void __launch_bounds__(kMergeWarps * 32) pa_merge_kernel(const MergeParams p) {
   constexpr int V = D / 32;  // output dims per lane
   static_assert(V == 2 || V == 4, "head dim 64 or 128");
-  __shared__ float s_m[kMergeWarps][G], s_l[kMergeWarps][G];
-  __shared__ __align__(16) float s_o[kMergeWarps][G][D];
+  __shared__ float s_m[kMergeWarps][H], s_l[kMergeWarps][H];
+  __shared__ __align__(16) float s_o[kMergeWarps][H][D];
   griddep_wait();  // the split-KV grid's partials and tasks
   const int W = __ldcg(&p.header->num_positions);
   int nw = p.num_workers;
   if (p.workers_from_header) nw = min(nw, __ldcg(&p.header->decode_workers));
   if (W <= 0) return;
-  int tok, kv, wf, wl;
+  int tok, kv, wf, wl, hb = 0;  // hb: the first of the CTA's heads
   if (p.all_units) {
     // overlapped cascade: (unit, kv head) blockIdx; its positions, and the
     // workers holding them, as the split-KV kernel sliced them
-    const int k = (int)blockIdx.x / p.num_kv_heads;
-    kv = (int)blockIdx.x % p.num_kv_heads;
-    if (k >= __ldcg(&p.header->num_units)) return;
+    const int pair = (int)blockIdx.x / (G / H), k = pair / p.num_kv_heads;
+    hb = (int)blockIdx.x % (G / H) * H;
+    kv = pair % p.num_kv_heads;
+    // (there are num_tokens units in memory at least)
     const int4 u = __ldcg(reinterpret_cast<const int4*>(p.units + k));
+    if (k >= __ldcg(&p.header->num_units)) return;
     const int nb = max(1, (u.z + kBlockSize - 1) / kBlockSize - p.key_start_blocks);
     const int first = u.w + (SHARED && p.token_major ? 0 : kv * nb);
     const int NW = plan_workers(W, nw, p.min_pos);
@@ -83,9 +89,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) pa_merge_kernel(const MergeP
   };
 
   // this warp's share: partials warp, warp + kMergeWarps, ...
-  float M[G], L[G], O[G][V];
+  float M[H], L[H], O[H][V];
 #pragma unroll
-  for (int h = 0; h < G; ++h) {
+  for (int h = 0; h < H; ++h) {
     M[h] = -INFINITY;
     L[h] = 0.f;
 #pragma unroll
@@ -95,17 +101,17 @@ __global__ void __launch_bounds__(kMergeWarps * 32) pa_merge_kernel(const MergeP
   for (int i = warp; i < n; i += kMergeWarps) {
     const float* sl = slot(i);
 #pragma unroll
-    for (int h = 0; h < G; ++h) {
-      const float m = __ldcg(sl + h), l = __ldcg(sl + G + h);
+    for (int h = 0; h < H; ++h) {
+      const float m = __ldcg(sl + hb + h), l = __ldcg(sl + G + hb + h);
       float o[V];
       if constexpr (V == 4) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(sl + 16 + h * D) + lane);
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(sl + 16 + (hb + h) * D) + lane);
         o[0] = v.x;
         o[1] = v.y;
         o[2] = v.z;
         o[3] = v.w;
       } else {
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(sl + 16 + h * D) + lane);
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(sl + 16 + (hb + h) * D) + lane);
         o[0] = v.x;
         o[1] = v.y;
       }
@@ -118,7 +124,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) pa_merge_kernel(const MergeP
     }
   }
 #pragma unroll
-  for (int h = 0; h < G; ++h) {
+  for (int h = 0; h < H; ++h) {
     if (lane == 0) {
       s_m[warp][h] = M[h];
       s_l[warp][h] = L[h];
@@ -130,7 +136,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) pa_merge_kernel(const MergeP
 
   // combine the warps' shares (a warp without partials has m = -inf), two
   // output dims per thread, stored as one bf16 pair
-  for (int e = threadIdx.x; e < G * D / 2; e += kMergeWarps * 32) {
+  for (int e = threadIdx.x; e < H * D / 2; e += kMergeWarps * 32) {
     const int h = e / (D / 2), d = 2 * (e - h * (D / 2));
     float mx = -INFINITY;
 #pragma unroll
@@ -144,7 +150,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) pa_merge_kernel(const MergeP
       o1 += s_o[k][h][d + 1] * f;
     }
     const float sc = p.v_scale / l;
-    *reinterpret_cast<uint32_t*>(p.out + ((size_t)tok * p.num_q_heads + (size_t)kv * G + h) * D +
+    *reinterpret_cast<uint32_t*>(p.out + ((size_t)tok * p.num_q_heads + (size_t)kv * G + hb + h) * D +
                                  d) = float2_to_bf16x2(o0 * sc, o1 * sc);
   }
 }
@@ -239,16 +245,18 @@ __global__ void __launch_bounds__(kMergeWarps * 32) pa_merge_tm_kernel(const Mer
   }
 }
 
-// Shared calls with many (unit, kv head) pairs: a warp each, which merges the few
-// partials of its pair - the split-KV workers' that hold its own keys, then its
+// Shared calls with many (unit, kv head) pairs: a warp per share of one, which merges the few
+// partials of its heads - the split-KV workers' that hold its own keys, then its
 // prefix's - on its own, a group of them loaded at a time.
-template <int D, int G>
+template <int D, int G, int H>
 __global__ void __launch_bounds__(kMergeWarps * 32) pa_merge_shared_kernel(const MergeParams p) {
   constexpr int V = D / 32;  // output dims per lane
   griddep_wait();
   const int W = __ldcg(&p.header->num_positions);
   const long long item = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
-  const int k = (int)(item / p.num_kv_heads), kv = (int)(item % p.num_kv_heads);
+  const long long pair = item / (G / H);
+  const int k = (int)(pair / p.num_kv_heads), kv = (int)(pair % p.num_kv_heads);
+  const int hb = (int)(item % (G / H)) * H;  // the first of the warp's heads
   const int lane = threadIdx.x & 31;
   if (W <= 0 || k >= __ldcg(&p.header->num_units)) return;
   const int4 u = __ldcg(reinterpret_cast<const int4*>(p.units + k));
@@ -266,10 +274,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) pa_merge_shared_kernel(const
                         (((size_t)(i - ns) * p.num_tokens + tok) * p.num_kv_heads + kv) *
                             p.slot_floats;
   };
-  constexpr int K = G <= 4 ? 4 : 2;
-  float am[G], al[G], ao[G][V], qm[K][G], ql[K][G], qo[K][G][V];
+  constexpr int K = H <= 4 ? 4 : 2;
+  float am[H], al[H], ao[H][V], qm[K][H], ql[K][H], qo[K][H][V];
 #pragma unroll
-  for (int h = 0; h < G; ++h) {
+  for (int h = 0; h < H; ++h) {
     am[h] = -INFINITY;
     al[h] = 0.f;
 #pragma unroll
@@ -280,17 +288,17 @@ __global__ void __launch_bounds__(kMergeWarps * 32) pa_merge_shared_kernel(const
     for (int j = 0; j < K; ++j) {
       const float* const sl = slot(min(i0 + j, n - 1));
 #pragma unroll
-      for (int h = 0; h < G; ++h) {
-        qm[j][h] = __ldcg(sl + h);
-        ql[j][h] = __ldcg(sl + G + h);
+      for (int h = 0; h < H; ++h) {
+        qm[j][h] = __ldcg(sl + hb + h);
+        ql[j][h] = __ldcg(sl + G + hb + h);
         if constexpr (V == 4) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(sl + 16 + h * D) + lane);
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(sl + 16 + (hb + h) * D) + lane);
           qo[j][h][0] = v.x;
           qo[j][h][1] = v.y;
           qo[j][h][2] = v.z;
           qo[j][h][3] = v.w;
         } else {
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(sl + 16 + h * D) + lane);
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(sl + 16 + (hb + h) * D) + lane);
           qo[j][h][0] = v.x;
           qo[j][h][1] = v.y;
         }
@@ -300,7 +308,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) pa_merge_shared_kernel(const
     for (int j = 0; j < K; ++j) {
       if (i0 + j >= n) break;
 #pragma unroll
-      for (int h = 0; h < G; ++h) {
+      for (int h = 0; h < H; ++h) {
         const float mn = fmaxf(am[h], qm[j][h]);
         const float a = exp2f(am[h] - mn), b = exp2f(qm[j][h] - mn);  // am = -inf: a = 0
         al[h] = al[h] * a + ql[j][h] * b;
@@ -311,9 +319,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) pa_merge_shared_kernel(const
     }
   }
 #pragma unroll
-  for (int h = 0; h < G; ++h) {
+  for (int h = 0; h < H; ++h) {
     const float sc = p.v_scale / al[h];
-    uint16_t* const orow = p.out + ((size_t)tok * p.num_q_heads + (size_t)kv * G + h) * D;
+    uint16_t* const orow = p.out + ((size_t)tok * p.num_q_heads + (size_t)kv * G + hb + h) * D;
     if constexpr (V == 4)
       *reinterpret_cast<uint2*>(orow + lane * V) =
           make_uint2(float2_to_bf16x2(ao[h][0] * sc, ao[h][1] * sc),
@@ -346,9 +354,14 @@ cudaError_t launch_merge_t(const MergeParams& p, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (p.tok_parts != nullptr) {
-    if (boundaries < kMergeWarpPairs) return cudaLaunchKernelEx(&cfg, pa_merge_kernel<D, G, true>, p);
-    cfg.gridDim = dim3((unsigned)((boundaries + kMergeWarps - 1) / kMergeWarps));
-    return cudaLaunchKernelEx(&cfg, pa_merge_shared_kernel<D, G>, p);
+    constexpr int H = G > kMergeHeads ? kMergeHeads : G;
+    const int shares = boundaries * (G / H);
+    if (shares < kMergeWarpShares) {
+      cfg.gridDim = dim3((unsigned)shares);
+      return cudaLaunchKernelEx(&cfg, pa_merge_kernel<D, G, true, H>, p);
+    }
+    cfg.gridDim = dim3((unsigned)(((long long)shares + kMergeWarps - 1) / kMergeWarps));
+    return cudaLaunchKernelEx(&cfg, pa_merge_shared_kernel<D, G, H>, p);
   }
   if (p.token_major) {  // a CTA per boundary, a warp per KV head
     cfg.blockDim = dim3(32 * p.num_kv_heads);

@@ -28,7 +28,7 @@
 // flight together, before anything depends on the position; the token's
 // cosines and sines and the kind's weight are loaded once for all of them, and
 // V skips the arithmetic. 2048 tokens of 32 + 8 + 8 heads of 128 take 10.8 us,
-// 4.8 TB/s (E4M3 12.9); 2, 6 or 8 groups a warp 12.3, 12.0 and 12.8 us (13.4, 14.3,
+// 4.8 TB/s (E4M3 12.9, row-scaled 12.3); 2, 6 or 8 groups a warp 12.3, 12.0 and 12.8 us (13.4, 14.3,
 // 15.6). Units that mix the kinds were 9% slower: the choice is made per head.
 #include <type_traits>
 

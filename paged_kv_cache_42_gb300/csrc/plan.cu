@@ -126,10 +126,14 @@ __device__ __forceinline__ int shared_parts(int tiles, int ct, bool split) {
 }
 
 // CTAs 1 .. of a shared call's plan: every request that shares its group's prefix
-// starts with the same blocks as the first one that does.
+// starts with the same blocks as the first one that does. kCheckCtas CTAs take a group
+// together, a share of its requests each.
+constexpr int kCheckCtas = 4;
 __device__ void check_shared_tables(const PlanParams& p) {
   __shared__ int s_leader;
-  for (int g = (int)blockIdx.x - 1; g < p.num_groups; g += (int)gridDim.x - 1) {
+  const int warps = blockDim.x >> 5, part = ((int)blockIdx.x - 1) % kCheckCtas;
+  for (int g = ((int)blockIdx.x - 1) / kCheckCtas; g < p.num_groups;
+       g += ((int)gridDim.x - 1) / kCheckCtas) {
     const int a = __ldg(p.group_start + g), b = __ldg(p.group_start + g + 1);
     const int len = __ldg(p.prefix_lens + g);
     if (threadIdx.x == 0) {
@@ -154,7 +158,8 @@ __device__ void check_shared_tables(const PlanParams& p) {
     if (leader < b) {
       const int32_t* const want = p.block_tables + (size_t)leader * p.max_blocks_per_req;
       // a warp takes a request at a time, with several loads in flight per lane
-      for (int r = leader + 1 + (int)(threadIdx.x >> 5); r < b; r += blockDim.x >> 5) {
+      for (int r = leader + 1 + part * warps + (int)(threadIdx.x >> 5); r < b;
+           r += kCheckCtas * warps) {
         if (!check_request(p, r, q0, qlen, L, false) || !shares(p, qlen, L, blocks)) continue;
         const int32_t* const got = p.block_tables + (size_t)r * p.max_blocks_per_req;
         bool same = true;
@@ -248,19 +253,24 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
   __shared__ int s_full[SHARED ? kMaxSharedGroups : 1], s_split[SHARED ? kMaxSharedGroups : 1];
   __shared__ int s_start[SHARED ? kMaxSharedGroups + 1 : 1], s_len[SHARED ? kMaxSharedGroups : 1];
   __shared__ unsigned long long s_best, s_saved;
+  bool sharing = false;  // whether any group does, and it pays (the same for every thread)
   // what this thread's (first) request is, kept from one pass over them to the next
   int my_q0 = 0, my_qlen = 0, my_L = 0, my_group = -1, my_blocks = 0;
   bool my_valid = false;
   if constexpr (SHARED) {
+    // a thread's first group is loaded beside its first request: one round trip
+    const int g0 = (int)threadIdx.x;
+    const int start0 = g0 <= p.num_groups ? __ldg(p.group_start + g0) : 0;
+    const int len0 = g0 < p.num_groups ? __ldg(p.prefix_lens + g0) : 0;
     if (threadIdx.x < p.num_reqs)
       my_valid = check(threadIdx.x, my_q0, my_qlen, my_L, true);
-    for (int g = threadIdx.x; g < p.num_groups; g += blockDim.x) {
-      s_start[g] = __ldg(p.group_start + g);
-      s_len[g] = __ldg(p.prefix_lens + g);
+    for (int g = g0; g <= p.num_groups; g += blockDim.x) {
+      s_start[g] = g == g0 ? start0 : __ldg(p.group_start + g);
+      if (g == p.num_groups) break;
+      s_len[g] = g == g0 ? len0 : __ldg(p.prefix_lens + g);
       s_first[g] = s_lo[g] = 0x7fffffff;
       s_count[g] = s_hi[g] = 0;
     }
-    if (threadIdx.x == 0) s_start[p.num_groups] = __ldg(p.group_start + p.num_groups);
     for (int t = threadIdx.x; t < T; t += blockDim.x) p.tok_parts[t] = 0;
     __syncthreads();
     for (int r = threadIdx.x; r < p.num_reqs; r += blockDim.x) {
@@ -285,17 +295,23 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
     }
     __syncthreads();
     // what sharing saves of reading, and whether that pays for the prefix pass
+    // (atomics of 64 bits on shared memory are loops: one per warp)
+    unsigned long long saved = 0;
     for (int g = threadIdx.x; g < p.num_groups; g += blockDim.x)
       if (s_count[g] >= kSharedMinTokens)
-        atomicAdd(&s_saved, s_len[g] >= kSharedLong
-                                ? p.shared_min_bytes
-                                : (unsigned long long)(s_count[g] - 1) *
-                                      (unsigned)(s_len[g] / kBlockSize) * (unsigned)p.position_bytes);
-    __syncthreads();
-    if (s_saved < p.shared_min_bytes) {
-      for (int g = threadIdx.x; g < p.num_groups; g += blockDim.x) s_count[g] = 0;
-      __syncthreads();
+        saved += s_len[g] >= kSharedLong
+                     ? max(p.shared_min_bytes, 1ull)
+                     : (unsigned long long)(s_count[g] - 1) * (unsigned)(s_len[g] / kBlockSize) *
+                           (unsigned)p.position_bytes;
+    if ((int)(threadIdx.x & ~31u) < p.num_groups) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) saved += __shfl_xor_sync(kFull, saved, o);
+      if ((threadIdx.x & 31) == 0) atomicAdd(&s_saved, saved);
     }
+    __syncthreads();
+    sharing = s_saved > 0 && s_saved >= p.shared_min_bytes;
+  }
+  if (SHARED && sharing) {
     for (int g = threadIdx.x; g < p.num_groups; g += blockDim.x) {
       s_tiles[g] = s_count[g] >= kSharedMinTokens ? (s_len[g] + 127) / 128 : 0;
       const int n = s_tiles[g] > 0 ? s_hi[g] - s_lo[g] : 1;
@@ -319,15 +335,19 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
         items += (float)full * ceilf((float)tiles * by) + (float)split * ceilf((float)tiles * by_split);
         longest = max(longest, min(ct, full > 0 ? tiles : (2 * tiles + 2) / 3));
       }
-      if (items > 0.f) {
-        const float rounds = ceilf(items * (float)p.num_kv_heads / (float)p.num_sms);
-        const float cost = rounds * (float)(longest + kSharedItemSteps);
-        atomicMin(&s_best, (unsigned long long)__float_as_uint(cost) << 32 | (unsigned)ct);
+      const float rounds = ceilf(items * (float)p.num_kv_heads / (float)p.num_sms);
+      const float cost = rounds * (float)(longest + kSharedItemSteps);
+      unsigned long long best = (unsigned long long)__float_as_uint(cost) << 32 | (unsigned)ct;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const unsigned long long other = __shfl_xor_sync(kFull, best, o);
+        best = other < best ? other : best;
       }
+      if ((threadIdx.x & 31) == 0) atomicMin(&s_best, best);
     }
     __syncthreads();
   }
-  const int chunk_tiles = SHARED && s_best != ~0ull ? (int)(unsigned)s_best : 1;
+  const int chunk_tiles = sharing ? (int)(unsigned)s_best : 1;
   for (int r = threadIdx.x; r < p.num_reqs; r += blockDim.x) {
     int q0 = my_q0, qlen = my_qlen, L = my_L;
     const bool mine = SHARED && r == (int)threadIdx.x;
@@ -349,12 +369,12 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
         g = shared_group(p, s_start, s_len, r, &blocks);
         if (g >= 0 && !shares(p, qlen, L, blocks)) g = -1;
       }
-      if (g < 0 || s_count[g] < kSharedMinTokens) blocks = 0;
+      if (!sharing || g < 0 || s_count[g] < kSharedMinTokens) blocks = 0;
       const int at = r * p.max_blocks_per_req + blocks;
       for (int j = 0; j < qlen; ++j) {
         raw[q0 + j] = make_int2(at, ctx + j + 1 - blocks * kBlockSize);
         if (blocks > 0) {
-          const int left = s_hi[g] - (q0 + j - (q0 + j - s_lo[g]) % tok_per_item);
+          const int left = s_hi[g] - (q0 + j - ((q0 + j - s_lo[g]) & (tok_per_item - 1)));
           p.tok_parts[q0 + j] = shared_parts((blocks + 7) / 8, chunk_tiles, shared_split(left, p.group));
         }
       }
@@ -386,7 +406,9 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
       }
     }
   }
-  if constexpr (SHARED) {  // the prefix pass's items, group after group
+  if (SHARED && !sharing) {
+    if (threadIdx.x == 0) p.header->num_prefix_items = 0;
+  } else if constexpr (SHARED) {  // the prefix pass's items, group after group
     __shared__ int s_at[kMaxSharedGroups + 1];
     long long run = 0;
     for (int c0 = 0; c0 < p.num_groups; c0 += blockDim.x) {
@@ -503,7 +525,10 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
   if (ubase) {
     const int NW = plan_workers(W, s_workers, p.min_pos);
     for (int w = threadIdx.x; w < NW; w += blockDim.x) {
-      const int S = (int)((long long)w * W / NW);
+      // (worker_begin; a division of 32 bits where it does)
+      const int S = (unsigned long long)W * (unsigned)NW < 1ull << 32
+                        ? (int)((unsigned)w * (unsigned)W / (unsigned)NW)
+                        : worker_begin(w, W, NW);
       int lo = 0, hi = K;  // ubase[lo] <= S < ubase[hi]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -541,12 +566,16 @@ cudaError_t launch_plan_t(const PlanParams& p, cudaStream_t s) {
   // a plan needs) before completing.
   cudaLaunchConfig_t cfg = {};
   // shared calls: CTAs of their own check the groups' tables
-  cfg.gridDim = dim3(SHARED ? 1 + (p.num_groups < 64 ? p.num_groups : 64) : 1);
+  cfg.gridDim = dim3(SHARED ? 1 + kCheckCtas * (p.num_groups < 32 ? p.num_groups : 32) : 1);
   // A batch with no tensor-core work needs no bucket sort: a block sized to the
   // batch (fewer warps per barrier) plans it faster.
   int threads = kPlanThreads;
-  if (!SHARED && !p.use_prefill) {
+  if (!p.use_prefill) {
     int need = p.num_tokens > p.num_reqs ? p.num_tokens : p.num_reqs;
+    // (on CUDA cores a shared call's tokens have several split-KV workers each, whose
+    // first units are looked up one per thread)
+    if (SHARED && !p.token_major) need *= 4;
+    if (SHARED && need < kSharedCandidates) need = kSharedCandidates;
     // a cascade's prefix check reads (requests - 1) x prefix blocks entries
     if (p.prefix_blocks > 0 && (long long)(p.num_reqs - 1) * p.prefix_blocks > need)
       need = kPlanThreads;

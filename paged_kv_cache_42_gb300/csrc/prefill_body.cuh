@@ -59,7 +59,7 @@
 // caches (KV 2, rows.cuh) the converters multiply each row by its 2^e, which is
 // exact in bf16 too, and nothing else differs.
 //
-// Warp roles (320 threads): warp 0 issues TMA loads (both Q tiles per work
+// Warp roles (320 threads over bf16 caches): warp 0 issues TMA loads (both Q tiles per work
 // item, K into a 3-stage ring released right after both S MMAs of a key tile,
 // V into a 2-stage ring released after both P*V), warp 1 allocates TMEM and
 // one thread issues the MMAs in order
@@ -125,6 +125,8 @@ struct PCfg {
   static constexpr int OFF_K = OFF_Q + 2 * Q_BYTES;
   static constexpr int OFF_V = OFF_K + KSTAGES * KV_BYTES;
   static constexpr int OFF_BAR = OFF_V + VSTAGES * KV_BYTES;
+  // E4M3: a byte for each of K's stages, then V's: which of its tile's blocks were copied
+  static constexpr int OFF_GOOD = OFF_BAR + 272;
   // row-max / row-sum exchange of the split softmax: [row tile][parity][half][128 rows]
   static constexpr int OFF_XCH = OFF_BAR + 320;
   static constexpr int XCH_BYTES = kSplit == 2 ? 2 * 2 * 2 * 128 * 4 : 0;
@@ -447,11 +449,15 @@ __global__ void __launch_bounds__(KV ? kThreadsF8 : kThreads, 1)
       // codes (and scales) to be widened there
       auto copy = [&](int pid, bool is_v, int st) {
         const bool mine = lane < 8 && pid >= 0;
-        const int nload = __popc(__ballot_sync(kAll, mine));
+        const uint32_t good = __ballot_sync(kAll, mine);
+        const int nload = __popc(good);
         const uint32_t stage = base + (is_v ? C::OFF_V : C::OFF_K) + st * C::KV_BYTES;
         const uint32_t bar = BAR((F8 ? (is_v ? B_V_RAW : B_K_RAW) : (is_v ? B_V_FULL : B_K_FULL)) + st);
         constexpr int kBytes = F8 ? kBlockSize * D + (KV == 2 ? kBlockSize : 0) : C::NCH * 2048;
-        if (lane == 0) mbar_arrive_expect_tx(bar, nload * kBytes);
+        if (lane == 0) {
+          if constexpr (F8) gbase[C::OFF_GOOD + (is_v ? C::KSTAGES : 0) + st] = (unsigned char)good;
+          mbar_arrive_expect_tx(bar, nload * kBytes);
+        }
         __syncwarp();
         if (!mine) return;
         if constexpr (F8) {  // a block's rows of one head, one behind the other
@@ -881,6 +887,7 @@ __global__ void __launch_bounds__(KV ? kThreadsF8 : kThreads, 1)
     const int full = is_v ? B_V_FULL : B_K_FULL, landed = is_v ? B_V_RAW : B_K_RAW;
     unsigned char* const ring = gbase + (is_v ? C::OFF_V : C::OFF_K);
     const unsigned char* const scs = gbase + C::OFF_SC + (is_v ? C::KSTAGES * 128 : 0);
+    const volatile unsigned char* const copied = gbase + C::OFF_GOOD + (is_v ? C::KSTAGES : 0);
     int st = 0, parity = 0, it = 0;
     bool ok = true;
     for (int t = snake_item(it, ctas); ok && t < ntiles; t = snake_item(++it, ctas)) {
@@ -894,6 +901,10 @@ __global__ void __launch_bounds__(KV ? kThreadsF8 : kThreads, 1)
           if (WIN ? item_sees(tl, key, 1, p.sinks) : key < tl.L) rows |= 1u << n;
         }
         if (!wait(landed + st, parity)) { ok = false; break; }
+        // the rows of a block outside the pool (reported) are zeros
+        const int good = copied[st] >> (2 * cw);
+        constexpr uint32_t kFirst = (1u << NI / 2) - 1u;
+        rows &= (good & 1 ? kFirst : 0u) | (good & 2 ? kFirst << NI / 2 : 0u);
         unsigned char* const stage = ring + st * C::KV_BYTES;
         widen_rows<D, KV == 2>(stage, stage + C::OFF_RAW, scs + st * 128, rows, cw, lane);
         if (lane == 0) mbar_arrive(BAR(full + st));

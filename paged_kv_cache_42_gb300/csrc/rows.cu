@@ -18,7 +18,8 @@ constexpr int kWriteThreads = 256;
 // A lane holds 8 elements of K and the matching 8 of V, a row is D / 8 lanes:
 // its largest element is three or four shuffles away, and the row is never read
 // twice. What bounds it: bytes for many tokens, for a few the launch and two
-// dependent loads.
+// dependent loads. 4 tokens 1.5 us, 2048 tokens of 8 heads at 128 dims 3.6 us (1.9 us
+// of bytes), in a graph of calls.
 // ---------------------------------------------------------------------------------------
 template <int D>
 __global__ void __launch_bounds__(kWriteThreads) pa_write_rows_kernel(const WriteRowsParams p) {
@@ -72,6 +73,7 @@ __global__ void __launch_bounds__(kWriteThreads) pa_write_rows_kernel(const Writ
 // shared memory: the dependent loads are paid once per CTA, and the copy that
 // follows has all of its loads independent. A thread then moves 16 elements of K
 // and of V at a time: one or two 16-byte loads and one 32-byte store each.
+// 64 requests of 512 to 4096 keys, row-scaled: 145 us, 0.93 of the measured copy rate.
 // ---------------------------------------------------------------------------------------
 constexpr int kReadThreads = 256;
 constexpr int kReadMost = 32;  // tokens of a CTA at most

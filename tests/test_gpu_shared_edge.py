@@ -278,3 +278,56 @@ def test_batches_that_do_not_share(pa_lib, fmt):
         binding.set_option("shared_min_kb", kb)
         close(b.run(g), b)
     assert binding.get_device_error(True)[0] == 0
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "rows"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_chunks_blocks_outside_the_pool_count_as_zeros(pa_lib, fmt, d):
+    """Over E4M3 caches the rows of such a block are keys and values of zero, and only its
+    own request's; and so they are in a shared prefix."""
+    from paged_kv_cache_42_gb300 import binding
+    b = sr.Batch([], 16, 4, d, 9, fmt=fmt, before=[(700, 40), (333, 64), (900, 20)])
+    g = b.gpu()
+    binding.get_device_error(True)
+    clean = b.plain(g)
+    empty = int((set(range(len(b.k))) - set(b.tables.flatten().tolist())).pop())
+    for t in ("k", "v"):
+        g[t][empty] = 0
+    g["scales"][empty] = 127
+    spots = [(1, 2), (1, 10), (1, 24)]  # first key tile, second, the chunk's last block
+    for r, c in spots:
+        g["tables"][r, c] = empty
+    want = b.plain(g)
+    assert binding.get_device_error(True)[0] == 0
+    for r, c in spots:
+        g["tables"][r, c] = len(b.k) + 5
+    got = b.plain(g)
+    assert binding.get_device_error(True)[0] == 2
+    assert torch.equal(got, want)
+    assert torch.equal(got[:40], clean[:40]) and torch.equal(got[104:], clean[104:])
+
+    b = sr.Batch([(640, [(9, 1), (40, 1), (7, 1)])], 16, 4, d, 2, fmt=fmt)
+    g = b.gpu()
+    empty = int((set(range(len(b.k))) - set(b.tables.flatten().tolist())).pop())
+    for t in ("k", "v"):
+        g[t][empty] = 0
+    g["scales"][empty] = 127
+    g["tables"][:, 17] = empty
+    want = b.run(g)
+    assert binding.get_device_error(True)[0] == 0
+    g["tables"][:, 17] = -3
+    assert torch.equal(b.run(g), want)
+    assert binding.get_device_error(True)[0] == 2
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group", [1, 2, 4, 8])
+def test_many_tokens_of_many_heads(pa_lib, group, d):
+    """Merged by a warp per (token, KV head) or part of its query heads."""
+    from paged_kv_cache_42_gb300 import binding
+    b = sr.Batch([(160, [(i % 37, 1) for i in range(40)]), (1040, [(i % 5, 1) for i in range(30)])],
+                 16 * group, 16, d, 4, before=[(70, 1)], trailing_tokens=1)
+    g = b.gpu()
+    binding.get_device_error(True)
+    close(b.run(g), b)
+    assert binding.get_device_error(True)[0] == 0
