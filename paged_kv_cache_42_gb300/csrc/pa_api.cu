@@ -644,6 +644,7 @@ pa_status attention_impl(const void* q, const void* k_cache, const void* v_cache
 // batch of its own: units whose `req` is an offset into the tables (row stride 1).
 pa_status shared_impl(const pa_shared_args& a) {
   const int fmt = a.kv_format, group = a.num_kv_heads > 0 ? a.num_q_heads / a.num_kv_heads : 0;
+  const unsigned char* const scales = fmt == 2 ? a.scales : nullptr;  // ignored otherwise
   const float k_scale = fmt == 1 ? a.k_scale : 1.f, v_scale = fmt == 1 ? a.v_scale : 1.f;
   if (fmt < 0 || fmt > 2 || a.num_groups < 0 || a.max_prefix_len < 0) return PA_ERR_INVALID_ARG;
   bool nothing = false;
@@ -655,7 +656,7 @@ pa_status shared_impl(const pa_shared_args& a) {
     return st;
   if (a.num_groups > kMaxSharedGroups) return PA_ERR_UNSUPPORTED;
   if (nothing) return PA_OK;
-  if (fmt == 2 && (!a.scales || !aligned16(a.scales))) return PA_ERR_INVALID_ARG;
+  if (fmt == 2 && (!scales || !aligned16(scales))) return PA_ERR_INVALID_ARG;
   if (a.num_blocks < 1) return PA_ERR_INVALID_ARG;  // no block to attend to
   if (a.num_groups > 0 && (!a.group_start_loc || !a.prefix_lens ||
                            (reinterpret_cast<uintptr_t>(a.group_start_loc) & 3u) ||
@@ -674,7 +675,7 @@ pa_status shared_impl(const pa_shared_args& a) {
                           a.scale, a.out, a.num_reqs, a.num_tokens, a.num_q_heads, a.num_kv_heads,
                           a.head_dim, a.block_size, a.num_blocks, a.max_blocks_per_req,
                           a.max_query_len, a.max_seq_len, 0, 0, 0, fmt, k_scale, v_scale, a.workspace,
-                          a.workspace_bytes, a.stream, a.scales);
+                          a.workspace_bytes, a.stream, scales);
   const WsLayout lay =
       ws_layout(a.num_reqs, a.num_tokens, a.num_q_heads, a.num_kv_heads, a.head_dim);
   DeviceState* d = nullptr;
@@ -747,7 +748,7 @@ pa_status shared_impl(const pa_shared_args& a) {
   pl.prefix_partials = prefix_partials;
   pl.kv_fp8 = fmt;
   pl.v_scale = v_scale;
-  pl.scales = a.scales;
+  pl.scales = scales;
   pl.q = a.q;
   pl.k_cache = a.k_cache;
   pl.v_cache = a.v_cache;
@@ -783,7 +784,7 @@ pa_status shared_impl(const pa_shared_args& a) {
   dp.q = static_cast<const uint16_t*>(a.q);
   dp.k_cache = a.k_cache;
   dp.v_cache = a.v_cache;
-  dp.scales = a.scales;
+  dp.scales = scales;
   dp.v_scale = v_scale;
   dp.block_tables = a.block_tables;
   dp.out = static_cast<uint16_t*>(a.out);

@@ -331,3 +331,18 @@ def test_many_tokens_of_many_heads(pa_lib, group, d):
     binding.get_device_error(True)
     close(b.run(g), b)
     assert binding.get_device_error(True)[0] == 0
+
+
+@pytest.mark.parametrize("groups", [[(640, [(9, 1), (40, 1), (7, 1)])], []])
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_scales_of_another_format_are_ignored(pa_lib, monkeypatch, fmt, groups):
+    from paged_kv_cache_42_gb300 import binding
+    b = sr.Batch(groups, 32, 8, 128, 2, fmt=fmt, before=[(300, 1), (50, 20)])
+    g = b.gpu()
+    want = b.run(g).clone()
+    pack = binding._pack_sh
+    assert pack is not None
+    stray = torch.full((len(b.k), 8, 2, 16), 120, dtype=torch.uint8, device="cuda")
+    monkeypatch.setattr(binding, "_pack_sh",
+                        lambda *a: pack(*a[:3], stray.data_ptr(), *a[4:]))
+    assert torch.equal(b.run(g), want)
