@@ -346,3 +346,36 @@ def test_scales_of_another_format_are_ignored(pa_lib, monkeypatch, fmt, groups):
     monkeypatch.setattr(binding, "_pack_sh",
                         lambda *a: pack(*a[:3], stray.data_ptr(), *a[4:]))
     assert torch.equal(b.run(g), want)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "rows"])
+def test_as_many_groups_as_there_may_be(pa_lib, fmt):
+    from paged_kv_cache_42_gb300 import binding
+    b = sr.Batch([(16 * (1 + i % 3), [(i % 40, 1), (i % 7, 1)] + [(i % 11, 2)] * (i % 5 == 0))
+                  for i in range(1024)], 4, 2, 64, 6, fmt=fmt)
+    g = b.gpu()
+    binding.get_device_error(True)
+    close(b.run(g), b)
+    assert binding.get_device_error(True)[0] == 0
+    for grp in (0, 31, 32, 700, 1023):
+        last = int(b.group_loc[grp + 1]) - 1
+        keep = int(g["tables"][last, 0])
+        other = int(b.group_loc[grp]) - 1 if grp else last + 1  # a request of the next group
+        g["tables"][last, 0] = int(g["tables"][other, 0])
+        b.run(g)
+        assert binding.get_device_error(True) == (6, last)
+        g["tables"][last, 0] = keep
+    b.run(g)
+    assert binding.get_device_error(True)[0] == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_more_tokens_than_the_planner_keeps_on_chip(pa_lib, fmt):
+    from paged_kv_cache_42_gb300 import binding
+    b = sr.Batch([(32, [(i % 9, 1) for i in range(15)])] * 280, 4, 2, 64, 6, fmt=fmt,
+                 after=[(5, 20), (40, 1)])
+    assert len(b.q) > 4096
+    g = b.gpu()
+    binding.get_device_error(True)
+    close(b.run(g), b)
+    assert binding.get_device_error(True)[0] == 0
