@@ -833,7 +833,8 @@ pa_status pa_set_kernel_timer(int kernel_id, void* start_event, void* stop_event
 /*
  *   PA_OPT_SHARED_MIN_KB (default 24576; negative is PA_ERR_INVALID_ARG): a
  *     pa_attention_shared call whose groups would save less reading of K and V
- *     than this many KB, and hold no shared prefix of 4096 keys or more, attends
+ *     than this many KB - for every round of its work that the SMs take, where
+ *     there are many groups - and hold no shared prefix of 4096 keys or more, attends
  *     without sharing: the prefix pass would cost more than it saves. 0: every
  *     group of two tokens shares. Results stay within the attention tolerances.
  */

@@ -222,13 +222,15 @@ constexpr int kMaxSharedGroups = 1024;  // the planner keeps them in shared memo
 // A group of fewer tokens than this on the split-KV path attends on its own: one
 // token reads its prefix once either way.
 constexpr int kSharedMinTokens = 2;
-// A batch whose groups would save less reading than this (PA_OPT_SHARED_MIN_KB), and
+// A batch whose groups would save less reading than this (PA_OPT_SHARED_MIN_KB) for
+// every round of pairs of row tiles that the SMs take, and
 // hold no prefix of kSharedLong keys, attends without sharing: the prefix pass costs some 7 us
 // before its first key. Measured (us, shared / not; G = 4 at 128 dims, bf16): 16 MB saved
 // (32 tokens behind 256 keys) 29.3 / 23.9, 33 MB (512 keys) 30.4 / 28.5, 63 MB (4 x 16
 // tokens, 512) 32.8 / 41.9, 132 MB 38.2 / 58.1; G = 8: 33 MB 34.3 / 36.1; row-scaled:
 // 16 MB 33.8 / 28.9, 31 MB 34.6 / 35.8; but three tokens behind 4096 keys (17 and 8 MB)
-// 26.6 / 29.1 and 31.9 / 35.5.
+// 26.6 / 29.1 and 31.9 / 35.5. Rounds: 256 pairs of tokens behind 128 to 512 keys 145 / 146,
+// behind 64 to 192 129 / 88, 1024 behind 32 to 64 (G = 2 at 64 dims) 125 / 40.
 constexpr int kSharedMinKb = 24 << 10;
 constexpr int kSharedLong = 4096;
 // Prefix work items that the workspace leaves room for at least (an item holds an

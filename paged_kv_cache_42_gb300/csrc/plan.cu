@@ -126,14 +126,15 @@ __device__ __forceinline__ int shared_parts(int tiles, int ct, bool split) {
 }
 
 // CTAs 1 .. of a shared call's plan: every request that shares its group's prefix
-// starts with the same blocks as the first one that does. kCheckCtas CTAs take a group
-// together, a share of its requests each.
-constexpr int kCheckCtas = 4;
+// starts with the same blocks as the first one that does. A few groups are taken by
+// four CTAs each, a share of the requests per CTA; many by one, in turn.
+__host__ __device__ inline int check_parts(int num_groups) { return num_groups > 32 ? 1 : 4; }
 __device__ void check_shared_tables(const PlanParams& p) {
   __shared__ int s_leader;
-  const int warps = blockDim.x >> 5, part = ((int)blockIdx.x - 1) % kCheckCtas;
-  for (int g = ((int)blockIdx.x - 1) / kCheckCtas; g < p.num_groups;
-       g += ((int)gridDim.x - 1) / kCheckCtas) {
+  const int warps = blockDim.x >> 5, parts = check_parts(p.num_groups);
+  const int part = ((int)blockIdx.x - 1) % parts;
+  for (int g = ((int)blockIdx.x - 1) / parts; g < p.num_groups;
+       g += ((int)gridDim.x - 1) / parts) {
     const int a = __ldg(p.group_start + g), b = __ldg(p.group_start + g + 1);
     const int len = __ldg(p.prefix_lens + g);
     if (threadIdx.x == 0) {
@@ -159,7 +160,7 @@ __device__ void check_shared_tables(const PlanParams& p) {
       const int32_t* const want = p.block_tables + (size_t)leader * p.max_blocks_per_req;
       // a warp takes a request at a time, with several loads in flight per lane
       for (int r = leader + 1 + part * warps + (int)(threadIdx.x >> 5); r < b;
-           r += kCheckCtas * warps) {
+           r += parts * warps) {
         if (!check_request(p, r, q0, qlen, L, false) || !shares(p, qlen, L, blocks)) continue;
         const int32_t* const got = p.block_tables + (size_t)r * p.max_blocks_per_req;
         bool same = true;
@@ -253,6 +254,9 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
   __shared__ int s_full[SHARED ? kMaxSharedGroups : 1], s_split[SHARED ? kMaxSharedGroups : 1];
   __shared__ int s_start[SHARED ? kMaxSharedGroups + 1 : 1], s_len[SHARED ? kMaxSharedGroups : 1];
   __shared__ unsigned long long s_best, s_saved;
+  __shared__ int s_pairs;  // pairs of row tiles of the groups that could share
+  // of each candidate for the chunk length: items of a kv head, steps of the longest
+  __shared__ int s_items[SHARED ? kSharedCandidates : 1], s_longest[SHARED ? kSharedCandidates : 1];
   bool sharing = false;  // whether any group does, and it pays (the same for every thread)
   // what this thread's (first) request is, kept from one pass over them to the next
   int my_q0 = 0, my_qlen = 0, my_L = 0, my_group = -1, my_blocks = 0;
@@ -289,27 +293,39 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
       atomicMin(&s_lo[g], q0);
       atomicMax(&s_hi[g], q0 + qlen);
     }
+    if (threadIdx.x < kSharedCandidates) s_items[threadIdx.x] = s_longest[threadIdx.x] = 0;
     if (threadIdx.x == 0) {
       s_best = ~0ull;
       s_saved = 0ull;
+      s_pairs = 0;
     }
     __syncthreads();
     // what sharing saves of reading, and whether that pays for the prefix pass
     // (atomics of 64 bits on shared memory are loops: one per warp)
     unsigned long long saved = 0;
+    int shared_pairs = 0;
     for (int g = threadIdx.x; g < p.num_groups; g += blockDim.x)
-      if (s_count[g] >= kSharedMinTokens)
-        saved += s_len[g] >= kSharedLong
-                     ? max(p.shared_min_bytes, 1ull)
-                     : (unsigned long long)(s_count[g] - 1) * (unsigned)(s_len[g] / kBlockSize) *
-                           (unsigned)p.position_bytes;
+      if (s_count[g] >= kSharedMinTokens) {
+        saved += (unsigned long long)(s_count[g] - 1) * (unsigned)(s_len[g] / kBlockSize) *
+                     (unsigned)p.position_bytes +
+                 (s_len[g] >= kSharedLong ? p.shared_min_bytes : 0ull);
+        shared_pairs += (s_hi[g] - s_lo[g] + tok_per_item - 1) / tok_per_item;
+      }
     if ((int)(threadIdx.x & ~31u) < p.num_groups) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) saved += __shfl_xor_sync(kFull, saved, o);
-      if ((threadIdx.x & 31) == 0) atomicAdd(&s_saved, saved);
+      for (int o = 16; o > 0; o >>= 1) {
+        saved += __shfl_xor_sync(kFull, saved, o);
+        shared_pairs += __shfl_xor_sync(kFull, shared_pairs, o);
+      }
+      if ((threadIdx.x & 31) == 0) {
+        atomicAdd(&s_saved, saved);
+        atomicAdd(&s_pairs, shared_pairs);
+      }
     }
     __syncthreads();
-    sharing = s_saved > 0 && s_saved >= p.shared_min_bytes;
+    const unsigned rounds =
+        (unsigned)(((long long)s_pairs * p.num_kv_heads + p.num_sms - 1) / p.num_sms);
+    sharing = s_saved > 0 && s_saved >= p.shared_min_bytes * rounds;
   }
   if (SHARED && sharing) {
     for (int g = threadIdx.x; g < p.num_groups; g += blockDim.x) {
@@ -320,23 +336,33 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(PlanParams p) {
       s_split[g] = pairs - s_full[g];
     }
     __syncthreads();
-    // The key chunks' length: of a thread's candidate, the time of the rounds that its
-    // items take on the SMs, in steps.
-    const int ct = p.chunk_tiles + (int)threadIdx.x;
-    if (threadIdx.x < kSharedCandidates) {
-      float items = 0.f;
-      int longest = 0;  // steps
+    // The key chunks' length: of each candidate, the time of the rounds that its items
+    // take on the SMs, in steps. Many groups: every fourth length, and more threads to
+    // each (planning of 256 groups 30 -> 20 us, of 1024 68 -> 33).
+    const int step = p.num_groups > 64 ? 4 : 1, cands = kSharedCandidates / step;
+    {
+      const int c = (int)threadIdx.x % cands, ct = p.chunk_tiles + c * step;
+      int items = 0, longest = 0;  // steps
       // (an estimate: the divisions need not be exact)
       const float by = 1.f / (float)ct, by_split = 1.f / (float)shared_len(ct, true);
-      for (int g = 0; g < p.num_groups; ++g) {
+      for (int g = (int)threadIdx.x / cands; g < p.num_groups; g += (int)blockDim.x / cands) {
         const int tiles = s_tiles[g];
         if (tiles == 0) continue;
         const int full = s_full[g], split = s_split[g];
-        items += (float)full * ceilf((float)tiles * by) + (float)split * ceilf((float)tiles * by_split);
+        items += full * (int)ceilf((float)tiles * by) + split * (int)ceilf((float)tiles * by_split);
         longest = max(longest, min(ct, full > 0 ? tiles : (2 * tiles + 2) / 3));
       }
-      const float rounds = ceilf(items * (float)p.num_kv_heads / (float)p.num_sms);
-      const float cost = rounds * (float)(longest + kSharedItemSteps);
+      if (items > 0) {
+        atomicAdd(&s_items[c], items);
+        atomicMax(&s_longest[c], longest);
+      }
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < cands) {
+      const int ct = p.chunk_tiles + (int)threadIdx.x * step;
+      const float rounds =
+          ceilf((float)s_items[threadIdx.x] * (float)p.num_kv_heads / (float)p.num_sms);
+      const float cost = rounds * (float)(s_longest[threadIdx.x] + kSharedItemSteps);
       unsigned long long best = (unsigned long long)__float_as_uint(cost) << 32 | (unsigned)ct;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
@@ -566,7 +592,12 @@ cudaError_t launch_plan_t(const PlanParams& p, cudaStream_t s) {
   // a plan needs) before completing.
   cudaLaunchConfig_t cfg = {};
   // shared calls: CTAs of their own check the groups' tables
-  cfg.gridDim = dim3(SHARED ? 1 + kCheckCtas * (p.num_groups < 32 ? p.num_groups : 32) : 1);
+  if (SHARED) {
+    const int checks = check_parts(p.num_groups) * p.num_groups;  // at most 128, or of one part
+    cfg.gridDim = dim3(1 + (checks > 128 && checks > p.num_sms - 1 ? max(128, p.num_sms - 1) : checks));
+  } else {
+    cfg.gridDim = dim3(1);
+  }
   // A batch with no tensor-core work needs no bucket sort: a block sized to the
   // batch (fewer warps per barrier) plans it faster.
   int threads = kPlanThreads;
